@@ -106,6 +106,7 @@ enum {
     ART_STATUS_BAD_PROBE = 16,  /* probe index out of range or repeated              */
     ART_STATUS_TIMEOUT = 32,    /* a bounded wait inside the kernel gave up          */
     ART_STATUS_INTERNAL = 64,   /* an internal consistency check failed (the access was skipped) */
+    ART_STATUS_BAD_OFFSETS = 128, /* q_offsets / group_offsets that do not rise within their range */
 };
 
 /* Bytes of device workspace art_decode / dense_decode need for `shape`.
@@ -267,6 +268,109 @@ int art_select_blocks(const void* q, const void* k_cache, const int32_t* block_t
                       const int32_t* seq_lens, float top_frac, int32_t keep_last,
                       int32_t order, int32_t* visit_order, const art_shape* shape,
                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The cache's other side: writing new tokens, attending with several of them,
+ * and decoding a batch that shares a prefix. (Additions of this library: the
+ * ART paper reads a cache that a serving engine has filled.) They take the
+ * shape of art_decode (its checks apply; max_visit and num_probe are not used),
+ * its cache and block-table layout, its workspace and status rules: bad device
+ * data never faults, sets a bit of the status word and leaves the results
+ * described below. Sequences of one call are independent of each other.
+ *
+ * q_offsets int32 [batch + 1]: the new tokens of sequence b are rows
+ * q_offsets[b] .. q_offsets[b+1]-1 of q (and k, v, out), and seq_lens[b] counts
+ * them already: they are the last ones of the sequence. 0 <= q_offsets[0] <=
+ * ... <= q_offsets[batch] <= num_tokens. Rows that no sequence holds are
+ * neither read nor written.
+ */
+
+/* The position rotation of art_append_kv. */
+typedef struct art_rope {
+    int32_t rot_dim;     /* leading columns of a head that turn: even, 0..head_dim */
+    int32_t interleaved; /* pairs 0: (j, j + rot_dim / 2), 1: (2j, 2j + 1)         */
+    float scale;         /* factor of the turned columns (1 where there is none)   */
+    int32_t reserved[5]; /* must be zero                                           */
+} art_rope;
+
+/*
+ * Appends keys and values to the paged cache and rotates keys and queries to
+ * their positions. For new token i (of n) of sequence b, with cache place
+ * s = seq_len - n + i and position pos = positions[t], or s where positions is
+ * NULL: angle_j = pos * inv_freq[j] (formed in 64 bits), and every pair (x, y)
+ * of a query or key head becomes scale * (x cos - y sin, y cos + x sin).
+ *   q, k, v    rows of num_q_heads (num_kv_heads) heads of head_dim; token t
+ *              starts q_stride (k_stride, v_stride) elements after token t - 1,
+ *              so that they may be slices of one projection's rows. Strides are
+ *              whole 16-byte chunks and no shorter than a row; pointers are
+ *              16-byte aligned. q and q_out may both be NULL.
+ *   q_offsets  NULL: one new token for each sequence, num_tokens = batch
+ *   positions  int32 [num_tokens] or NULL
+ *   inv_freq   fp32 [rot_dim / 2] (any scaling of the frequencies is in it)
+ *   q_out      [num_tokens][num_q_heads][head_dim]; may be q itself where
+ *              q_stride is num_q_heads * head_dim
+ *   k_cache, v_cache: the pool; only the new tokens' rows are written. Two
+ *              tokens of a call must not share a cache row.
+ *   workspace  art_append_workspace_bytes(shape) bytes: the status word
+ * A sequence with a bad length (below its new tokens, or beyond the table)
+ * appends nothing and its q_out rows are zero; a token whose page id lies
+ * outside the pool is not appended; tokens of a sequence with bad offsets are
+ * skipped. One kernel, nothing else on the stream.
+ */
+size_t art_append_workspace_bytes(const art_shape* shape);
+int art_append_kv(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                  int64_t v_stride, const int32_t* q_offsets, int32_t num_tokens, const int32_t* positions,
+                  const int32_t* block_table, const int32_t* seq_lens, const float* inv_freq,
+                  const art_rope* rope, void* q_out, void* k_cache, void* v_cache, const art_shape* shape,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of several new tokens of each sequence over its cached tokens:
+ * prompt chunks, drafted tokens to verify; with causal 0 cross attention to an
+ * encoder's states of another length.
+ *   causal 1: new token i of n sees the keys below seq_len - n + i + 1 (the new
+ *             tokens' own keys are in the cache already); seq_len >= n
+ *   causal 0: every new token sees all seq_len keys, whatever n is
+ *   q, out    [num_tokens][num_q_heads][head_dim]
+ *   workspace dense_extend_workspace_bytes(shape, num_tokens) bytes (0: sizes
+ *             beyond the supported range)
+ * A token that sees no key, and every token of a sequence with a bad length or
+ * page, gets a zero output. With bad offsets no output is written. Keys and
+ * values outside a sequence's length may hold anything, NaN included; a value
+ * that some new tokens of a sequence see must be finite for the others too.
+ * Supported: 2^30 rows num_tokens * G and 2^30 tokens a sequence.
+ */
+size_t dense_extend_workspace_bytes(const art_shape* shape, int32_t num_tokens);
+int dense_extend(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                 const int32_t* seq_lens, const int32_t* q_offsets, int32_t num_tokens, int32_t causal,
+                 void* out, const art_shape* shape, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Decode attention (one query token per sequence, full scan, as dense_decode in
+ * the natural order) of a batch whose sequences share prefixes: the keys of a
+ * shared prefix are read once for its group.
+ *   group_offsets int32 [num_groups + 1]: group j is sequences
+ *                 group_offsets[j] .. group_offsets[j+1]-1; 0 <= rising <= batch.
+ *                 Sequences of no group share nothing.
+ *   prefix_lens   int32 [num_groups]: the tokens [0, prefix_lens[j]) of every
+ *                 member are those of the group's first sequence, read through
+ *                 ITS block_table row (which holds their pages whatever its own
+ *                 length); a member's own row is read from the page that holds
+ *                 its token prefix_lens[j] on. A prefix may end inside a page.
+ *   seq_lens      the whole length, prefix included; a member shorter than the
+ *                 prefix sees only its own length of it, one of length 0 (a
+ *                 padded batch) nothing: zero output.
+ *   num_groups 0: group_offsets and prefix_lens may be NULL
+ *   workspace     dense_decode_shared_workspace_bytes(shape, num_groups) bytes
+ * A sequence with a bad length or page gets a zero output; a bad prefix length
+ * or prefix page gives the whole group zero outputs; with bad offsets no output
+ * is written. Values that some members see must be finite for the others too.
+ */
+size_t dense_decode_shared_workspace_bytes(const art_shape* shape, int32_t num_groups);
+int dense_decode_shared(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                        const int32_t* seq_lens, const int32_t* group_offsets, const int32_t* prefix_lens,
+                        int32_t num_groups, void* out, const art_shape* shape, void* workspace,
+                        size_t workspace_bytes, void* stream);
 
 /* Copies the device status word out of `workspace` (a blocking copy; call it
  * after the stream has finished the call of interest). Returns ART_OK or

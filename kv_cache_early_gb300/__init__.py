@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels of libart.so. The names follow the C ABI: `art_decode`,
-`dense_decode`, `art_workspace_bytes`, `art_read_device_status`.
+`dense_decode`, `art_append_kv`, `dense_extend`, `dense_decode_shared`,
+`art_workspace_bytes`, `art_read_device_status`.
 Tensors are torch CUDA tensors; PyTorch supplies device memory and streams.
 
 The library must have been built (`kv_cache_early_gb300.build.build()`);
@@ -20,12 +21,15 @@ LIB_PATH = os.path.join(HERE, "libart.so")
 ART_DTYPE_BF16, ART_DTYPE_F32 = 0, 1
 ART_OK, ART_ERR_INVALID_ARG, ART_ERR_UNSUPPORTED, ART_ERR_WORKSPACE, ART_ERR_LAUNCH = 0, -1, -2, -3, -4
 STATUS_BITS = {1: "bad visit entry", 2: "duplicate visit entry", 4: "bad page id", 8: "bad seq_len",
-               16: "bad probe index", 32: "wait timeout", 64: "internal check failed"}
+               16: "bad probe index", 32: "wait timeout", 64: "internal check failed",
+               128: "bad offsets"}
 EXPORTS = ("art_workspace_bytes", "art_decode_path", "dense_decode_path", "art_decode", "art_decode_ex",
            "dense_decode",
            "art_decode_static", "art_read_static_status", "art_read_device_status",
            "art_status_string", "art_last_cuda_error", "art_set_timing_events",
-           "art_select_workspace_bytes", "art_select_blocks")
+           "art_select_workspace_bytes", "art_select_blocks",
+           "art_append_workspace_bytes", "art_append_kv", "dense_extend_workspace_bytes", "dense_extend",
+           "dense_decode_shared_workspace_bytes", "dense_decode_shared")
 
 
 class ArtShape(ctypes.Structure):
@@ -36,6 +40,11 @@ class ArtShape(ctypes.Structure):
 
 class ArtOptions(ctypes.Structure):
     _fields_ = [("probe_heads", ctypes.c_int32), ("reserved", ctypes.c_int32 * 7)]
+
+
+class ArtRope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32 * 5)]
 
 
 class ArtError(RuntimeError):
@@ -86,6 +95,19 @@ def lib(path: str = LIB_PATH) -> ctypes.CDLL:
             L.art_select_workspace_bytes.restype = SZ
             L.art_select_blocks.argtypes = [P, P, P, P, F32, I32, I32, P, SP, P, SZ, P]
             L.art_select_blocks.restype = ctypes.c_int
+            I64, RP = ctypes.c_int64, ctypes.POINTER(ArtRope)
+            L.art_append_workspace_bytes.argtypes = [SP]
+            L.art_append_workspace_bytes.restype = SZ
+            L.art_append_kv.argtypes = [P, P, P, I64, I64, I64, P, I32, P, P, P, P, RP, P, P, P, SP, P, SZ, P]
+            L.art_append_kv.restype = ctypes.c_int
+            L.dense_extend_workspace_bytes.argtypes = [SP, I32]
+            L.dense_extend_workspace_bytes.restype = SZ
+            L.dense_extend.argtypes = [P, P, P, P, P, P, I32, I32, P, SP, P, SZ, P]
+            L.dense_extend.restype = ctypes.c_int
+            L.dense_decode_shared_workspace_bytes.argtypes = [SP, I32]
+            L.dense_decode_shared_workspace_bytes.restype = SZ
+            L.dense_decode_shared.argtypes = [P, P, P, P, P, P, P, I32, P, SP, P, SZ, P]
+            L.dense_decode_shared.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -205,6 +227,129 @@ def art_select_blocks(q, k_cache, block_table, seq_lens, top_frac, keep_last, vi
                                  int(keep_last), int(order), _ptr(visit_order), ctypes.byref(shape),
                                  _ptr(workspace), ws_bytes,
                                  _stream(stream))
+    if check:
+        _check(rc)
+    return rc
+
+
+def _checked(shape: ArtShape, data=(), ints=()):
+    """Raises ArtError unless the tensors have the shape's dtype (`data`) or int32 (`ints`), lie on the
+    current device and are dense in the sizes given. Entries: (name, tensor, sizes); a size of None is
+    any, a tensor may be None. What the C ABI takes as bare pointers cannot be checked below it."""
+    import torch
+    want = torch.bfloat16 if shape.dtype == ART_DTYPE_BF16 else torch.float32
+    for group, dt in ((data, want), (ints, torch.int32)):
+        for name, t, sizes in group:
+            if t is None:
+                continue
+            if t.dtype != dt:
+                raise ArtError(f"{name} is {t.dtype}, not {dt}")
+            _here(name, t)
+            if len(t.shape) != len(sizes) or any(w is not None and n != w for n, w in zip(t.shape, sizes)):
+                raise ArtError(f"{name} is {tuple(t.shape)}, not {sizes}")
+            if not t.is_contiguous():
+                raise ArtError(f"{name} is not contiguous")
+
+
+def _here(name, t):
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ArtError(f"{name} is on {t.device}, not on the current CUDA device")
+
+
+def _scratch(workspace):
+    _here("workspace", workspace)
+    if not workspace.is_contiguous():
+        raise ArtError("workspace is not contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
+def art_append_workspace_bytes(shape: ArtShape) -> int:
+    return int(lib().art_append_workspace_bytes(ctypes.byref(shape)))
+
+
+def art_append_kv(q, k, v, block_table, seq_lens, q_offsets, inv_freq, q_out, k_cache, v_cache, shape: ArtShape,
+                  workspace, rot_dim: int, interleaved: bool = False, scale: float = 1.0, positions=None,
+                  stream=None, check: bool = True) -> int:
+    """Append new tokens' keys and values to the paged cache and rotate keys and queries to their
+    positions (see include/art.h). q, k, v: [tokens, heads, head_dim], dense in the last two
+    dimensions (slices of one projection's rows will do); q and q_out may be None; q_offsets None:
+    one new token for each sequence."""
+    tokens, hkv, d = int(k.shape[0]), shape.num_kv_heads, shape.head_dim
+    pool = (shape.num_pages_total, hkv, shape.page_size, d)
+    _checked(shape, (("q_out", q_out, (tokens, shape.num_q_heads, d)), ("k_cache", k_cache, pool),
+                     ("v_cache", v_cache, pool)),
+             (("block_table", block_table, (shape.batch, shape.max_pages_per_seq)),
+              ("seq_lens", seq_lens, (shape.batch,)), ("q_offsets", q_offsets, (shape.batch + 1,)),
+              ("positions", positions, (tokens,))))
+    for name, t, heads in (("q", q, shape.num_q_heads), ("k", k, hkv), ("v", v, hkv)):
+        if t is None:
+            continue
+        if t.dtype != k_cache.dtype or t.device != k_cache.device:
+            raise ArtError(f"{name} is {t.dtype} on {t.device}, the cache {k_cache.dtype} on {k_cache.device}")
+        dense = tokens == 0 or (t.stride(2) == 1 and (heads == 1 or t.stride(1) == d))
+        if tuple(t.shape) != (tokens, heads, d) or not dense:
+            raise ArtError(f"{name} is {tuple(t.shape)} with strides {t.stride()}: not dense rows of {heads} x {d}")
+    if inv_freq is not None and (inv_freq.dtype.itemsize != 4 or not inv_freq.is_floating_point() or
+                                 inv_freq.numel() != rot_dim // 2 or inv_freq.device != k_cache.device or
+                                 not inv_freq.is_contiguous()):
+        raise ArtError(f"inv_freq is not fp32 [{rot_dim // 2}] beside the cache")
+    if tokens <= 1:  # a lone row's stride is never used: any dense one
+        step = lambda t, h: h * d
+    else:
+        step = lambda t, h: t.stride(0)
+    rope = ArtRope(rot_dim=int(rot_dim), interleaved=int(bool(interleaved)), scale=float(scale))
+    rc = lib().art_append_kv(_ptr(q), _ptr(k), _ptr(v), 0 if q is None else step(q, shape.num_q_heads), step(k, hkv),
+                             step(v, hkv), _ptr(q_offsets), tokens, _ptr(positions), _ptr(block_table),
+                             _ptr(seq_lens), _ptr(inv_freq), ctypes.byref(rope), _ptr(q_out), _ptr(k_cache),
+                             _ptr(v_cache), ctypes.byref(shape), _ptr(workspace), _scratch(workspace),
+                             _stream(stream))
+    if check:
+        _check(rc)
+    return rc
+
+
+def _attend_checked(q, k_cache, v_cache, block_table, seq_lens, out, shape, tokens, ints):
+    pool = (shape.num_pages_total, shape.num_kv_heads, shape.page_size, shape.head_dim)
+    rows = (tokens, shape.num_q_heads, shape.head_dim)
+    _checked(shape, (("q", q, rows), ("k_cache", k_cache, pool), ("v_cache", v_cache, pool), ("out", out, rows)),
+             (("block_table", block_table, (shape.batch, shape.max_pages_per_seq)),
+              ("seq_lens", seq_lens, (shape.batch,))) + ints)
+
+
+def dense_extend_workspace_bytes(shape: ArtShape, num_tokens: int) -> int:
+    return int(lib().dense_extend_workspace_bytes(ctypes.byref(shape), int(num_tokens)))
+
+
+def dense_extend(q, k_cache, v_cache, block_table, seq_lens, q_offsets, out, shape: ArtShape, workspace,
+                 causal: bool = True, stream=None, check: bool = True) -> int:
+    """Attention of several new tokens of each sequence over its cached tokens (see include/art.h);
+    causal False: every new token sees all of them (cross attention)."""
+    tokens = int(q.shape[0])
+    _attend_checked(q, k_cache, v_cache, block_table, seq_lens, out, shape, tokens,
+                    (("q_offsets", q_offsets, (shape.batch + 1,)),))
+    rc = lib().dense_extend(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
+                            _ptr(q_offsets), tokens, int(bool(causal)), _ptr(out), ctypes.byref(shape),
+                            _ptr(workspace), _scratch(workspace), _stream(stream))
+    if check:
+        _check(rc)
+    return rc
+
+
+def dense_decode_shared_workspace_bytes(shape: ArtShape, num_groups: int) -> int:
+    return int(lib().dense_decode_shared_workspace_bytes(ctypes.byref(shape), int(num_groups)))
+
+
+def dense_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offsets, prefix_lens, out,
+                        shape: ArtShape, workspace, stream=None, check: bool = True) -> int:
+    """Decode attention of a batch whose groups of sequences share prefixes (see include/art.h);
+    group_offsets and prefix_lens None: no groups."""
+    groups = 0 if prefix_lens is None else int(prefix_lens.shape[0])
+    _attend_checked(q, k_cache, v_cache, block_table, seq_lens, out, shape, shape.batch,
+                    (("group_offsets", group_offsets, (groups + 1,)), ("prefix_lens", prefix_lens, (groups,))))
+    rc = lib().dense_decode_shared(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
+                                   _ptr(group_offsets), _ptr(prefix_lens), groups, _ptr(out), ctypes.byref(shape),
+                                   _ptr(workspace), _scratch(workspace), _stream(stream))
     if check:
         _check(rc)
     return rc

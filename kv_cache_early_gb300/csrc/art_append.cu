@@ -1,0 +1,358 @@
+// art_append.cu -- appending new tokens to the paged cache, with the position
+// rotation applied on the way.
+//
+// For token t of sequence b, the i-th of its n_b new tokens, with cache place
+// s = seq_len_b - n_b + i (seq_lens count the new tokens already) and position
+// pos (s, or the caller's):
+//     angle_j = pos * inv_freq_j                              j < rot_dim / 2
+//     (x_j, x_j') -> scale * (x_j cos - x_j' sin, x_j' cos + x_j sin)
+// for every query head (into q_out) and every key head (into the cache); the
+// pairs are (j, j + rot_dim / 2) or, interleaved, (2j, 2j + 1); columns from
+// rot_dim on and the values are copied. The cache row of KV head g is
+// (page(s / Ps) * Hkv + g) * Ps + s % Ps.
+//
+// The angle is formed and reduced to [-pi, pi] in 64 bits: pos * inv_freq reaches
+// 1e5..1e6 radians, where a 32-bit product is off by hundredths of a radian. The
+// reduced angle is rounded once to 32 bits (2^-24 * pi), and sine, cosine and the
+// rotation are 32-bit; a bf16 result is rounded once at the store.
+//
+// Bound: HBM, 2 (Hq + 2 Hkv) d bytes in and as many out a token. One CTA per
+// token: its rows are loaded (independent of the position) before the chain
+// offsets -> seq_len -> page id -> angles, so a decode step waits for the longer
+// of the two and not for their sum. One more CTA (block 0) checks the device
+// data of the call and stores the status word, so that no memset precedes the
+// kernel; every token's CTA checks what it uses by itself.
+#include "art_common.cuh"
+
+namespace art {
+
+constexpr int kAppendThreads = 256;
+constexpr int kMaxRotHalf = 64;  // rot_dim / 2 at most (head_dim 128)
+
+struct AppendParams {
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;  // elements between tokens
+    const int32_t* q_offsets;                // null: token b is sequence b's only new one
+    const int32_t* positions;                // null: the token's place in the cache
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    const float* inv_freq;
+    void *q_out, *k_cache, *v_cache;
+    WsHeader* hdr;
+    int B, T, Hq, Hkv, Ps, max_pages, num_pages;
+    int rot, interleaved;
+    float scale;
+};
+
+template <bool kBF16>
+struct Vec16 {  // 16 bytes of a row as fp32 values
+    static constexpr int N = kBF16 ? 8 : 4;
+    float x[N];
+    __device__ __forceinline__ explicit Vec16(const uint4& u) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kBF16) {
+                x[2 * i] = bf16_lo_f(w[i]);
+                x[2 * i + 1] = bf16_hi_f(w[i]);
+            } else {
+                x[i] = __uint_as_float(w[i]);
+            }
+        }
+    }
+    __device__ __forceinline__ uint4 pack() const {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kBF16) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+            else w[i] = __float_as_uint(x[i]);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// The call's device data: offsets, lengths and the pages of the new tokens. One
+// thread per sequence; sequences with many pages are shared out over its warp.
+__device__ void append_check(const AppendParams& p) {
+    __shared__ int s_err;
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid == 0) s_err = 0;
+    __syncthreads();
+    int err = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kAppendThreads) {
+        const int b = b0 + tid;
+        int first = 0, np = 0;
+        if (b < p.B) {
+            const int len = p.seq_lens[b];
+            const int lo = p.q_offsets ? p.q_offsets[b] : b, hi = p.q_offsets ? p.q_offsets[b + 1] : b + 1;
+            if (lo < 0 || hi < lo || hi > p.T) {
+                err |= ART_STATUS_BAD_OFFSETS;
+            } else if (len < hi - lo || (long long)len > (long long)p.max_pages * p.Ps) {
+                err |= ART_STATUS_BAD_SEQLEN;
+            } else if (hi > lo) {
+                first = (len - (hi - lo)) / p.Ps;
+                np = (len - 1) / p.Ps - first + 1;
+            }
+        }
+        auto check = [&](int row, int col) {
+            const int pg = p.block_table[(size_t)row * p.max_pages + col];
+            if (pg < 0 || pg >= p.num_pages) err |= ART_STATUS_BAD_PAGE;
+        };
+        const bool few = np <= 4;
+        if (few)
+            for (int k = 0; k < np; ++k) check(b, first + k);
+        unsigned many = __ballot_sync(0xffffffffu, !few);
+        while (many) {
+            const int src = __ffs(many) - 1;
+            many &= many - 1;
+            const int f = __shfl_sync(0xffffffffu, first, src), n = __shfl_sync(0xffffffffu, np, src);
+            for (int k = lane; k < n; k += 32) check(b0 + (tid & ~31) + src, f + k);
+        }
+    }
+    if (err) atomicOr(&s_err, err);
+    __syncthreads();
+    if (tid == 0) p.hdr->status = s_err;
+}
+
+// kVec: every 16-byte chunk of a row is copied, or rotated with itself or with one
+// other chunk (rot_dim / 2, or interleaved rot_dim, a multiple of the chunk's
+// elements); otherwise element by element.
+template <bool kBF16, int D, bool kVec>
+__global__ void __launch_bounds__(kAppendThreads) art_append_kernel(const AppendParams p) {
+    using E = Elem<kBF16>;
+    constexpr int N = Vec16<kBF16>::N;
+    constexpr int ROWB = D * E::kBytes;
+    constexpr int PF = 2;  // units a thread loads at once
+    __shared__ float s_cos[kMaxRotHalf], s_sin[kMaxRotHalf];
+    if (blockIdx.x == 0) {
+        append_check(p);
+        return;
+    }
+    const int t = blockIdx.x - 1, tid = threadIdx.x;
+    const int nq = p.q ? p.Hq : 0, half = p.rot / 2;
+    // units: of a rotated row (queries, then keys) its chunk pairs, or its single chunks; then the values' chunks
+    const bool pairs = kVec && !p.interleaved && half > 0;
+    const int npair = pairs ? half / N : 0;
+    const int per = kVec ? (pairs ? npair + (D - p.rot) / N : D / N) : D;
+    const int vper = kVec ? D / N : D;
+    const int nrot = (nq + p.Hkv) * per, units = nrot + p.Hkv * vper;
+    auto row_of = [&](int r, const char*& src) {  // r: query heads, key heads, value heads
+        if (r < nq) src = static_cast<const char*>(p.q) + ((size_t)t * p.q_stride + (size_t)r * D) * E::kBytes;
+        else if (r < nq + p.Hkv) src = static_cast<const char*>(p.k) + ((size_t)t * p.k_stride + (size_t)(r - nq) * D) * E::kBytes;
+        else src = static_cast<const char*>(p.v) + ((size_t)t * p.v_stride + (size_t)(r - nq - p.Hkv) * D) * E::kBytes;
+    };
+    auto unit_of = [&](int u, int& r, int& c) {
+        if (u < nrot) {
+            r = u / per;
+            c = u - r * per;
+        } else {
+            r = (u - nrot) / vper;
+            c = (u - nrot) - r * vper;
+            r += nq + p.Hkv;
+        }
+    };
+    uint4 a[PF], b2[PF];
+    auto load = [&](int u0) {
+        if constexpr (kVec) {
+#pragma unroll
+            for (int k = 0; k < PF; ++k) {
+                const int u = u0 + k * kAppendThreads;
+                if (u >= units) continue;
+                int r, c;
+                const char* src;
+                unit_of(u, r, c);
+                row_of(r, src);
+                const bool pair = pairs && u < nrot && c < npair;
+                const int ch = pairs && u < nrot && !pair ? c + npair : c;  // copied chunks follow the rotated ones
+                a[k] = *reinterpret_cast<const uint4*>(src + ch * 16);
+                if (pair) b2[k] = *reinterpret_cast<const uint4*>(src + (ch + npair) * 16);
+            }
+        }
+    };
+    load(tid);
+
+    // the token's sequence, place and page
+    int b = t, i = 0, n = 1;
+    if (p.q_offsets) {
+        int cnt = 0;  // sequences that end at or before t
+        for (int base = 0; base < p.B; base += kAppendThreads)
+            cnt += __syncthreads_count(base + tid < p.B && p.q_offsets[base + tid + 1] <= t);
+        if (cnt >= p.B) return;  // behind the last sequence
+        b = cnt;
+        const int lo = p.q_offsets[b];
+        i = t - lo;
+        n = p.q_offsets[b + 1] - lo;
+        if (i < 0 || i >= n) return;  // offsets that do not hold t (flagged by block 0)
+    }
+    const int len = p.seq_lens[b];
+    const bool ok = len >= n && (long long)len <= (long long)p.max_pages * p.Ps;
+    const int s = len - n + i;
+    int page = -1;
+    if (ok) {
+        page = p.block_table[(size_t)b * p.max_pages + s / p.Ps];
+        if (page < 0 || page >= p.num_pages) page = -1;
+    }
+    if (tid < half) {
+        const int pos = p.positions ? p.positions[t] : s;
+        double x = (double)pos * (double)p.inv_freq[tid];
+        x -= 6.283185307179586476925 * rint(x * 0.159154943091895335769);
+        float sn, cs;
+        sincosf((float)x, &sn, &cs);
+        s_cos[tid] = cs * p.scale;
+        s_sin[tid] = sn * p.scale;
+    }
+    __syncthreads();
+
+    char* kdst = static_cast<char*>(p.k_cache);
+    char* vdst = static_cast<char*>(p.v_cache);
+    auto dst_of = [&](int r) -> char* {
+        if (r < nq) return static_cast<char*>(p.q_out) + ((size_t)t * p.Hq + r) * ROWB;
+        if (page < 0) return nullptr;
+        const int g = r < nq + p.Hkv ? r - nq : r - nq - p.Hkv;
+        const size_t row = ((size_t)page * p.Hkv + g) * p.Ps + (s & (p.Ps - 1));
+        return (r < nq + p.Hkv ? kdst : vdst) + row * ROWB;
+    };
+    for (int u0 = tid; u0 < units; u0 += PF * kAppendThreads) {
+        if (kVec && u0 != tid) load(u0);
+#pragma unroll
+        for (int k = 0; k < PF; ++k) {
+            const int u = u0 + k * kAppendThreads;
+            if (u >= units) continue;
+            int r, c;
+            unit_of(u, r, c);
+            char* dst = dst_of(r);
+            if (!dst) continue;
+            const bool turned = u < nrot;
+            if constexpr (kVec) {
+                const bool pair = pairs && turned && c < npair;
+                const int ch = pairs && turned && !pair ? c + npair : c;
+                if (!ok) {  // no position: queries of a bad sequence are zero
+                    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>(dst + ch * 16) = z;
+                    if (pair) *reinterpret_cast<uint4*>(dst + (ch + npair) * 16) = z;
+                } else if (pair) {
+                    Vec16<kBF16> x(a[k]), y(b2[k]);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const float cs = s_cos[c * N + e], sn = s_sin[c * N + e], xe = x.x[e], ye = y.x[e];
+                        x.x[e] = xe * cs - ye * sn;
+                        y.x[e] = ye * cs + xe * sn;
+                    }
+                    *reinterpret_cast<uint4*>(dst + ch * 16) = x.pack();
+                    *reinterpret_cast<uint4*>(dst + (ch + npair) * 16) = y.pack();
+                } else if (turned && p.interleaved && ch * N < p.rot) {
+                    Vec16<kBF16> x(a[k]);
+#pragma unroll
+                    for (int e = 0; e < N; e += 2) {
+                        const int j = (ch * N + e) / 2;
+                        const float cs = s_cos[j], sn = s_sin[j], xe = x.x[e], ye = x.x[e + 1];
+                        x.x[e] = xe * cs - ye * sn;
+                        x.x[e + 1] = ye * cs + xe * sn;
+                    }
+                    *reinterpret_cast<uint4*>(dst + ch * 16) = x.pack();
+                } else {
+                    *reinterpret_cast<uint4*>(dst + ch * 16) = a[k];
+                }
+            } else {
+                // one thread per element of the first of a pair; c counts elements
+                const char* src;
+                row_of(r, src);
+                const int c2 = p.interleaved ? c + 1 : c + half;
+                const bool first = turned && c < p.rot && (p.interleaved ? (c & 1) == 0 : c < half);
+                if (turned && c < p.rot && !first) continue;  // written with its partner
+                auto get = [&](int e) -> float {
+                    if constexpr (kBF16) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(src)[e] << 16);
+                    else return reinterpret_cast<const float*>(src)[e];
+                };
+                const float x = ok ? get(c) : 0.f;
+                if (first) {
+                    const int j = p.interleaved ? c / 2 : c;
+                    const float y = ok ? get(c2) : 0.f;
+                    E::store(dst, c, x * s_cos[j] - y * s_sin[j]);
+                    E::store(dst, c2, y * s_cos[j] + x * s_sin[j]);
+                } else {
+                    E::store(dst, c, x);
+                }
+            }
+        }
+    }
+}
+
+int check_shape(const art_shape* s);  // art_api.cu
+
+}  // namespace art
+
+using namespace art;
+
+extern "C" {
+
+size_t art_append_workspace_bytes(const art_shape* shape) { return shape ? sizeof(WsHeader) : 0; }
+
+int art_append_kv(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                  const int32_t* q_offsets, int32_t num_tokens, const int32_t* positions, const int32_t* block_table,
+                  const int32_t* seq_lens, const float* inv_freq, const art_rope* rope, void* q_out, void* k_cache,
+                  void* v_cache, const art_shape* shape, void* workspace, size_t workspace_bytes, void* stream) {
+    const int rc = check_shape(shape);
+    if (rc != ART_OK) return rc;
+    const art_shape& s = *shape;
+    if (!block_table || !seq_lens || !k_cache || !v_cache || !workspace || !rope) return ART_ERR_INVALID_ARG;
+    if (num_tokens != 0 && (!k || !v)) return ART_ERR_INVALID_ARG;
+    if (num_tokens != 0 && (q != nullptr) != (q_out != nullptr)) return ART_ERR_INVALID_ARG;
+    if (num_tokens < 0 || (!q_offsets && num_tokens != s.batch)) return ART_ERR_INVALID_ARG;
+    if (num_tokens == 0x7fffffff) return ART_ERR_UNSUPPORTED;  // one block more than tokens
+    for (int i = 0; i < 5; ++i)
+        if (rope->reserved[i] != 0) return ART_ERR_INVALID_ARG;
+    if (rope->rot_dim < 0 || rope->rot_dim > s.head_dim || (rope->rot_dim & 1)) return ART_ERR_INVALID_ARG;
+    if (rope->interleaved != 0 && rope->interleaved != 1) return ART_ERR_INVALID_ARG;
+    if (rope->rot_dim > 0 && !inv_freq) return ART_ERR_INVALID_ARG;
+    const int elt = s.dtype == ART_DTYPE_BF16 ? 2 : 4, chunk = 16 / elt;
+    auto bad = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) != 0; };
+    if (bad(q) || bad(k) || bad(v) || bad(q_out) || bad(k_cache) || bad(v_cache) || bad(workspace))
+        return ART_ERR_INVALID_ARG;
+    const int64_t kvw = (int64_t)s.num_kv_heads * s.head_dim;
+    if ((q && (q_stride < (int64_t)s.num_q_heads * s.head_dim || q_stride % chunk)) || k_stride < kvw ||
+        k_stride % chunk || v_stride < kvw || v_stride % chunk)
+        return ART_ERR_INVALID_ARG;
+    if (workspace_bytes < sizeof(WsHeader)) return ART_ERR_WORKSPACE;
+
+    AppendParams p;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_offsets = q_offsets;
+    p.positions = positions;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.inv_freq = inv_freq;
+    p.q_out = q_out;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.hdr = static_cast<WsHeader*>(workspace);
+    p.B = s.batch;
+    p.T = num_tokens;
+    p.Hq = s.num_q_heads;
+    p.Hkv = s.num_kv_heads;
+    p.Ps = s.page_size;
+    p.max_pages = s.max_pages_per_seq;
+    p.num_pages = s.num_pages_total;
+    p.rot = rope->rot_dim;
+    p.interleaved = rope->interleaved;
+    p.scale = rope->scale;
+    const bool bf = s.dtype == ART_DTYPE_BF16;
+    const bool vec = (p.interleaved ? p.rot : p.rot / 2) % chunk == 0;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const unsigned grid = (unsigned)num_tokens + 1u;
+#define ART_APPEND(BF, DD, VEC) art_append_kernel<BF, DD, VEC><<<grid, kAppendThreads, 0, st>>>(p)
+    if (bf && s.head_dim == 128) { if (vec) ART_APPEND(true, 128, true); else ART_APPEND(true, 128, false); }
+    else if (bf) { if (vec) ART_APPEND(true, 64, true); else ART_APPEND(true, 64, false); }
+    else if (s.head_dim == 128) { if (vec) ART_APPEND(false, 128, true); else ART_APPEND(false, 128, false); }
+    else { if (vec) ART_APPEND(false, 64, true); else ART_APPEND(false, 64, false); }
+#undef ART_APPEND
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? ART_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,208 @@
+// art_attend_simt.cu -- the segments of art_attend.cuh on CUDA cores.
+//
+// A CTA takes the segments of its share one after another: up to 64 rows against
+// 64 keys at a time, all in fp32. Thread (ty, tx) of 16 x 16 forms the scores of
+// rows 4 ty .. 4 ty + 3 and keys tx + 16 j, and the output columns 4 tx + 64 j of
+// the same rows; the running maximum and sum of a row live in the 16 threads of a
+// half warp, so the weights need no block-wide barrier.
+#include "art_attend.cuh"
+
+namespace art {
+
+constexpr int kSimtThreads = 256;
+constexpr int kSimtKeys = 64;
+constexpr int kPStride = kSimtKeys + 4;
+
+template <int D>
+constexpr size_t simt_smem() {
+    return sizeof(float) * (size_t)(kItemRows * (D + 4) + 2 * kSimtKeys * (D + 4) + kItemRows * kPStride);
+}
+
+// 16 bytes of a row into shared memory as fp32
+template <bool kBF16>
+__device__ __forceinline__ void put_chunk(float* dst, const uint4& u) {
+    if constexpr (kBF16) {
+        *reinterpret_cast<float4*>(dst) = make_float4(bf16_lo_f(u.x), bf16_hi_f(u.x), bf16_lo_f(u.y), bf16_hi_f(u.y));
+        *reinterpret_cast<float4*>(dst + 4) = make_float4(bf16_lo_f(u.z), bf16_hi_f(u.z), bf16_lo_f(u.w), bf16_hi_f(u.w));
+    } else {
+        *reinterpret_cast<uint4*>(dst) = u;
+    }
+}
+
+__device__ __forceinline__ float f4(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+template <bool kBF16, int D>
+__global__ void __launch_bounds__(kSimtThreads) art_attend_simt_kernel(const AttendParams p) {
+    using E = Elem<kBF16>;
+    constexpr int S = D + 4, N = 16 / E::kBytes, CH = D / N, OC = D / 64;
+    extern __shared__ __align__(16) unsigned char smem[];
+    float* sq = reinterpret_cast<float*>(smem);
+    float* sk = sq + kItemRows * S;
+    float* sv = sk + kSimtKeys * S;
+    float* sp = sv + kSimtKeys * S;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int s_end = p.cta_first[blockIdx.x + 1];
+    for (int si = p.cta_first[blockIdx.x]; si < s_end; ++si) {
+        const Seg sg = p.seg[si];
+        if (sg.nrow == 0) continue;
+        __syncthreads();
+        for (int c = tid; c < kItemRows * CH; c += kSimtThreads) {
+            const int r = c / CH, ch = c - r * CH;
+            uint4 u = make_uint4(0u, 0u, 0u, 0u);
+            if (r < sg.nrow) {
+                const int R = sg.r0 + r, t = R / p.G;
+                const size_t row = (size_t)(sg.tok0 + t) * p.Hq + sg.g * p.G + (R - t * p.G);
+                u = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.q) + row * (D * E::kBytes)) + ch);
+            }
+            put_chunk<kBF16>(sq + r * S + ch * N, u);
+        }
+        int lim[4];
+        float m[4], l[4];
+        float4 o[4][OC];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty * 4 + i, R = sg.r0 + r;
+            lim[i] = sg.k1;
+            if (sg.kind == kLimCausal) lim[i] = min(lim[i], sg.lim0 + R / p.G);
+            if (sg.kind == kLimSeq && r < sg.nrow) lim[i] = min(lim[i], p.row_lim[sg.tok0 + R / p.G]);
+            if (r >= sg.nrow) lim[i] = 0;
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < OC; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const int32_t* trow = p.block_table + (size_t)sg.table_row * p.max_pages;
+        for (int kb = sg.k0 / kSimtKeys * kSimtKeys; kb < sg.k1; kb += kSimtKeys) {
+            __syncthreads();
+            for (int c = tid; c < kSimtKeys * CH; c += kSimtThreads) {
+                const int r = c / CH, ch = c - r * CH, key = kb + r;
+                uint4 uk = make_uint4(0u, 0u, 0u, 0u), uv = uk;
+                if (key >= sg.k0 && key < sg.k1) {
+                    const size_t row = ((size_t)__ldg(&trow[key / p.Ps]) * p.Hkv + sg.g) * p.Ps + (key & (p.Ps - 1));
+                    uk = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.k) + row * (D * E::kBytes)) + ch);
+                    uv = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.v) + row * (D * E::kBytes)) + ch);
+                }
+                put_chunk<kBF16>(sk + r * S + ch * N, uk);
+                put_chunk<kBF16>(sv + r * S + ch * N, uv);
+            }
+            __syncthreads();
+            float s[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+            for (int d = 0; d < D; d += 4) {
+                float4 a[4], b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sq + (ty * 4 + i) * S + d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * S + d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+                        s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+                        s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+                        s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+                    }
+            }
+            __syncwarp();  // the half warp's reads of the weights before have finished
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int key = kb + tx + 16 * j;
+                    s[i][j] = key >= sg.k0 && key < lim[i] ? s[i][j] * p.scale_log2 : -INFINITY;
+                    mx = fmaxf(mx, s[i][j]);
+                }
+#pragma unroll
+                for (int x = 8; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                const float mn = fmaxf(m[i], mx), base = mn == -INFINITY ? 0.f : mn;
+                const float a = m[i] == -INFINITY ? 0.f : exp2f(m[i] - base);
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float w = exp2f(s[i][j] - base);
+                    sum += w;
+                    sp[(ty * 4 + i) * kPStride + tx + 16 * j] = w;
+                }
+#pragma unroll
+                for (int x = 8; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                l[i] = l[i] * a + sum;
+                m[i] = mn;
+#pragma unroll
+                for (int c = 0; c < OC; ++c) {
+                    o[i][c].x *= a;
+                    o[i][c].y *= a;
+                    o[i][c].z *= a;
+                    o[i][c].w *= a;
+                }
+            }
+            __syncwarp();
+            for (int k = 0; k < kSimtKeys; k += 4) {
+                float4 w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(sp + (ty * 4 + i) * kPStride + k);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                    for (int c = 0; c < OC; ++c) {
+                        const float4 v = *reinterpret_cast<const float4*>(sv + (k + kk) * S + c * 64 + tx * 4);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float x = f4(w[i], kk);
+                            o[i][c].x = fmaf(x, v.x, o[i][c].x);
+                            o[i][c].y = fmaf(x, v.y, o[i][c].y);
+                            o[i][c].z = fmaf(x, v.z, o[i][c].z);
+                            o[i][c].w = fmaf(x, v.w, o[i][c].w);
+                        }
+                    }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty * 4 + i;
+            if (r >= sg.nrow) continue;
+            if (sg.prow >= 0) {
+                if (tx == 0) p.part_ml[sg.prow + r] = make_float2(m[i], l[i]);
+#pragma unroll
+                for (int c = 0; c < OC; ++c)
+                    *reinterpret_cast<float4*>(p.part_o + (size_t)(sg.prow + r) * D + c * 64 + tx * 4) = o[i][c];
+                continue;
+            }
+            const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
+            const int R = sg.r0 + r, t = R / p.G;
+            const size_t row = (size_t)(sg.tok0 + t) * p.Hq + sg.g * p.G + (R - t * p.G);
+#pragma unroll
+            for (int c = 0; c < OC; ++c) {
+                const float x[4] = {o[i][c].x * inv, o[i][c].y * inv, o[i][c].z * inv, o[i][c].w * inv};
+                const size_t at = row * D + c * 64 + tx * 4;
+                if constexpr (kBF16) {
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+                        make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+                } else {
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
+                }
+            }
+        }
+    }
+}
+
+template <bool kBF16, int D>
+static cudaError_t launch_one(const AttendParams& p, cudaStream_t st) {
+    constexpr size_t smem = simt_smem<D>();
+    const cudaError_t e = cudaFuncSetAttribute(art_attend_simt_kernel<kBF16, D>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    art_attend_simt_kernel<kBF16, D><<<p.ctas, kSimtThreads, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attend_simt(const AttendParams& p, bool bf16, cudaStream_t st) {
+    if (bf16) return p.D == 128 ? launch_one<true, 128>(p, st) : launch_one<true, 64>(p, st);
+    return p.D == 128 ? launch_one<false, 128>(p, st) : launch_one<false, 64>(p, st);
+}
+
+}  // namespace art
