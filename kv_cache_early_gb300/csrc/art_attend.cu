@@ -1,6 +1,7 @@
 // art_attend.cu -- dense_extend and dense_decode_shared: argument checks, the plan
 // kernel that builds the work list (art_attend.cuh), and the merge kernel.
 #include <cmath>
+#include <cstdlib>
 
 #include "art_attend.cuh"
 
@@ -494,7 +495,7 @@ static void fill_shape(AttendParams& p, const art_shape& s) {
     p.Ps = s.page_size;
     p.max_pages = s.max_pages_per_seq;
     p.num_pages = s.num_pages_total;
-    p.rt = kItemRows;
+    p.rt = s.dtype == ART_DTYPE_BF16 ? kRowsTc : kItemRows;
     p.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)s.head_dim));
 }
 
@@ -508,11 +509,21 @@ static int attend_run(AttendParams& p, const art_shape& s, void* workspace, size
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e);
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return cuda_fail(e);
     p.ctas = sms < kAttendCtas ? sms : kAttendCtas;
+    // the failure-path test hook of art_decode (ART_TEST_STALL_NS)
+    p.wait_ns = kWaitLimitNs;
+    p.stall = 0;
+    if (const char* es = std::getenv("ART_TEST_STALL_NS")) {
+        const long long ns = std::atoll(es);
+        if (ns > 0) {
+            p.stall = 1;
+            p.wait_ns = (unsigned long long)(ns < (long long)kWaitLimitNs ? ns : (long long)kWaitLimitNs);
+        }
+    }
     if ((e = cudaMemsetAsync(p.hdr, 0, sizeof(WsHeader), st)) != cudaSuccess) return cuda_fail(e);
     art_attend_plan_kernel<<<p.NE, kPlanBlock, 0, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
     const bool bf = s.dtype == ART_DTYPE_BF16;
-    if ((e = launch_attend_simt(p, bf, st)) != cudaSuccess) return cuda_fail(e);
+    if ((e = bf ? launch_attend_tc(p, st) : launch_attend_simt(p, st)) != cudaSuccess) return cuda_fail(e);
     const long long rows = p.shared ? (long long)p.B * p.Hq : (long long)p.ctas * p.rt;
     const long long want = (rows + kMergeBlock / 32 - 1) / (kMergeBlock / 32);
     const unsigned grid = (unsigned)(want < 4LL * p.ctas ? (want > 0 ? want : 1) : 4LL * p.ctas);

@@ -23,7 +23,8 @@ namespace art {
 
 constexpr int kKeyTile = 128;      // keys of a tile
 constexpr int kAttendCtas = 160;   // CTAs of the main kernel at most (one per SM)
-constexpr int kItemRows = 64;      // rows of an item's tile
+constexpr int kRowsTc = 256;       // rows of an item's tile, bf16
+constexpr int kItemRows = 64;      // ... and fp32
 
 // How far a row sees: all keys of the segment; up to its own token; up to the
 // limit of its sequence (row_lim).
@@ -68,6 +69,8 @@ struct AttendParams {
     int Hq, Hkv, G, D, Ps, max_pages, num_pages;
     int rt, ctas, max_items, part_rows;
     float scale_log2;  // log2(e) / sqrt(d)
+    unsigned long long wait_ns;  // limit of the bounded waits
+    int stall;         // test hook: the consumer warps first wait for what nothing completes
     // workspace
     WsHeader* hdr;
     Entity* ent;
@@ -90,6 +93,7 @@ struct AttendParams {
 // the pieces of an item lie apart.
 __host__ __device__ inline int piece_row_extend(int c, bool first, int rt) { return (2 * c + (first ? 1 : 0)) * rt; }
 
-cudaError_t launch_attend_simt(const AttendParams& p, bool bf16, cudaStream_t st);
+cudaError_t launch_attend_simt(const AttendParams& p, cudaStream_t st);  // fp32
+cudaError_t launch_attend_tc(const AttendParams& p, cudaStream_t st);    // bf16
 
 }  // namespace art

@@ -1,4 +1,5 @@
-// art_attend_simt.cu -- the segments of art_attend.cuh on CUDA cores.
+// art_attend_simt.cu -- the segments of art_attend.cuh for fp32, on CUDA cores (the
+// tensor cores would round the operands).
 //
 // A CTA takes the segments of its share one after another: up to 64 rows against
 // 64 keys at a time, all in fp32. Thread (ty, tx) of 16 x 16 forms the scores of
@@ -18,23 +19,11 @@ constexpr size_t simt_smem() {
     return sizeof(float) * (size_t)(kItemRows * (D + 4) + 2 * kSimtKeys * (D + 4) + kItemRows * kPStride);
 }
 
-// 16 bytes of a row into shared memory as fp32
-template <bool kBF16>
-__device__ __forceinline__ void put_chunk(float* dst, const uint4& u) {
-    if constexpr (kBF16) {
-        *reinterpret_cast<float4*>(dst) = make_float4(bf16_lo_f(u.x), bf16_hi_f(u.x), bf16_lo_f(u.y), bf16_hi_f(u.y));
-        *reinterpret_cast<float4*>(dst + 4) = make_float4(bf16_lo_f(u.z), bf16_hi_f(u.z), bf16_lo_f(u.w), bf16_hi_f(u.w));
-    } else {
-        *reinterpret_cast<uint4*>(dst) = u;
-    }
-}
-
 __device__ __forceinline__ float f4(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-template <bool kBF16, int D>
+template <int D>
 __global__ void __launch_bounds__(kSimtThreads) art_attend_simt_kernel(const AttendParams p) {
-    using E = Elem<kBF16>;
-    constexpr int S = D + 4, N = 16 / E::kBytes, CH = D / N, OC = D / 64;
+    constexpr int S = D + 4, CH = D / 4, OC = D / 64;
     extern __shared__ __align__(16) unsigned char smem[];
     float* sq = reinterpret_cast<float*>(smem);
     float* sk = sq + kItemRows * S;
@@ -48,13 +37,13 @@ __global__ void __launch_bounds__(kSimtThreads) art_attend_simt_kernel(const Att
         __syncthreads();
         for (int c = tid; c < kItemRows * CH; c += kSimtThreads) {
             const int r = c / CH, ch = c - r * CH;
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
+            float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < sg.nrow) {
                 const int R = sg.r0 + r, t = R / p.G;
                 const size_t row = (size_t)(sg.tok0 + t) * p.Hq + sg.g * p.G + (R - t * p.G);
-                u = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.q) + row * (D * E::kBytes)) + ch);
+                u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + row * D) + ch);
             }
-            put_chunk<kBF16>(sq + r * S + ch * N, u);
+            *reinterpret_cast<float4*>(sq + r * S + ch * 4) = u;
         }
         int lim[4];
         float m[4], l[4];
@@ -76,14 +65,14 @@ __global__ void __launch_bounds__(kSimtThreads) art_attend_simt_kernel(const Att
             __syncthreads();
             for (int c = tid; c < kSimtKeys * CH; c += kSimtThreads) {
                 const int r = c / CH, ch = c - r * CH, key = kb + r;
-                uint4 uk = make_uint4(0u, 0u, 0u, 0u), uv = uk;
+                float4 uk = make_float4(0.f, 0.f, 0.f, 0.f), uv = uk;
                 if (key >= sg.k0 && key < sg.k1) {
                     const size_t row = ((size_t)__ldg(&trow[key / p.Ps]) * p.Hkv + sg.g) * p.Ps + (key & (p.Ps - 1));
-                    uk = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.k) + row * (D * E::kBytes)) + ch);
-                    uv = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.v) + row * (D * E::kBytes)) + ch);
+                    uk = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.k) + row * D) + ch);
+                    uv = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.v) + row * D) + ch);
                 }
-                put_chunk<kBF16>(sk + r * S + ch * N, uk);
-                put_chunk<kBF16>(sv + r * S + ch * N, uv);
+                *reinterpret_cast<float4*>(sk + r * S + ch * 4) = uk;
+                *reinterpret_cast<float4*>(sv + r * S + ch * 4) = uv;
             }
             __syncthreads();
             float s[4][4];
@@ -177,32 +166,26 @@ __global__ void __launch_bounds__(kSimtThreads) art_attend_simt_kernel(const Att
             const size_t row = (size_t)(sg.tok0 + t) * p.Hq + sg.g * p.G + (R - t * p.G);
 #pragma unroll
             for (int c = 0; c < OC; ++c) {
-                const float x[4] = {o[i][c].x * inv, o[i][c].y * inv, o[i][c].z * inv, o[i][c].w * inv};
                 const size_t at = row * D + c * 64 + tx * 4;
-                if constexpr (kBF16) {
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
-                        make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-                } else {
-                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
-                }
+                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
+                    make_float4(o[i][c].x * inv, o[i][c].y * inv, o[i][c].z * inv, o[i][c].w * inv);
             }
         }
     }
 }
 
-template <bool kBF16, int D>
+template <int D>
 static cudaError_t launch_one(const AttendParams& p, cudaStream_t st) {
     constexpr size_t smem = simt_smem<D>();
-    const cudaError_t e = cudaFuncSetAttribute(art_attend_simt_kernel<kBF16, D>,
+    const cudaError_t e = cudaFuncSetAttribute(art_attend_simt_kernel<D>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    art_attend_simt_kernel<kBF16, D><<<p.ctas, kSimtThreads, smem, st>>>(p);
+    art_attend_simt_kernel<D><<<p.ctas, kSimtThreads, smem, st>>>(p);
     return cudaGetLastError();
 }
 
-cudaError_t launch_attend_simt(const AttendParams& p, bool bf16, cudaStream_t st) {
-    if (bf16) return p.D == 128 ? launch_one<true, 128>(p, st) : launch_one<true, 64>(p, st);
-    return p.D == 128 ? launch_one<false, 128>(p, st) : launch_one<false, 64>(p, st);
+cudaError_t launch_attend_simt(const AttendParams& p, cudaStream_t st) {
+    return p.D == 128 ? launch_one<128>(p, st) : launch_one<64>(p, st);
 }
 
 }  // namespace art
