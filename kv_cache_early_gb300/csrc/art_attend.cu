@@ -492,6 +492,8 @@ static void fill_shape(AttendParams& p, const art_shape& s) {
     p.Hq = s.num_q_heads;
     p.Hkv = s.num_kv_heads;
     p.D = s.head_dim;
+    const int G = s.num_q_heads / s.num_kv_heads;
+    p.g_mul = ((1ull << 34) + G - 1) / G;
     p.Ps = s.page_size;
     p.max_pages = s.max_pages_per_seq;
     p.num_pages = s.num_pages_total;

@@ -69,6 +69,7 @@ struct AttendParams {
     int Hq, Hkv, G, D, Ps, max_pages, num_pages;
     int rt, ctas, max_items, part_rows;
     float scale_log2;  // log2(e) / sqrt(d)
+    unsigned long long g_mul;  // ceil(2^34 / G): R / G = R * g_mul >> 34
     unsigned long long wait_ns;  // limit of the bounded waits
     int stall;         // test hook: the consumer warps first wait for what nothing completes
     // workspace

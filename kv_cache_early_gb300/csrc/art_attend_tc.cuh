@@ -5,7 +5,8 @@
 //
 //   producer warp   resolves the tiles' pages (the ids of 32 pages at a time, one
 //                   batch ahead) and copies each page by one tensor copy
-//   issuer warp     one thread issues the tcgen05 products of large segments
+//   issuer warp     issues the tcgen05 products of large segments
+//   edge warp       zeroes rows of V in shared memory that are no keys of a segment
 //   8 consumer warps: softmax, and the whole computation of small segments
 //
 // Large segments (more than 16 rows): 128 rows are one stream; S = Q K^T (128 x 128)
@@ -55,16 +56,17 @@ struct TcCfg {
 
 constexpr int kTcConsumers = 8, kTcThreads = (kTcConsumers + 4) * 32;  // three warpgroups
 // Registers: 12 warps at 168 at launch (64512); then the two consumer warpgroups take
-// 208 each (a row's 128 scores live in registers) and the third keeps 80: 63488.
-constexpr int kRegConsumer = 208, kRegHelper = 80;
+// 192 each and the third keeps 120: 64512.
+constexpr int kRegConsumer = 192, kRegHelper = 120;
 static_assert(128 * (2 * kRegConsumer + kRegHelper) <= kTcThreads * 168, "no more than the launch's registers");
 constexpr int kSmallRows = 16;   // rows of a segment that the consumer warps take by themselves
-constexpr float kRescale = 8.f;  // log2 units by which a row's maximum may lead its reference
+constexpr float kRescale = 8.f;  // small segments: log2 units by which a row's maximum may lead its reference
+constexpr float kMaxSum = 1.0995116e12f;  // 2^40, large segments: the sum of a tile's weights from which it moves
 
 template <int NS>
 struct alignas(16) TcCtrl {
     uint64_t full[NS], empty_t[NS], empty_s[NS];  // empty: after a large / a small segment's use
-    uint64_t s_full[2], p_full[2], o_full[2], q_full, cons, fin, stall;
+    uint64_t s_full[2], p_full[2], o_full[2], q_full, edge_go, edge_done, cons, fin, stall;
     float2 ml[kTcConsumers * kSmallRows > 128 ? kTcConsumers * kSmallRows : 128];  // (m, l) exchanged between warps
     float2 ml2[128];
     uint32_t tmem;
@@ -96,7 +98,6 @@ __device__ __forceinline__ void tc_dealloc(uint32_t t) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // arrives on `bar` when every product issued so far by this thread has finished
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
@@ -122,7 +123,10 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
 #define ART_F8(a, o) "f"(a[o]), "f"(a[o + 1]), "f"(a[o + 2]), "f"(a[o + 3]), "f"(a[o + 4]), "f"(a[o + 5]), "f"(a[o + 6]), "f"(a[o + 7])
 #define ART_U8(a, o) "r"(a[o]), "r"(a[o + 1]), "r"(a[o + 2]), "r"(a[o + 3]), "r"(a[o + 4]), "r"(a[o + 5]), "r"(a[o + 6]), "r"(a[o + 7])
 
-// 32 columns of the warp's 32 lanes: thread = lane, register = column
+#define ART_IO8(a, o) "+f"(a[o]), "+f"(a[o + 1]), "+f"(a[o + 2]), "+f"(a[o + 3]), "+f"(a[o + 4]), "+f"(a[o + 5]), "+f"(a[o + 6]), "+f"(a[o + 7])
+
+// 32 columns of the warp's 32 lanes: thread = lane, register = column. The registers
+// are valid after tc_wait_ld on them (which no use of theirs can then pass).
 __device__ __forceinline__ void tc_ld32(uint32_t t, float* r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -130,6 +134,22 @@ __device__ __forceinline__ void tc_ld32(uint32_t t, float* r) {
         "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : ART_R8(r, 0), ART_R8(r, 8), ART_R8(r, 16), ART_R8(r, 24)
         : "r"(t));
+}
+// 16 columns, waited for
+__device__ __forceinline__ void tc_ld16(uint32_t t, float* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : ART_R8(r, 0), ART_R8(r, 8)
+        : "r"(t)
+        : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld(float* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : ART_IO8(r, 0), ART_IO8(r, 8), ART_IO8(r, 16), ART_IO8(r, 24)
+                 :
+                 : "memory");
 }
 __device__ __forceinline__ void tc_st32(uint32_t t, const float* r) {
     asm volatile(
@@ -154,6 +174,20 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+template <int N>
+__device__ __forceinline__ float row_max(const float* s) {
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < N; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], s[i], s[i + 1]);
+    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
 // Shared-memory operand descriptor: 128B swizzle; lead, stride in bytes.
 __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, int lead, int stride) {
     return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
@@ -168,11 +202,12 @@ __host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_mn) {
 // the status bit and the CTA's abort flag) or when another warp has: every warp then
 // leaves its loop, and none is left in a barrier, since all waits are of this kind.
 __device__ __forceinline__ bool wait_tc(uint64_t* bar, uint32_t parity, int* abort, const AttendParams& p) {
-    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    // the clock is read once the wait is long: reading it takes longer than most waits
+    for (int k = 0; k < 64; ++k)
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     const unsigned long long t0 = global_ns();
     for (;;) {
-        for (int k = 0; k < 16; ++k)
+        for (int k = 0; k < 64; ++k)
             if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
         const bool late = (threadIdx.x & 31) == 0 && global_ns() - t0 > p.wait_ns;
         if (__any_sync(0xffffffffu, late)) {
@@ -223,16 +258,21 @@ struct Stage {  // position in the ring
     }
 };
 
+// R / G for R < 2^30: g_mul = ceil(2^34 / G)
+__device__ __forceinline__ int token_of(const AttendParams& p, int R) {
+    return (int)((unsigned long long)R * p.g_mul >> 34);
+}
+
 // A row's place in q and out.
 __device__ __forceinline__ size_t row_index(const AttendParams& p, const Seg& sg, int r) {
-    const int R = sg.r0 + r, t = R / p.G;
+    const int R = sg.r0 + r, t = token_of(p, R);
     return (size_t)(sg.tok0 + t) * p.Hq + sg.g * p.G + (R - t * p.G);
 }
 // Keys that row r sees lie below this.
 __device__ __forceinline__ int row_limit(const AttendParams& p, const Seg& sg, int r) {
     if (r >= sg.nrow) return sg.k0;
     if (sg.kind == kLimAll) return sg.k1;
-    const int t = (sg.r0 + r) / p.G;
+    const int t = token_of(p, sg.r0 + r);
     return min(sg.k1, sg.kind == kLimCausal ? sg.lim0 + t : __ldg(&p.row_lim[sg.tok0 + t]));
 }
 
@@ -318,51 +358,78 @@ __device__ void tc_producer(const AttendParams& p, uint32_t smem, TcCtrl<TcCfg<D
 // ---------------------------------------------------------------------------
 // issuer warp (large segments)
 // ---------------------------------------------------------------------------
+// The whole warp runs the loop on warp-uniform values and one elected lane issues.
+// Written so, the descriptors stay in uniform registers and 8 products are issued in
+// 70 cycles (the queue then holds them); issued by one lane of a divergent branch they
+// take 400, and many times that when the consumer warps leave few issue slots.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// The keys of tile t of a segment, as rows [lo, hi) of the tile; where a border lies
+// inside a 16-key step, that step's rows of V beyond it are zeroed.
+__device__ __forceinline__ bool tile_rows(const Seg& sg, int t, int& lo, int& hi) {
+    lo = max(sg.k0 - t * kKeyTile, 0);
+    hi = min(sg.k1 - t * kKeyTile, kKeyTile);
+    return ((lo | hi) & 15) != 0;
+}
+
 template <int D>
-__device__ void tc_issuer(const AttendParams& p, uint32_t smem, unsigned char* gen, TcCtrl<TcCfg<D>::NS>* c,
-                          uint32_t tmem, int s0, int s1) {
+__device__ void tc_issuer(const AttendParams& p, uint32_t smem, TcCtrl<TcCfg<D>::NS>* c, uint32_t tmem_, int s0, int s1) {
     using C = TcCfg<D>;
     constexpr uint32_t kIdQK = tc_idesc(kKeyTile, false), kIdPV = tc_idesc(D, true);
-    const int lane = threadIdx.x & 31;
-    Stage<C::NS> st;           // next stage to take
-    uint32_t ph_q = 0, ph_p = 0;  // ph_p: a bit per stream
-    bool issued = false;
-    auto wait = [&](uint64_t* b, uint32_t ph) { return wait_tc(b, ph, &c->abort, p); };
+    const uint32_t tmem = (uint32_t)uniform((int)tmem_);
+    Stage<C::NS> st;  // first stage of the segment: K of tile j lies 2j stages on, V of tile j 2j + 1
+    uint32_t ph_q = 0, ph_p = 0, ph_e = 0;  // ph_p: a bit per stream
+    bool issued = false, ok = true;
+    auto wait = [&](uint64_t* b, uint32_t ph) { return ok = wait_tc(b, ph, &c->abort, p); };
+    // The descriptors of all stages follow from that of the first by addition (the
+    // addresses stay below 2^18).
+    const uint64_t qd0 = tc_desc(smem, 16, C::GRP), kd0 = tc_desc(smem + C::RING, 16, C::GRP),
+                   vd0 = tc_desc(smem + C::RING, 1024, C::GRP);
     // S_x = Q_(tile) K^T
-    auto qk = [&](int x, int qt, const Stage<C::NS>& k) {
-        if (lane == 0) {
+    auto qk = [&](int x, int qt, int stage) {
+        const uint64_t qd = qd0 + (uint64_t)(qt * (C::TILE >> 4)), kd = kd0 + (uint64_t)(stage * (C::TILE >> 4));
+        const uint32_t d = tmem + 256 + x * 128;
+        if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 32;
-                tc_mma_ss(tmem + 256 + x * 128, tc_desc(smem + qt * C::TILE + off, 16, C::GRP),
-                          tc_desc(smem + C::RING + k.s * C::TILE + off, 16, C::GRP), kIdQK, kk > 0);
+                const int off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
+                tc_mma_ss(d, qd + off, kd + off, kIdQK, kk > 0);
             }
             tc_commit(&c->s_full[x]);
         }
-        issued = true;
-    };
-    // O_x += P_x V over the 16-key steps [a, z)
-    auto pv = [&](int x, const Stage<C::NS>& v, int a, int z, bool acc) {
-        if (lane == 0)
-            for (int kk = a; kk < z; ++kk)
-                tc_mma_ts(tmem + x * 128, tmem + 256 + x * 128 + kk * 8,
-                          tc_desc(smem + C::RING + v.s * C::TILE + kk * 2 * C::GRP, 1024, C::GRP), kIdPV, acc || kk > a);
-    };
-    // rows of V of the first and last step that lie outside [lo, hi) of the tile
-    auto zero_edges = [&](const Stage<C::NS>& v, int a, int z, int lo, int hi) {
-        unsigned char* base = gen + C::RING + v.s * C::TILE;
-        for (int i = lane; i < 32 * C::NH * 8; i += 32) {
-            const int row = (i / (C::NH * 8)) < 16 ? a * 16 + i / (C::NH * 8) : (z - 1) * 16 + i / (C::NH * 8) - 16;
-            if (row >= lo && row < hi) continue;
-            const int col = i % (C::NH * 8);
-            *reinterpret_cast<uint4*>(base + (row >> 3) * C::GRP + (col >> 3) * 1024 + (row & 7) * 128 + (col & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
         __syncwarp();
     };
-    for (int si = s0; si < s1; ++si) {
-        const Seg sg = load_seg(&p.seg[si]);
+    // O_x += P_x V over the 16-key steps [a, z)
+    auto pv = [&](int x, int stage, int a, int z, bool acc) {
+        const uint64_t vd = vd0 + (uint64_t)(stage * (C::TILE >> 4));
+        const uint32_t d = tmem + x * 128, pp = tmem + 256 + x * 128;
+        if (elect_one()) {
+            if (a == 0 && z == kKeyTile / 16) {
+#pragma unroll
+                for (int kk = 0; kk < kKeyTile / 16; ++kk)
+                    tc_mma_ts(d, pp + kk * 8, vd + (uint64_t)(kk * (2 * C::GRP >> 4)), kIdPV, acc || kk > 0);
+            } else {
+#pragma unroll 1
+                for (int kk = a; kk < z; ++kk)
+                    tc_mma_ts(d, pp + kk * 8, vd + (uint64_t)(kk * (2 * C::GRP >> 4)), kIdPV, acc || kk > a);
+            }
+        }
+        __syncwarp();
+    };
+    auto commit = [&](uint64_t* b) {
+        if (elect_one()) tc_commit(b);
+        __syncwarp();
+    };
+    for (int si = s0; si < s1 && ok; ++si) {
+        Seg sg = load_seg(&p.seg[si]);
+        sg.nrow = uniform(sg.nrow);
+        sg.k0 = uniform(sg.k0);
+        sg.k1 = uniform(sg.k1);
         if (sg.nrow == 0) continue;
         const int t0 = sg.k0 / kKeyTile, nt = (sg.k1 + kKeyTile - 1) / kKeyTile - t0;
         if (sg.nrow <= kSmallRows) {
@@ -373,61 +440,100 @@ __device__ void tc_issuer(const AttendParams& p, uint32_t smem, unsigned char* g
         if (!wait(&c->q_full, ph_q)) break;
         ph_q ^= 1u;
         tc_fence_after();
-        // K of tile j is at ring place 2j of the segment, V at 2j + 1
-        auto at = [&](int n) {
-            Stage<C::NS> x = st;
-            x.skip(n);
-            return x;
-        };
-        bool ok = true;
+        issued = true;
         const int ahead = dual ? 1 : 2;  // tiles whose S may be under way
-        for (int j = 0; j < min(ahead, nt) && ok; ++j) {
-            const Stage<C::NS> k = at(2 * j);
-            if (!(ok = wait(&c->full[k.s], k.ph))) break;
-            if (dual) {
-                qk(0, 0, k);
-                qk(1, 1, k);
-            } else {
-                qk(j, 0, k);
-            }
-            if (lane == 0) tc_commit(&c->empty_t[k.s]);
+        Stage<C::NS> ks = st, vs = st;
+        vs.next();
+        for (int j = 0; j < ahead && j < nt; ++j) {
+            if (!wait(&c->full[ks.s], ks.ph)) break;
+            qk(dual ? 0 : j, 0, ks.s);
+            if (dual) qk(1, 1, ks.s);
+            commit(&c->empty_t[ks.s]);
+            ks.next();
+            ks.next();
         }
         for (int j = 0; j < nt && ok; ++j) {
-            const Stage<C::NS> v = at(2 * j + 1);
-            if (!(ok = wait(&c->full[v.s], v.ph))) break;
-            const int lo = max(sg.k0 - (t0 + j) * kKeyTile, 0), hi = min(sg.k1 - (t0 + j) * kKeyTile, kKeyTile);
-            const int a = lo >> 4, z = (hi + 15) >> 4;
-            if ((lo | hi) & 15) zero_edges(v, a, z, lo, hi);
-            const int jn = j + ahead;
-            const Stage<C::NS> k = at(2 * jn);
-            for (int x = dual ? 0 : (j & 1); x < (dual ? 2 : (j & 1) + 1) && ok; ++x) {
-                if (!(ok = wait(&c->p_full[x], (ph_p >> x) & 1u))) break;
+            int lo, hi;
+            const bool edge = tile_rows(sg, t0 + j, lo, hi);
+            const bool more = j + ahead < nt;
+            // the operands first: they are seldom what is waited for
+            if (!wait(&c->full[vs.s], vs.ph)) break;
+            if (edge) {
+                if (elect_one()) mbar_arrive(&c->edge_go);
+                __syncwarp();
+                if (!wait(&c->edge_done, ph_e)) break;
+                ph_e ^= 1u;
+            }
+            if (more && !wait(&c->full[ks.s], ks.ph)) break;
+            const int x0 = dual ? 0 : (j & 1), x1 = dual ? 1 : x0;
+#pragma unroll 1
+            for (int x = x0; x <= x1; ++x) {
+                if (!wait(&c->p_full[x], (ph_p >> x) & 1u)) break;
                 ph_p ^= 1u << x;
                 tc_fence_after();
-                pv(x, v, a, z, j >= (dual ? 1 : 2));
-                if ((!dual || x == 1) && lane == 0) tc_commit(&c->empty_t[v.s]);
-                if (jn < nt) {
-                    if ((!dual || x == 0) && !(ok = wait(&c->full[k.s], k.ph))) break;
-                    qk(x, dual ? x : 0, k);
-                    if ((!dual || x == 1) && lane == 0) tc_commit(&c->empty_t[k.s]);
-                } else if (dual && lane == 0) {
-                    tc_commit(&c->o_full[x]);
-                }
+                pv(x, vs.s, lo >> 4, (hi + 15) >> 4, j >= ahead);
+                if (more) qk(x, dual ? x : 0, ks.s);
+                else if (dual) commit(&c->o_full[x]);
             }
+            if (!ok) break;
+            commit(&c->empty_t[vs.s]);
+            if (more) commit(&c->empty_t[ks.s]);
+            ks.next();
+            ks.next();
+            vs.next();
+            vs.next();
         }
         if (!ok) break;
-        if (!dual && lane == 0) {
-            tc_commit(&c->o_full[0]);
-            tc_commit(&c->o_full[1]);
+        if (!dual) {
+            commit(&c->o_full[0]);
+            commit(&c->o_full[1]);
         }
         st.skip(2 * nt);
     }
     // the products have finished before the tensor memory is given back
     if (issued) {
-        if (lane == 0) tc_commit(&c->fin);
+        commit(&c->fin);
         const unsigned long long w0 = global_ns();
         while (!__all_sync(0xffffffffu, mbar_try_wait(&c->fin, 0u)))
-            if (__any_sync(0xffffffffu, lane == 0 && global_ns() - w0 > kWaitLimitNs)) break;
+            if (__any_sync(0xffffffffu, global_ns() - w0 > kWaitLimitNs)) break;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// edge warp (large segments): zeroes rows of V that are no keys of the segment, when
+// the issuer, which has seen the tile arrive, asks for it
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ void tc_edges(const AttendParams& p, unsigned char* gen, TcCtrl<TcCfg<D>::NS>* c, int s0, int s1) {
+    using C = TcCfg<D>;
+    const int lane = threadIdx.x & 31;
+    Stage<C::NS> st;
+    uint32_t ph = 0;
+    for (int si = s0; si < s1; ++si) {
+        const Seg sg = load_seg(&p.seg[si]);
+        if (sg.nrow == 0) continue;
+        const int t0 = sg.k0 / kKeyTile, nt = (sg.k1 + kKeyTile - 1) / kKeyTile - t0;
+        for (int j = 0; sg.nrow > kSmallRows && j < nt; j += nt > 1 ? nt - 1 : 1) {  // the first and the last tile
+            int lo, hi;
+            if (!tile_rows(sg, t0 + j, lo, hi)) continue;
+            Stage<C::NS> v = st;
+            v.skip(2 * j + 1);
+            if (!wait_tc(&c->edge_go, ph, &c->abort, p)) return;
+            ph ^= 1u;
+            const int a = lo >> 4, z = (hi + 15) >> 4;  // steps with a key
+            unsigned char* base = gen + C::RING + v.s * C::TILE;
+            for (int i = lane; i < 32 * C::NH * 8; i += 32) {
+                const int k = i / (C::NH * 8), col = i % (C::NH * 8);
+                const int row = k < 16 ? a * 16 + k : (z - 1) * 16 + k - 16;
+                if (row >= lo && row < hi) continue;
+                *reinterpret_cast<uint4*>(base + (row >> 3) * C::GRP + (col >> 3) * 1024 + (row & 7) * 128 +
+                                          (col & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->edge_done);
+        }
+        st.skip(2 * nt);
     }
 }
 
@@ -480,21 +586,56 @@ struct TcConsumer {
         }
     }
 
+    // The row's 64 weights at t, and its D sums at t, times f (seldom).
+    __device__ __noinline__ static void scale_weights(uint32_t t, float f) {
+#pragma unroll 1
+        for (int k = 0; k < 32; k += 16) {
+            float v[16];
+            tc_ld16(t + k, v);
+            uint32_t u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                u[i] = __float_as_uint(v[i]);
+                u[i] = pack_bf16(bf16_lo_f(u[i]) * f, bf16_hi_f(u[i]) * f);
+            }
+            tc_st16(t + k, u);
+        }
+    }
+    __device__ __noinline__ static void scale_sums(uint32_t t, float f) {
+#pragma unroll 1
+        for (int k = 0; k < D; k += 16) {
+            float v[16];
+            tc_ld16(t + k, v);
+            uint32_t u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i] * f);
+            tc_st16(t + k, u);
+        }
+    }
+
     __device__ bool large(const Seg& sg, int t0, int nt) {
         const bool dual = sg.nrow > 128;
         const int x = w >> 2, quad = w & 3;
         if (!sync()) return false;  // the tiles of Q are free (small segments use them too)
         // Q: 16 bytes a lane, whole rows side by side
         {
-            const int rows = dual ? 32 : 16, first = w * rows;
-            constexpr int CPR = D / 8;
-            for (int i = lane; i < rows * CPR; i += 32) {
-                const int r = first + i / CPR, ch = i % CPR;
-                uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                if (r < sg.nrow)
-                    u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row_index(p, sg, r) * D) + ch);
-                *reinterpret_cast<uint4*>(gen + (r >> 3) * C::GRP + (ch >> 3) * 1024 + (r & 7) * 128 +
-                                          (((ch & 7) ^ (r & 7)) << 4)) = u;
+            constexpr int CPR = D / 8, RPI = 32 / CPR, NB = 8;  // chunks of a row; rows of a warp's load; loads at once
+            const int rows = dual ? 32 : 16, ch = lane % CPR;
+            for (int i0 = 0; i0 < rows; i0 += NB * RPI) {
+                uint4 u[NB];
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const int r = w * rows + i0 + i * RPI + lane / CPR;
+                    u[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < sg.nrow)
+                        u[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row_index(p, sg, r) * D) + ch);
+                }
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const int r = w * rows + i0 + i * RPI + lane / CPR;
+                    *reinterpret_cast<uint4*>(gen + (r >> 3) * C::GRP + (ch >> 3) * 1024 + (r & 7) * 128 +
+                                              (((ch & 7) ^ (r & 7)) << 4)) = u[i];
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -504,68 +645,85 @@ struct TcConsumer {
         const bool live = (dual ? x * 128 : 0) + quad * 32 < sg.nrow;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t tS = tmem + lanes + 256 + x * 128, tO = tmem + lanes + x * 128;
-        const int lim = row_limit(p, sg, r);
-        const int wlim = (int)__reduce_min_sync(0xffffffffu, (unsigned)(r < sg.nrow ? lim : 0x7fffffff));
-        float m = -INFINITY, l = 0.f;
+        // a row that sees no key here is computed as if it saw all, and reported as empty
+        const int rlim = row_limit(p, sg, r);
+        const bool none = rlim <= sg.k0;
+        const int lim = none ? sg.k1 : rlim;
+        const int wlim = (int)__reduce_min_sync(0xffffffffu, (unsigned)lim);
+        float m = -INFINITY, l = 0.f, fO = 1.f;
         bool first = true;
+        const uint64_t c2 = pk2(p.scale_log2, p.scale_log2), one = pk2(1.f, 1.f);
         for (int j = dual ? 0 : x; j < nt; j += dual ? 1 : 2) {
             if (!wait(&c->s_full[x], ph_s)) return false;
             ph_s ^= 1u;
             if (live) {
                 tc_fence_after();
-                float s[128];
-#pragma unroll
-                for (int k = 0; k < 128; k += 32) tc_ld32(tS + k, s + k);
-                tc_wait_ld();
                 const int tb = (t0 + j) * kKeyTile;
-                if (tb < sg.k0 || tb + kKeyTile > wlim) {
-                    const int lo = sg.k0 - tb, hi = lim - tb;
+                const bool edge = tb < sg.k0 || tb + kKeyTile > wlim;
+                const int lo = sg.k0 - tb, hi = lim - tb;
+                // 64 columns at a time, one loop body for both halves (the instruction cache feeds
+                // eight warps from it)
+#pragma unroll 1
+                for (int h = 0; h < 128; h += 64) {
+                    float s[64];
+                    tc_ld32(tS + h, s);
+                    tc_ld32(tS + h + 32, s + 32);
+                    tc_wait_ld(s);
+                    tc_wait_ld(s + 32);
+                    if (edge) {
 #pragma unroll
-                    for (int k = 0; k < 128; ++k)
-                        if (k < lo || k >= hi) s[k] = -INFINITY;
-                }
-                float mx[4] = {s[0], s[1], s[2], s[3]};
+                        for (int k = 0; k < 64; ++k)
+                            if (h + k < lo || h + k >= hi) s[k] = -INFINITY;
+                    }
+                    // Steady state: no maximum is formed. Weights and their sum are taken against the
+                    // row's reference m; where none is set yet, or the sum passes kMaxSum (or is not a
+                    // number), m moves to these columns' maximum and they are done once more.
+                    float rowsum = m == -INFINITY ? INFINITY : 0.f;
+                    for (bool again = __any_sync(0xffffffffu, m == -INFINITY);;) {
+                        if (again) {
+                            const float top = row_max<64>(s) * p.scale_log2;
+                            if (!(rowsum <= kMaxSum) && top > m) {
+                                // a row that had a reference: what it has summed is scaled down
+                                const float f = ex2(m - top);
+                                l *= f;
+                                fO *= f;
+                                m = top;
+                            }
+                        }
+                        const float nb = m == -INFINITY ? 0.f : -m;
+                        const uint64_t b2 = pk2(nb, nb);
+                        uint64_t sum[4] = {pk2(0.f, 0.f), pk2(0.f, 0.f), pk2(0.f, 0.f), pk2(0.f, 0.f)};
 #pragma unroll
-                for (int k = 4; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-                const bool up = top > m + kRescale || (m == -INFINITY && top > m);
-                const float f = up ? ex2(m - top) : 1.f;
-                if (up) {
-                    m = top;
-                    l *= f;
-                }
-                if (!first && __any_sync(0xffffffffu, up)) {
-                    float o[32];
-                    for (int k = 0; k < D; k += 32) {
-                        tc_ld32(tO + k, o);
-                        tc_wait_ld();
+                        for (int k = 0; k < 64; k += 32) {
+                            uint32_t pw[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] *= f;
-                        tc_st32(tO + k, o);
+                            for (int i = 0; i < 16; ++i) {
+                                float e0, e1;
+                                up2(fma2(pk2(s[k + 2 * i], s[k + 2 * i + 1]), c2, b2), e0, e1);
+                                e0 = ex2(e0);
+                                e1 = ex2(e1);
+                                sum[i & 3] = fma2(pk2(e0, e1), one, sum[i & 3]);
+                                pw[i] = pack_bf16(e0, e1);
+                            }
+                            tc_st16(tS + (h + k) / 2, pw);
+                        }
+                        float a[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) up2(sum[i], a[2 * i], a[2 * i + 1]);
+                        rowsum = ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
+                        if (again || !__any_sync(0xffffffffu, !(rowsum <= kMaxSum))) break;
+                        tc_wait_st();
+                        again = true;
+                    }
+                    l += rowsum;
+                    if (__any_sync(0xffffffffu, fO != 1.f)) {
+                        // what the row has summed: O, and the weights of the first half of this tile
+                        tc_wait_st();
+                        if (h) scale_weights(tS, fO);
+                        if (!first) scale_sums(tO, fO);
+                        fO = 1.f;
                     }
                 }
-                const float nb = m == -INFINITY ? 0.f : -m;
-                const uint64_t c2 = pk2(p.scale_log2, p.scale_log2), b2 = pk2(nb, nb), one = pk2(1.f, 1.f);
-                uint64_t sum0 = pk2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-                for (int k = 0; k < 128; k += 32) {
-                    uint32_t pw[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float e0, e1;
-                        up2(fma2(pk2(s[k + 2 * i], s[k + 2 * i + 1]), c2, b2), e0, e1);
-                        e0 = ex2(e0);
-                        e1 = ex2(e1);
-                        if (i & 1) sum1 = fma2(pk2(e0, e1), one, sum1);
-                        else sum0 = fma2(pk2(e0, e1), one, sum0);
-                        pw[i] = pack_bf16(e0, e1);
-                    }
-                    tc_st16(tS + k / 2, pw);
-                }
-                float a0, a1, b0, b1;
-                up2(sum0, a0, a1);
-                up2(sum1, b0, b1);
-                l += (a0 + a1) + (b0 + b1);
                 tc_wait_st();
                 tc_fence_before();
             }
@@ -576,12 +734,18 @@ struct TcConsumer {
         if (!wait(&c->o_full[x], ph_o)) return false;
         ph_o ^= 1u;
         tc_fence_after();
+        if (none) {
+            m = -INFINITY;
+            l = 0.f;
+        }
         if (dual) {
             if (live) {
                 for (int k = 0; k < D; k += 32) {
                     float o[32];
                     tc_ld32(tO + k, o);
-                    tc_wait_ld();
+                    tc_wait_ld(o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i];
                     if (r < sg.nrow) put<32>(sg, r, k, o, l);
                 }
                 if (r < sg.nrow && sg.prow >= 0) p.part_ml[sg.prow + r] = make_float2(m, l);
@@ -600,10 +764,15 @@ struct TcConsumer {
                 for (int k = x * (D / 2); k < (x + 1) * (D / 2); k += 32) {
                     float o[32], o2[32];
                     tc_ld32(tmem + lanes + k, o);
-                    if (odd) tc_ld32(tmem + lanes + 128 + k, o2);
-                    tc_wait_ld();
+                    tc_wait_ld(o);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = odd ? o[i] * fe + o2[i] * fd : o[i] * fe;
+                    for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * fe;
+                    if (odd) {
+                        tc_ld32(tmem + lanes + 128 + k, o2);
+                        tc_wait_ld(o2);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] += none ? 0.f : o2[i] * fd;
+                    }
                     if (r < sg.nrow) put<32>(sg, r, k, o, ll);
                 }
                 if (x == 0 && r < sg.nrow && sg.prow >= 0) p.part_ml[sg.prow + r] = make_float2(mm, ll);
@@ -797,7 +966,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return;
     }
     TcCtrl<C::NS>* c = reinterpret_cast<TcCtrl<C::NS>*>(gen + C::CTRL);
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NS; ++i) {
             mbar_init(&c->full[i], 1);
@@ -810,6 +979,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&c->o_full[i], 1);
         }
         mbar_init(&c->q_full, kTcConsumers);
+        mbar_init(&c->edge_go, 1);
+        mbar_init(&c->edge_done, 1);
         mbar_init(&c->cons, kTcConsumers);
         mbar_init(&c->fin, 1);
         mbar_init(&c->stall, 1);
@@ -824,7 +995,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (w >= kTcConsumers) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegHelper));
         if (w == kTcConsumers) tc_producer<D>(p, smem, c, &tk, &tv, s0, s1);
-        else if (w == kTcConsumers + 1) tc_issuer<D>(p, smem, gen, c, tmem, s0, s1);
+        else if (w == kTcConsumers + 1) tc_issuer<D>(p, smem, c, tmem, s0, s1);
+        else if (w == kTcConsumers + 2) tc_edges<D>(p, gen, c, s0, s1);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegConsumer));
         if (!p.stall || wait_tc(&c->stall, 0u, &c->abort, p)) {
