@@ -1,5 +1,5 @@
-// art_attend.cu -- dense_extend and dense_decode_shared: argument checks, the plan
-// kernel that builds the work list (art_attend.cuh), and the merge kernel.
+// art_attend.cu -- dense_extend and dense_decode_shared: argument checks and the merge
+// kernel (the work and its shares: art_attend.cuh).
 #include <cmath>
 #include <cstdlib>
 
@@ -9,436 +9,164 @@ namespace art {
 
 int check_shape(const art_shape* s);  // art_api.cu
 
-constexpr int kPlanBlock = 512;
 constexpr int kMergeBlock = 256;
-constexpr int kEntSmem = 2048;  // entities whose first items are searched in shared memory
 
-// Inclusive sums over the block; returns the exclusive one, `total` the block's.
-__device__ __forceinline__ long long block_scan(long long v, long long* s_warp, long long& total) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    long long x = v;
+// One row's pieces joined: a lane holds one piece's (m, l), up to 32 at a time, then the
+// pieces' columns are read side by side (no load waits for another).
+template <bool kBF16, int D>
+struct MergeRow {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    int lane;
+    // at(k, prow, nrow): piece k's partial row and its segment's rows; false where it is empty
+    template <class F>
+    __device__ __forceinline__ void add(const AttendParams& p, int n, int r, F at) {
+        for (int k0 = 0; k0 < n; k0 += 32) {
+            int prow = 0, nrow = 1;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (k0 + lane < n && at(k0 + lane, prow, nrow)) ml = __ldcg(&p.part_ml[prow + r]);
+            const bool live = ml.y != 0.f;  // saw a key (or a NaN)
+            float top = live ? ml.x : -INFINITY;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) s_warp[w] = x;
-    __syncthreads();
-    if (w == 0) {
-        long long t = lane < kPlanBlock / 32 ? s_warp[lane] : 0;
+            for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const float mn = fmaxf(m, top);
+            const float a = m == -INFINITY ? 0.f : exp2f(m - mn);
+            const float w = live ? exp2f(ml.x - mn) : 0.f;
+            float sum = live ? ml.y * w : 0.f;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane >= o) t += y;
+            for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+            l = l * a + sum;
+            o.x *= a;
+            o.y *= a;
+            o.z *= a;
+            o.w *= a;
+            m = mn;
+            unsigned todo = __ballot_sync(0xffffffffu, live);
+            while (todo) {
+                float4 v[4];
+                float f[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int src = todo ? __ffs(todo) - 1 : 0;
+                    f[u] = __shfl_sync(0xffffffffu, w, src);
+                    const int pr = __shfl_sync(0xffffffffu, prow, src), nr = __shfl_sync(0xffffffffu, nrow, src);
+                    v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (!todo) f[u] = 0.f;
+                    else if (lane < D / 4)
+                        v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (size_t)pr * D) + (size_t)lane * nr + r);
+                    todo &= todo - 1;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    o.x += v[u].x * f[u];
+                    o.y += v[u].y * f[u];
+                    o.z += v[u].z * f[u];
+                    o.w += v[u].w * f[u];
+                }
+            }
         }
-        if (lane < kPlanBlock / 32) s_warp[lane] = t;
     }
-    __syncthreads();
-    total = s_warp[kPlanBlock / 32 - 1];
-    const long long before = w > 0 ? s_warp[w - 1] : 0;
-    __syncthreads();
-    return before + x - v;
-}
-
-// Another CTA's entity: read past the L1.
-__device__ __forceinline__ Entity load_entity(const Entity* e) {
-    const int4 a = __ldcg(reinterpret_cast<const int4*>(e)), b = __ldcg(reinterpret_cast<const int4*>(e) + 1);
-    Entity r;
-    r.table_row = a.x;
-    r.tok0 = a.y;
-    r.nrows = a.z;
-    r.k0 = a.w;
-    r.k1 = b.x;
-    r.lim0 = b.y;
-    r.kind = b.z;
-    r.bad = b.w;
-    return r;
-}
-
-struct Item {
-    int e, g, rt;   // entity, KV head, row tile
-    int r0, nrow;
-    int k0, k1;     // keys of the tile's last row
-    int t0, tiles;  // first key tile, number of key tiles
+    __device__ __forceinline__ void store(const AttendParams& p, size_t row) {
+        if (lane >= D / 4) return;
+        const float inv = l > 0.f ? 1.f / l : l;  // no key seen: 0; NaN stays
+        if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if constexpr (kBF16)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + lane * 4) =
+                make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        else
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D + lane * 4) =
+                make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    }
 };
 
-__device__ __forceinline__ Item item_of(const AttendParams& p, const int* item0, int i) {
-    int lo = 0, hi = p.NE - 1;  // the last entity with item0 <= i
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (item0[mid] <= i) lo = mid;
-        else hi = mid - 1;
-    }
-    const Entity en = load_entity(&p.ent[lo]);
-    Item it;
-    it.e = lo;
-    const int nrt = (en.nrows + p.rt - 1) / p.rt, j = i - item0[lo];
-    it.g = j / nrt;
-    it.rt = j - it.g * nrt;
-    it.r0 = it.rt * p.rt;
-    it.nrow = min(p.rt, en.nrows - it.r0);
-    it.k0 = en.k0;
-    it.k1 = en.k1;
-    if (en.kind == kLimCausal && !en.bad) it.k1 = en.lim0 + (it.r0 + it.nrow - 1) / p.G;
-    it.t0 = it.k0 / kKeyTile;
-    it.tiles = it.k1 > it.k0 ? (it.k1 + kKeyTile - 1) / kKeyTile - it.t0 : 0;
-    return it;
-}
-
-// Whether the block-table entries [c0, c1) of a row all lie in the pool (block-wide).
-__device__ __forceinline__ bool pages_bad(const AttendParams& p, int row, int c0, int c1) {
-    int bad = 0;
-    const int32_t* t = p.block_table + (size_t)row * p.max_pages;
-    for (int c = c0 + (int)threadIdx.x; c < c1; c += kPlanBlock) {
-        const int pg = t[c];
-        bad |= pg < 0 || pg >= p.num_pages;
-    }
-    return __syncthreads_or(bad) != 0;
-}
-
-__device__ __forceinline__ int pages_of(int tokens, int Ps) { return (tokens + Ps - 1) / Ps; }
-
-// dense_extend, CTA b: sequence b's rows, keys and checks.
-__device__ void plan_extend(const AttendParams& p, int b, int& err) {
-    const int lo = p.offsets[b], hi = p.offsets[b + 1], len = p.seq_lens[b];
-    const bool off_ok = lo >= 0 && hi >= lo && hi <= p.T;
-    const int n = off_ok ? hi - lo : 0;
-    bool ok = len >= 0 && (long long)len <= (long long)p.max_pages * p.Ps && (!p.causal || len >= n);
-    if (!ok && off_ok) err |= ART_STATUS_BAD_SEQLEN;
-    if (ok && n > 0 && pages_bad(p, b, 0, pages_of(len, p.Ps))) {
-        err |= ART_STATUS_BAD_PAGE;
-        ok = false;
-    }
-    if (threadIdx.x == 0) {
-        Entity e;
-        e.table_row = b;
-        e.tok0 = lo;
-        e.nrows = n * p.G;
-        e.k0 = 0;
-        e.k1 = ok ? len : 0;
-        e.lim0 = len - n + 1;
-        e.kind = p.causal ? kLimCausal : kLimAll;
-        e.bad = !ok;
-        p.ent[b] = e;
-    }
-}
-
-// dense_decode_shared, CTA j < NG: group j's prefix.
-__device__ void plan_group(const AttendParams& p, int j, int& err) {
-    __shared__ int s_top;
-    const int lo = p.offsets[j], hi = p.offsets[j + 1], pre = p.prefix[j];
-    const long long cap = (long long)p.max_pages * p.Ps;
-    const bool off_ok = lo >= 0 && hi >= lo && hi <= p.B;
-    bool ok = pre >= 0 && pre <= cap;
-    if (threadIdx.x == 0) s_top = 0;
-    __syncthreads();
-    int top = 0;  // keys that the farthest member sees of the prefix
-    if (off_ok && ok)
-        for (int b = lo + (int)threadIdx.x; b < hi; b += kPlanBlock) {
-            const int len = p.seq_lens[b];
-            if (len >= 0 && len <= cap) top = max(top, min(len, pre));
-        }
-    if (top) atomicMax(&s_top, top);
-    __syncthreads();
-    top = s_top;
-    if (off_ok && hi > lo) {
-        if (!ok) err |= ART_STATUS_BAD_SEQLEN;
-        else if (pages_bad(p, lo, 0, pages_of(top, p.Ps))) {
-            err |= ART_STATUS_BAD_PAGE;
-            ok = false;
+// Whether a page of sequence b's own tokens, or of the prefix that group j's first
+// sequence (lead) holds, lies outside the pool: only asked when some CTA met such a page.
+__device__ bool seq_bad(const AttendParams& p, int b, int lead, int lane) {
+    bool bad = false;
+    for (int c = 0; c < p.ctas; ++c) {
+        if (!(p.cta_status[c] & ART_STATUS_BAD_PAGE)) continue;
+        const int2 r = p.cta_segs[c];
+        for (int i = r.x + lane; i < r.y; i += 32) {
+            const Seg& s = p.seg[i];
+            if (s.nrow > 0 && s.bad) bad |= s.kind == kLimSeq ? s.table_row == lead : s.table_row == b;
         }
     }
-    if (threadIdx.x == 0) {
-        Entity e;
-        e.table_row = lo;
-        e.tok0 = lo;
-        e.nrows = off_ok && ok && top > 0 ? (hi - lo) * p.G : 0;
-        e.k0 = 0;
-        e.k1 = top;
-        e.lim0 = 0;
-        e.kind = kLimSeq;
-        e.bad = !ok;
-        p.ent[j] = e;
-    }
-}
-
-// dense_decode_shared, CTA NG + b: sequence b's own tokens.
-__device__ void plan_own(const AttendParams& p, int b, int& err) {
-    int cnt = 0;  // group offsets at or below b
-    for (int i0 = 0; i0 <= p.NG; i0 += kPlanBlock) {
-        const int i = i0 + (int)threadIdx.x;
-        cnt += __syncthreads_count(i <= p.NG && p.NG > 0 && p.offsets[i] <= b);
-    }
-    const int j = cnt >= 1 && cnt <= p.NG ? cnt - 1 : -1;
-    const int len = p.seq_lens[b];
-    bool ok = len >= 0 && (long long)len <= (long long)p.max_pages * p.Ps;
-    if (!ok) err |= ART_STATUS_BAD_SEQLEN;
-    const int pre = ok && j >= 0 ? max(0, min(len, p.prefix[j])) : 0;
-    if (ok && pages_bad(p, b, pre / p.Ps, len > pre ? pages_of(len, p.Ps) : 0)) {
-        err |= ART_STATUS_BAD_PAGE;
-        ok = false;
-    }
-    if (threadIdx.x == 0) {
-        Entity e;
-        e.table_row = b;
-        e.tok0 = b;
-        e.nrows = ok && len > pre ? p.G : 0;
-        e.k0 = pre;
-        e.k1 = ok ? len : 0;
-        e.lim0 = 0;
-        e.kind = kLimAll;
-        e.bad = !ok;
-        p.ent[p.NG + b] = e;
-        p.group_of[b] = j;
-        p.row_lim[b] = ok ? pre : 0;
-    }
-}
-
-// One CTA per entity checks its device data; the last one to finish lays out the
-// work: items, their tiles end to end, the CTAs' shares and segments.
-__global__ void __launch_bounds__(kPlanBlock) art_attend_plan_kernel(const AttendParams p) {
-    __shared__ long long s_warp[kPlanBlock / 32];
-    __shared__ int s_item0[kEntSmem + 1];
-    __shared__ int s_last;
-    const int tid = threadIdx.x, lane = tid & 31;
-    int err = 0;
-    if (!p.shared) plan_extend(p, blockIdx.x, err);
-    else if ((int)blockIdx.x < p.NG) plan_group(p, blockIdx.x, err);
-    else plan_own(p, blockIdx.x - p.NG, err);
-    if (tid == 0) {
-        if (err) atomicOr(&p.hdr->status, err);
-        __threadfence();
-        s_last = atomicAdd(&p.hdr->plan_done, 1u) == gridDim.x - 1;
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-
-    // offsets that do not rise from 0 to their end: nothing is computed or written
-    const int noff = p.shared ? p.NG : p.B, top = p.shared ? p.B : p.T;
-    int bad = 0;
-    if (noff > 0)
-        for (int i = tid; i <= noff; i += kPlanBlock) {
-            const int o = p.offsets[i];
-            bad |= o < 0 || o > top || (i < noff && p.offsets[i + 1] < o);
-        }
-    bad = __syncthreads_or(bad);
-    if (bad) {
-        if (tid == 0) {
-            atomicOr(&p.hdr->status, ART_STATUS_BAD_OFFSETS);
-            p.hdr->n_units = -1;  // the merge kernel writes nothing either
-            *p.merge_n = 0;
-        }
-        for (int c = tid; c <= p.ctas; c += kPlanBlock) p.cta_first[c] = 0;
-        return;
-    }
-    // a group whose prefix is bad takes its sequences with it
-    if (p.shared)
-        for (int b = tid; b < p.B; b += kPlanBlock) {
-            const int j = __ldcg(&p.group_of[b]);
-            if (j >= 0 && __ldcg(&p.ent[j].bad)) {
-                p.ent[p.NG + b].nrows = 0;
-                p.row_lim[b] = 0;
-            }
-        }
-    __syncthreads();
-    // items and partial rows before each entity
-    int* item0 = p.NE <= kEntSmem ? s_item0 : p.item0;
-    long long items = 0, prows = 0;
-    for (int e0 = 0; e0 < p.NE; e0 += kPlanBlock) {
-        const int e = e0 + tid;
-        const int nrows = e < p.NE ? __ldcg(&p.ent[e].nrows) : 0;
-        const long long mine = (long long)((nrows + p.rt - 1) / p.rt) * p.Hkv;
-        long long tot;
-        const long long before = block_scan(mine, s_warp, tot);
-        long long rtot;
-        const long long rbefore = block_scan((long long)nrows * p.Hkv, s_warp, rtot);
-        if (e < p.NE) {
-            item0[e] = (int)(items + before);
-            p.item0[e] = (int)(items + before);
-            p.prow0[e] = (int)(prows + rbefore);
-        }
-        items += tot;
-        prows += rtot;
-    }
-    const int NI = (int)items;
-    if (tid == 0) {
-        p.item0[p.NE] = NI;
-        *p.merge_n = 0;
-    }
-    __syncthreads();
-    // the whole work and a CTA's share of it
-    long long part = 0;
-    for (int i = tid; i < NI; i += kPlanBlock) part += item_of(p, item0, i).tiles;
-    long long W;
-    (void)block_scan(part, s_warp, W);
-    const long long quota = W > p.ctas ? (W + p.ctas - 1) / p.ctas : 1;
-    // segments: piece c of item i is segment i + c (both rise along the work; where an
-    // item ends at the end of a share one number stays free and is marked empty)
-    const int c_end = W > 0 ? (int)((W - 1) / quota) : 0;
-    for (int c = tid; c <= p.ctas; c += kPlanBlock)
-        if ((long long)c * quota >= W) p.cta_first[c] = W > 0 ? NI + c_end : 0;
-    Seg none;
-    none.table_row = none.tok0 = none.r0 = none.nrow = none.g = none.k0 = none.k1 = none.lim0 = none.kind = 0;
-    none.prow = -1;
-    none.pad[0] = none.pad[1] = 0;
-    long long start = 0;
-    for (int i0 = 0; i0 < NI; i0 += kPlanBlock) {
-        const int i = i0 + tid;
-        Item it;
-        it.tiles = 0;
-        if (i < NI) it = item_of(p, item0, i);
-        long long tot;
-        const long long s = start + block_scan(it.tiles, s_warp, tot);
-        start += tot;
-        int c0 = 0, np = 0;
-        Seg sg = none;
-        if (i < NI) {
-            c0 = (int)(s / quota);
-            const Entity en = load_entity(&p.ent[it.e]);
-            sg.table_row = en.table_row;
-            sg.tok0 = en.tok0;
-            sg.r0 = it.r0;
-            sg.nrow = it.nrow;
-            sg.g = it.g;
-            sg.lim0 = en.lim0;
-            sg.kind = en.kind;
-            if (it.tiles == 0) {
-                p.seg[i + c0] = none;
-            } else {
-                np = (int)((s + it.tiles - 1) / quota) - c0 + 1;
-                if ((s + it.tiles) % quota == 0) p.seg[i + c0 + np] = none;
-            }
-            p.item_c[i] = make_int2(c0, np);
-            if (!p.shared && np != 1) {  // split, or no keys: the merge kernel writes its rows
-                MergeItem m;
-                m.tok0 = en.tok0;
-                m.r0 = it.r0;
-                m.nrow = it.nrow;
-                m.g = it.g;
-                m.c0 = c0;
-                m.np = np;
-                m.pad[0] = m.pad[1] = 0;
-                p.merge[atomicAdd(p.merge_n, 1)] = m;
-            }
-        }
-        const int prow_i = i < NI && p.shared ? p.prow0[it.e] + it.g * __ldcg(&p.ent[it.e].nrows) + it.r0 : 0;
-        auto emit = [&](const Seg& base, int idx, long long s0, int t0, int tiles, int k0, int k1, int cf, int n, int c,
-                        int prow) {
-            Seg o = base;
-            const long long a = max(s0, (long long)c * quota) - s0, z = min(s0 + tiles, (long long)(c + 1) * quota) - s0;
-            o.k0 = max(k0, (t0 + (int)a) * kKeyTile);
-            o.k1 = min(k1, (t0 + (int)z) * kKeyTile);
-            o.prow = p.shared ? prow + c * p.rt : (n == 1 ? -1 : piece_row_extend(c, c == cf, p.rt));
-            p.seg[idx + c] = o;
-            if (s0 <= (long long)c * quota) p.cta_first[c] = idx + c;
-        };
-        const bool few = np <= 2;
-        if (few)
-            for (int c = c0; c < c0 + np; ++c) emit(sg, i, s, it.t0, it.tiles, it.k0, it.k1, c0, np, c, prow_i);
-        unsigned many = __ballot_sync(0xffffffffu, !few);
-        while (many) {
-            const int src = __ffs(many) - 1;
-            many &= many - 1;
-            Seg b;
-            b.table_row = __shfl_sync(0xffffffffu, sg.table_row, src);
-            b.tok0 = __shfl_sync(0xffffffffu, sg.tok0, src);
-            b.r0 = __shfl_sync(0xffffffffu, sg.r0, src);
-            b.nrow = __shfl_sync(0xffffffffu, sg.nrow, src);
-            b.g = __shfl_sync(0xffffffffu, sg.g, src);
-            b.lim0 = __shfl_sync(0xffffffffu, sg.lim0, src);
-            b.kind = __shfl_sync(0xffffffffu, sg.kind, src);
-            b.pad[0] = b.pad[1] = 0;
-            const long long s0 = __shfl_sync(0xffffffffu, s, src);
-            const int t0 = __shfl_sync(0xffffffffu, it.t0, src), tiles = __shfl_sync(0xffffffffu, it.tiles, src);
-            const int k0 = __shfl_sync(0xffffffffu, it.k0, src), k1 = __shfl_sync(0xffffffffu, it.k1, src);
-            const int cf = __shfl_sync(0xffffffffu, c0, src), n = __shfl_sync(0xffffffffu, np, src);
-            const int pr = __shfl_sync(0xffffffffu, prow_i, src);
-            for (int c = cf + lane; c < cf + n; c += 32)
-                emit(b, i0 + (tid & ~31) + src, s0, t0, tiles, k0, k1, cf, n, c, pr);
-        }
-    }
-}
-
-// One warp per output row: joins the row's partial results and rounds once.
-template <bool kBF16, int D>
-__device__ __forceinline__ void merge_row(const AttendParams& p, float4 o, float l, size_t out_row, int lane) {
-    constexpr int PER = D / 32;  // columns of a lane: 4 or 2
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no key seen: 0; NaN stays
-    const float x[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-    if constexpr (kBF16) {
-        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + out_row * D + lane * PER);
-        dst[0] = pack_bf16(x[0], x[1]);
-        if constexpr (PER == 4) dst[1] = pack_bf16(x[2], x[3]);
-    } else {
-        float* dst = static_cast<float*>(p.out) + out_row * D + lane * PER;
-#pragma unroll
-        for (int k = 0; k < PER; ++k) dst[k] = x[k];
-    }
-}
-
-// Adds the partial row `pr` into the running (m, l, o).
-template <int D>
-__device__ __forceinline__ void merge_add(const AttendParams& p, int pr, float& m, float& l, float4& o, int lane) {
-    constexpr int PER = D / 32;
-    const float2 ml = __ldcg(&p.part_ml[pr]);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* src = p.part_o + (size_t)pr * D + lane * PER;
-    if constexpr (PER == 4) {
-        x = __ldcg(reinterpret_cast<const float4*>(src));
-    } else {
-        const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
-        x.x = t.x;
-        x.y = t.y;
-    }
-    if (ml.y == 0.f) return;  // saw no key
-    const float mn = fmaxf(m, ml.x);
-    const float a = m == -INFINITY ? 0.f : exp2f(m - mn);
-    const float b = exp2f(ml.x - mn);
-    l = l * a + ml.y * b;
-    o.x = o.x * a + x.x * b;
-    o.y = o.y * a + x.y * b;
-    o.z = o.z * a + x.z * b;
-    o.w = o.w * a + x.w * b;
-    m = mn;
+    return __any_sync(0xffffffffu, bad);
 }
 
 template <bool kBF16, int D>
 __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const AttendParams p) {
     constexpr int WPB = kMergeBlock / 32;
-    const int lane = threadIdx.x & 31;
-    const int warp = blockIdx.x * WPB + (threadIdx.x >> 5), warps = gridDim.x * WPB;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ int s_status;
+    if (tid == 0) s_status = 0;
+    __syncthreads();
+    if (tid < p.ctas && p.cta_status[tid]) atomicOr(&s_status, p.cta_status[tid]);
+    __syncthreads();
+    const int status = s_status;
+    if (blockIdx.x == 0 && tid == 0) p.hdr->status = status;
+    if (!p.info->ok) return;
+    const long long quota = p.info->quota;
+    const bool slow = (status & ART_STATUS_BAD_PAGE) != 0;
+    MergeRow<kBF16, D> z;
+    z.lane = lane;
     if (p.shared) {
-        if (p.hdr->n_units < 0) return;  // bad offsets
-        for (int row = warp; row < p.B * p.Hq; row += warps) {
+        for (int row = blockIdx.x * WPB + w; row < p.B * p.Hq; row += gridDim.x * WPB) {
             const int b = row / p.Hq, h = row - b * p.Hq, g = h / p.G, hg = h - g * p.G;
-            float m = -INFINITY, l = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int j = p.group_of[b];
-            auto add_item = [&](int e, int R) {
-                const Entity en = p.ent[e];
-                if (en.nrows == 0) return;
-                const int nrt = (en.nrows + p.rt - 1) / p.rt, t = R / p.rt;
-                const int2 c = p.item_c[p.item0[e] + g * nrt + t];
-                const int pr = p.prow0[e] + g * en.nrows + R;
-                for (int k = 0; k < c.y; ++k) merge_add<D>(p, pr + (c.x + k) * p.rt, m, l, o, lane);
-            };
-            if (j >= 0 && p.row_lim[b] > 0) add_item(j, (b - p.ent[j].tok0) * p.G + hg);
-            add_item(p.NG + b, hg);
-            merge_row<kBF16, D>(p, o, l, row, lane);
+            const int j = p.group_of[b], lim = p.row_lim[b];
+            MergeRow<kBF16, D> m;
+            m.lane = lane;
+            const int lead = j >= 0 ? p.offsets[j] : -1;
+            if (lim >= 0 && !(slow && seq_bad(p, b, lead, lane))) {
+                // the item of entity e that holds its row R: pieces by the plan's arithmetic
+                auto item = [&](int e, int R) {
+                    const EntityPlace q = p.place[e];
+                    if (q.nrows == 0) return;
+                    const int nrt = (q.nrows + p.rt - 1) / p.rt, r = R / p.rt, n = min(p.rt, q.nrows - r * p.rt);
+                    const int tiles = (q.k1 + kKeyTile - 1) / kKeyTile - q.k0 / kKeyTile;
+                    const int base = item_cost_base(p, n), per = item_cost_tile(p, n), last = q.nrows - (nrt - 1) * p.rt;
+                    const long long full = item_cost_base(p, p.rt) + (long long)item_cost_tile(p, p.rt) * tiles;
+                    const long long hc = (nrt - 1) * full + item_cost_base(p, last) + (long long)item_cost_tile(p, last) * tiles;
+                    const long long x = q.start + g * hc + r * full, end = x + base + (long long)per * tiles;
+                    const int c0 = (int)(x / quota), np = (int)((end - 1) / quota) - c0 + 1;
+                    const int pr = (int)(q.prow + (long long)g * q.nrows + r * p.rt);
+                    m.add(p, np, R - r * p.rt, [&](int k, int& prow, int& nrow) {
+                        const long long a = max((c0 + k) * quota, x), y = min((c0 + k + 1) * quota, end);
+                        prow = pr + (c0 + k) * p.rt;
+                        nrow = n;
+                        return tiles_before(y - x, base, per, tiles) > tiles_before(a - x, base, per, tiles);
+                    });
+                };
+                if (lim > 0) item(j, (b - lead) * p.G + hg);
+                item(p.NG + b, hg);
+            }
+            m.store(p, row);
         }
         return;
     }
-    const long long n = (long long)*p.merge_n * p.rt;
-    for (long long w = warp; w < n; w += warps) {
-        const MergeItem it = p.merge[w / p.rt];
-        const int r = (int)(w % p.rt);
-        if (r >= it.nrow) continue;
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < it.np; ++k) merge_add<D>(p, piece_row_extend(it.c0 + k, k == 0, p.rt) + r, m, l, o, lane);
-        const int R = it.r0 + r, t = R / p.G;
-        merge_row<kBF16, D>(p, o, l, (size_t)(it.tok0 + t) * p.Hq + it.g * p.G + (R - t * p.G), lane);
+    for (int c = blockIdx.x; c < p.ctas; c += gridDim.x) {
+        const MergeItem it = p.merge[c];
+        if (it.np == 0 || (slow && seq_bad(p, it.seq, -1, lane))) continue;
+        const int base = item_cost_base(p, it.nrow), per = item_cost_tile(p, it.nrow);
+        for (int r = w; r < it.nrow; r += WPB) {
+            MergeRow<kBF16, D> m;
+            m.lane = lane;
+            m.add(p, it.np, r, [&](int k, int& prow, int& nrow) {
+                const long long a = k == 0 ? 0 : it.off + (k - 1) * quota;
+                prow = piece_row_extend(it.c0 + k, k == 0, p.rt);
+                nrow = it.nrow;
+                return tiles_before(it.off + k * quota, base, per, it.tiles) > tiles_before(a, base, per, it.tiles);
+            });
+            const int R = it.r0 + r, t = R / p.G;
+            m.store(p, (size_t)(it.tok0 + t) * p.Hq + it.g * p.G + (R - t * p.G));
+        }
+    }
+    // sequences without keys, and bad ones: zero
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        const int lo = p.offsets[b], hi = p.offsets[b + 1];
+        if (lo == hi || !(p.place[b].nrows == 0 || (slow && seq_bad(p, b, -1, lane)))) continue;
+        for (size_t row = (size_t)lo * p.Hq + w; row < (size_t)hi * p.Hq; row += WPB) z.store(p, row);
     }
 }
 
@@ -453,17 +181,15 @@ static size_t attend_layout(AttendParams& p, unsigned char* base) {
     p.G = p.Hq / p.Hkv;
     p.NE = p.shared ? p.NG + p.B : p.B;
     const long long rows = (long long)(p.shared ? p.B : p.T) * p.G;  // of one KV head
-    // rows of an item's tile; items and partial rows at most
-    const long long ent = p.shared ? p.NG : p.B;
-    long long items = (rows / p.rt + ent) * p.Hkv;
+    // items and partial rows at most
+    long long items = (rows / p.rt + (p.shared ? p.NG : p.B)) * p.Hkv;
     if (p.shared) items += (long long)p.B * p.Hkv;
     const long long prows =
         p.shared ? 2 * rows * p.Hkv + (long long)(kAttendCtas + 1) * p.rt : 2LL * kAttendCtas * p.rt;
     // 32-bit row and key counts in the work list
-    if (rows > (1LL << 30) || items > (1LL << 28) || prows > (1LL << 30) ||
+    if (rows > (1LL << 30) || items > (1LL << 28) || prows > (1LL << 30) || p.NG > kMaxGroups ||
         (long long)p.max_pages * p.Ps > (1LL << 30))
         return 0;
-    p.max_items = (int)items;
     p.part_rows = (int)prows;
     size_t o = sizeof(WsHeader);
     auto take = [&](size_t bytes) {
@@ -472,20 +198,21 @@ static size_t attend_layout(AttendParams& p, unsigned char* base) {
         return base ? base + at : nullptr;
     };
     p.hdr = reinterpret_cast<WsHeader*>(base);
-    p.ent = reinterpret_cast<Entity*>(take(sizeof(Entity) * (size_t)p.NE));
+    p.info = reinterpret_cast<PlanInfo*>(take(sizeof(PlanInfo)));
+    p.place = reinterpret_cast<EntityPlace*>(take(sizeof(EntityPlace) * (size_t)p.NE));
     p.row_lim = reinterpret_cast<int*>(take(sizeof(int) * (size_t)p.B));
     p.group_of = reinterpret_cast<int*>(take(sizeof(int) * (size_t)p.B));
-    p.item0 = reinterpret_cast<int*>(take(sizeof(int) * ((size_t)p.NE + 1)));
-    p.prow0 = reinterpret_cast<int*>(take(sizeof(int) * (size_t)p.NE));
-    p.item_c = reinterpret_cast<int2*>(take(sizeof(int2) * (size_t)items));
-    p.cta_first = reinterpret_cast<int*>(take(sizeof(int) * (kAttendCtas + 1)));
-    p.seg = reinterpret_cast<Seg*>(take(sizeof(Seg) * ((size_t)items + kAttendCtas + 2)));
-    p.merge = reinterpret_cast<MergeItem*>(take(sizeof(MergeItem) * (size_t)(p.shared ? 1 : items)));
-    p.merge_n = reinterpret_cast<int*>(take(sizeof(int)));
+    p.cta_status = reinterpret_cast<int*>(take(sizeof(int) * kAttendCtas));
+    p.cta_segs = reinterpret_cast<int2*>(take(sizeof(int2) * kAttendCtas));
+    p.merge = reinterpret_cast<MergeItem*>(take(sizeof(MergeItem) * kAttendCtas));
+    p.seg = reinterpret_cast<Seg*>(take(sizeof(Seg) * ((size_t)items + kAttendCtas)));
     p.part_ml = reinterpret_cast<float2*>(take(sizeof(float2) * (size_t)prows));
     p.part_o = reinterpret_cast<float*>(take(sizeof(float) * (size_t)prows * p.D));
     return up256(o);
 }
+
+// Cost units (about 0.35 us): what segments of each kind take beside their neighbours.
+constexpr CostRule kCostBf16 = {3, 4, 10, 5, 12, 5}, kCostF32 = {1, 4, 1, 4, 1, 4};
 
 static void fill_shape(AttendParams& p, const art_shape& s) {
     p.B = s.batch;
@@ -498,6 +225,7 @@ static void fill_shape(AttendParams& p, const art_shape& s) {
     p.max_pages = s.max_pages_per_seq;
     p.num_pages = s.num_pages_total;
     p.rt = s.dtype == ART_DTYPE_BF16 ? kRowsTc : kItemRows;
+    p.cost = s.dtype == ART_DTYPE_BF16 ? kCostBf16 : kCostF32;
     p.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)s.head_dim));
 }
 
@@ -521,19 +249,24 @@ static int attend_run(AttendParams& p, const art_shape& s, void* workspace, size
             p.wait_ns = (unsigned long long)(ns < (long long)kWaitLimitNs ? ns : (long long)kWaitLimitNs);
         }
     }
-    if ((e = cudaMemsetAsync(p.hdr, 0, sizeof(WsHeader), st)) != cudaSuccess) return cuda_fail(e);
-    art_attend_plan_kernel<<<p.NE, kPlanBlock, 0, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
     const bool bf = s.dtype == ART_DTYPE_BF16;
     if ((e = bf ? launch_attend_tc(p, st) : launch_attend_simt(p, st)) != cudaSuccess) return cuda_fail(e);
-    const long long rows = p.shared ? (long long)p.B * p.Hq : (long long)p.ctas * p.rt;
-    const long long want = (rows + kMergeBlock / 32 - 1) / (kMergeBlock / 32);
-    const unsigned grid = (unsigned)(want < 4LL * p.ctas ? (want > 0 ? want : 1) : 4LL * p.ctas);
-    if (bf && p.D == 128) art_attend_merge_kernel<true, 128><<<grid, kMergeBlock, 0, st>>>(p);
-    else if (bf) art_attend_merge_kernel<true, 64><<<grid, kMergeBlock, 0, st>>>(p);
-    else if (p.D == 128) art_attend_merge_kernel<false, 128><<<grid, kMergeBlock, 0, st>>>(p);
-    else art_attend_merge_kernel<false, 64><<<grid, kMergeBlock, 0, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
+    // the merge kernel's launch overlaps the main kernel's end
+    const long long blocks = p.shared ? ((long long)p.B * p.Hq + kMergeBlock / 32 - 1) / (kMergeBlock / 32) : p.ctas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks < 8LL * p.ctas ? blocks : 8LL * p.ctas));
+    cfg.blockDim = dim3(kMergeBlock);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (bf && p.D == 128) e = cudaLaunchKernelEx(&cfg, art_attend_merge_kernel<true, 128>, p);
+    else if (bf) e = cudaLaunchKernelEx(&cfg, art_attend_merge_kernel<true, 64>, p);
+    else if (p.D == 128) e = cudaLaunchKernelEx(&cfg, art_attend_merge_kernel<false, 128>, p);
+    else e = cudaLaunchKernelEx(&cfg, art_attend_merge_kernel<false, 64>, p);
+    if (e != cudaSuccess) return cuda_fail(e);
     return ART_OK;
 }
 

@@ -6,7 +6,7 @@
 // rows 4 ty .. 4 ty + 3 and keys tx + 16 j, and the output columns 4 tx + 64 j of
 // the same rows; the running maximum and sum of a row live in the 16 threads of a
 // half warp, so the weights need no block-wide barrier.
-#include "art_attend.cuh"
+#include "art_attend_plan.cuh"
 
 namespace art {
 
@@ -16,7 +16,8 @@ constexpr int kPStride = kSimtKeys + 4;
 
 template <int D>
 constexpr size_t simt_smem() {
-    return sizeof(float) * (size_t)(kItemRows * (D + 4) + 2 * kSimtKeys * (D + 4) + kItemRows * kPStride);
+    const size_t tiles = sizeof(float) * (size_t)(kItemRows * (D + 4) + 2 * kSimtKeys * (D + 4) + kItemRows * kPStride);
+    return tiles > sizeof(PlanScratch) ? tiles : sizeof(PlanScratch);
 }
 
 __device__ __forceinline__ float f4(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
@@ -30,17 +31,17 @@ __global__ void __launch_bounds__(kSimtThreads) art_attend_simt_kernel(const Att
     float* sv = sk + kSimtKeys * S;
     float* sp = sv + kSimtKeys * S;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int s_end = p.cta_first[blockIdx.x + 1];
-    for (int si = p.cta_first[blockIdx.x]; si < s_end; ++si) {
-        const Seg sg = p.seg[si];
+    int s_begin, s_end;
+    plan_share<kSimtThreads>(p, reinterpret_cast<PlanScratch*>(smem), s_begin, s_end);
+    for (int si = s_begin; si < s_end; ++si) {
+        const Seg sg = load_seg(&p.seg[si]);
         if (sg.nrow == 0) continue;
         __syncthreads();
         for (int c = tid; c < kItemRows * CH; c += kSimtThreads) {
             const int r = c / CH, ch = c - r * CH;
             float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < sg.nrow) {
-                const int R = sg.r0 + r, t = R / p.G;
-                const size_t row = (size_t)(sg.tok0 + t) * p.Hq + sg.g * p.G + (R - t * p.G);
+                const size_t row = row_index(p, sg, r);
                 u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + row * D) + ch);
             }
             *reinterpret_cast<float4*>(sq + r * S + ch * 4) = u;
@@ -50,16 +51,13 @@ __global__ void __launch_bounds__(kSimtThreads) art_attend_simt_kernel(const Att
         float4 o[4][OC];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = ty * 4 + i, R = sg.r0 + r;
-            lim[i] = sg.k1;
-            if (sg.kind == kLimCausal) lim[i] = min(lim[i], sg.lim0 + R / p.G);
-            if (sg.kind == kLimSeq && r < sg.nrow) lim[i] = min(lim[i], p.row_lim[sg.tok0 + R / p.G]);
-            if (r >= sg.nrow) lim[i] = 0;
+            lim[i] = row_limit(p, sg, ty * 4 + i);
             m[i] = -INFINITY;
             l[i] = 0.f;
 #pragma unroll
             for (int c = 0; c < OC; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        int bad = 0;
         const int32_t* trow = p.block_table + (size_t)sg.table_row * p.max_pages;
         for (int kb = sg.k0 / kSimtKeys * kSimtKeys; kb < sg.k1; kb += kSimtKeys) {
             __syncthreads();
@@ -67,7 +65,12 @@ __global__ void __launch_bounds__(kSimtThreads) art_attend_simt_kernel(const Att
                 const int r = c / CH, ch = c - r * CH, key = kb + r;
                 float4 uk = make_float4(0.f, 0.f, 0.f, 0.f), uv = uk;
                 if (key >= sg.k0 && key < sg.k1) {
-                    const size_t row = ((size_t)__ldg(&trow[key / p.Ps]) * p.Hkv + sg.g) * p.Ps + (key & (p.Ps - 1));
+                    int pg = __ldg(&trow[key / p.Ps]);
+                    if (pg < 0 || pg >= p.num_pages) {  // the merge kernel zeroes the rows
+                        bad = 1;
+                        pg = 0;
+                    }
+                    const size_t row = ((size_t)pg * p.Hkv + sg.g) * p.Ps + (key & (p.Ps - 1));
                     uk = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.k) + row * D) + ch);
                     uv = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.v) + row * D) + ch);
                 }
@@ -150,6 +153,10 @@ __global__ void __launch_bounds__(kSimtThreads) art_attend_simt_kernel(const Att
                     }
             }
         }
+        if (bad) {
+            p.seg[si].bad = 1;
+            atomicOr(&p.cta_status[blockIdx.x], ART_STATUS_BAD_PAGE);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = ty * 4 + i;
@@ -158,12 +165,11 @@ __global__ void __launch_bounds__(kSimtThreads) art_attend_simt_kernel(const Att
                 if (tx == 0) p.part_ml[sg.prow + r] = make_float2(m[i], l[i]);
 #pragma unroll
                 for (int c = 0; c < OC; ++c)
-                    *reinterpret_cast<float4*>(p.part_o + (size_t)(sg.prow + r) * D + c * 64 + tx * 4) = o[i][c];
+                    *reinterpret_cast<float4*>(part_at(p, sg, r, c * 64 + tx * 4)) = o[i][c];
                 continue;
             }
             const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
-            const int R = sg.r0 + r, t = R / p.G;
-            const size_t row = (size_t)(sg.tok0 + t) * p.Hq + sg.g * p.G + (R - t * p.G);
+            const size_t row = row_index(p, sg, r);
 #pragma unroll
             for (int c = 0; c < OC; ++c) {
                 const size_t at = row * D + c * 64 + tx * 4;

@@ -40,7 +40,7 @@
 // Every wait is bounded (AttendParams::wait_ns); see wait_tc.
 #pragma once
 
-#include "art_attend.cuh"
+#include "art_attend_plan.cuh"
 
 namespace art {
 
@@ -59,7 +59,6 @@ constexpr int kTcConsumers = 8, kTcThreads = (kTcConsumers + 4) * 32;  // three 
 // 192 each and the third keeps 120: 64512.
 constexpr int kRegConsumer = 192, kRegHelper = 120;
 static_assert(128 * (2 * kRegConsumer + kRegHelper) <= kTcThreads * 168, "no more than the launch's registers");
-constexpr int kSmallRows = 16;   // rows of a segment that the consumer warps take by themselves
 constexpr float kRescale = 8.f;  // small segments: log2 units by which a row's maximum may lead its reference
 constexpr float kMaxSum = 1.0995116e12f;  // 2^40, large segments: the sum of a tile's weights from which it moves
 
@@ -213,29 +212,12 @@ __device__ __forceinline__ bool wait_tc(uint64_t* bar, uint32_t parity, int* abo
         if (__any_sync(0xffffffffu, late)) {
             if ((threadIdx.x & 31) == 0) {
                 st_volatile_shared(abort, 1);
-                atomicOr(&p.hdr->status, ART_STATUS_TIMEOUT);
+                atomicOr(&p.cta_status[blockIdx.x], ART_STATUS_TIMEOUT);
             }
             return false;
         }
         if (__any_sync(0xffffffffu, ld_volatile_shared(abort) != 0)) return false;
     }
-}
-
-__device__ __forceinline__ Seg load_seg(const Seg* s) {
-    Seg r;
-    const int4 a = __ldg(reinterpret_cast<const int4*>(s)), b = __ldg(reinterpret_cast<const int4*>(s) + 1),
-               c = __ldg(reinterpret_cast<const int4*>(s) + 2);
-    r.table_row = a.x;
-    r.tok0 = a.y;
-    r.r0 = a.z;
-    r.nrow = a.w;
-    r.g = b.x;
-    r.k0 = b.y;
-    r.k1 = b.z;
-    r.lim0 = b.w;
-    r.kind = c.x;
-    r.prow = c.y;
-    return r;
 }
 
 template <int NS>
@@ -258,24 +240,6 @@ struct Stage {  // position in the ring
     }
 };
 
-// R / G for R < 2^30: g_mul = ceil(2^34 / G)
-__device__ __forceinline__ int token_of(const AttendParams& p, int R) {
-    return (int)((unsigned long long)R * p.g_mul >> 34);
-}
-
-// A row's place in q and out.
-__device__ __forceinline__ size_t row_index(const AttendParams& p, const Seg& sg, int r) {
-    const int R = sg.r0 + r, t = token_of(p, R);
-    return (size_t)(sg.tok0 + t) * p.Hq + sg.g * p.G + (R - t * p.G);
-}
-// Keys that row r sees lie below this.
-__device__ __forceinline__ int row_limit(const AttendParams& p, const Seg& sg, int r) {
-    if (r >= sg.nrow) return sg.k0;
-    if (sg.kind == kLimAll) return sg.k1;
-    const int t = token_of(p, sg.r0 + r);
-    return min(sg.k1, sg.kind == kLimCausal ? sg.lim0 + t : __ldg(&p.row_lim[sg.tok0 + t]));
-}
-
 // ---------------------------------------------------------------------------
 // producer warp
 // ---------------------------------------------------------------------------
@@ -291,7 +255,8 @@ __device__ void tc_producer(const AttendParams& p, uint32_t smem, TcCtrl<TcCfg<D
     auto ids_of = [&](const Seg& sg, int bt) -> int {
         const int key = (sg.k0 / kKeyTile + bt * tpb) * kKeyTile + lane * prow;
         if (sg.nrow == 0 || key >= sg.k1 || key + prow <= sg.k0) return -1;
-        return __ldg(&p.block_table[(size_t)sg.table_row * p.max_pages + key / p.Ps]);
+        const int pg = __ldg(&p.block_table[(size_t)sg.table_row * p.max_pages + key / p.Ps]);
+        return pg < 0 || pg >= p.num_pages ? -2 : pg;
     };
     Stage<C::NS> st;
     uint32_t used = 0, small_use = 0, ph_t = 0, ph_s = 0;  // per stage: filled once; last use; parities to wait for
@@ -313,6 +278,13 @@ __device__ void tc_producer(const AttendParams& p, uint32_t smem, TcCtrl<TcCfg<D
         for (int bt = 0; bt * tpb < nt && ok; ++bt) {
             const int more = (bt + 1) * tpb < nt ? ids_of(sg, bt + 1) : ids_of(nx, 0);
             const int nb = min(tpb, nt - bt * tpb);
+            if (__any_sync(0xffffffffu, ids == -2)) {  // outside the pool: page 0 instead, the merge kernel zeroes the rows
+                if (lane == 0) {
+                    p.seg[si].bad = 1;
+                    atomicOr(&p.cta_status[blockIdx.x], ART_STATUS_BAD_PAGE);
+                }
+                if (ids == -2) ids = 0;
+            }
             for (int t = 0; t < nb && ok; ++t) {
                 const bool mine = lane / ppt == t && ids >= 0;
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * prow * (D * 2);
@@ -566,10 +538,9 @@ struct TcConsumer {
     template <int N>
     __device__ __forceinline__ void put(const Seg& sg, int r, int col, const float* o, float l) {
         if (sg.prow >= 0) {
-            float* dst = p.part_o + (size_t)(sg.prow + r) * D + col;
 #pragma unroll
             for (int i = 0; i < N; i += 4)
-                *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                *reinterpret_cast<float4*>(part_at(p, sg, r, col + i)) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             return;
         }
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no key seen: 0; NaN stays
@@ -958,13 +929,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                          const __grid_constant__ CUtensorMap tv) {
     using C = TcCfg<D>;
     extern __shared__ __align__(1024) unsigned char gen[];  // no static shared memory: the window's start
-    const int s0 = p.cta_first[blockIdx.x], s1 = p.cta_first[blockIdx.x + 1];
-    if (s0 >= s1) return;
     const uint32_t smem = smem_addr(gen);
     if (smem & 1023u) {  // the swizzle goes by address bits
-        if (threadIdx.x == 0) atomicOr(&p.hdr->status, ART_STATUS_INTERNAL);
+        if (threadIdx.x == 0) {
+            p.cta_status[blockIdx.x] = ART_STATUS_INTERNAL;
+            if (blockIdx.x == 0) p.info->ok = 0;
+        }
         return;
     }
+    int s0, s1;
+    static_assert(sizeof(PlanScratch) <= C::CTRL, "the scratch lies in the tiles");
+    plan_share<kTcThreads>(p, reinterpret_cast<PlanScratch*>(gen), s0, s1);
+    if (s0 >= s1) return;
     TcCtrl<C::NS>* c = reinterpret_cast<TcCtrl<C::NS>*>(gen + C::CTRL);
     const int w = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -988,6 +964,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         fence_mbar_init();
     }
     if (w == kTcConsumers + 1) tc_alloc(&c->tmem);
+    fence_proxy_async_smem();  // the scratch's accesses before the copies over it
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
