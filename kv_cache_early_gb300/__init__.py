@@ -232,36 +232,62 @@ def art_select_blocks(q, k_cache, block_table, seq_lens, top_frac, keep_last, vi
     return rc
 
 
-def _checked(shape: ArtShape, data=(), ints=()):
-    """Raises ArtError unless the tensors have the shape's dtype (`data`) or int32 (`ints`), lie on the
-    current device and are dense in the sizes given. Entries: (name, tensor, sizes); a size of None is
-    any, a tensor may be None. What the C ABI takes as bare pointers cannot be checked below it."""
-    import torch
-    want = torch.bfloat16 if shape.dtype == ART_DTYPE_BF16 else torch.float32
+# The wrappers below check their tensors, since the C ABI takes bare pointers. A decode
+# step calls them once a layer, so the checks are one condition of attribute reads, and
+# only a failed one goes through the tensors again to say what is wrong.
+_torch = None
+
+
+def _t():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _raw_stream(stream, device: int) -> int:
+    if stream is None:
+        torch = _t()
+        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return get(device) if get is not None else torch.cuda.current_stream(device).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _refuse(device, want, data, ints):
+    """Raises ArtError for the first tensor that does not have the dtype (`want`, or int32), the
+    device or the sizes given, or is not contiguous. Entries: (name, tensor or None, sizes)."""
+    torch = _t()
+    here = torch.device("cuda", device)
+    if torch.cuda.current_device() != device:
+        raise ArtError(f"the tensors are on {here}, the current device is {torch.cuda.current_device()}")
     for group, dt in ((data, want), (ints, torch.int32)):
         for name, t, sizes in group:
             if t is None:
                 continue
             if t.dtype != dt:
                 raise ArtError(f"{name} is {t.dtype}, not {dt}")
-            _here(name, t)
-            if len(t.shape) != len(sizes) or any(w is not None and n != w for n, w in zip(t.shape, sizes)):
-                raise ArtError(f"{name} is {tuple(t.shape)}, not {sizes}")
+            if t.device != here:
+                raise ArtError(f"{name} is on {t.device}, not on {here}")
+            if sizes is not None and tuple(t.shape) != tuple(sizes):
+                raise ArtError(f"{name} is {tuple(t.shape)}, not {tuple(sizes)}")
             if not t.is_contiguous():
                 raise ArtError(f"{name} is not contiguous")
 
 
-def _here(name, t):
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ArtError(f"{name} is on {t.device}, not on the current CUDA device")
+def _device_of(cache) -> int:
+    d = cache.get_device()
+    if d < 0:
+        raise ArtError(f"the cache is on {cache.device}, not on a CUDA device")
+    return d
 
 
-def _scratch(workspace):
-    _here("workspace", workspace)
-    if not workspace.is_contiguous():
-        raise ArtError("workspace is not contiguous")
-    return workspace.numel() * workspace.element_size()
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _int_ok(t, n, device, i32) -> bool:
+    return t.dtype is i32 and t.get_device() == device and t.shape == n and t.is_contiguous()
 
 
 def art_append_workspace_bytes(shape: ArtShape) -> int:
@@ -275,46 +301,79 @@ def art_append_kv(q, k, v, block_table, seq_lens, q_offsets, inv_freq, q_out, k_
     positions (see include/art.h). q, k, v: [tokens, heads, head_dim], dense in the last two
     dimensions (slices of one projection's rows will do); q and q_out may be None; q_offsets None:
     one new token for each sequence."""
-    tokens, hkv, d = int(k.shape[0]), shape.num_kv_heads, shape.head_dim
+    L = _lib or lib()
+    torch = _t()
+    i32, dt = torch.int32, torch.bfloat16 if shape.dtype == ART_DTYPE_BF16 else torch.float32
+    batch, hq, hkv, d = shape.batch, shape.num_q_heads, shape.num_kv_heads, shape.head_dim
+    device = _device_of(k_cache)
+    tokens = k.shape[0]
     pool = (shape.num_pages_total, hkv, shape.page_size, d)
-    _checked(shape, (("q_out", q_out, (tokens, shape.num_q_heads, d)), ("k_cache", k_cache, pool),
-                     ("v_cache", v_cache, pool)),
-             (("block_table", block_table, (shape.batch, shape.max_pages_per_seq)),
-              ("seq_lens", seq_lens, (shape.batch,)), ("q_offsets", q_offsets, (shape.batch + 1,)),
-              ("positions", positions, (tokens,))))
-    for name, t, heads in (("q", q, shape.num_q_heads), ("k", k, hkv), ("v", v, hkv)):
+    step = [0, 0, 0]
+    dense = True
+    for i, t, heads in ((0, q, hq), (1, k, hkv), (2, v, hkv)):
         if t is None:
             continue
-        if t.dtype != k_cache.dtype or t.device != k_cache.device:
-            raise ArtError(f"{name} is {t.dtype} on {t.device}, the cache {k_cache.dtype} on {k_cache.device}")
-        dense = tokens == 0 or (t.stride(2) == 1 and (heads == 1 or t.stride(1) == d))
-        if tuple(t.shape) != (tokens, heads, d) or not dense:
-            raise ArtError(f"{name} is {tuple(t.shape)} with strides {t.stride()}: not dense rows of {heads} x {d}")
-    if inv_freq is not None and (inv_freq.dtype.itemsize != 4 or not inv_freq.is_floating_point() or
-                                 inv_freq.numel() != rot_dim // 2 or inv_freq.device != k_cache.device or
-                                 not inv_freq.is_contiguous()):
-        raise ArtError(f"inv_freq is not fp32 [{rot_dim // 2}] beside the cache")
-    if tokens <= 1:  # a lone row's stride is never used: any dense one
-        step = lambda t, h: h * d
-    else:
-        step = lambda t, h: t.stride(0)
-    rope = ArtRope(rot_dim=int(rot_dim), interleaved=int(bool(interleaved)), scale=float(scale))
-    rc = lib().art_append_kv(_ptr(q), _ptr(k), _ptr(v), 0 if q is None else step(q, shape.num_q_heads), step(k, hkv),
-                             step(v, hkv), _ptr(q_offsets), tokens, _ptr(positions), _ptr(block_table),
-                             _ptr(seq_lens), _ptr(inv_freq), ctypes.byref(rope), _ptr(q_out), _ptr(k_cache),
-                             _ptr(v_cache), ctypes.byref(shape), _ptr(workspace), _scratch(workspace),
-                             _stream(stream))
-    if check:
+        st = t.stride()
+        # a lone row's stride is never used: any whole one
+        step[i] = st[0] if tokens > 1 else heads * d
+        if not (t.dtype is dt and t.get_device() == device and t.shape == (tokens, heads, d) and
+                (tokens == 0 or (st[2] == 1 and (heads == 1 or st[1] == d)))):
+            dense = False
+    if not (dense and torch.cuda.current_device() == device and
+            k_cache.dtype is dt and k_cache.shape == pool and k_cache.is_contiguous() and
+            v_cache.dtype is dt and v_cache.shape == pool and v_cache.is_contiguous() and
+            v_cache.get_device() == device and
+            (q_out is None or (q_out.dtype is dt and q_out.shape == (tokens, hq, d) and q_out.is_contiguous() and
+                               q_out.get_device() == device)) and
+            _int_ok(block_table, (batch, shape.max_pages_per_seq), device, i32) and
+            _int_ok(seq_lens, (batch,), device, i32) and
+            (q_offsets is None or _int_ok(q_offsets, (batch + 1,), device, i32)) and
+            (positions is None or _int_ok(positions, (tokens,), device, i32)) and
+            (inv_freq is None or (inv_freq.dtype is torch.float32 and inv_freq.shape == (rot_dim // 2,) and
+                                  inv_freq.get_device() == device and inv_freq.is_contiguous())) and
+            workspace.get_device() == device and workspace.is_contiguous()):
+        _refuse(device, dt, (("k_cache", k_cache, pool), ("v_cache", v_cache, pool), ("q_out", q_out, (tokens, hq, d))),
+                (("block_table", block_table, (batch, shape.max_pages_per_seq)), ("seq_lens", seq_lens, (batch,)),
+                 ("q_offsets", q_offsets, (batch + 1,)), ("positions", positions, (tokens,))))
+        _refuse(device, torch.float32, (("inv_freq", inv_freq, (rot_dim // 2,)),), ())
+        _refuse(device, workspace.dtype, (("workspace", workspace, None),), ())
+        raise ArtError("q, k and v are not [tokens, heads, head_dim] rows of the cache's dtype and device, dense in "
+                       "their last two dimensions: " +
+                       ", ".join(f"{tuple(t.shape)} {t.dtype} strides {t.stride()}" for t in (q, k, v) if t is not None))
+    rope = ArtRope(int(rot_dim), 1 if interleaved else 0, scale)
+    rc = L.art_append_kv(_addr(q), k.data_ptr(), v.data_ptr(), step[0], step[1], step[2], _addr(q_offsets), tokens,
+                         _addr(positions), block_table.data_ptr(), seq_lens.data_ptr(), _addr(inv_freq),
+                         ctypes.byref(rope), _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
+                         ctypes.byref(shape), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, device))
+    if check and rc != ART_OK:
         _check(rc)
     return rc
 
 
-def _attend_checked(q, k_cache, v_cache, block_table, seq_lens, out, shape, tokens, ints):
-    pool = (shape.num_pages_total, shape.num_kv_heads, shape.page_size, shape.head_dim)
-    rows = (tokens, shape.num_q_heads, shape.head_dim)
-    _checked(shape, (("q", q, rows), ("k_cache", k_cache, pool), ("v_cache", v_cache, pool), ("out", out, rows)),
-             (("block_table", block_table, (shape.batch, shape.max_pages_per_seq)),
-              ("seq_lens", seq_lens, (shape.batch,))) + ints)
+def _attend_checked(q, k_cache, v_cache, block_table, seq_lens, out, shape, workspace, tokens, a, a_n, b, b_n) -> int:
+    """Checks the tensors of the two attention calls (a, b: int32 tensors or None with their lengths);
+    returns the device."""
+    torch = _t()
+    i32, dt = torch.int32, torch.bfloat16 if shape.dtype == ART_DTYPE_BF16 else torch.float32
+    batch, d = shape.batch, shape.head_dim
+    device = _device_of(k_cache)
+    pool = (shape.num_pages_total, shape.num_kv_heads, shape.page_size, d)
+    rows = (tokens, shape.num_q_heads, d)
+    if not (torch.cuda.current_device() == device and
+            q.dtype is dt and q.shape == rows and q.is_contiguous() and q.get_device() == device and
+            out.dtype is dt and out.shape == rows and out.is_contiguous() and out.get_device() == device and
+            k_cache.dtype is dt and k_cache.shape == pool and k_cache.is_contiguous() and
+            v_cache.dtype is dt and v_cache.shape == pool and v_cache.is_contiguous() and
+            v_cache.get_device() == device and
+            _int_ok(block_table, (batch, shape.max_pages_per_seq), device, i32) and
+            _int_ok(seq_lens, (batch,), device, i32) and
+            (a is None or _int_ok(a, (a_n,), device, i32)) and (b is None or _int_ok(b, (b_n,), device, i32)) and
+            workspace.get_device() == device and workspace.is_contiguous()):
+        _refuse(device, dt, (("q", q, rows), ("k_cache", k_cache, pool), ("v_cache", v_cache, pool), ("out", out, rows)),
+                (("block_table", block_table, (batch, shape.max_pages_per_seq)), ("seq_lens", seq_lens, (batch,)),
+                 ("offsets", a, (a_n,)), ("prefix_lens", b, (b_n,))))
+        _refuse(device, workspace.dtype, (("workspace", workspace, None),), ())
+    return device
 
 
 def dense_extend_workspace_bytes(shape: ArtShape, num_tokens: int) -> int:
@@ -325,13 +384,14 @@ def dense_extend(q, k_cache, v_cache, block_table, seq_lens, q_offsets, out, sha
                  causal: bool = True, stream=None, check: bool = True) -> int:
     """Attention of several new tokens of each sequence over its cached tokens (see include/art.h);
     causal False: every new token sees all of them (cross attention)."""
-    tokens = int(q.shape[0])
-    _attend_checked(q, k_cache, v_cache, block_table, seq_lens, out, shape, tokens,
-                    (("q_offsets", q_offsets, (shape.batch + 1,)),))
-    rc = lib().dense_extend(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
-                            _ptr(q_offsets), tokens, int(bool(causal)), _ptr(out), ctypes.byref(shape),
-                            _ptr(workspace), _scratch(workspace), _stream(stream))
-    if check:
+    L = _lib or lib()
+    tokens = q.shape[0]
+    device = _attend_checked(q, k_cache, v_cache, block_table, seq_lens, out, shape, workspace, tokens,
+                             q_offsets, shape.batch + 1, None, 0)
+    rc = L.dense_extend(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                        seq_lens.data_ptr(), q_offsets.data_ptr(), tokens, 1 if causal else 0, out.data_ptr(),
+                        ctypes.byref(shape), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, device))
+    if check and rc != ART_OK:
         _check(rc)
     return rc
 
@@ -344,13 +404,15 @@ def dense_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offset
                         shape: ArtShape, workspace, stream=None, check: bool = True) -> int:
     """Decode attention of a batch whose groups of sequences share prefixes (see include/art.h);
     group_offsets and prefix_lens None: no groups."""
-    groups = 0 if prefix_lens is None else int(prefix_lens.shape[0])
-    _attend_checked(q, k_cache, v_cache, block_table, seq_lens, out, shape, shape.batch,
-                    (("group_offsets", group_offsets, (groups + 1,)), ("prefix_lens", prefix_lens, (groups,))))
-    rc = lib().dense_decode_shared(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
-                                   _ptr(group_offsets), _ptr(prefix_lens), groups, _ptr(out), ctypes.byref(shape),
-                                   _ptr(workspace), _scratch(workspace), _stream(stream))
-    if check:
+    L = _lib or lib()
+    groups = 0 if prefix_lens is None else prefix_lens.shape[0]
+    device = _attend_checked(q, k_cache, v_cache, block_table, seq_lens, out, shape, workspace, shape.batch,
+                             group_offsets, groups + 1, prefix_lens, groups)
+    rc = L.dense_decode_shared(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                               seq_lens.data_ptr(), _addr(group_offsets), _addr(prefix_lens), groups,
+                               out.data_ptr(), ctypes.byref(shape), workspace.data_ptr(), workspace.nbytes,
+                               _raw_stream(stream, device))
+    if check and rc != ART_OK:
         _check(rc)
     return rc
 

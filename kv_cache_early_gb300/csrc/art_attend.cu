@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
     if (tid < p.ctas && p.cta_status[tid]) atomicOr(&s_status, p.cta_status[tid]);
     __syncthreads();
     const int status = s_status;
-    if (blockIdx.x == 0 && tid == 0) p.hdr->status = status;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) p.hdr->status = status;
     if (!p.info->ok) return;
     const long long quota = p.info->quota;
     const bool slow = (status & ART_STATUS_BAD_PAGE) != 0;
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
         const MergeItem it = p.merge[c];
         if (it.np == 0 || (slow && seq_bad(p, it.seq, -1, lane))) continue;
         const int base = item_cost_base(p, it.nrow), per = item_cost_tile(p, it.nrow);
-        for (int r = w; r < it.nrow; r += WPB) {
+        for (int r = blockIdx.y * WPB + w; r < it.nrow; r += gridDim.y * WPB) {
             MergeRow<kBF16, D> m;
             m.lane = lane;
             m.add(p, it.np, r, [&](int k, int& prow, int& nrow) {
@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         const int lo = p.offsets[b], hi = p.offsets[b + 1];
         if (lo == hi || !(p.place[b].nrows == 0 || (slow && seq_bad(p, b, -1, lane)))) continue;
-        for (size_t row = (size_t)lo * p.Hq + w; row < (size_t)hi * p.Hq; row += WPB) z.store(p, row);
+        for (size_t row = (size_t)lo * p.Hq + blockIdx.y * WPB + w; row < (size_t)hi * p.Hq; row += gridDim.y * WPB)
+            z.store(p, row);
     }
 }
 
@@ -254,7 +255,7 @@ static int attend_run(AttendParams& p, const art_shape& s, void* workspace, size
     // the merge kernel's launch overlaps the main kernel's end
     const long long blocks = p.shared ? ((long long)p.B * p.Hq + kMergeBlock / 32 - 1) / (kMergeBlock / 32) : p.ctas;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(blocks < 8LL * p.ctas ? blocks : 8LL * p.ctas));
+    cfg.gridDim = dim3((unsigned)(blocks < 8LL * p.ctas ? blocks : 8LL * p.ctas), p.shared ? 1 : p.rt / 32);
     cfg.blockDim = dim3(kMergeBlock);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
