@@ -338,7 +338,9 @@ int art_append_kv(const void* q, const void* k, const void* v, int64_t q_stride,
  * page, gets a zero output. With bad offsets no output is written. Keys and
  * values outside a sequence's length may hold anything, NaN included; a value
  * that some new tokens of a sequence see must be finite for the others too.
- * Supported: 2^30 rows num_tokens * G and 2^30 tokens a sequence.
+ * Supported: num_tokens * G and a table row's tokens up to 2^30, and
+ * (num_tokens * G / rows + batch) * num_kv_heads * (a table row's tokens / 128) up
+ * to 2^30, with rows = 256 for bf16 and 64 for fp32.
  */
 size_t dense_extend_workspace_bytes(const art_shape* shape, int32_t num_tokens);
 int dense_extend(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
@@ -365,6 +367,8 @@ int dense_extend(const void* q, const void* k_cache, const void* v_cache, const 
  * A sequence with a bad length or page gets a zero output; a bad prefix length
  * or prefix page gives the whole group zero outputs; with bad offsets no output
  * is written. Values that some members see must be finite for the others too.
+ * Supported: as dense_extend, with batch query tokens and num_groups more
+ * sequences; num_groups up to 8192.
  */
 size_t dense_decode_shared_workspace_bytes(const art_shape* shape, int32_t num_groups);
 int dense_decode_shared(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
     const int status = s_status;
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) p.hdr->status = status;
     if (!p.info->ok) return;
-    const long long quota = p.info->quota;
+    const int quota = p.info->quota;
     const bool slow = (status & ART_STATUS_BAD_PAGE) != 0;
     MergeRow<kBF16, D> z;
     z.lane = lane;
@@ -123,16 +123,15 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
                 auto item = [&](int e, int R) {
                     const EntityPlace q = p.place[e];
                     if (q.nrows == 0) return;
-                    const int nrt = (q.nrows + p.rt - 1) / p.rt, r = R / p.rt, n = min(p.rt, q.nrows - r * p.rt);
+                    const int r = R / p.rt, n = min(p.rt, q.nrows - r * p.rt);
                     const int tiles = (q.k1 + kKeyTile - 1) / kKeyTile - q.k0 / kKeyTile;
-                    const int base = item_cost_base(p, n), per = item_cost_tile(p, n), last = q.nrows - (nrt - 1) * p.rt;
-                    const long long full = item_cost_base(p, p.rt) + (long long)item_cost_tile(p, p.rt) * tiles;
-                    const long long hc = (nrt - 1) * full + item_cost_base(p, last) + (long long)item_cost_tile(p, last) * tiles;
-                    const long long x = q.start + g * hc + r * full, end = x + base + (long long)per * tiles;
-                    const int c0 = (int)(x / quota), np = (int)((end - 1) / quota) - c0 + 1;
-                    const int pr = (int)(q.prow + (long long)g * q.nrows + r * p.rt);
+                    const int base = item_cost_base(p, n), per = item_cost_tile(p, n);
+                    const int full = item_cost_base(p, p.rt) + item_cost_tile(p, p.rt) * tiles;
+                    const int x = q.start + g * q.hc + r * full, end = x + base + per * tiles;
+                    const int c0 = x / quota, np = (end - 1) / quota - c0 + 1;
+                    const int pr = q.prow + g * q.nrows + r * p.rt;
                     m.add(p, np, R - r * p.rt, [&](int k, int& prow, int& nrow) {
-                        const long long a = max((c0 + k) * quota, x), y = min((c0 + k + 1) * quota, end);
+                        const int a = max((c0 + k) * quota, x), y = min((c0 + k + 1) * quota, end);
                         prow = pr + (c0 + k) * p.rt;
                         nrow = n;
                         return tiles_before(y - x, base, per, tiles) > tiles_before(a - x, base, per, tiles);
@@ -153,7 +152,7 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
             MergeRow<kBF16, D> m;
             m.lane = lane;
             m.add(p, it.np, r, [&](int k, int& prow, int& nrow) {
-                const long long a = k == 0 ? 0 : it.off + (k - 1) * quota;
+                const int a = k == 0 ? 0 : it.off + (k - 1) * quota;
                 prow = piece_row_extend(it.c0 + k, k == 0, p.rt);
                 nrow = it.nrow;
                 return tiles_before(it.off + k * quota, base, per, it.tiles) > tiles_before(a, base, per, it.tiles);
@@ -192,6 +191,11 @@ static size_t attend_layout(AttendParams& p, unsigned char* base) {
         (long long)p.max_pages * p.Ps > (1LL << 30))
         return 0;
     p.part_rows = (int)prows;
+    // cost units fit 31 bits, with room for sums of one share beyond the end
+    const long long tiles = ((long long)p.max_pages * p.Ps + kKeyTile - 1) / kKeyTile;
+    const long long per = p.cost.two_tile > p.cost.small_tile ? p.cost.two_tile : p.cost.small_tile;
+    if (items * (per * tiles + p.cost.two_item) > (1LL << 30)) p.cost = {0, 1, 0, 1, 0, 1};
+    if (items * tiles > (1LL << 30)) return 0;
     size_t o = sizeof(WsHeader);
     auto take = [&](size_t bytes) {
         const size_t at = up256(o);

@@ -63,7 +63,7 @@ struct Entity {
 // ... and its place in the work, for the merge kernel
 struct alignas(16) EntityPlace {
     int nrows, k0, k1, item0;  // item0: its first item
-    long long start, prow;     // its first cost unit; its first partial row (dense_decode_shared)
+    int start, prow, hc, pad;  // its first cost unit, its first partial row (dense_decode_shared), a KV head's cost
 };
 static_assert(sizeof(EntityPlace) == 32, "two 16-byte words");
 
@@ -76,9 +76,9 @@ struct alignas(16) MergeItem {
 };
 
 struct PlanInfo {
-    long long quota, total;  // cost units of a share, of the whole work
-    int ok;                  // 0: bad offsets, nothing is computed
-    int pad[3];
+    int quota, total;  // cost units of a share, of the whole work
+    int ok;            // 0: bad offsets, nothing is computed
+    int pad;
 };
 
 // Cost units of an item and of a key tile, by rows.
@@ -124,10 +124,9 @@ __device__ __forceinline__ int item_cost_base(const AttendParams& p, int nrow) {
     return nrow <= kSmallRows ? p.cost.small_item : nrow <= 128 ? p.cost.one_item : p.cost.two_item;
 }
 // Key tiles of an item before cost unit x of it.
-__device__ __forceinline__ int tiles_before(long long x, int base, int per, int tiles) {
+__device__ __forceinline__ int tiles_before(int x, int base, int per, int tiles) {
     if (x <= base) return 0;
-    const long long t = (x - base + per - 1) / per;
-    return t < tiles ? (int)t : tiles;
+    return min(tiles, (x - base + per - 1) / per);
 }
 
 // First partial row of the piece of an item that CTA c holds. dense_extend keeps two

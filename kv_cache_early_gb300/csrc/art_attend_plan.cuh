@@ -11,35 +11,56 @@ __device__ __forceinline__ int token_of(const AttendParams& p, int R) {
     return (int)((unsigned long long)R * p.g_mul >> 34);
 }
 
+// An entity with its place in the work.
+struct alignas(16) PlanEntity {
+    Entity en;
+    int nrt;           // row tiles (0: no work)
+    int hc, start;     // cost of one KV head, first cost unit
+    int item0, prow;   // first item, first partial row
+};
+static_assert(sizeof(PlanEntity) == 48, "three 16-byte words");
+
 struct PlanScratch {  // shared memory; may be reused once plan_share has returned
-    long long warp_sum[32];
-    int first, last, status;
-    int pad;
+    int4 warp_sum[12];
+    int first, last, status, listed;
+    PlanEntity list[384];
     int offs[kMaxGroups + 1];  // dense_decode_shared: group_offsets
     int top[kMaxGroups];       // ... and the keys that the farthest member sees of the prefix
 };
 
+// The code below runs once in a CTA's life, and most of its time is the fetch of its
+// instructions: loops stay rolled, functions are not repeated, counts have 32 bits (the
+// host bounds them, attend_layout).
+
+__device__ __forceinline__ void scan3(int (&v)[3]) {  // inclusive, over a warp
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int y = __shfl_up_sync(0xffffffffu, v[i], o);
+            if (lane >= o) v[i] += y;
+        }
+}
+
+// Exclusive sums of three values over the block, and their totals.
 template <int NT>
-__device__ __forceinline__ long long plan_scan(long long v, long long* s_warp, long long& total) {
+__device__ __forceinline__ void plan_scan(int (&v)[3], int (&total)[3], int4* s_warp) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    long long x = v;
+    const int own[3] = {v[0], v[1], v[2]};
+    scan3(v);
+    if (lane == 31) s_warp[w] = make_int4(v[0], v[1], v[2], 0);
+    named_bar_sync(1, NT);
+    const int4 t = lane < NT / 32 ? s_warp[lane] : make_int4(0, 0, 0, 0);
+    int u[3] = {t.x, t.y, t.z};
+    scan3(u);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+    for (int i = 0; i < 3; ++i) {
+        const int before = __shfl_sync(0xffffffffu, u[i], w > 0 ? w - 1 : 0);
+        total[i] = __shfl_sync(0xffffffffu, u[i], NT / 32 - 1);
+        v[i] += (w > 0 ? before : 0) - own[i];
     }
-    if (lane == 31) s_warp[w] = x;
-    __syncthreads();
-    long long before = 0, all = 0;
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) {
-        const long long t = s_warp[i];
-        before += i < w ? t : 0;
-        all += t;
-    }
-    total = all;
-    __syncthreads();
-    return before + x - v;
+    named_bar_sync(1, NT);
 }
 
 // Whether sequence b's length is one that its table row can hold.
@@ -47,56 +68,53 @@ __device__ __forceinline__ bool len_ok(const AttendParams& p, int len) {
     return len >= 0 && (long long)len <= (long long)p.max_pages * p.Ps;
 }
 
-// Entity e; `err` collects status bits. Keys none (k1 <= k0) where it has no work.
-__device__ __forceinline__ Entity entity_of(const AttendParams& p, const PlanScratch* s, int e, int& err) {
+// Entity e; `err` collects status bits. Keys none (k1 <= k0) where it has no work. A
+// group's needs the tops, which the own tokens of its members set.
+static __device__ __noinline__ Entity entity_of(const AttendParams& p, PlanScratch* s, int e, int& err) {
     Entity en;
-    if (!p.shared) {
-        const int lo = p.offsets[e], n = p.offsets[e + 1] - lo, len = p.seq_lens[e];
-        const bool ok = len_ok(p, len) && (!p.causal || len >= n);
-        if (!ok) err |= ART_STATUS_BAD_SEQLEN;
-        en.table_row = e;
-        en.tok0 = lo;
-        en.nrows = n * p.G;
-        en.k0 = 0;
-        en.k1 = ok && n > 0 ? len : 0;
-        en.lim0 = len - n + 1;
-        en.kind = p.causal ? kLimCausal : kLimAll;
-    } else if (e < p.NG) {
+    en.k0 = en.lim0 = 0;
+    if (p.shared && e < p.NG) {
         en.table_row = en.tok0 = s->offs[e];
         en.nrows = (s->offs[e + 1] - s->offs[e]) * p.G;
-        en.k0 = 0;
-        en.k1 = en.nrows > 0 ? s->top[e] : 0;
-        en.lim0 = 0;
+        en.k1 = s->top[e];
         en.kind = kLimSeq;
-    } else {
-        const int b = e - p.NG, len = p.seq_lens[b];
-        int lo = -1, hi = p.NG;  // offs[lo] <= b < offs[hi], as far as there are such
+        return en;
+    }
+    const int b = p.shared ? e - p.NG : e;
+    const int len = p.seq_lens[b];
+    bool ok = len_ok(p, len);
+    en.table_row = en.tok0 = b;
+    en.nrows = p.G;
+    en.k1 = len;
+    en.kind = kLimAll;
+    if (!p.shared) {
+        const int lo = p.offsets[b], n = p.offsets[b + 1] - lo;
+        ok = ok && (!p.causal || len >= n);
+        en.tok0 = lo;
+        en.nrows = n * p.G;
+        en.lim0 = len - n + 1;
+        if (p.causal) en.kind = kLimCausal;
+        if (n == 0) en.k1 = 0;
+    } else if (p.NG > 0 && b >= s->offs[0] && b < s->offs[p.NG]) {
+        int lo = 0, hi = p.NG;  // its group: the last that starts at or before b
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (s->offs[mid] <= b) lo = mid;
             else hi = mid;
         }
-        const int j = lo >= 0 && p.NG > 0 && b < s->offs[p.NG] ? lo : -1;
-        bool ok = len_ok(p, len);
-        if (!ok) err |= ART_STATUS_BAD_SEQLEN;
-        int pre = 0;
-        if (j >= 0) {
-            pre = p.prefix[j];
-            if (!len_ok(p, pre)) {
-                err |= ART_STATUS_BAD_SEQLEN;
-                ok = false;
-            }
-        }
-        en.table_row = en.tok0 = b;
-        en.nrows = p.G;
-        en.k0 = ok ? min(len, pre) : 0;
-        en.k1 = ok ? len : 0;
-        en.lim0 = ok ? en.k0 : -1;  // what its rows see of the prefix
-        en.kind = kLimAll;
-        if (blockIdx.x == 0) {
-            p.group_of[b] = j;
-        }
+        const int pre = p.prefix[lo];
+        ok = ok && len_ok(p, pre);
+        en.k0 = min(len, pre);
+        if (ok && en.k0 > 0) atomicMax(&s->top[lo], en.k0);
+        if (blockIdx.x == 0) p.group_of[b] = lo;
+    } else if (blockIdx.x == 0) {
+        p.group_of[b] = -1;
     }
+    if (!ok) {
+        err |= ART_STATUS_BAD_SEQLEN;
+        en.k0 = en.k1 = 0;
+    }
+    if (p.shared && blockIdx.x == 0) p.row_lim[b] = ok ? en.k0 : -1;
     return en;
 }
 
@@ -105,94 +123,86 @@ __device__ __forceinline__ int entity_tiles(const AttendParams& p, const Entity&
     if (en.kind == kLimCausal) k1 = en.lim0 + token_of(p, min((r + 1) * p.rt, en.nrows) - 1);
     return (k1 + kKeyTile - 1) / kKeyTile - en.k0 / kKeyTile;
 }
+__device__ __forceinline__ int item_cost(const AttendParams& p, const Entity& en, int r, int& tiles) {
+    const int n = min(p.rt, en.nrows - r * p.rt);
+    tiles = entity_tiles(p, en, r);
+    return item_cost_base(p, n) + item_cost_tile(p, n) * tiles;
+}
 
-// The cost of one KV head of an entity (0: no keys), and its row tiles.
-__device__ __forceinline__ long long head_cost(const AttendParams& p, const Entity& en, int& nrt) {
-    nrt = 0;
-    if (en.nrows <= 0 || en.k1 <= en.k0) return 0;
-    nrt = (en.nrows + p.rt - 1) / p.rt;
-    long long c = 0;
-    if (en.kind != kLimCausal) {
-        const int tiles = entity_tiles(p, en, 0), last = en.nrows - (nrt - 1) * p.rt;
-        c = (long long)(nrt - 1) * (item_cost_base(p, p.rt) + (long long)item_cost_tile(p, p.rt) * tiles);
-        return c + item_cost_base(p, last) + (long long)item_cost_tile(p, last) * tiles;
-    }
-    for (int r = 0; r < nrt; ++r) {
+// The segments of a listed entity that lie in CTA c's share [lo, hi): one warp, an item
+// a lane.
+static __device__ void emit_entity(const AttendParams& p, PlanScratch* s, const PlanEntity& q, int lo, int hi, int quota,
+                                   int c) {
+    const int lane = threadIdx.x & 31;
+    const Entity en = q.en;
+    const int g0 = q.start >= lo ? 0 : (lo - q.start) / q.hc, items = p.Hkv * q.nrt;
+    int x0 = q.start + g0 * q.hc;  // first unit of the items that follow
+#pragma unroll 1
+    for (int i0 = g0 * q.nrt; i0 < items && x0 < hi; i0 += 32) {
+        const int i = i0 + lane, g = i / q.nrt, r = i - g * q.nrt;
+        int tiles = 0;
+        const int cost = i < items ? item_cost(p, en, r, tiles) : 0;
+        int z = cost;  // inclusive sum, then the item's end
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, z, o);
+            if (lane >= o) z += y;
+        }
+        z += x0;
+        const int x = z - cost;
+        x0 = __shfl_sync(0xffffffffu, z, 31);
+        if (i >= items || x >= hi || z <= lo) continue;
         const int n = min(p.rt, en.nrows - r * p.rt);
-        c += item_cost_base(p, n) + (long long)item_cost_tile(p, n) * entity_tiles(p, en, r);
-    }
-    return c;
-}
-
-// The segments of entity en (first item item0, first cost unit start, first partial row
-// prow) that lie in CTA c's share [lo, hi).
-static __device__ void emit_entity(const AttendParams& p, PlanScratch* s, const Entity& en, long long hc, int nrt, int item0,
-                            long long start, long long prow, long long lo, long long hi, long long quota, int c) {
-    int g = start >= lo ? 0 : (int)((lo - start) / hc);
-    for (; g < p.Hkv && start + g * hc < hi; ++g) {
-        long long x = start + g * hc;  // first unit of the row tile
-        int r = 0;
-        if (en.kind != kLimCausal && x < lo) {  // equal row tiles but the last: skip by division
-            const long long ic = item_cost_base(p, p.rt) + (long long)item_cost_tile(p, p.rt) * entity_tiles(p, en, 0);
-            r = (int)min((lo - x) / ic, (long long)(nrt - 1));
-            x += r * ic;
-        }
-        for (; r < nrt && x < hi; ++r) {
-            const int n = min(p.rt, en.nrows - r * p.rt), tiles = entity_tiles(p, en, r);
-            const int base = item_cost_base(p, n), per = item_cost_tile(p, n);
-            const long long z = x + base + (long long)per * tiles;
-            if (z > lo) {
-                const int i = item0 + g * nrt + r;
-                const int ta = tiles_before(lo - x, base, per, tiles), tz = tiles_before(min(z, hi) - x, base, per, tiles);
-                const int t0 = en.k0 / kKeyTile;
-                const int c0 = (int)(x / quota), np = (int)((z - 1) / quota) - c0 + 1;
-                int k1 = en.k1;
-                if (en.kind == kLimCausal) k1 = en.lim0 + token_of(p, r * p.rt + n - 1);
-                Seg o;
-                o.table_row = en.table_row;
-                o.tok0 = en.tok0;
-                o.r0 = r * p.rt;
-                o.nrow = tz > ta ? n : 0;
-                o.g = g;
-                o.k0 = max(en.k0, (t0 + ta) * kKeyTile);
-                o.k1 = min(k1, (t0 + tz) * kKeyTile);
-                o.lim0 = en.lim0;
-                o.kind = en.kind;
-                o.prow = p.shared ? (int)(prow + (long long)g * en.nrows + r * p.rt) + c * p.rt
-                                  : (np == 1 ? -1 : piece_row_extend(c, c == c0, p.rt));
-                o.bad = o.pad = 0;
-                p.seg[i + c] = o;
-                if (x <= lo) s->first = i + c;
-                if (z >= hi) s->last = i + c + 1;
-                if (!p.shared && x < lo && c == c0 + 1) {
-                    MergeItem m;
-                    m.tok0 = en.tok0;
-                    m.r0 = o.r0;
-                    m.nrow = n;
-                    m.g = g;
-                    m.c0 = c0;
-                    m.np = np;
-                    m.tiles = tiles;
-                    m.off = (int)(lo - x);  // less than a share
-                    m.seq = en.table_row;
-                    m.pad[0] = m.pad[1] = m.pad[2] = 0;
-                    p.merge[c] = m;
-                }
-            }
-            x = z;
+        const int base = item_cost_base(p, n), per = item_cost_tile(p, n), t0 = en.k0 / kKeyTile;
+        const int ta = tiles_before(lo - x, base, per, tiles), tz = tiles_before(min(z, hi) - x, base, per, tiles);
+        // the CTAs that hold its first and its last unit; nearly always this one
+        const int c0 = x >= lo ? c : x / quota, c1 = z <= hi ? c : (z - 1) / quota;
+        int k1 = en.k1;
+        if (en.kind == kLimCausal) k1 = en.lim0 + token_of(p, r * p.rt + n - 1);
+        Seg o;
+        o.table_row = en.table_row;
+        o.tok0 = en.tok0;
+        o.r0 = r * p.rt;
+        o.nrow = tz > ta ? n : 0;
+        o.g = g;
+        o.k0 = max(en.k0, (t0 + ta) * kKeyTile);
+        o.k1 = min(k1, (t0 + tz) * kKeyTile);
+        o.lim0 = en.lim0;
+        o.kind = en.kind;
+        o.prow = p.shared ? q.prow + g * en.nrows + r * p.rt + c * p.rt : (c0 == c1 ? -1 : piece_row_extend(c, c == c0, p.rt));
+        o.bad = o.pad = 0;
+        p.seg[q.item0 + i + c] = o;
+        if (x <= lo) s->first = q.item0 + i + c;
+        if (z >= hi) s->last = q.item0 + i + c + 1;
+        if (!p.shared && x < lo && c == c0 + 1) {
+            MergeItem m;
+            m.tok0 = en.tok0;
+            m.r0 = o.r0;
+            m.nrow = n;
+            m.g = g;
+            m.c0 = c0;
+            m.np = c1 - c0 + 1;
+            m.tiles = tiles;
+            m.off = lo - x;
+            m.seq = en.table_row;
+            m.pad[0] = m.pad[1] = m.pad[2] = 0;
+            p.merge[c] = m;
         }
     }
 }
 
-// The CTA's segments are seg[s0 .. s1). All threads of the block.
+// The CTA's segments are seg[s0 .. s1). The first NT threads of the block (named
+// barrier 1).
 template <int NT>
 __device__ void plan_share(const AttendParams& p, PlanScratch* s, int& s0, int& s1) {
+    static_assert(NT <= 384, "list");
     const int tid = threadIdx.x, c = blockIdx.x;
     if (tid == 0) {
-        s->first = s->last = 0;
+        s->first = s->last = s->listed = 0;
         s->status = 0;
         p.merge[c].np = 0;
     }
+    named_bar_sync(1, NT);
     // offsets that do not rise within 0 .. their end: nothing is computed or written
     const int noff = p.shared ? p.NG : p.B, end = p.shared ? p.B : p.T;
     int bad = 0;
@@ -202,8 +212,9 @@ __device__ void plan_share(const AttendParams& p, PlanScratch* s, int& s0, int& 
         if (p.shared) s->offs[i] = o;
         if (p.shared && i < noff) s->top[i] = 0;
     }
-    bad = __syncthreads_or(bad);
-    if (bad) {
+    if (bad) atomicOr(&s->status, ART_STATUS_BAD_OFFSETS);
+    named_bar_sync(1, NT);
+    if (s->status) {
         if (tid == 0) {
             p.cta_status[c] = ART_STATUS_BAD_OFFSETS;
             p.cta_segs[c] = make_int2(0, 0);
@@ -212,80 +223,82 @@ __device__ void plan_share(const AttendParams& p, PlanScratch* s, int& s0, int& 
         s0 = s1 = 0;
         return;
     }
-    // the whole work: own tokens first (they tell how much of the prefixes is seen)
-    int err = 0;
-    long long W = 0, tot;
-    if (p.shared) {
-        for (int b = tid; b < p.B; b += NT) {
-            const Entity en = entity_of(p, s, p.NG + b, err);
-            if (c == 0) p.row_lim[b] = en.lim0;
-            if (en.lim0 > 0) {
-                int lo = 0, hi = p.NG;  // its group
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (s->offs[mid] <= b) lo = mid;
-                    else hi = mid;
-                }
-                atomicMax(&s->top[lo], en.lim0);
-            }
+    // Rounds over the entities, as many as threads in each: with more than one, a first
+    // sweep for the tops, a second for the whole work, and the last lays it out.
+    const int rounds = (p.NE + NT - 1) / NT;
+    int err = 0, W = 0, quota = 1, lo = 0, hi = 0, start = 0, items = 0, prows = 0;
+    int v[3], tot[3];
+    PlanEntity q;
+#pragma unroll 1
+    for (int k = rounds == 1 ? 2 * rounds : 0; k < 3 * rounds; ++k) {
+        const int sweep = k / rounds, e = (k - sweep * rounds) * NT + tid;
+        const bool own = !p.shared || e >= p.NG;
+        q.en.nrows = 0;
+        if (e < p.NE && own) q.en = entity_of(p, s, e, err);
+        if (p.shared) named_bar_sync(1, NT);  // the tops of a single round
+        if (sweep == 0 && rounds > 1) continue;
+        if (e < p.NE && !own) q.en = entity_of(p, s, e, err);
+        q.nrt = e < p.NE && q.en.nrows > 0 && q.en.k1 > q.en.k0 ? (q.en.nrows + p.rt - 1) / p.rt : 0;
+        q.hc = 0;
+#pragma unroll 1
+        for (int r = 0; r < q.nrt; ++r) {
+            int tiles;
+            const int cost = item_cost(p, q.en, r, tiles);
+            // equal row tiles but the last, where the keys do not go by the row
+            const int skip = q.en.kind != kLimCausal && r == 0 && q.nrt > 2 ? q.nrt - 2 : 0;
+            q.hc += cost * (skip + 1);
+            r += skip;
         }
-        __syncthreads();
-    }
-    for (int e0 = 0; e0 < p.NE; e0 += NT) {
-        long long cost = 0;
-        int nrt;
-        if (e0 + tid < p.NE) cost = head_cost(p, entity_of(p, s, e0 + tid, err), nrt) * p.Hkv;
-        (void)plan_scan<NT>(cost, s->warp_sum, tot);
-        W += tot;
-    }
-    const long long quota = W > p.ctas ? (W + p.ctas - 1) / p.ctas : 1;
-    const long long lo = (long long)c * quota, hi = min(lo + quota, W);
-    long long start = 0, items = 0, prows = 0;
-    for (int e0 = 0; e0 < p.NE && (lo < hi || c == 0); e0 += NT) {
-        const int e = e0 + tid;
-        long long hc = 0;
-        int nrt = 0;
-        Entity en;
-        en.nrows = 0;
-        if (e < p.NE) {
-            en = entity_of(p, s, e, err);
-            hc = head_cost(p, en, nrt);
+        v[0] = q.hc * p.Hkv;
+        v[1] = q.nrt * p.Hkv;
+        v[2] = p.shared && q.nrt > 0 ? q.en.nrows * p.Hkv : 0;
+        plan_scan<NT>(v, tot, s->warp_sum);
+        if (sweep == 1 || rounds == 1) {
+            W += tot[0];
+            quota = W > p.ctas ? (W + p.ctas - 1) / p.ctas : 1;
+            lo = min(c * quota, W);
+            hi = min(lo + quota, W);
+            if (rounds > 1) continue;
         }
-        const long long x = start + plan_scan<NT>(hc * p.Hkv, s->warp_sum, tot);
-        start += tot;
-        const int i0 = (int)(items + plan_scan<NT>((long long)nrt * p.Hkv, s->warp_sum, tot));
-        items += tot;
-        long long pr = 0;
-        if (p.shared) {
-            pr = prows + plan_scan<NT>(nrt > 0 ? (long long)en.nrows * p.Hkv : 0, s->warp_sum, tot);
-            prows += tot;
-        }
+        q.start = start + v[0];
+        q.item0 = items + v[1];
+        q.prow = prows + v[2];
+        start += tot[0];
+        items += tot[1];
+        prows += tot[2];
         if (c == 0 && e < p.NE) {
-            EntityPlace q;
-            q.nrows = nrt > 0 ? en.nrows : 0;
-            q.k0 = en.k0;
-            q.k1 = en.k1;
-            q.item0 = i0;
-            q.start = x;
-            q.prow = pr;
-            p.place[e] = q;
+            EntityPlace pl;
+            pl.nrows = q.nrt > 0 ? q.en.nrows : 0;
+            pl.k0 = q.en.k0;
+            pl.k1 = q.en.k1;
+            pl.item0 = q.item0;
+            pl.start = q.start;
+            pl.prow = q.prow;
+            pl.hc = q.hc;
+            pl.pad = 0;
+            p.place[e] = pl;
         }
-        if (hc > 0 && x < hi && x + hc * p.Hkv > lo) emit_entity(p, s, en, hc, nrt, i0, x, pr, lo, hi, quota, c);
+        if (q.nrt > 0 && q.start < hi && q.start + q.hc * p.Hkv > lo) s->list[atomicAdd(&s->listed, 1)] = q;
+        named_bar_sync(1, NT);
+        const int n = s->listed;
+        for (int i = tid >> 5; i < n; i += NT / 32) emit_entity(p, s, s->list[i], lo, hi, quota, c);
+        named_bar_sync(1, NT);
+        if (tid == 0) s->listed = 0;
     }
     if (err) atomicOr(&s->status, err);
-    __syncthreads();
+    named_bar_sync(1, NT);
+    s0 = s->first;
+    s1 = s->last;
     if (tid == 0) {
         p.cta_status[c] = s->status;
+        p.cta_segs[c] = make_int2(s0, s1);
         if (c == 0) {
             p.info->quota = quota;
             p.info->total = W;
             p.info->ok = 1;
         }
     }
-    s0 = s->first;
-    s1 = s->last;
-    if (tid == 0) p.cta_segs[c] = make_int2(s0, s1);
-    __syncthreads();  // the segments are written, the scratch is free
+    named_bar_sync(1, NT);  // the segments are written, the scratch is free
 }
 
 // Segments are written by the same kernel: not through the read-only path.

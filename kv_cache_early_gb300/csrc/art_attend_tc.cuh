@@ -12,10 +12,10 @@
 // Large segments (more than 16 rows): 128 rows are one stream; S = Q K^T (128 x 128)
 // and O (128 x d) are accumulators in tensor memory, and the weights P go back there
 // as the bf16 operand of O += P V, over the first half of their S. A thread owns a
-// row, so maximum and sum need no shuffles. Two streams run at once, one in the
-// tensor cores while the other is in the softmax: the two row tiles of a segment
-// with more than 128 rows, else the even and the odd key tiles of its one row tile
-// (their O meet in the epilogue: equal rows lie in equal lanes of tensor memory).
+// row, so sums need no shuffles. Two streams run at once, one in the tensor cores
+// while the other is in the softmax: the two row tiles of a segment with more than
+// 128 rows, else the two halves of each key tile for its one row tile (their O meet
+// in the epilogue: equal rows lie in equal lanes of tensor memory).
 //
 // Small segments (16 rows or fewer: one sequence's own tokens, drafted tokens) are
 // bound by the copies; the tensor memory path would spend 128 rows on them. Each
@@ -69,7 +69,7 @@ struct alignas(16) TcCtrl {
     float2 ml[kTcConsumers * kSmallRows > 128 ? kTcConsumers * kSmallRows : 128];  // (m, l) exchanged between warps
     float2 ml2[128];
     uint32_t tmem;
-    int abort;
+    int abort, seg0, seg1;
 };
 
 template <int D>
@@ -352,7 +352,7 @@ __device__ __forceinline__ bool tile_rows(const Seg& sg, int t, int& lo, int& hi
 template <int D>
 __device__ void tc_issuer(const AttendParams& p, uint32_t smem, TcCtrl<TcCfg<D>::NS>* c, uint32_t tmem_, int s0, int s1) {
     using C = TcCfg<D>;
-    constexpr uint32_t kIdQK = tc_idesc(kKeyTile, false), kIdPV = tc_idesc(D, true);
+    constexpr uint32_t kIdQK = tc_idesc(kKeyTile, false), kIdHalf = tc_idesc(kKeyTile / 2, false), kIdPV = tc_idesc(D, true);
     const uint32_t tmem = (uint32_t)uniform((int)tmem_);
     Stage<C::NS> st;  // first stage of the segment: K of tile j lies 2j stages on, V of tile j 2j + 1
     uint32_t ph_q = 0, ph_p = 0, ph_e = 0;  // ph_p: a bit per stream
@@ -362,24 +362,25 @@ __device__ void tc_issuer(const AttendParams& p, uint32_t smem, TcCtrl<TcCfg<D>:
     // addresses stay below 2^18).
     const uint64_t qd0 = tc_desc(smem, 16, C::GRP), kd0 = tc_desc(smem + C::RING, 16, C::GRP),
                    vd0 = tc_desc(smem + C::RING, 1024, C::GRP);
-    // S_x = Q_(tile) K^T
-    auto qk = [&](int x, int qt, int stage) {
-        const uint64_t qd = qd0 + (uint64_t)(qt * (C::TILE >> 4)), kd = kd0 + (uint64_t)(stage * (C::TILE >> 4));
-        const uint32_t d = tmem + 256 + x * 128;
+    // two row tiles: S_x = Q_x K^T; one: S_x = Q_0 K^T over the keys of half x
+    auto qk = [&](int x, bool dual, int stage) {
+        const uint64_t qd = qd0 + (uint64_t)(dual ? x * (C::TILE >> 4) : 0);
+        const uint64_t kd = kd0 + (uint64_t)(stage * (C::TILE >> 4) + (dual ? 0 : x * (8 * C::GRP >> 4)));
+        const uint32_t d = tmem + 256 + x * 128, id = dual ? kIdQK : kIdHalf;
         if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const int off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
-                tc_mma_ss(d, qd + off, kd + off, kIdQK, kk > 0);
+                tc_mma_ss(d, qd + off, kd + off, id, kk > 0);
             }
             tc_commit(&c->s_full[x]);
         }
         __syncwarp();
     };
-    // O_x += P_x V over the 16-key steps [a, z)
-    auto pv = [&](int x, int stage, int a, int z, bool acc) {
+    // O_x += P_x V over the 16-key steps [a, z) of the tile; P's columns start at step p0
+    auto pv = [&](int x, int stage, int a, int z, int p0, bool acc) {
         const uint64_t vd = vd0 + (uint64_t)(stage * (C::TILE >> 4));
-        const uint32_t d = tmem + x * 128, pp = tmem + 256 + x * 128;
+        const uint32_t d = tmem + x * 128, pp = tmem + 256 + x * 128 - p0 * 8;
         if (elect_one()) {
             if (a == 0 && z == kKeyTile / 16) {
 #pragma unroll
@@ -413,21 +414,19 @@ __device__ void tc_issuer(const AttendParams& p, uint32_t smem, TcCtrl<TcCfg<D>:
         ph_q ^= 1u;
         tc_fence_after();
         issued = true;
-        const int ahead = dual ? 1 : 2;  // tiles whose S may be under way
         Stage<C::NS> ks = st, vs = st;
         vs.next();
-        for (int j = 0; j < ahead && j < nt; ++j) {
-            if (!wait(&c->full[ks.s], ks.ph)) break;
-            qk(dual ? 0 : j, 0, ks.s);
-            if (dual) qk(1, 1, ks.s);
-            commit(&c->empty_t[ks.s]);
-            ks.next();
-            ks.next();
-        }
+        if (!wait(&c->full[ks.s], ks.ph)) break;
+        qk(0, dual, ks.s);
+        qk(1, dual, ks.s);
+        commit(&c->empty_t[ks.s]);
+        uint32_t acc = 0;  // streams whose O holds something
         for (int j = 0; j < nt && ok; ++j) {
+            ks.next();
+            ks.next();
             int lo, hi;
             const bool edge = tile_rows(sg, t0 + j, lo, hi);
-            const bool more = j + ahead < nt;
+            const bool more = j + 1 < nt;
             // the operands first: they are seldom what is waited for
             if (!wait(&c->full[vs.s], vs.ph)) break;
             if (edge) {
@@ -437,29 +436,28 @@ __device__ void tc_issuer(const AttendParams& p, uint32_t smem, TcCtrl<TcCfg<D>:
                 ph_e ^= 1u;
             }
             if (more && !wait(&c->full[ks.s], ks.ph)) break;
-            const int x0 = dual ? 0 : (j & 1), x1 = dual ? 1 : x0;
 #pragma unroll 1
-            for (int x = x0; x <= x1; ++x) {
+            for (int x = 0; x < 2; ++x) {
                 if (!wait(&c->p_full[x], (ph_p >> x) & 1u)) break;
                 ph_p ^= 1u << x;
                 tc_fence_after();
-                pv(x, vs.s, lo >> 4, (hi + 15) >> 4, j >= ahead);
-                if (more) qk(x, dual ? x : 0, ks.s);
-                else if (dual) commit(&c->o_full[x]);
+                int a = lo >> 4, z = (hi + 15) >> 4;
+                if (!dual) {
+                    a = max(a, x * 4);
+                    z = min(z, x * 4 + 4);
+                }
+                pv(x, vs.s, a, z, dual ? 0 : x * 4, (acc >> x) & 1u);
+                if (z > a) acc |= 1u << x;
+                if (more) qk(x, dual, ks.s);
+                else commit(&c->o_full[x]);
             }
             if (!ok) break;
             commit(&c->empty_t[vs.s]);
             if (more) commit(&c->empty_t[ks.s]);
-            ks.next();
-            ks.next();
             vs.next();
             vs.next();
         }
         if (!ok) break;
-        if (!dual) {
-            commit(&c->o_full[0]);
-            commit(&c->o_full[1]);
-        }
         st.skip(2 * nt);
     }
     // the products have finished before the tensor memory is given back
@@ -534,26 +532,58 @@ struct TcConsumer {
         return ok;
     }
 
-    // N columns of output row r, from column col: finished, or a partial result
-    template <int N>
-    __device__ __forceinline__ void put(const Seg& sg, int r, int col, const float* o, float l) {
+    __device__ __forceinline__ static float inverse(float l) { return l > 0.f ? 1.f / l : l; }  // 0 stays, NaN stays
+
+    // Four columns of row r: finished, or a partial result.
+    __device__ __forceinline__ void put4(const Seg& sg, int r, int col, const float* o, float l) {
         if (sg.prow >= 0) {
-#pragma unroll
-            for (int i = 0; i < N; i += 4)
-                *reinterpret_cast<float4*>(part_at(p, sg, r, col + i)) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            *reinterpret_cast<float4*>(part_at(p, sg, r, col)) = make_float4(o[0], o[1], o[2], o[3]);
             return;
         }
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no key seen: 0; NaN stays
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + row_index(p, sg, r) * D + col;
-        if constexpr (N % 8 == 0) {
+        const float inv = inverse(l);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row_index(p, sg, r) * D + col) =
+            make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+    }
+
+    // 32 columns of the warp's 32 rows, a row a thread. Partial results lie row by row for
+    // each four columns, so that a warp's store is one run. Of finished rows, four lanes
+    // exchange their 16-byte chunks and store 64 bytes of one row after the other.
+    __device__ __forceinline__ void put32(const Seg& sg, int row0, int col, const float* o, float l) {
+        if (sg.prow >= 0) {
+            if (row0 + lane < sg.nrow)
 #pragma unroll
-            for (int i = 0; i < N; i += 8)
-                *reinterpret_cast<uint4*>(dst + i) =
-                    make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
-                               pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
-        } else {
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<float4*>(part_at(p, sg, row0 + lane, col + i)) =
+                        make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            return;
+        }
+        const float inv = inverse(l);
+        uint32_t u[4][4];  // chunk, word
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[k][i] = pack_bf16(o[8 * k + 2 * i] * inv, o[8 * k + 2 * i + 1] * inv);
+        // 4 x 4 transposition within the quad: lane q gets chunk q of its four rows
+#pragma unroll
+        for (int step = 1; step <= 2; step <<= 1) {
+            const bool high = (lane & step) != 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k & step) continue;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? u[k][i] : u[k + step][i], step);
+                    if (high) u[k][i] = got;
+                    else u[k + step][i] = got;
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = row0 + (lane & ~3) + k;
+            if (r < sg.nrow)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row_index(p, sg, r) * D + col + (lane & 3) * 8) =
+                    make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
         }
     }
 
@@ -590,7 +620,7 @@ struct TcConsumer {
         if (!sync()) return false;  // the tiles of Q are free (small segments use them too)
         // Q: 16 bytes a lane, whole rows side by side
         {
-            constexpr int CPR = D / 8, RPI = 32 / CPR, NB = 8;  // chunks of a row; rows of a warp's load; loads at once
+            constexpr int CPR = D / 8, RPI = 32 / CPR, NB = 16 / RPI;  // chunks of a row; rows of a warp's load; loads at once
             const int rows = dual ? 32 : 16, ch = lane % CPR;
             for (int i0 = 0; i0 < rows; i0 += NB * RPI) {
                 uint4 u[NB];
@@ -612,8 +642,8 @@ struct TcConsumer {
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->q_full);
         }
-        const int r = (dual ? x * 128 : 0) + quad * 32 + lane;  // this thread's row
-        const bool live = (dual ? x * 128 : 0) + quad * 32 < sg.nrow;
+        const int first_row = (dual ? x * 128 : 0) + quad * 32, r = first_row + lane;  // the warp's, this thread's row
+        const bool live = first_row < sg.nrow;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t tS = tmem + lanes + 256 + x * 128, tO = tmem + lanes + x * 128;
         // a row that sees no key here is computed as if it saw all, and reported as empty
@@ -622,20 +652,21 @@ struct TcConsumer {
         const int lim = none ? sg.k1 : rlim;
         const int wlim = (int)__reduce_min_sync(0xffffffffu, (unsigned)lim);
         float m = -INFINITY, l = 0.f, fO = 1.f;
-        bool first = true;
+        bool first = true;  // O holds nothing yet
+        const int cols = dual ? kKeyTile : kKeyTile / 2;  // of S and P
         const uint64_t c2 = pk2(p.scale_log2, p.scale_log2), one = pk2(1.f, 1.f);
-        for (int j = dual ? 0 : x; j < nt; j += dual ? 1 : 2) {
+        for (int j = 0; j < nt; ++j) {
             if (!wait(&c->s_full[x], ph_s)) return false;
             ph_s ^= 1u;
             if (live) {
                 tc_fence_after();
-                const int tb = (t0 + j) * kKeyTile;
-                const bool edge = tb < sg.k0 || tb + kKeyTile > wlim;
+                const int tb = (t0 + j) * kKeyTile + (dual ? 0 : x * 64);  // the key of column 0
+                const bool edge = tb < sg.k0 || tb + cols > wlim;
                 const int lo = sg.k0 - tb, hi = lim - tb;
                 // 64 columns at a time, one loop body for both halves (the instruction cache feeds
                 // eight warps from it)
 #pragma unroll 1
-                for (int h = 0; h < 128; h += 64) {
+                for (int h = 0; h < cols; h += 64) {
                     float s[64];
                     tc_ld32(tS + h, s);
                     tc_ld32(tS + h + 32, s + 32);
@@ -717,34 +748,30 @@ struct TcConsumer {
                     tc_wait_ld(o);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i];
-                    if (r < sg.nrow) put<32>(sg, r, k, o, l);
+                    put32(sg, first_row, k, o, l);
                 }
                 if (r < sg.nrow && sg.prow >= 0) p.part_ml[sg.prow + r] = make_float2(m, l);
                 tc_fence_before();
             }
         } else {
-            // the even and the odd tiles' results of a row meet; each stream writes half of the columns
+            // the two halves' results of a row meet; each stream writes half of the columns
             (x ? c->ml2 : c->ml)[quad * 32 + lane] = make_float2(m, l);
             if (!sync()) return false;
             if (live) {
                 const float2 e = c->ml[quad * 32 + lane], d = c->ml2[quad * 32 + lane];
-                const float mm = fmaxf(e.x, d.x);
-                const float fe = e.x == -INFINITY ? 0.f : ex2(e.x - mm), fd = d.x == -INFINITY ? 0.f : ex2(d.x - mm);
-                const float ll = (e.y == 0.f ? 0.f : e.y * fe) + (d.y == 0.f ? 0.f : d.y * fd);
-                const bool odd = nt > 1;  // otherwise the odd stream's O holds nothing
+                const bool he = e.y != 0.f, hd = d.y != 0.f;  // saw a key; otherwise O may hold anything
+                const float mm = fmaxf(he ? e.x : -INFINITY, hd ? d.x : -INFINITY);
+                const float fe = he ? ex2(e.x - mm) : 0.f, fd = hd ? ex2(d.x - mm) : 0.f;
+                const float ll = (he ? e.y * fe : 0.f) + (hd ? d.y * fd : 0.f);
                 for (int k = x * (D / 2); k < (x + 1) * (D / 2); k += 32) {
                     float o[32], o2[32];
                     tc_ld32(tmem + lanes + k, o);
+                    tc_ld32(tmem + lanes + 128 + k, o2);
                     tc_wait_ld(o);
+                    tc_wait_ld(o2);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * fe;
-                    if (odd) {
-                        tc_ld32(tmem + lanes + 128 + k, o2);
-                        tc_wait_ld(o2);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] += none ? 0.f : o2[i] * fd;
-                    }
-                    if (r < sg.nrow) put<32>(sg, r, k, o, ll);
+                    for (int i = 0; i < 32; ++i) o[i] = (he ? o[i] * fe : 0.f) + (hd ? o2[i] * fd : 0.f);
+                    put32(sg, first_row, k, o, ll);
                 }
                 if (x == 0 && r < sg.nrow && sg.prow >= 0) p.part_ml[sg.prow + r] = make_float2(mm, ll);
                 tc_fence_before();
@@ -902,7 +929,7 @@ struct TcConsumer {
                 acc[2] += v.z * f;
                 acc[3] += v.w * f;
             }
-            put<4>(sg, r, col, acc, ll);
+            put4(sg, r, col, acc, ll);
             if (col == 0 && sg.prow >= 0) p.part_ml[sg.prow + r] = make_float2(mm, ll);
         }
         return true;
@@ -937,10 +964,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         return;
     }
-    int s0, s1;
-    static_assert(sizeof(PlanScratch) <= C::CTRL, "the scratch lies in the tiles");
-    plan_share<kTcThreads>(p, reinterpret_cast<PlanScratch*>(gen), s0, s1);
-    if (s0 >= s1) return;
     TcCtrl<C::NS>* c = reinterpret_cast<TcCtrl<C::NS>*>(gen + C::CTRL);
     const int w = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -963,13 +986,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         c->abort = 0;
         fence_mbar_init();
     }
-    if (w == kTcConsumers + 1) tc_alloc(&c->tmem);
+    static_assert(sizeof(PlanScratch) <= C::CTRL, "the scratch lies in the tiles");
+    // the tensor memory takes some microseconds to be had: beside the plan
+    if (w == kTcConsumers + 1) {
+        tc_alloc(&c->tmem);
+    } else if (w < kTcConsumers) {
+        int a, z;
+        plan_share<kTcConsumers * 32>(p, reinterpret_cast<PlanScratch*>(gen), a, z);
+        if (threadIdx.x == 0) {
+            c->seg0 = a;
+            c->seg1 = z;
+        }
+    }
     fence_proxy_async_smem();  // the scratch's accesses before the copies over it
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = c->tmem;
-    if (w >= kTcConsumers) {
+    const int s0 = c->seg0, s1 = c->seg1;
+    if (s0 >= s1) {
+        // nothing to do
+    } else if (w >= kTcConsumers) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegHelper));
         if (w == kTcConsumers) tc_producer<D>(p, smem, c, &tk, &tv, s0, s1);
         else if (w == kTcConsumers + 1) tc_issuer<D>(p, smem, c, tmem, s0, s1);

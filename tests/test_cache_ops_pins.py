@@ -140,6 +140,7 @@ def call_shared(lib, shape=None, q=FAKE, off=FAKE, pre=FAKE, groups=1, out=FAKE,
 @pytest.mark.parametrize("case,expect", [
     (dict(shape=good_shape(block_size=32)), UNS),
     (dict(q=0), BAD), (dict(out=0), BAD), (dict(off=0), BAD), (dict(pre=0), BAD), (dict(groups=-1), BAD),
+    (dict(groups=8193), UNS), (dict(shape=good_shape(batch=1 << 20, max_pages_per_seq=1 << 20)), UNS),
     (dict(q=FAKE + 8), BAD), (dict(ws=FAKE + 4), BAD),
     (dict(off=0, pre=0, groups=0), WS),                      # no groups need neither array
     (dict(), WS),
