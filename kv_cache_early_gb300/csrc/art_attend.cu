@@ -99,22 +99,27 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
     constexpr int WPB = kMergeBlock / 32;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the first loads all at once
+    const int first = p.shared ? min(blockIdx.x * WPB + w, p.B * p.Hq - 1) / p.Hq : 0;
+    const int j0 = p.shared ? p.group_of[first] : -1, lim0 = p.shared ? p.row_lim[first] : 0;
+    const int quota = p.info->quota, computed = p.info->ok;
     __shared__ int s_status;
     if (tid == 0) s_status = 0;
-    __syncthreads();
-    if (tid < p.ctas && p.cta_status[tid]) atomicOr(&s_status, p.cta_status[tid]);
-    __syncthreads();
+    const int mine = tid < p.ctas ? p.cta_status[tid] : 0;
+    if (__syncthreads_or(mine)) {
+        if (mine) atomicOr(&s_status, mine);
+        __syncthreads();
+    }
     const int status = s_status;
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) p.hdr->status = status;
-    if (!p.info->ok) return;
-    const int quota = p.info->quota;
+    if (!computed) return;
     const bool slow = (status & ART_STATUS_BAD_PAGE) != 0;
     MergeRow<kBF16, D> z;
     z.lane = lane;
     if (p.shared) {
         for (int row = blockIdx.x * WPB + w; row < p.B * p.Hq; row += gridDim.x * WPB) {
             const int b = row / p.Hq, h = row - b * p.Hq, g = h / p.G, hg = h - g * p.G;
-            const int j = p.group_of[b], lim = p.row_lim[b];
+            const int j = b == first ? j0 : p.group_of[b], lim = b == first ? lim0 : p.row_lim[b];
             MergeRow<kBF16, D> m;
             m.lane = lane;
             const int lead = j >= 0 ? p.offsets[j] : -1;
@@ -216,8 +221,8 @@ static size_t attend_layout(AttendParams& p, unsigned char* base) {
     return up256(o);
 }
 
-// Cost units (about 0.35 us): what segments of each kind take beside their neighbours.
-constexpr CostRule kCostBf16 = {3, 4, 10, 5, 12, 5}, kCostF32 = {1, 4, 1, 4, 1, 4};
+// Cost units (about 0.3 us): what segments of each kind take beside their neighbours.
+constexpr CostRule kCostBf16 = {3, 4, 10, 6, 16, 6}, kCostF32 = {1, 4, 1, 4, 1, 4};
 
 static void fill_shape(AttendParams& p, const art_shape& s) {
     p.B = s.batch;

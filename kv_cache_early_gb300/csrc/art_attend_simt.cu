@@ -33,6 +33,7 @@ __global__ void __launch_bounds__(kSimtThreads) art_attend_simt_kernel(const Att
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     int s_begin, s_end;
     plan_share<kSimtThreads>(p, reinterpret_cast<PlanScratch*>(smem), s_begin, s_end);
+    asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel may be set up; it waits for this grid's end
     for (int si = s_begin; si < s_end; ++si) {
         const Seg sg = load_seg(&p.seg[si]);
         if (sg.nrow == 0) continue;

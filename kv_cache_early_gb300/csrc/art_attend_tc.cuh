@@ -620,7 +620,7 @@ struct TcConsumer {
         if (!sync()) return false;  // the tiles of Q are free (small segments use them too)
         // Q: 16 bytes a lane, whole rows side by side
         {
-            constexpr int CPR = D / 8, RPI = 32 / CPR, NB = 16 / RPI;  // chunks of a row; rows of a warp's load; loads at once
+            constexpr int CPR = D / 8, RPI = 32 / CPR, NB = 16;  // chunks of a row; rows of a warp's load; loads at once
             const int rows = dual ? 32 : 16, ch = lane % CPR;
             for (int i0 = 0; i0 < rows; i0 += NB * RPI) {
                 uint4 u[NB];
@@ -628,13 +628,13 @@ struct TcConsumer {
                 for (int i = 0; i < NB; ++i) {
                     const int r = w * rows + i0 + i * RPI + lane / CPR;
                     u[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < sg.nrow)
+                    if (i0 + i * RPI < rows && r < sg.nrow)
                         u[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row_index(p, sg, r) * D) + ch);
                 }
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
                     const int r = w * rows + i0 + i * RPI + lane / CPR;
-                    *reinterpret_cast<uint4*>(gen + (r >> 3) * C::GRP + (ch >> 3) * 1024 + (r & 7) * 128 +
+                    if (i0 + i * RPI < rows) *reinterpret_cast<uint4*>(gen + (r >> 3) * C::GRP + (ch >> 3) * 1024 + (r & 7) * 128 +
                                               (((ch & 7) ^ (r & 7)) << 4)) = u[i];
                 }
             }
@@ -935,9 +935,24 @@ struct TcConsumer {
         return true;
     }
 
+    // Brings a segment's queries into the L2, a row a thread: under the load of the copies
+    // they take microseconds from memory.
+    __device__ __forceinline__ void prefetch(const Seg& sg) {
+        const int r = w * 32 + lane;
+        if (r >= sg.nrow) return;
+        const uint16_t* q = static_cast<const uint16_t*>(p.q) + row_index(p, sg, r) * D;
+#pragma unroll
+        for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i));
+    }
+
     __device__ void run(int s0, int s1) {
+        Seg nx = load_seg(&p.seg[s0]);
         for (int si = s0; si < s1; ++si) {
-            const Seg sg = load_seg(&p.seg[si]);
+            const Seg sg = nx;
+            if (si + 1 < s1) {
+                nx = load_seg(&p.seg[si + 1]);
+                prefetch(nx);
+            }
             if (sg.nrow == 0) continue;
             const int t0 = sg.k0 / kKeyTile, nt = (sg.k1 + kKeyTile - 1) / kKeyTile - t0;
             if (sg.nrow <= kSmallRows) {
@@ -1002,6 +1017,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel may be set up; it waits for this grid's end
     const uint32_t tmem = c->tmem;
     const int s0 = c->seg0, s1 = c->seg1;
     if (s0 >= s1) {
