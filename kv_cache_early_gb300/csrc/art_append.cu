@@ -16,10 +16,10 @@
 // reduced angle is rounded once to 32 bits (2^-24 * pi), and sine, cosine and the
 // rotation are 32-bit; a bf16 result is rounded once at the store.
 //
-// Bound: HBM, 2 (Hq + 2 Hkv) d bytes in and as many out a token. One CTA per
-// token: its rows are loaded (independent of the position) before the chain
-// offsets -> seq_len -> page id -> angles, so a decode step waits for the longer
-// of the two and not for their sum. One more CTA (block 0) checks the device
+// Bound: HBM, 2 (Hq + 2 Hkv) d bytes in and as many out a token. A CTA takes one
+// token, or four: their first rows are loaded (independent of the position) before
+// the chain offsets -> seq_len -> page id -> angles, so a decode step waits for the
+// longer of the two and not for their sum. One more CTA (block 0) checks the device
 // data of the call and stores the status word, so that no memset precedes the
 // kernel; every token's CTA checks what it uses by itself.
 #include "art_common.cuh"
@@ -28,6 +28,7 @@ namespace art {
 
 constexpr int kAppendThreads = 256;
 constexpr int kMaxRotHalf = 64;  // rot_dim / 2 at most (head_dim 128)
+constexpr int kFewTokens = 1024;
 
 struct AppendParams {
     const void *q, *k, *v;
@@ -114,165 +115,204 @@ __device__ void append_check(const AppendParams& p) {
     if (tid == 0) p.hdr->status = s_err;
 }
 
-// kVec: every 16-byte chunk of a row is copied, or rotated with itself or with one
-// other chunk (rot_dim / 2, or interleaved rot_dim, a multiple of the chunk's
-// elements); otherwise element by element.
-template <bool kBF16, int D, bool kVec>
+// kVec: a row is taken in units of two 16-byte chunks: of a rotated row in pairs
+// (j, j + rot_dim / 2) the chunks c and c + npair for c < npair, then the copied chunks
+// two by two; otherwise neighbours. It needs rot_dim / 2 (interleaved: rot_dim) to be a
+// multiple of a chunk's elements; without it a thread takes an element, or a pair.
+// kTok: tokens of a CTA.
+template <bool kBF16, int D, bool kVec, int kTok>
 __global__ void __launch_bounds__(kAppendThreads) art_append_kernel(const AppendParams p) {
     using E = Elem<kBF16>;
     constexpr int N = Vec16<kBF16>::N;
     constexpr int ROWB = D * E::kBytes;
-    constexpr int PF = 2;  // units a thread loads at once
-    __shared__ float s_cos[kMaxRotHalf], s_sin[kMaxRotHalf];
+    constexpr int PER = kVec ? D / N / 2 : D;          // units of a row
+    constexpr int RPS = kAppendThreads / PER > 0 ? kAppendThreads / PER : 1;  // rows of a step of the CTA
+    constexpr int PF = 3;                              // steps whose loads a thread has under way
+    __shared__ float s_cos[kTok * kMaxRotHalf], s_sin[kTok * kMaxRotHalf];
+    __shared__ int s_place[kTok], s_page[kTok], s_state[kTok];  // place in the cache; its page or -1; kState*
+    enum { kStateNone = 0, kStateBad = 1, kStateOk = 2 };
     if (blockIdx.x == 0) {
         append_check(p);
         return;
     }
-    const int t = blockIdx.x - 1, tid = threadIdx.x;
-    const int nq = p.q ? p.Hq : 0, half = p.rot / 2;
-    // units: of a rotated row (queries, then keys) its chunk pairs, or its single chunks; then the values' chunks
-    const bool pairs = kVec && !p.interleaved && half > 0;
-    const int npair = pairs ? half / N : 0;
-    const int per = kVec ? (pairs ? npair + (D - p.rot) / N : D / N) : D;
-    const int vper = kVec ? D / N : D;
-    const int nrot = (nq + p.Hkv) * per, units = nrot + p.Hkv * vper;
-    auto row_of = [&](int r, const char*& src) {  // r: query heads, key heads, value heads
-        if (r < nq) src = static_cast<const char*>(p.q) + ((size_t)t * p.q_stride + (size_t)r * D) * E::kBytes;
-        else if (r < nq + p.Hkv) src = static_cast<const char*>(p.k) + ((size_t)t * p.k_stride + (size_t)(r - nq) * D) * E::kBytes;
-        else src = static_cast<const char*>(p.v) + ((size_t)t * p.v_stride + (size_t)(r - nq - p.Hkv) * D) * E::kBytes;
+    const int t0 = (blockIdx.x - 1) * kTok, tid = threadIdx.x;
+    const int ntok = min(kTok, p.T - t0);
+    const int nq = p.q ? p.Hq : 0, half = p.rot / 2, rows = nq + 2 * p.Hkv;
+    const int npair = kVec && !p.interleaved ? half / N : 0;
+    // row R of the CTA: token, then query heads, key heads, value heads
+    auto split = [&](int R, int& tok, int& r) {
+        tok = 0;
+#pragma unroll
+        for (int k = 1; k < kTok; ++k) tok += R >= k * rows;
+        r = R - tok * rows;
     };
-    auto unit_of = [&](int u, int& r, int& c) {
-        if (u < nrot) {
-            r = u / per;
-            c = u - r * per;
+    auto src_of = [&](int tok, int r) -> const char* {
+        const size_t t = (size_t)(t0 + tok);
+        if (r < nq) return static_cast<const char*>(p.q) + (t * p.q_stride + (size_t)r * D) * E::kBytes;
+        if (r < nq + p.Hkv) return static_cast<const char*>(p.k) + (t * p.k_stride + (size_t)(r - nq) * D) * E::kBytes;
+        return static_cast<const char*>(p.v) + (t * p.v_stride + (size_t)(r - nq - p.Hkv) * D) * E::kBytes;
+    };
+    const int c = kVec ? tid % PER : 0;
+    // the unit's chunks (of a rotated row; the values' rows take neighbours)
+    auto chunks = [&](bool turned, int& ca, int& cb) {
+        if (turned && npair > 0 && c < npair) {
+            ca = c;
+            cb = c + npair;
         } else {
-            r = (u - nrot) / vper;
-            c = (u - nrot) - r * vper;
-            r += nq + p.Hkv;
+            ca = 2 * c;  // past the pairs: 2 npair + 2 (c - npair)
+            cb = 2 * c + 1;
         }
     };
     uint4 a[PF], b2[PF];
-    auto load = [&](int u0) {
-        if constexpr (kVec) {
+    auto load = [&](int R0) {
 #pragma unroll
-            for (int k = 0; k < PF; ++k) {
-                const int u = u0 + k * kAppendThreads;
-                if (u >= units) continue;
-                int r, c;
-                const char* src;
-                unit_of(u, r, c);
-                row_of(r, src);
-                const bool pair = pairs && u < nrot && c < npair;
-                const int ch = pairs && u < nrot && !pair ? c + npair : c;  // copied chunks follow the rotated ones
-                a[k] = *reinterpret_cast<const uint4*>(src + ch * 16);
-                if (pair) b2[k] = *reinterpret_cast<const uint4*>(src + (ch + npair) * 16);
-            }
+        for (int k = 0; k < PF; ++k) {
+            const int R = R0 + k * RPS;
+            if (R >= ntok * rows) continue;
+            int tok, r, ca, cb;
+            split(R, tok, r);
+            chunks(r < nq + p.Hkv, ca, cb);
+            const uint4* src = reinterpret_cast<const uint4*>(src_of(tok, r));
+            a[k] = __ldcs(src + ca);
+            b2[k] = __ldcs(src + cb);
         }
     };
-    load(tid);
+    if constexpr (kVec) load(tid / PER);
 
-    // the token's sequence, place and page
-    int b = t, i = 0, n = 1;
+    // the tokens' sequences, places and pages
+    int b0 = t0;
     if (p.q_offsets) {
-        int cnt = 0;  // sequences that end at or before t
+        b0 = 0;  // sequences that end at or before t0
         for (int base = 0; base < p.B; base += kAppendThreads)
-            cnt += __syncthreads_count(base + tid < p.B && p.q_offsets[base + tid + 1] <= t);
-        if (cnt >= p.B) return;  // behind the last sequence
-        b = cnt;
-        const int lo = p.q_offsets[b];
-        i = t - lo;
-        n = p.q_offsets[b + 1] - lo;
-        if (i < 0 || i >= n) return;  // offsets that do not hold t (flagged by block 0)
+            b0 += __syncthreads_count(base + tid < p.B && p.q_offsets[base + tid + 1] <= t0);
     }
-    const int len = p.seq_lens[b];
-    const bool ok = len >= n && (long long)len <= (long long)p.max_pages * p.Ps;
-    const int s = len - n + i;
-    int page = -1;
-    if (ok) {
-        page = p.block_table[(size_t)b * p.max_pages + s / p.Ps];
-        if (page < 0 || page >= p.num_pages) page = -1;
+    if (tid < ntok) {
+        int b = p.q_offsets ? b0 : t0 + tid, i = 0, n = 1, state = kStateNone, page = -1, s = 0;
+        if (p.q_offsets) {
+            while (b < p.B && p.q_offsets[b + 1] <= t0 + tid) ++b;
+            if (b < p.B) {
+                const int lo = p.q_offsets[b];
+                i = t0 + tid - lo;
+                n = p.q_offsets[b + 1] - lo;
+            } else {
+                n = 0;  // behind the last sequence
+            }
+        }
+        if (i >= 0 && i < n) {  // offsets that do not hold the token are flagged by block 0
+            const int len = p.seq_lens[b];
+            s = len - n + i;
+            if (len >= n && (long long)len <= (long long)p.max_pages * p.Ps) {
+                state = kStateOk;
+                page = p.block_table[(size_t)b * p.max_pages + s / p.Ps];
+                if (page < 0 || page >= p.num_pages) page = -1;
+            } else {
+                state = kStateBad;
+            }
+        }
+        s_place[tid] = s;
+        s_page[tid] = page;
+        s_state[tid] = state;
     }
-    if (tid < half) {
-        const int pos = p.positions ? p.positions[t] : s;
-        double x = (double)pos * (double)p.inv_freq[tid];
-        x -= 6.283185307179586476925 * rint(x * 0.159154943091895335769);
+    __syncthreads();
+    for (int x = tid; x < ntok * half; x += kAppendThreads) {
+        const int tok = x / half, j = x - tok * half;
+        const int pos = p.positions ? p.positions[t0 + tok] : s_place[tok];
+        double y = (double)pos * (double)p.inv_freq[j];
+        y -= 6.283185307179586476925 * rint(y * 0.159154943091895335769);
         float sn, cs;
-        sincosf((float)x, &sn, &cs);
-        s_cos[tid] = cs * p.scale;
-        s_sin[tid] = sn * p.scale;
+        sincosf((float)y, &sn, &cs);
+        s_cos[tok * kMaxRotHalf + j] = cs * p.scale;
+        s_sin[tok * kMaxRotHalf + j] = sn * p.scale;
     }
     __syncthreads();
 
-    char* kdst = static_cast<char*>(p.k_cache);
-    char* vdst = static_cast<char*>(p.v_cache);
-    auto dst_of = [&](int r) -> char* {
-        if (r < nq) return static_cast<char*>(p.q_out) + ((size_t)t * p.Hq + r) * ROWB;
-        if (page < 0) return nullptr;
+    auto dst_of = [&](int tok, int r) -> char* {
+        if (r < nq) return static_cast<char*>(p.q_out) + ((size_t)(t0 + tok) * p.Hq + r) * ROWB;
+        if (s_page[tok] < 0) return nullptr;
         const int g = r < nq + p.Hkv ? r - nq : r - nq - p.Hkv;
-        const size_t row = ((size_t)page * p.Hkv + g) * p.Ps + (s & (p.Ps - 1));
-        return (r < nq + p.Hkv ? kdst : vdst) + row * ROWB;
+        const size_t row = ((size_t)s_page[tok] * p.Hkv + g) * p.Ps + (s_place[tok] & (p.Ps - 1));
+        return static_cast<char*>(r < nq + p.Hkv ? p.k_cache : p.v_cache) + row * ROWB;
     };
-    for (int u0 = tid; u0 < units; u0 += PF * kAppendThreads) {
-        if (kVec && u0 != tid) load(u0);
+    if constexpr (kVec) {
+        // a chunk rotated with itself: neighbouring pairs
+        auto turn_inside = [&](Vec16<kBF16>& x, int ch, const float* cosv, const float* sinv) {
 #pragma unroll
-        for (int k = 0; k < PF; ++k) {
-            const int u = u0 + k * kAppendThreads;
-            if (u >= units) continue;
-            int r, c;
-            unit_of(u, r, c);
-            char* dst = dst_of(r);
+            for (int e = 0; e < N; e += 2) {
+                const int j = (ch * N + e) / 2;
+                const float cs = cosv[j], sn = sinv[j], xe = x.x[e], ye = x.x[e + 1];
+                x.x[e] = xe * cs - ye * sn;
+                x.x[e + 1] = ye * cs + xe * sn;
+            }
+        };
+        for (int R0 = tid / PER; R0 < ntok * rows; R0 += PF * RPS) {
+            if (R0 != tid / PER) load(R0);
+#pragma unroll
+            for (int k = 0; k < PF; ++k) {
+                const int R = R0 + k * RPS;
+                if (R >= ntok * rows) continue;
+                int tok, r, ca, cb;
+                split(R, tok, r);
+                const bool turned = r < nq + p.Hkv;
+                chunks(turned, ca, cb);
+                const int state = s_state[tok];
+                char* dst = state == kStateNone ? nullptr : dst_of(tok, r);
+                if (!dst) continue;
+                const float *cosv = s_cos + tok * kMaxRotHalf, *sinv = s_sin + tok * kMaxRotHalf;
+                uint4 u = a[k], v = b2[k];
+                if (state == kStateBad) {  // no position: queries of a bad sequence are zero
+                    u = v = make_uint4(0u, 0u, 0u, 0u);
+                } else if (turned && npair > 0) {
+                    if (c < npair) {
+                        Vec16<kBF16> x(u), y(v);
+#pragma unroll
+                        for (int e = 0; e < N; ++e) {
+                            const float cs = cosv[c * N + e], sn = sinv[c * N + e], xe = x.x[e], ye = y.x[e];
+                            x.x[e] = xe * cs - ye * sn;
+                            y.x[e] = ye * cs + xe * sn;
+                        }
+                        u = x.pack();
+                        v = y.pack();
+                    }
+                } else if (turned && p.interleaved) {
+                    if (ca * N < p.rot) {
+                        Vec16<kBF16> x(u);
+                        turn_inside(x, ca, cosv, sinv);
+                        u = x.pack();
+                    }
+                    if (cb * N < p.rot) {
+                        Vec16<kBF16> x(v);
+                        turn_inside(x, cb, cosv, sinv);
+                        v = x.pack();
+                    }
+                }
+                *reinterpret_cast<uint4*>(dst + ca * 16) = u;
+                *reinterpret_cast<uint4*>(dst + cb * 16) = v;
+            }
+        }
+    } else {
+        for (int x = tid; x < ntok * rows * D; x += kAppendThreads) {
+            int tok, r;
+            const int R = x / D, e = x - R * D;
+            split(R, tok, r);
+            const int state = s_state[tok];
+            char* dst = state == kStateNone ? nullptr : dst_of(tok, r);
             if (!dst) continue;
-            const bool turned = u < nrot;
-            if constexpr (kVec) {
-                const bool pair = pairs && turned && c < npair;
-                const int ch = pairs && turned && !pair ? c + npair : c;
-                if (!ok) {  // no position: queries of a bad sequence are zero
-                    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4*>(dst + ch * 16) = z;
-                    if (pair) *reinterpret_cast<uint4*>(dst + (ch + npair) * 16) = z;
-                } else if (pair) {
-                    Vec16<kBF16> x(a[k]), y(b2[k]);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        const float cs = s_cos[c * N + e], sn = s_sin[c * N + e], xe = x.x[e], ye = y.x[e];
-                        x.x[e] = xe * cs - ye * sn;
-                        y.x[e] = ye * cs + xe * sn;
-                    }
-                    *reinterpret_cast<uint4*>(dst + ch * 16) = x.pack();
-                    *reinterpret_cast<uint4*>(dst + (ch + npair) * 16) = y.pack();
-                } else if (turned && p.interleaved && ch * N < p.rot) {
-                    Vec16<kBF16> x(a[k]);
-#pragma unroll
-                    for (int e = 0; e < N; e += 2) {
-                        const int j = (ch * N + e) / 2;
-                        const float cs = s_cos[j], sn = s_sin[j], xe = x.x[e], ye = x.x[e + 1];
-                        x.x[e] = xe * cs - ye * sn;
-                        x.x[e + 1] = ye * cs + xe * sn;
-                    }
-                    *reinterpret_cast<uint4*>(dst + ch * 16) = x.pack();
-                } else {
-                    *reinterpret_cast<uint4*>(dst + ch * 16) = a[k];
-                }
+            const bool turned = r < nq + p.Hkv && e < p.rot;
+            if (turned && (p.interleaved ? (e & 1) != 0 : e >= half)) continue;  // written with its partner
+            const char* src = src_of(tok, r);
+            auto get = [&](int i) -> float {
+                if (state == kStateBad) return 0.f;
+                if constexpr (kBF16) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(src)[i] << 16);
+                else return reinterpret_cast<const float*>(src)[i];
+            };
+            const float v = get(e);
+            if (turned) {
+                const int j = p.interleaved ? e / 2 : e, e2 = p.interleaved ? e + 1 : e + half;
+                const float y = get(e2), cs = s_cos[tok * kMaxRotHalf + j], sn = s_sin[tok * kMaxRotHalf + j];
+                E::store(dst, e, v * cs - y * sn);
+                E::store(dst, e2, y * cs + v * sn);
             } else {
-                // one thread per element of the first of a pair; c counts elements
-                const char* src;
-                row_of(r, src);
-                const int c2 = p.interleaved ? c + 1 : c + half;
-                const bool first = turned && c < p.rot && (p.interleaved ? (c & 1) == 0 : c < half);
-                if (turned && c < p.rot && !first) continue;  // written with its partner
-                auto get = [&](int e) -> float {
-                    if constexpr (kBF16) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(src)[e] << 16);
-                    else return reinterpret_cast<const float*>(src)[e];
-                };
-                const float x = ok ? get(c) : 0.f;
-                if (first) {
-                    const int j = p.interleaved ? c / 2 : c;
-                    const float y = ok ? get(c2) : 0.f;
-                    E::store(dst, c, x * s_cos[j] - y * s_sin[j]);
-                    E::store(dst, c2, y * s_cos[j] + x * s_sin[j]);
-                } else {
-                    E::store(dst, c, x);
-                }
+                E::store(dst, e, v);
             }
         }
     }
@@ -344,8 +384,13 @@ int art_append_kv(const void* q, const void* k, const void* v, int64_t q_stride,
     const bool bf = s.dtype == ART_DTYPE_BF16;
     const bool vec = (p.interleaved ? p.rot : p.rot / 2) % chunk == 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const unsigned grid = (unsigned)num_tokens + 1u;
-#define ART_APPEND(BF, DD, VEC) art_append_kernel<BF, DD, VEC><<<grid, kAppendThreads, 0, st>>>(p)
+    // one token a CTA while they are few (a step waits for one chain of loads), else four
+    // (which share the chain)
+    const int tok = num_tokens <= kFewTokens ? 1 : 4;
+    const unsigned grid = (unsigned)((num_tokens + tok - 1) / tok) + 1u;
+#define ART_APPEND(BF, DD, VEC)                                                               \
+    (tok == 1 ? art_append_kernel<BF, DD, VEC, 1><<<grid, kAppendThreads, 0, st>>>(p)         \
+              : art_append_kernel<BF, DD, VEC, 4><<<grid, kAppendThreads, 0, st>>>(p))
     if (bf && s.head_dim == 128) { if (vec) ART_APPEND(true, 128, true); else ART_APPEND(true, 128, false); }
     else if (bf) { if (vec) ART_APPEND(true, 64, true); else ART_APPEND(true, 64, false); }
     else if (s.head_dim == 128) { if (vec) ART_APPEND(false, 128, true); else ART_APPEND(false, 128, false); }

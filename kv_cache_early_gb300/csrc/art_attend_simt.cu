@@ -23,7 +23,7 @@ constexpr size_t simt_smem() {
 __device__ __forceinline__ float f4(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 template <int D>
-__global__ void __launch_bounds__(kSimtThreads) art_attend_simt_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(kSimtThreads, 1) art_attend_simt_kernel(const AttendParams p) {
     constexpr int S = D + 4, CH = D / 4, OC = D / 64;
     extern __shared__ __align__(16) unsigned char smem[];
     float* sq = reinterpret_cast<float*>(smem);
@@ -60,11 +60,14 @@ __global__ void __launch_bounds__(kSimtThreads) art_attend_simt_kernel(const Att
         }
         int bad = 0;
         const int32_t* trow = p.block_table + (size_t)sg.table_row * p.max_pages;
-        for (int kb = sg.k0 / kSimtKeys * kSimtKeys; kb < sg.k1; kb += kSimtKeys) {
-            __syncthreads();
-            for (int c = tid; c < kSimtKeys * CH; c += kSimtThreads) {
-                const int r = c / CH, ch = c - r * CH, key = kb + r;
-                float4 uk = make_float4(0.f, 0.f, 0.f, 0.f), uv = uk;
+        // the next 64 keys and values are on their way, in registers, while these are used
+        constexpr int LD = kSimtKeys * CH / kSimtThreads;
+        float4 nk[LD], nv[LD];
+        auto fetch = [&](int kb) {
+#pragma unroll
+            for (int i = 0; i < LD; ++i) {
+                const int c = tid + i * kSimtThreads, r = c / CH, ch = c - r * CH, key = kb + r;
+                nk[i] = nv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (key >= sg.k0 && key < sg.k1) {
                     int pg = __ldg(&trow[key / p.Ps]);
                     if (pg < 0 || pg >= p.num_pages) {  // the merge kernel zeroes the rows
@@ -72,13 +75,22 @@ __global__ void __launch_bounds__(kSimtThreads) art_attend_simt_kernel(const Att
                         pg = 0;
                     }
                     const size_t row = ((size_t)pg * p.Hkv + sg.g) * p.Ps + (key & (p.Ps - 1));
-                    uk = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.k) + row * D) + ch);
-                    uv = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.v) + row * D) + ch);
+                    nk[i] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.k) + row * D) + ch);
+                    nv[i] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.v) + row * D) + ch);
                 }
-                *reinterpret_cast<float4*>(sk + r * S + ch * 4) = uk;
-                *reinterpret_cast<float4*>(sv + r * S + ch * 4) = uv;
+            }
+        };
+        fetch(sg.k0 / kSimtKeys * kSimtKeys);
+        for (int kb = sg.k0 / kSimtKeys * kSimtKeys; kb < sg.k1; kb += kSimtKeys) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < LD; ++i) {
+                const int c = tid + i * kSimtThreads, r = c / CH, ch = c - r * CH;
+                *reinterpret_cast<float4*>(sk + r * S + ch * 4) = nk[i];
+                *reinterpret_cast<float4*>(sv + r * S + ch * 4) = nv[i];
             }
             __syncthreads();
+            if (kb + kSimtKeys < sg.k1) fetch(kb + kSimtKeys);
             float s[4][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
