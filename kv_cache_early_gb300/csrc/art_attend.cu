@@ -18,13 +18,14 @@ struct MergeRow {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     int lane;
-    // at(k, prow, nrow): piece k's partial row and its segment's rows; false where it is empty
+    // at(k, prow, nrow, r): piece k's first partial row, its segment's rows, the row's place
+    // among them; false where it is empty
     template <class F>
-    __device__ __forceinline__ void add(const AttendParams& p, int n, int r, F at) {
+    __device__ __forceinline__ void add(const AttendParams& p, int n, F at) {
         for (int k0 = 0; k0 < n; k0 += 32) {
-            int prow = 0, nrow = 1;
+            int prow = 0, nrow = 1, r = 0;
             float2 ml = make_float2(-INFINITY, 0.f);
-            if (k0 + lane < n && at(k0 + lane, prow, nrow)) ml = __ldcg(&p.part_ml[prow + r]);
+            if (k0 + lane < n && at(k0 + lane, prow, nrow, r)) ml = __ldcg(&p.part_ml[prow + r]);
             const bool live = ml.y != 0.f;  // saw a key (or a NaN)
             float top = live ? ml.x : -INFINITY;
 #pragma unroll
@@ -50,10 +51,11 @@ struct MergeRow {
                     const int src = todo ? __ffs(todo) - 1 : 0;
                     f[u] = __shfl_sync(0xffffffffu, w, src);
                     const int pr = __shfl_sync(0xffffffffu, prow, src), nr = __shfl_sync(0xffffffffu, nrow, src);
+                    const int rr = __shfl_sync(0xffffffffu, r, src);
                     v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (!todo) f[u] = 0.f;
                     else if (lane < D / 4)
-                        v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (size_t)pr * D) + (size_t)lane * nr + r);
+                        v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (size_t)pr * D) + (size_t)lane * nr + rr);
                     todo &= todo - 1;
                 }
 #pragma unroll
@@ -81,7 +83,7 @@ struct MergeRow {
 
 // Whether a page of sequence b's own tokens, or of the prefix that group j's first
 // sequence (lead) holds, lies outside the pool: only asked when some CTA met such a page.
-__device__ bool seq_bad(const AttendParams& p, int b, int lead, int lane) {
+static __device__ __noinline__ bool seq_bad(const AttendParams& p, int b, int lead, int lane) {
     bool bad = false;
     for (int c = 0; c < p.ctas; ++c) {
         if (!(p.cta_status[c] & ART_STATUS_BAD_PAGE)) continue;
@@ -94,14 +96,14 @@ __device__ bool seq_bad(const AttendParams& p, int b, int lead, int lane) {
     return __any_sync(0xffffffffu, bad);
 }
 
-template <bool kBF16, int D>
+template <bool kBF16, int D, bool kShared>
 __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const AttendParams p) {
     constexpr int WPB = kMergeBlock / 32;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // the first loads all at once
-    const int first = p.shared ? min(blockIdx.x * WPB + w, p.B * p.Hq - 1) / p.Hq : 0;
-    const int j0 = p.shared ? p.group_of[first] : -1, lim0 = p.shared ? p.row_lim[first] : 0;
+    const int first = kShared ? min(blockIdx.x * WPB + w, p.B * p.Hq - 1) / p.Hq : 0;
+    const int j0 = kShared ? p.group_of[first] : -1, lim0 = kShared ? p.row_lim[first] : 0;
     const int quota = p.info->quota, computed = p.info->ok;
     __shared__ int s_status;
     if (tid == 0) s_status = 0;
@@ -114,9 +116,7 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) p.hdr->status = status;
     if (!computed) return;
     const bool slow = (status & ART_STATUS_BAD_PAGE) != 0;
-    MergeRow<kBF16, D> z;
-    z.lane = lane;
-    if (p.shared) {
+    if constexpr (kShared) {
         for (int row = blockIdx.x * WPB + w; row < p.B * p.Hq; row += gridDim.x * WPB) {
             const int b = row / p.Hq, h = row - b * p.Hq, g = h / p.G, hg = h - g * p.G;
             const int j = b == first ? j0 : p.group_of[b], lim = b == first ? lim0 : p.row_lim[b];
@@ -124,54 +124,71 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
             m.lane = lane;
             const int lead = j >= 0 ? p.offsets[j] : -1;
             if (lim >= 0 && !(slow && seq_bad(p, b, lead, lane))) {
-                // the item of entity e that holds its row R: pieces by the plan's arithmetic
-                auto item = [&](int e, int R) {
-                    const EntityPlace q = p.place[e];
-                    if (q.nrows == 0) return;
-                    const int r = R / p.rt, n = min(p.rt, q.nrows - r * p.rt);
-                    const int tiles = (q.k1 + kKeyTile - 1) / kKeyTile - q.k0 / kKeyTile;
-                    const int base = item_cost_base(p, n), per = item_cost_tile(p, n);
-                    const int full = item_cost_base(p, p.rt) + item_cost_tile(p, p.rt) * tiles;
-                    const int x = q.start + g * q.hc + r * full, end = x + base + per * tiles;
-                    const int c0 = x / quota, np = (end - 1) / quota - c0 + 1;
-                    const int pr = q.prow + g * q.nrows + r * p.rt;
-                    m.add(p, np, R - r * p.rt, [&](int k, int& prow, int& nrow) {
-                        const int a = max((c0 + k) * quota, x), y = min((c0 + k + 1) * quota, end);
-                        prow = pr + (c0 + k) * p.rt;
-                        nrow = n;
-                        return tiles_before(y - x, base, per, tiles) > tiles_before(a - x, base, per, tiles);
-                    });
-                };
-                if (lim > 0) item(j, (b - lead) * p.G + hg);
-                item(p.NG + b, hg);
+                // the items that hold the row, of its group and its own: their pieces by the
+                // plan's arithmetic, those of the group first
+                struct Pieces {
+                    int x, end, base, per, tiles, c0, np, prow, nrow, r;
+                } it[2];
+                const EntityPlace q[2] = {p.place[lim > 0 ? j : p.NG + b], p.place[p.NG + b]};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int R = i == 0 ? (b - lead) * p.G + hg : hg, t = R / p.rt;
+                    Pieces& e = it[i];
+                    e.np = 0;
+                    if (q[i].nrows == 0 || (i == 0 && lim <= 0)) continue;
+                    e.nrow = min(p.rt, q[i].nrows - t * p.rt);
+                    e.tiles = (q[i].k1 + kKeyTile - 1) / kKeyTile - q[i].k0 / kKeyTile;
+                    e.base = item_cost_base(p, e.nrow);
+                    e.per = item_cost_tile(p, e.nrow);
+                    e.x = q[i].start + g * q[i].hc + t * (item_cost_base(p, p.rt) + item_cost_tile(p, p.rt) * e.tiles);
+                    e.end = e.x + e.base + e.per * e.tiles;
+                    e.c0 = e.x / quota;
+                    e.np = (e.end - 1) / quota - e.c0 + 1;
+                    e.prow = q[i].prow + g * q[i].nrows + t * p.rt;
+                    e.r = R - t * p.rt;
+                }
+                m.add(p, it[0].np + it[1].np, [&](int k, int& prow, int& nrow, int& r) {
+                    const bool own = k >= it[0].np;
+                    const Pieces e = own ? it[1] : it[0];
+                    const int c = e.c0 + (own ? k - it[0].np : k);
+                    const int a = max(c * quota, e.x), y = min((c + 1) * quota, e.end);
+                    prow = e.prow + c * p.rt;
+                    nrow = e.nrow;
+                    r = e.r;
+                    return tiles_before(y - e.x, e.base, e.per, e.tiles) > tiles_before(a - e.x, e.base, e.per, e.tiles);
+                });
             }
             m.store(p, row);
         }
-        return;
-    }
-    for (int c = blockIdx.x; c < p.ctas; c += gridDim.x) {
-        const MergeItem it = p.merge[c];
-        if (it.np == 0 || (slow && seq_bad(p, it.seq, -1, lane))) continue;
-        const int base = item_cost_base(p, it.nrow), per = item_cost_tile(p, it.nrow);
-        for (int r = blockIdx.y * WPB + w; r < it.nrow; r += gridDim.y * WPB) {
-            MergeRow<kBF16, D> m;
-            m.lane = lane;
-            m.add(p, it.np, r, [&](int k, int& prow, int& nrow) {
-                const int a = k == 0 ? 0 : it.off + (k - 1) * quota;
-                prow = piece_row_extend(it.c0 + k, k == 0, p.rt);
-                nrow = it.nrow;
-                return tiles_before(it.off + k * quota, base, per, it.tiles) > tiles_before(a, base, per, it.tiles);
-            });
-            const int R = it.r0 + r, t = R / p.G;
-            m.store(p, (size_t)(it.tok0 + t) * p.Hq + it.g * p.G + (R - t * p.G));
+    } else {
+        MergeRow<kBF16, D> z;
+        z.lane = lane;
+        for (int c = blockIdx.x; c < p.ctas; c += gridDim.x) {
+            const MergeItem it = p.merge[c];
+            if (it.np == 0 || (slow && seq_bad(p, it.seq, -1, lane))) continue;
+            const int base = item_cost_base(p, it.nrow), per = item_cost_tile(p, it.nrow);
+            for (int r = blockIdx.y * WPB + w; r < it.nrow; r += gridDim.y * WPB) {
+                MergeRow<kBF16, D> m;
+                m.lane = lane;
+                m.add(p, it.np, [&](int k, int& prow, int& nrow, int& row) {
+                    const int a = k == 0 ? 0 : it.off + (k - 1) * quota;
+                    prow = piece_row_extend(it.c0 + k, k == 0, p.rt);
+                    nrow = it.nrow;
+                    row = r;
+                    const int to = k == it.np - 1 ? it.tiles : tiles_before(it.off + k * quota, base, per, it.tiles);
+                    return to > tiles_before(a, base, per, it.tiles);
+                });
+                const int R = it.r0 + r, t = R / p.G;
+                m.store(p, (size_t)(it.tok0 + t) * p.Hq + it.g * p.G + (R - t * p.G));
+            }
         }
-    }
-    // sequences without keys, and bad ones: zero
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        const int lo = p.offsets[b], hi = p.offsets[b + 1];
-        if (lo == hi || !(p.place[b].nrows == 0 || (slow && seq_bad(p, b, -1, lane)))) continue;
-        for (size_t row = (size_t)lo * p.Hq + blockIdx.y * WPB + w; row < (size_t)hi * p.Hq; row += gridDim.y * WPB)
-            z.store(p, row);
+        // sequences without keys, and bad ones: zero
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+            const int lo = p.offsets[b], hi = p.offsets[b + 1];
+            if (lo == hi || !(p.place[b].nrows == 0 || (slow && seq_bad(p, b, -1, lane)))) continue;
+            for (size_t row = (size_t)lo * p.Hq + blockIdx.y * WPB + w; row < (size_t)hi * p.Hq; row += gridDim.y * WPB)
+                z.store(p, row);
+        }
     }
 }
 
@@ -263,19 +280,15 @@ static int attend_run(AttendParams& p, const art_shape& s, void* workspace, size
     if ((e = bf ? launch_attend_tc(p, st) : launch_attend_simt(p, st)) != cudaSuccess) return cuda_fail(e);
     // the merge kernel's launch overlaps the main kernel's end
     const long long blocks = p.shared ? ((long long)p.B * p.Hq + kMergeBlock / 32 - 1) / (kMergeBlock / 32) : p.ctas;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(blocks < 8LL * p.ctas ? blocks : 8LL * p.ctas), p.shared ? 1 : p.rt / 32);
-    cfg.blockDim = dim3(kMergeBlock);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (bf && p.D == 128) e = cudaLaunchKernelEx(&cfg, art_attend_merge_kernel<true, 128>, p);
-    else if (bf) e = cudaLaunchKernelEx(&cfg, art_attend_merge_kernel<true, 64>, p);
-    else if (p.D == 128) e = cudaLaunchKernelEx(&cfg, art_attend_merge_kernel<false, 128>, p);
-    else e = cudaLaunchKernelEx(&cfg, art_attend_merge_kernel<false, 64>, p);
+    const dim3 grid((unsigned)(blocks < 8LL * p.ctas ? blocks : 8LL * p.ctas), p.shared ? 1 : p.rt / 32);
+#define ART_MERGE(BF, DD)                                                                                    \
+    e = p.shared ? launch_after(art_attend_merge_kernel<BF, DD, true>, grid, dim3(kMergeBlock), 0, st, p)   \
+                 : launch_after(art_attend_merge_kernel<BF, DD, false>, grid, dim3(kMergeBlock), 0, st, p)
+    if (bf && p.D == 128) ART_MERGE(true, 128);
+    else if (bf) ART_MERGE(true, 64);
+    else if (p.D == 128) ART_MERGE(false, 128);
+    else ART_MERGE(false, 64);
+#undef ART_MERGE
     if (e != cudaSuccess) return cuda_fail(e);
     return ART_OK;
 }

@@ -35,6 +35,7 @@ constexpr int kAttendCtas = 160;   // CTAs of the main kernel at most (one per S
 constexpr int kRowsTc = 256;       // rows of an item's tile, bf16
 constexpr int kItemRows = 64;      // ... and fp32
 constexpr int kSmallRows = 16;     // bf16: rows of an item that the consumer warps take by themselves
+constexpr int kSplitSlack = 16;    // dense_extend: a share may grow by 1 / 16 at an end so that an item is not split
 constexpr int kMaxGroups = 8192;   // groups of a dense_decode_shared call (their offsets are kept in shared memory)
 
 // How far a row sees: all keys of the segment; up to its own token; up to the
@@ -134,6 +135,24 @@ __device__ __forceinline__ int tiles_before(int x, int base, int per, int tiles)
 // dense_decode_shared keeps every item's rows, shifted by one tile per CTA so that
 // the pieces of an item lie apart.
 __device__ __forceinline__ int piece_row_extend(int c, bool first, int rt) { return (2 * c + (first ? 1 : 0)) * rt; }
+
+// Launches a kernel whose set-up may overlap the end of what runs before it on the
+// stream (it waits by griddepcontrol.wait before it touches memory).
+template <class... A>
+inline cudaError_t launch_after(void (*kernel)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                                const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 cudaError_t launch_attend_simt(const AttendParams& p, cudaStream_t st);  // fp32
 cudaError_t launch_attend_tc(const AttendParams& p, cudaStream_t st);    // bf16

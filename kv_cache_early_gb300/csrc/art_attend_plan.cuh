@@ -132,7 +132,7 @@ __device__ __forceinline__ int item_cost(const AttendParams& p, const Entity& en
 // The segments of a listed entity that lie in CTA c's share [lo, hi): one warp, an item
 // a lane.
 static __device__ void emit_entity(const AttendParams& p, PlanScratch* s, const PlanEntity& q, int lo, int hi, int quota,
-                                   int c) {
+                                   int slack, int c) {
     const int lane = threadIdx.x & 31;
     const Entity en = q.en;
     const int g0 = q.start >= lo ? 0 : (lo - q.start) / q.hc, items = p.Hkv * q.nrt;
@@ -154,9 +154,15 @@ static __device__ void emit_entity(const AttendParams& p, PlanScratch* s, const 
         if (i >= items || x >= hi || z <= lo) continue;
         const int n = min(p.rt, en.nrows - r * p.rt);
         const int base = item_cost_base(p, n), per = item_cost_tile(p, n), t0 = en.k0 / kKeyTile;
-        const int ta = tiles_before(lo - x, base, per, tiles), tz = tiles_before(min(z, hi) - x, base, per, tiles);
-        // the CTAs that hold its first and its last unit; nearly always this one
-        const int c0 = x >= lo ? c : x / quota, c1 = z <= hi ? c : (z - 1) / quota;
+        // the CTAs that hold its first and its last unit; nearly always this one. Where little
+        // of it lies on one side of a border between shares, it moves to the other whole:
+        // a split costs the partial results' way through memory.
+        int c0 = x >= lo ? c : x / quota, c1 = z <= hi ? c : (z - 1) / quota;
+        if (c0 < c1 && (c0 + 1) * quota - x <= slack) ++c0;
+        if (c0 < c1 && z - c1 * quota <= slack) --c1;
+        if (c < c0 || c > c1) continue;
+        const int ta = c == c0 ? 0 : tiles_before(lo - x, base, per, tiles);
+        const int tz = c == c1 ? tiles : tiles_before(hi - x, base, per, tiles);
         int k1 = en.k1;
         if (en.kind == kLimCausal) k1 = en.lim0 + token_of(p, r * p.rt + n - 1);
         Seg o;
@@ -172,9 +178,9 @@ static __device__ void emit_entity(const AttendParams& p, PlanScratch* s, const 
         o.prow = p.shared ? q.prow + g * en.nrows + r * p.rt + c * p.rt : (c0 == c1 ? -1 : piece_row_extend(c, c == c0, p.rt));
         o.bad = o.pad = 0;
         p.seg[q.item0 + i + c] = o;
-        if (x <= lo) s->first = q.item0 + i + c;
-        if (z >= hi) s->last = q.item0 + i + c + 1;
-        if (!p.shared && x < lo && c == c0 + 1) {
+        atomicMin(&s->first, q.item0 + i + c);
+        atomicMax(&s->last, q.item0 + i + c + 1);
+        if (!p.shared && c == c0 + 1) {
             MergeItem m;
             m.tok0 = en.tok0;
             m.r0 = o.r0;
@@ -198,7 +204,8 @@ __device__ void plan_share(const AttendParams& p, PlanScratch* s, int& s0, int& 
     static_assert(NT <= 384, "list");
     const int tid = threadIdx.x, c = blockIdx.x;
     if (tid == 0) {
-        s->first = s->last = s->listed = 0;
+        s->first = 0x7fffffff;
+        s->last = s->listed = 0;
         s->status = 0;
         p.merge[c].np = 0;
     }
@@ -280,15 +287,15 @@ __device__ void plan_share(const AttendParams& p, PlanScratch* s, int& s0, int& 
         }
         if (q.nrt > 0 && q.start < hi && q.start + q.hc * p.Hkv > lo) s->list[atomicAdd(&s->listed, 1)] = q;
         named_bar_sync(1, NT);
-        const int n = s->listed;
-        for (int i = tid >> 5; i < n; i += NT / 32) emit_entity(p, s, s->list[i], lo, hi, quota, c);
+        const int n = s->listed, slack = p.shared ? 0 : quota / kSplitSlack;
+        for (int i = tid >> 5; i < n; i += NT / 32) emit_entity(p, s, s->list[i], lo, hi, quota, slack, c);
         named_bar_sync(1, NT);
         if (tid == 0) s->listed = 0;
     }
     if (err) atomicOr(&s->status, err);
     named_bar_sync(1, NT);
-    s0 = s->first;
     s1 = s->last;
+    s0 = min(s->first, s1);
     if (tid == 0) {
         p.cta_status[c] = s->status;
         p.cta_segs[c] = make_int2(s0, s1);

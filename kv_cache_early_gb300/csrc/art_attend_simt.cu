@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) art_attend_simt_kernel(const 
     float* sv = sk + kSimtKeys * S;
     float* sp = sv + kSimtKeys * S;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what ran before on the stream has ended
     int s_begin, s_end;
     plan_share<kSimtThreads>(p, reinterpret_cast<PlanScratch*>(smem), s_begin, s_end);
     asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel may be set up; it waits for this grid's end
@@ -199,8 +200,7 @@ static cudaError_t launch_one(const AttendParams& p, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(art_attend_simt_kernel<D>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    art_attend_simt_kernel<D><<<p.ctas, kSimtThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch_after(art_attend_simt_kernel<D>, dim3(p.ctas), dim3(kSimtThreads), smem, st, p);
 }
 
 cudaError_t launch_attend_simt(const AttendParams& p, cudaStream_t st) {

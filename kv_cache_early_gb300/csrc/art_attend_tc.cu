@@ -32,8 +32,7 @@ static cudaError_t launch_tc(const AttendParams& p, cudaStream_t st) {
     if ((e = cudaFuncSetAttribute(art_attend_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
         cudaSuccess)
         return e;
-    art_attend_tc_kernel<D><<<p.ctas, kTcThreads, smem, st>>>(p, tk, tv);
-    return cudaGetLastError();
+    return launch_after(art_attend_tc_kernel<D>, dim3(p.ctas), dim3(kTcThreads), smem, st, p, tk, tv);
 }
 
 cudaError_t launch_attend_tc(const AttendParams& p, cudaStream_t st) {

@@ -200,24 +200,31 @@ __host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_mn) {
 // Waits, the whole warp, for the phase with `parity`. Gives up after wait_ns (setting
 // the status bit and the CTA's abort flag) or when another warp has: every warp then
 // leaves its loop, and none is left in a barrier, since all waits are of this kind.
-__device__ __forceinline__ bool wait_tc(uint64_t* bar, uint32_t parity, int* abort, const AttendParams& p) {
-    // the clock is read once the wait is long: reading it takes longer than most waits
-    for (int k = 0; k < 64; ++k)
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+// The long wait is a function of its own: inlined at every use it made the kernel
+// several times larger than the instruction cache.
+static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* abort, unsigned long long wait_ns,
+                                              int* status) {
     const unsigned long long t0 = global_ns();
     for (;;) {
+#pragma unroll 1
         for (int k = 0; k < 64; ++k)
             if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        const bool late = (threadIdx.x & 31) == 0 && global_ns() - t0 > p.wait_ns;
+        const bool late = (threadIdx.x & 31) == 0 && global_ns() - t0 > wait_ns;
         if (__any_sync(0xffffffffu, late)) {
             if ((threadIdx.x & 31) == 0) {
                 st_volatile_shared(abort, 1);
-                atomicOr(&p.cta_status[blockIdx.x], ART_STATUS_TIMEOUT);
+                atomicOr(status, ART_STATUS_TIMEOUT);
             }
             return false;
         }
         if (__any_sync(0xffffffffu, ld_volatile_shared(abort) != 0)) return false;
     }
+}
+__device__ __forceinline__ bool wait_tc(uint64_t* bar, uint32_t parity, int* abort, const AttendParams& p) {
+#pragma unroll 1
+    for (int k = 0; k < 64; ++k)
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return wait_long(bar, parity, abort, p.wait_ns, &p.cta_status[blockIdx.x]);
 }
 
 template <int NS>
@@ -1003,9 +1010,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     static_assert(sizeof(PlanScratch) <= C::CTRL, "the scratch lies in the tiles");
     // the tensor memory takes some microseconds to be had: beside the plan
-    if (w == kTcConsumers + 1) {
-        tc_alloc(&c->tmem);
-    } else if (w < kTcConsumers) {
+    if (w == kTcConsumers + 1) tc_alloc(&c->tmem);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what ran before on the stream has ended
+    if (w < kTcConsumers) {
         int a, z;
         plan_share<kTcConsumers * 32>(p, reinterpret_cast<PlanScratch*>(gen), a, z);
         if (threadIdx.x == 0) {
