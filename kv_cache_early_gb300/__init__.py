@@ -12,6 +12,7 @@ importing works without it, but the first call raises if it is missing.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -269,7 +270,7 @@ def _refuse(device, want, data, ints):
                 raise ArtError(f"{name} is {t.dtype}, not {dt}")
             if t.device != here:
                 raise ArtError(f"{name} is on {t.device}, not on {here}")
-            if sizes is not None and tuple(t.shape) != tuple(sizes):
+            if sizes is not None and t.numel() != math.prod(sizes):
                 raise ArtError(f"{name} is {tuple(t.shape)}, not {tuple(sizes)}")
             if not t.is_contiguous():
                 raise ArtError(f"{name} is not contiguous")
@@ -284,10 +285,6 @@ def _device_of(cache) -> int:
 
 def _addr(t):
     return None if t is None else t.data_ptr()
-
-
-def _int_ok(t, n, device, i32) -> bool:
-    return t.dtype is i32 and t.get_device() == device and t.shape == n and t.is_contiguous()
 
 
 def art_append_workspace_bytes(shape: ArtShape) -> int:
@@ -307,7 +304,8 @@ def art_append_kv(q, k, v, block_table, seq_lens, q_offsets, inv_freq, q_out, k_
     batch, hq, hkv, d = shape.batch, shape.num_q_heads, shape.num_kv_heads, shape.head_dim
     device = _device_of(k_cache)
     tokens = k.shape[0]
-    pool = (shape.num_pages_total, hkv, shape.page_size, d)
+    pages, ps = shape.num_pages_total, shape.page_size
+    pool, pool_n = (pages, hkv, ps, d), pages * hkv * ps * d
     step = [0, 0, 0]
     dense = True
     for i, t, heads in ((0, q, hq), (1, k, hkv), (2, v, hkv)):
@@ -320,16 +318,20 @@ def art_append_kv(q, k, v, block_table, seq_lens, q_offsets, inv_freq, q_out, k_
                 (tokens == 0 or (st[2] == 1 and (heads == 1 or st[1] == d)))):
             dense = False
     if not (dense and torch.cuda.current_device() == device and
-            k_cache.dtype is dt and k_cache.shape == pool and k_cache.is_contiguous() and
-            v_cache.dtype is dt and v_cache.shape == pool and v_cache.is_contiguous() and
+            k_cache.dtype is dt and k_cache.numel() == pool_n and k_cache.is_contiguous() and
+            v_cache.dtype is dt and v_cache.numel() == pool_n and v_cache.is_contiguous() and
             v_cache.get_device() == device and
-            (q_out is None or (q_out.dtype is dt and q_out.shape == (tokens, hq, d) and q_out.is_contiguous() and
+            (q_out is None or (q_out.dtype is dt and q_out.numel() == tokens * hq * d and q_out.is_contiguous() and
                                q_out.get_device() == device)) and
-            _int_ok(block_table, (batch, shape.max_pages_per_seq), device, i32) and
-            _int_ok(seq_lens, (batch,), device, i32) and
-            (q_offsets is None or _int_ok(q_offsets, (batch + 1,), device, i32)) and
-            (positions is None or _int_ok(positions, (tokens,), device, i32)) and
-            (inv_freq is None or (inv_freq.dtype is torch.float32 and inv_freq.shape == (rot_dim // 2,) and
+            block_table.dtype is i32 and block_table.numel() == batch * shape.max_pages_per_seq and
+            block_table.is_contiguous() and block_table.get_device() == device and
+            seq_lens.dtype is i32 and seq_lens.numel() == batch and seq_lens.is_contiguous() and
+            seq_lens.get_device() == device and
+            (q_offsets is None or (q_offsets.dtype is i32 and q_offsets.numel() == batch + 1 and
+                                   q_offsets.is_contiguous() and q_offsets.get_device() == device)) and
+            (positions is None or (positions.dtype is i32 and positions.numel() == tokens and
+                                   positions.is_contiguous() and positions.get_device() == device)) and
+            (inv_freq is None or (inv_freq.dtype is torch.float32 and inv_freq.numel() == rot_dim // 2 and
                                   inv_freq.get_device() == device and inv_freq.is_contiguous())) and
             workspace.get_device() == device and workspace.is_contiguous()):
         _refuse(device, dt, (("k_cache", k_cache, pool), ("v_cache", v_cache, pool), ("q_out", q_out, (tokens, hq, d))),
@@ -357,17 +359,21 @@ def _attend_checked(q, k_cache, v_cache, block_table, seq_lens, out, shape, work
     i32, dt = torch.int32, torch.bfloat16 if shape.dtype == ART_DTYPE_BF16 else torch.float32
     batch, d = shape.batch, shape.head_dim
     device = _device_of(k_cache)
-    pool = (shape.num_pages_total, shape.num_kv_heads, shape.page_size, d)
-    rows = (tokens, shape.num_q_heads, d)
+    pages, hkv, ps, hq = shape.num_pages_total, shape.num_kv_heads, shape.page_size, shape.num_q_heads
+    pool, pool_n = (pages, hkv, ps, d), pages * hkv * ps * d
+    rows, rows_n = (tokens, hq, d), tokens * hq * d
     if not (torch.cuda.current_device() == device and
-            q.dtype is dt and q.shape == rows and q.is_contiguous() and q.get_device() == device and
-            out.dtype is dt and out.shape == rows and out.is_contiguous() and out.get_device() == device and
-            k_cache.dtype is dt and k_cache.shape == pool and k_cache.is_contiguous() and
-            v_cache.dtype is dt and v_cache.shape == pool and v_cache.is_contiguous() and
+            q.dtype is dt and q.numel() == rows_n and q.is_contiguous() and q.get_device() == device and
+            out.dtype is dt and out.numel() == rows_n and out.is_contiguous() and out.get_device() == device and
+            k_cache.dtype is dt and k_cache.numel() == pool_n and k_cache.is_contiguous() and
+            v_cache.dtype is dt and v_cache.numel() == pool_n and v_cache.is_contiguous() and
             v_cache.get_device() == device and
-            _int_ok(block_table, (batch, shape.max_pages_per_seq), device, i32) and
-            _int_ok(seq_lens, (batch,), device, i32) and
-            (a is None or _int_ok(a, (a_n,), device, i32)) and (b is None or _int_ok(b, (b_n,), device, i32)) and
+            block_table.dtype is i32 and block_table.numel() == batch * shape.max_pages_per_seq and
+            block_table.is_contiguous() and block_table.get_device() == device and
+            seq_lens.dtype is i32 and seq_lens.numel() == batch and seq_lens.is_contiguous() and
+            seq_lens.get_device() == device and
+            (a is None or (a.dtype is i32 and a.numel() == a_n and a.is_contiguous() and a.get_device() == device)) and
+            (b is None or (b.dtype is i32 and b.numel() == b_n and b.is_contiguous() and b.get_device() == device)) and
             workspace.get_device() == device and workspace.is_contiguous()):
         _refuse(device, dt, (("q", q, rows), ("k_cache", k_cache, pool), ("v_cache", v_cache, pool), ("out", out, rows)),
                 (("block_table", block_table, (batch, shape.max_pages_per_seq)), ("seq_lens", seq_lens, (batch,)),

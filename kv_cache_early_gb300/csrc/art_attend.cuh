@@ -127,7 +127,7 @@ __device__ __forceinline__ int item_cost_base(const AttendParams& p, int nrow) {
 // Key tiles of an item before cost unit x of it.
 __device__ __forceinline__ int tiles_before(int x, int base, int per, int tiles) {
     if (x <= base) return 0;
-    return min(tiles, (x - base + per - 1) / per);
+    return min(tiles, (int)((unsigned)(x - base + per - 1) / (unsigned)per));
 }
 
 // First partial row of the piece of an item that CTA c holds. dense_extend keeps two

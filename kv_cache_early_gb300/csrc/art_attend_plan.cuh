@@ -97,6 +97,7 @@ static __device__ __noinline__ Entity entity_of(const AttendParams& p, PlanScrat
         if (n == 0) en.k1 = 0;
     } else if (p.NG > 0 && b >= s->offs[0] && b < s->offs[p.NG]) {
         int lo = 0, hi = p.NG;  // its group: the last that starts at or before b
+#pragma unroll 1
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (s->offs[mid] <= b) lo = mid;
@@ -135,11 +136,11 @@ static __device__ void emit_entity(const AttendParams& p, PlanScratch* s, const 
                                    int slack, int c) {
     const int lane = threadIdx.x & 31;
     const Entity en = q.en;
-    const int g0 = q.start >= lo ? 0 : (lo - q.start) / q.hc, items = p.Hkv * q.nrt;
+    const int g0 = q.start >= lo ? 0 : (int)((unsigned)(lo - q.start) / (unsigned)q.hc), items = p.Hkv * q.nrt;
     int x0 = q.start + g0 * q.hc;  // first unit of the items that follow
 #pragma unroll 1
     for (int i0 = g0 * q.nrt; i0 < items && x0 < hi; i0 += 32) {
-        const int i = i0 + lane, g = i / q.nrt, r = i - g * q.nrt;
+        const int i = i0 + lane, g = (int)((unsigned)i / (unsigned)q.nrt), r = i - g * q.nrt;
         int tiles = 0;
         const int cost = i < items ? item_cost(p, en, r, tiles) : 0;
         int z = cost;  // inclusive sum, then the item's end
@@ -157,7 +158,7 @@ static __device__ void emit_entity(const AttendParams& p, PlanScratch* s, const 
         // the CTAs that hold its first and its last unit; nearly always this one. Where little
         // of it lies on one side of a border between shares, it moves to the other whole:
         // a split costs the partial results' way through memory.
-        int c0 = x >= lo ? c : x / quota, c1 = z <= hi ? c : (z - 1) / quota;
+        int c0 = x >= lo ? c : (int)((unsigned)x / (unsigned)quota), c1 = z <= hi ? c : (int)((unsigned)(z - 1) / (unsigned)quota);
         if (c0 < c1 && (c0 + 1) * quota - x <= slack) ++c0;
         if (c0 < c1 && z - c1 * quota <= slack) --c1;
         if (c < c0 || c > c1) continue;
@@ -213,6 +214,7 @@ __device__ void plan_share(const AttendParams& p, PlanScratch* s, int& s0, int& 
     // offsets that do not rise within 0 .. their end: nothing is computed or written
     const int noff = p.shared ? p.NG : p.B, end = p.shared ? p.B : p.T;
     int bad = 0;
+#pragma unroll 1
     for (int i = tid; i <= noff && noff > 0; i += NT) {
         const int o = p.offsets[i], prev = i > 0 ? p.offsets[i - 1] : 0;
         bad |= o < prev || o > end || o < 0;
@@ -288,6 +290,7 @@ __device__ void plan_share(const AttendParams& p, PlanScratch* s, int& s0, int& 
         if (q.nrt > 0 && q.start < hi && q.start + q.hc * p.Hkv > lo) s->list[atomicAdd(&s->listed, 1)] = q;
         named_bar_sync(1, NT);
         const int n = s->listed, slack = p.shared ? 0 : quota / kSplitSlack;
+#pragma unroll 1
         for (int i = tid >> 5; i < n; i += NT / 32) emit_entity(p, s, s->list[i], lo, hi, quota, slack, c);
         named_bar_sync(1, NT);
         if (tid == 0) s->listed = 0;

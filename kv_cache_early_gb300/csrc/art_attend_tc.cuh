@@ -299,6 +299,7 @@ __device__ void tc_producer(const AttendParams& p, uint32_t smem, TcCtrl<TcCfg<D
                 const int in_tile = (lane - t * ppt) * prow;  // first row of this lane's page in the tile
                 const int group = mine ? (int)((((long long)ids * p.Hkv + sg.g) * p.Ps + ((tb + in_tile) & (p.Ps - 1))) >> 3)
                                        : 0;
+#pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t bit = 1u << st.s;
                     if (used & bit) {
@@ -629,6 +630,7 @@ struct TcConsumer {
         {
             constexpr int CPR = D / 8, RPI = 32 / CPR, NB = 16;  // chunks of a row; rows of a warp's load; loads at once
             const int rows = dual ? 32 : 16, ch = lane % CPR;
+#pragma unroll 1
             for (int i0 = 0; i0 < rows; i0 += NB * RPI) {
                 uint4 u[NB];
 #pragma unroll
@@ -749,6 +751,7 @@ struct TcConsumer {
         }
         if (dual) {
             if (live) {
+#pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
                     float o[32];
                     tc_ld32(tO + k, o);
@@ -770,6 +773,7 @@ struct TcConsumer {
                 const float mm = fmaxf(he ? e.x : -INFINITY, hd ? d.x : -INFINITY);
                 const float fe = he ? ex2(e.x - mm) : 0.f, fd = hd ? ex2(d.x - mm) : 0.f;
                 const float ll = (he ? e.y * fe : 0.f) + (hd ? d.y * fd : 0.f);
+#pragma unroll 1
                 for (int k = x * (D / 2); k < (x + 1) * (D / 2); k += 32) {
                     float o[32], o2[32];
                     tc_ld32(tmem + lanes + k, o);
@@ -809,6 +813,7 @@ struct TcConsumer {
 #pragma unroll
         for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         const int mat = lane >> 3, mr = lane & 7;
+#pragma unroll 1
         for (int j = 0; j < nt; ++j) {
             const int kb = (t0 + j) * kKeyTile + w * 16;  // first key of this warp's slice
             const bool any = kb + 16 > sg.k0 && kb < sg.k1;
