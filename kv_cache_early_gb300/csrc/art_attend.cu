@@ -239,7 +239,7 @@ static size_t attend_layout(AttendParams& p, unsigned char* base) {
 }
 
 // Cost units (about 0.15 us): what segments of each kind take beside their neighbours.
-constexpr CostRule kCostBf16 = {13, 7, 27, 10, 44, 12}, kCostF32 = {2, 8, 2, 8, 2, 8};
+constexpr CostRule kCostBf16 = {13, 7, 35, 11, 50, 13}, kCostF32 = {2, 8, 2, 8, 2, 8};
 
 static void fill_shape(AttendParams& p, const art_shape& s) {
     p.B = s.batch;

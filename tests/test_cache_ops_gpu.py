@@ -152,6 +152,13 @@ def test_append_bad_device_data():
         assert K.art_read_device_status(ws) & 128
 
 
+@pytest.mark.parametrize("dtype,rot,interleaved", [("bf16", 64, False), ("f32", 64, True), ("bf16", 22, False)])
+def test_append_many_tokens(dtype, rot, interleaved):
+    """More than 1024 tokens: four to a CTA, whose tokens belong to several sequences, to none, or to one."""
+    new = [1, 2, 3, 0, 5, 700, 1, 1, 350, 13]
+    append_case(11, dtype, 2, 1, 64, 16, new, np.arange(10) * 7, rot, interleaved, fused=True, pad=(3, 5))
+
+
 # ----------------------------------------------------------------------------
 # dense_extend
 # ----------------------------------------------------------------------------
@@ -259,6 +266,161 @@ def test_extend_no_tokens():
 def test_extend_large_scores(dtype):
     """Scores of several hundred: weights of zero and one, maxima that rise late."""
     extend_case(30, dtype, 4, 2, 128, 16, [33], [700], True, q_scale=16.0)
+
+
+def steep(pool, up):
+    """Keys along one direction whose scores with q = unit * 8 climb (or fall) by hundreds in steps of 37 keys."""
+    d = pool.d
+    u = np.zeros(d, np.float32)
+    u[::2] = 1.0
+    for b, n in enumerate(pool.seq_lens):
+        for t in range(int(n)):
+            pg, r = pool.table[b, t // pool.page], t % pool.page
+            level = float((t if up else int(n) - 1 - t) // 37 - 6)
+            pool.k[pg, :, r] = rounded(u * level + 0.0, pool.dtype)
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 8, 1, 128), ("bf16", 4, 2, 64), ("f32", 4, 2, 64)])
+@pytest.mark.parametrize("new", [3, 20, 70])
+@pytest.mark.parametrize("up", [True, False])
+def test_extend_maxima_that_move_far(dtype, hq, hkv, d, new, up):
+    """A row's maximum climbs by far more than 2^40 between and inside key tiles, or is met first and everything
+    after it underflows; the rows of a tile do so in opposite directions (the sign of q)."""
+    rng = np.random.default_rng(33)
+    seq = [new + 400]
+    pool = Pool(rng, dtype, hkv, d, 16, seq)
+    steep(pool, up)
+    q = np.zeros((new, hq, d), np.float32)
+    q[..., ::2] = 8.0
+    q[::2] *= -1.0
+    q[:, ::3] *= 0.125
+    shape = K.make_shape(**pool.shape(hq))
+    ws = workspace(K.dense_extend_workspace_bytes(shape, new))
+    out = torch.full((new, hq, d), SENTINEL, dtype=torch.bfloat16 if dtype == "bf16" else torch.float32, device="cuda")
+    K.dense_extend(dev(q, dtype), dev(pool.k, dtype), dev(pool.v, dtype), dev(pool.table), dev(pool.seq_lens),
+                   dev(np.array([0, new], np.int32)), out, shape, ws)
+    torch.cuda.synchronize()
+    assert K.art_read_device_status(ws) == 0
+    rows = {g: [O.gather(c, pool.table[0], seq[0], g) for c in (pool.k, pool.v)] for g in range(hkv)}
+    attend_close(host(out), q, lambda t, h: [c[:401 + t] for c in rows[h // (hq // hkv)]], dtype)
+
+
+def test_extend_nan_and_infinity_in_seen_keys():
+    """A NaN key makes the rows that see it NaN, of its KV head only; a score of +infinity likewise; keys that
+    no row sees change nothing."""
+    rng = np.random.default_rng(34)
+    for new in (3, 40):
+        pool = Pool(rng, "bf16", 2, 64, 16, [new + 300])
+        n = new + 300
+        pool.k[pool.table[0, 50 // 16], 0, 50 % 16, 3] = np.nan          # head 0: seen by all
+        last = n - 2                                                     # head 1: seen by the last two rows
+        pool.k[pool.table[0, last // 16], 1, last % 16, 5] = np.inf
+        q = rounded(1 + np.abs(rng.standard_normal((new, 4, 64))), "bf16")  # q > 0: the score is +infinity
+        shape = K.make_shape(**pool.shape(4))
+        ws = workspace(K.dense_extend_workspace_bytes(shape, new))
+        out = torch.zeros((new, 4, 64), dtype=torch.bfloat16, device="cuda")
+        K.dense_extend(dev(q, "bf16"), dev(pool.k, "bf16"), dev(pool.v, "bf16"), dev(pool.table), dev(pool.seq_lens),
+                       dev(np.array([0, new], np.int32)), out, shape, ws)
+        torch.cuda.synchronize()
+        got = host(out)
+        assert np.isnan(got[:, :2]).all()
+        assert np.isnan(got[-2:, 2:]).all()
+        k, v = (O.gather(c, pool.table[0], n, 1) for c in (pool.k, pool.v))
+        attend_close(got[:-2, 2:], q[:-2, 2:], lambda t, h: (k[:301 + t], v[:301 + t]), "bf16")
+
+
+def test_extend_many_sequences():
+    """More sequences than the plan takes in one round, some without tokens or keys, split over all CTAs."""
+    rng = np.random.default_rng(35)
+    new = [(b * 5) % 4 for b in range(700)]
+    seq = [n + (b * 13) % 40 for b, n in enumerate(new)]
+    for causal in (True, False):
+        extend_case(35, "bf16", 2, 1, 64, 8, new, seq, causal, check_rows=lambda i, h: h == 0)
+    extend_case(36, "f32", 1, 1, 64, 8, new[:300], seq[:300], True)
+
+
+def test_extend_wide_table():
+    """A table whose longest possible sequences would pass 31-bit cost units: plain tile counts are used."""
+    rng = np.random.default_rng(37)
+    new, seq = [3] * 40, [200] * 40
+    pool = Pool(rng, "bf16", 1, 64, 4096, seq)
+    cols = 1 << 18
+    table = torch.full((40, cols), -1, dtype=torch.int32, device="cuda")
+    table[:, : pool.table.shape[1]] = dev(pool.table)
+    q = rounded(rng.standard_normal((120, 2, 64)), "bf16")
+    shape = K.make_shape(**pool.shape(2, max_pages_per_seq=cols))
+    n = K.dense_extend_workspace_bytes(shape, 120)
+    assert n > 0
+    ws = workspace(n)
+    out = torch.zeros((120, 2, 64), dtype=torch.bfloat16, device="cuda")
+    K.dense_extend(dev(q, "bf16"), dev(pool.k, "bf16"), dev(pool.v, "bf16"), table, dev(pool.seq_lens),
+                   dev(np.arange(0, 121, 3).astype(np.int32)), out, shape, ws)
+    torch.cuda.synchronize()
+    assert K.art_read_device_status(ws) == 0
+    rows = [[O.gather(c, pool.table[b], 200, 0) for c in (pool.k, pool.v)] for b in range(40)]
+    attend_close(host(out), q, lambda t, h: [r[:198 + t % 3] for r in rows[t // 3]], "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_cache_past_32_bit_offsets(dtype):
+    """A pool of more than 2^32 elements, whose last pages the tokens lie in: append, extend and shared decode."""
+    hq, hkv, d, page = 4, 2, 64, 64
+    pages = (1 << 32) // (hkv * page * d) + 40
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    kc = torch.empty((pages, hkv, page, d), dtype=dt, device="cuda")
+    vc = torch.empty_like(kc)
+    rng = np.random.default_rng(38)
+    n = 150
+    table = np.array([[pages - 1, pages - 7, pages - 3], [pages - 1, pages - 5, pages - 2]], np.int32)
+    k, v = (rounded(rng.standard_normal((2 * n, hkv, d)), dtype) for _ in range(2))
+    q = rounded(rng.standard_normal((2 * n, hq, d)), dtype)
+    k[n:n + page], v[n:n + page] = k[:page], v[:page]  # the first page is the same for both
+    shape = K.make_shape(batch=2, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, page_size=page, block_size=64,
+                         max_pages_per_seq=3, max_visit=1, num_probe=1, num_pages_total=pages,
+                         dtype=0 if dtype == "bf16" else 1)
+    off, lens = dev(np.array([0, n, 2 * n], np.int32)), dev(np.array([n, n], np.int32))
+    tq, tt = dev(q, dtype), dev(table)
+    ws = workspace(max(K.dense_extend_workspace_bytes(shape, 2 * n), K.dense_decode_shared_workspace_bytes(shape, 1)))
+    q_out = torch.empty_like(tq)
+    K.art_append_kv(tq, dev(k, dtype), dev(v, dtype), tt, lens, off, None, q_out, kc, vc, shape, ws, rot_dim=0)
+    out = torch.empty_like(tq)
+    K.dense_extend(q_out, kc, vc, tt, lens, off, out, shape, ws)
+    dec = torch.empty((2, hq, d), dtype=dt, device="cuda")
+    ql = q_out[[n - 1, 2 * n - 1]].contiguous()
+    K.dense_decode_shared(ql, kc, vc, tt, lens, dev(np.array([0, 2], np.int32)), dev(np.array([page], np.int32)), dec,
+                          shape, ws)
+    torch.cuda.synchronize()
+    assert K.art_read_device_status(ws) == 0
+    k64, v64 = k.astype(np.float64), v.astype(np.float64)
+    seen = lambda t, h: [x[t // n * n:t + 1, h // 2] for x in (k64, v64)]
+    some = [0, 1, 63, 64, 149, 150, 213, 214, 299]
+    attend_close(host(out)[some], q[some], lambda i, h: seen(some[i], h), dtype)
+    attend_close(host(dec), q[[n - 1, 2 * n - 1]], lambda i, h: seen((i + 1) * n - 1, h), dtype)
+
+
+def test_bounded_wait_expires_and_next_call_is_clean(monkeypatch):
+    """The consumer warps wait for what nothing completes (test hook): the call ends with the timeout bit, the
+    context stays usable and the next call on the same buffers is right."""
+    rng = np.random.default_rng(39)
+    for new, seq in ([40, 3], [300, 150]), ([2], [5000]):
+        pool = Pool(rng, "bf16", 2, 128, 16, seq)
+        T = sum(new)
+        q = rounded(rng.standard_normal((T, 8, 128)), "bf16")
+        shape = K.make_shape(**pool.shape(8))
+        ws = workspace(K.dense_extend_workspace_bytes(shape, T))
+        off = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        args = (dev(q, "bf16"), dev(pool.k, "bf16"), dev(pool.v, "bf16"), dev(pool.table), dev(pool.seq_lens), dev(off),
+                torch.zeros((T, 8, 128), dtype=torch.bfloat16, device="cuda"), shape, ws)
+        monkeypatch.setenv("ART_TEST_STALL_NS", "200000")
+        K.dense_extend(*args)
+        torch.cuda.synchronize()
+        assert K.art_read_device_status(ws) & 32
+        monkeypatch.delenv("ART_TEST_STALL_NS")
+        K.dense_extend(*args)
+        torch.cuda.synchronize()
+        assert K.art_read_device_status(ws) == 0
+        ref = O.extend(q, pool.k, pool.v, pool.table, seq, off, True)
+        assert np.abs(host(args[6]) - ref).max() <= 8 * U["bf16"]  # |out| < 4 here: output and weight roundings
 
 
 def test_extend_bad_device_data():
@@ -395,6 +557,12 @@ def test_shared_short_and_empty_members():
 def test_shared_long_prefix_split():
     shared_case(47, "bf16", 4, 1, 128, 16, [(9001, [1, 200])], [])
     shared_case(48, "f32", 2, 2, 64, 64, [(5003, [1, 20])], [])
+
+
+def test_shared_many_sequences_and_groups():
+    """More groups and sequences than the plan takes in one round."""
+    groups = [(10 + j % 60, [1 + (j + i) % 5 for i in range(j % 4)]) for j in range(300)]
+    shared_case(52, "bf16", 2, 1, 64, 8, groups, [1 + b % 30 for b in range(50)], before=20)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -594,6 +762,26 @@ def test_captured_and_replayed():
     c.pk, c.sk = other.pk, other.sk
     for _ in range(3):
         g.replay()
+    torch.cuda.synchronize()
+    c.check()
+
+
+def test_two_graphs_share_their_workspaces():
+    """Graphs of the same program captured twice and replayed in turn on one stream."""
+    c = Chain(67)
+    c.run()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run()
+        graphs.append(g)
+    for n in ("pq", "po", "sq", "so", "dd"):
+        c.t[n].fill_(SENTINEL)
+    for _ in range(4):
+        for g in graphs:
+            g.replay()
     torch.cuda.synchronize()
     c.check()
 
