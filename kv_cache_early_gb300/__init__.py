@@ -287,6 +287,9 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+_ropes = {}  # by (rot_dim, interleaved, scale): a program has one or two
+
+
 def art_append_workspace_bytes(shape: ArtShape) -> int:
     return int(lib().art_append_workspace_bytes(ctypes.byref(shape)))
 
@@ -306,18 +309,22 @@ def art_append_kv(q, k, v, block_table, seq_lens, q_offsets, inv_freq, q_out, k_
     tokens = k.shape[0]
     pages, ps = shape.num_pages_total, shape.page_size
     pool, pool_n = (pages, hkv, ps, d), pages * hkv * ps * d
-    step = [0, 0, 0]
+    # a lone row's stride is never used: any whole one
+    many = tokens > 1
+    qs = 0
     dense = True
-    for i, t, heads in ((0, q, hq), (1, k, hkv), (2, v, hkv)):
-        if t is None:
-            continue
-        st = t.stride()
-        # a lone row's stride is never used: any whole one
-        step[i] = st[0] if tokens > 1 else heads * d
-        if not (t.dtype is dt and t.get_device() == device and t.shape == (tokens, heads, d) and
-                (tokens == 0 or (st[2] == 1 and (heads == 1 or st[1] == d)))):
-            dense = False
-    if not (dense and torch.cuda.current_device() == device and
+    if q is not None:
+        st = q.stride()
+        qs = st[0] if many else hq * d
+        dense = (q.dtype is dt and q.get_device() == device and q.shape == (tokens, hq, d) and
+                 (tokens == 0 or (st[2] == 1 and (hq == 1 or st[1] == d))))
+    sk, sv = k.stride(), v.stride()
+    ks, vs = (sk[0], sv[0]) if many else (hkv * d, hkv * d)
+    rows = (tokens, hkv, d)
+    if not (dense and k.dtype is dt and v.dtype is dt and k.shape == rows and v.shape == rows and
+            k.get_device() == device and v.get_device() == device and
+            (tokens == 0 or (sk[2] == 1 and sv[2] == 1 and (hkv == 1 or (sk[1] == d and sv[1] == d)))) and
+            torch.cuda.current_device() == device and
             k_cache.dtype is dt and k_cache.numel() == pool_n and k_cache.is_contiguous() and
             v_cache.dtype is dt and v_cache.numel() == pool_n and v_cache.is_contiguous() and
             v_cache.get_device() == device and
@@ -342,8 +349,10 @@ def art_append_kv(q, k, v, block_table, seq_lens, q_offsets, inv_freq, q_out, k_
         raise ArtError("q, k and v are not [tokens, heads, head_dim] rows of the cache's dtype and device, dense in "
                        "their last two dimensions: " +
                        ", ".join(f"{tuple(t.shape)} {t.dtype} strides {t.stride()}" for t in (q, k, v) if t is not None))
-    rope = ArtRope(int(rot_dim), 1 if interleaved else 0, scale)
-    rc = L.art_append_kv(_addr(q), k.data_ptr(), v.data_ptr(), step[0], step[1], step[2], _addr(q_offsets), tokens,
+    rope = _ropes.get((rot_dim, interleaved, scale))
+    if rope is None:
+        rope = _ropes.setdefault((rot_dim, interleaved, scale), ArtRope(int(rot_dim), 1 if interleaved else 0, scale))
+    rc = L.art_append_kv(_addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(q_offsets), tokens,
                          _addr(positions), block_table.data_ptr(), seq_lens.data_ptr(), _addr(inv_freq),
                          ctypes.byref(rope), _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
                          ctypes.byref(shape), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, device))

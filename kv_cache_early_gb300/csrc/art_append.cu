@@ -11,13 +11,13 @@
 // rot_dim on and the values are copied. The cache row of KV head g is
 // (page(s / Ps) * Hkv + g) * Ps + s % Ps.
 //
-// The angle is formed and reduced to [-pi, pi] in 64 bits: pos * inv_freq reaches
-// 1e5..1e6 radians, where a 32-bit product is off by hundredths of a radian. The
-// reduced angle is rounded once to 32 bits (2^-24 * pi), and sine, cosine and the
-// rotation are 32-bit; a bf16 result is rounded once at the store.
+// pos * inv_freq reaches 1e5..1e6 radians, where a 32-bit product is off by hundredths
+// of a radian: the angle is formed and reduced to one turn with more than 32 bits
+// (turn_of). Sine, cosine and the rotation are 32-bit; a bf16 result is rounded once
+// at the store.
 //
 // Bound: HBM, 2 (Hq + 2 Hkv) d bytes in and as many out a token. A CTA takes one
-// token, or four: their first rows are loaded (independent of the position) before
+// token, or two: their first rows are loaded (independent of the position) before
 // the chain offsets -> seq_len -> page id -> angles, so a decode step waits for the
 // longer of the two and not for their sum. One more CTA (block 0) checks the device
 // data of the call and stores the status word, so that no memset precedes the
@@ -115,6 +115,35 @@ __device__ void append_check(const AppendParams& p) {
     if (tid == 0) p.hdr->status = s_err;
 }
 
+// Cosine and sine of pos * f. The product is held as h + e (exact, by the fused
+// product), 2 pi in three parts (Cody and Waite's reduction): with k = the nearest
+// number of turns, h - k C1 is exact, k C2 is taken with its own rounding error, and what
+// the sums round off (Knuth's two-sum) is kept; in 32-bit arithmetic the remainder
+// r + low is within 2e-14 of the true one for products below 2^24. low enters to first order.
+// Beyond, in 64 bits. (64-bit arithmetic for every angle cost 5 of 150 us: its pipe
+// gives two results a clock and SM.)
+__device__ __forceinline__ float2 turn_of(int pos, float f) {
+    const float p = (float)pos, h = __fmul_rn(p, f);  // _rn: not contracted
+    float r, low;
+    if (pos > -(1 << 24) && pos < (1 << 24) && fabsf(h) < 16777216.f) {
+        constexpr float C1 = 6.2831854820251465f, C2 = -1.7484555314695172e-07f, C3 = -6.8604980400235275e-15f;
+        const float e = fmaf(p, f, -h), k = rintf(h * 0.15915494f);
+        const float r1 = fmaf(-k, C1, h), t = __fmul_rn(k, C2), tl = fmaf(k, C2, -t);
+        const float a = r1 - t, ab = a - r1, ae = (r1 - (a - ab)) + (-t - ab);
+        r = a + e;
+        const float rb = r - a, re = (a - (r - rb)) + (e - rb);
+        low = ((ae - tl) - k * C3) + re;
+    } else {
+        double y = (double)pos * (double)f;
+        y -= 6.283185307179586476925 * rint(y * 0.159154943091895335769);
+        r = (float)y;
+        low = (float)(y - (double)r);
+    }
+    float s, c;
+    sincosf(r, &s, &c);
+    return make_float2(c - low * s, s + low * c);
+}
+
 // kVec: a row is taken in units of two 16-byte chunks: of a rotated row in pairs
 // (j, j + rot_dim / 2) the chunks c and c + npair for c < npair, then the copied chunks
 // two by two; otherwise neighbours. It needs rot_dim / 2 (interleaved: rot_dim) to be a
@@ -173,8 +202,8 @@ __global__ void __launch_bounds__(kAppendThreads) art_append_kernel(const Append
             split(R, tok, r);
             chunks(r < nq + p.Hkv, ca, cb);
             const uint4* src = reinterpret_cast<const uint4*>(src_of(tok, r));
-            a[k] = __ldcs(src + ca);
-            b2[k] = __ldcs(src + cb);
+            a[k] = src[ca];
+            b2[k] = src[cb];
         }
     };
     if constexpr (kVec) load(tid / PER);
@@ -216,13 +245,9 @@ __global__ void __launch_bounds__(kAppendThreads) art_append_kernel(const Append
     __syncthreads();
     for (int x = tid; x < ntok * half; x += kAppendThreads) {
         const int tok = x / half, j = x - tok * half;
-        const int pos = p.positions ? p.positions[t0 + tok] : s_place[tok];
-        double y = (double)pos * (double)p.inv_freq[j];
-        y -= 6.283185307179586476925 * rint(y * 0.159154943091895335769);
-        float sn, cs;
-        sincosf((float)y, &sn, &cs);
-        s_cos[tok * kMaxRotHalf + j] = cs * p.scale;
-        s_sin[tok * kMaxRotHalf + j] = sn * p.scale;
+        const float2 cs = turn_of(p.positions ? p.positions[t0 + tok] : s_place[tok], p.inv_freq[j]);
+        s_cos[tok * kMaxRotHalf + j] = cs.x * p.scale;
+        s_sin[tok * kMaxRotHalf + j] = cs.y * p.scale;
     }
     __syncthreads();
 
@@ -384,13 +409,13 @@ int art_append_kv(const void* q, const void* k, const void* v, int64_t q_stride,
     const bool bf = s.dtype == ART_DTYPE_BF16;
     const bool vec = (p.interleaved ? p.rot : p.rot / 2) % chunk == 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // one token a CTA while they are few (a step waits for one chain of loads), else four
+    // one token a CTA while they are few (a step waits for one chain of loads), else two
     // (which share the chain)
-    const int tok = num_tokens <= kFewTokens ? 1 : 4;
+    const int tok = num_tokens <= kFewTokens ? 1 : 2;
     const unsigned grid = (unsigned)((num_tokens + tok - 1) / tok) + 1u;
 #define ART_APPEND(BF, DD, VEC)                                                               \
     (tok == 1 ? art_append_kernel<BF, DD, VEC, 1><<<grid, kAppendThreads, 0, st>>>(p)         \
-              : art_append_kernel<BF, DD, VEC, 4><<<grid, kAppendThreads, 0, st>>>(p))
+              : art_append_kernel<BF, DD, VEC, 2><<<grid, kAppendThreads, 0, st>>>(p))
     if (bf && s.head_dim == 128) { if (vec) ART_APPEND(true, 128, true); else ART_APPEND(true, 128, false); }
     else if (bf) { if (vec) ART_APPEND(true, 64, true); else ART_APPEND(true, 64, false); }
     else if (s.head_dim == 128) { if (vec) ART_APPEND(false, 128, true); else ART_APPEND(false, 128, false); }
