@@ -339,8 +339,8 @@ int art_append_kv(const void* q, const void* k, const void* v, int64_t q_stride,
  * values outside a sequence's length may hold anything, NaN included; a value
  * that some new tokens of a sequence see must be finite for the others too.
  * Supported: num_tokens * G and a table row's tokens up to 2^30, and
- * (num_tokens * G / rows + batch) * num_kv_heads * (a table row's tokens / 128) up
- * to 2^30, with rows = 256 for bf16 and 64 for fp32.
+ * (num_tokens * G / rows + batch) * num_kv_heads * (a table row's tokens / keys)
+ * up to 2^30, with rows = 256 and keys = 128 for bf16, both 64 for fp32.
  */
 size_t dense_extend_workspace_bytes(const art_shape* shape, int32_t num_tokens);
 int dense_extend(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
                     e.np = 0;
                     if (q[i].nrows == 0 || (i == 0 && lim <= 0)) continue;
                     e.nrow = min(p.rt, q[i].nrows - t * p.rt);
-                    e.tiles = (q[i].k1 + kKeyTile - 1) / kKeyTile - q[i].k0 / kKeyTile;
+                    e.tiles = tiles_of(p, q[i].k0, q[i].k1);
                     e.base = item_cost_base(p, e.nrow);
                     e.per = item_cost_tile(p, e.nrow);
                     e.x = q[i].start + g * q[i].hc + t * (item_cost_base(p, p.rt) + item_cost_tile(p, p.rt) * e.tiles);
@@ -214,7 +214,7 @@ static size_t attend_layout(AttendParams& p, unsigned char* base) {
         return 0;
     p.part_rows = (int)prows;
     // cost units fit 31 bits, with room for sums of one share beyond the end
-    const long long tiles = ((long long)p.max_pages * p.Ps + kKeyTile - 1) / kKeyTile;
+    const long long tiles = (((long long)p.max_pages * p.Ps) >> p.kt_log2) + 1;
     const long long per = p.cost.two_tile > p.cost.small_tile ? p.cost.two_tile : p.cost.small_tile;
     if (items * (per * tiles + p.cost.two_item) > (1LL << 30)) p.cost = {0, 1, 0, 1, 0, 1};
     if (items * tiles > (1LL << 30)) return 0;
@@ -239,7 +239,7 @@ static size_t attend_layout(AttendParams& p, unsigned char* base) {
 }
 
 // Cost units (about 0.15 us): what segments of each kind take beside their neighbours.
-constexpr CostRule kCostBf16 = {13, 7, 35, 11, 50, 13}, kCostF32 = {2, 8, 2, 8, 2, 8};
+constexpr CostRule kCostBf16 = {13, 7, 35, 11, 50, 13}, kCostF32 = {10, 8, 10, 16, 10, 16};
 
 static void fill_shape(AttendParams& p, const art_shape& s) {
     p.B = s.batch;
@@ -252,6 +252,9 @@ static void fill_shape(AttendParams& p, const art_shape& s) {
     p.max_pages = s.max_pages_per_seq;
     p.num_pages = s.num_pages_total;
     p.rt = s.dtype == ART_DTYPE_BF16 ? kRowsTc : kItemRows;
+    p.kt_log2 = s.dtype == ART_DTYPE_BF16 ? 7 : 6;
+    p.small_rows = s.dtype == ART_DTYPE_BF16 ? kSmallRows : kSmallRowsF32;
+    static_assert(kKeyTile == 1 << 7 && kKeyTileF32 == 1 << 6, "tiles");
     p.cost = s.dtype == ART_DTYPE_BF16 ? kCostBf16 : kCostF32;
     p.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)s.head_dim));
 }

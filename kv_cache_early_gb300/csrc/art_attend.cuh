@@ -9,7 +9,7 @@
 // into tiles of at most `rt` rows. Items are numbered entity by entity (a group, or
 // a sequence), KV head by KV head, row tile by row tile.
 //
-// The items' costs (a part for the item and one for each key tile of kKeyTile tokens,
+// The items' costs (a part for the item and one for each key tile of 128 tokens (fp32: 64),
 // on the absolute grid of the sequence) are laid end to end and cut into equal shares,
 // one for each CTA of the main kernel; what a CTA gets of one item is a segment. An
 // item inside one share is finished by its CTA; otherwise each segment leaves, per
@@ -30,11 +30,13 @@
 
 namespace art {
 
-constexpr int kKeyTile = 128;      // keys of a tile
+constexpr int kKeyTile = 128;      // keys of a tile, bf16
+constexpr int kKeyTileF32 = 64;    // ... and fp32
 constexpr int kAttendCtas = 160;   // CTAs of the main kernel at most (one per SM)
 constexpr int kRowsTc = 256;       // rows of an item's tile, bf16
 constexpr int kItemRows = 64;      // ... and fp32
-constexpr int kSmallRows = 16;     // bf16: rows of an item that the consumer warps take by themselves
+constexpr int kSmallRows = 16;     // rows of an item that the warps take key by key, bf16
+constexpr int kSmallRowsF32 = 8;   // ... and fp32
 constexpr int kSplitSlack = 16;    // dense_extend: a share may grow by 1 / 16 at an end so that an item is not split
 constexpr int kMaxGroups = 8192;   // groups of a dense_decode_shared call (their offsets are kept in shared memory)
 
@@ -84,7 +86,7 @@ struct PlanInfo {
 
 // Cost units of an item and of a key tile, by rows.
 struct CostRule {
-    int small_item, small_tile;  // up to kSmallRows rows
+    int small_item, small_tile;  // up to small_rows rows
     int one_item, one_tile;      // up to 128 rows
     int two_item, two_tile;
 };
@@ -99,6 +101,7 @@ struct AttendParams {
     int B, T, NG, NE;  // sequences, query tokens, groups, entities
     int Hq, Hkv, G, D, Ps, max_pages, num_pages;
     int rt, ctas, part_rows;
+    int kt_log2, small_rows;  // keys of a tile; rows of a small item
     CostRule cost;
     float scale_log2;  // log2(e) / sqrt(d)
     unsigned long long g_mul;  // ceil(2^34 / G): R / G = R * g_mul >> 34
@@ -119,10 +122,13 @@ struct AttendParams {
 };
 
 __device__ __forceinline__ int item_cost_tile(const AttendParams& p, int nrow) {
-    return nrow <= kSmallRows ? p.cost.small_tile : nrow <= 128 ? p.cost.one_tile : p.cost.two_tile;
+    return nrow <= p.small_rows ? p.cost.small_tile : nrow <= 128 ? p.cost.one_tile : p.cost.two_tile;
 }
 __device__ __forceinline__ int item_cost_base(const AttendParams& p, int nrow) {
-    return nrow <= kSmallRows ? p.cost.small_item : nrow <= 128 ? p.cost.one_item : p.cost.two_item;
+    return nrow <= p.small_rows ? p.cost.small_item : nrow <= 128 ? p.cost.one_item : p.cost.two_item;
+}
+__device__ __forceinline__ int tiles_of(const AttendParams& p, int k0, int k1) {
+    return ((k1 + (1 << p.kt_log2) - 1) >> p.kt_log2) - (k0 >> p.kt_log2);
 }
 // Key tiles of an item before cost unit x of it.
 __device__ __forceinline__ int tiles_before(int x, int base, int per, int tiles) {

@@ -122,7 +122,7 @@ static __device__ __noinline__ Entity entity_of(const AttendParams& p, PlanScrat
 __device__ __forceinline__ int entity_tiles(const AttendParams& p, const Entity& en, int r) {  // row tile r's key tiles
     int k1 = en.k1;
     if (en.kind == kLimCausal) k1 = en.lim0 + token_of(p, min((r + 1) * p.rt, en.nrows) - 1);
-    return (k1 + kKeyTile - 1) / kKeyTile - en.k0 / kKeyTile;
+    return tiles_of(p, en.k0, k1);
 }
 __device__ __forceinline__ int item_cost(const AttendParams& p, const Entity& en, int r, int& tiles) {
     const int n = min(p.rt, en.nrows - r * p.rt);
@@ -154,7 +154,7 @@ static __device__ void emit_entity(const AttendParams& p, PlanScratch* s, const 
         x0 = __shfl_sync(0xffffffffu, z, 31);
         if (i >= items || x >= hi || z <= lo) continue;
         const int n = min(p.rt, en.nrows - r * p.rt);
-        const int base = item_cost_base(p, n), per = item_cost_tile(p, n), t0 = en.k0 / kKeyTile;
+        const int base = item_cost_base(p, n), per = item_cost_tile(p, n), t0 = en.k0 >> p.kt_log2;
         // the CTAs that hold its first and its last unit; nearly always this one. Where little
         // of it lies on one side of a border between shares, it moves to the other whole:
         // a split costs the partial results' way through memory.
@@ -172,8 +172,8 @@ static __device__ void emit_entity(const AttendParams& p, PlanScratch* s, const 
         o.r0 = r * p.rt;
         o.nrow = tz > ta ? n : 0;
         o.g = g;
-        o.k0 = max(en.k0, (t0 + ta) * kKeyTile);
-        o.k1 = min(k1, (t0 + tz) * kKeyTile);
+        o.k0 = max(en.k0, (t0 + ta) << p.kt_log2);
+        o.k1 = min(k1, (t0 + tz) << p.kt_log2);
         o.lim0 = en.lim0;
         o.kind = en.kind;
         o.prow = p.shared ? q.prow + g * en.nrows + r * p.rt + c * p.rt : (c0 == c1 ? -1 : piece_row_extend(c, c == c0, p.rt));
