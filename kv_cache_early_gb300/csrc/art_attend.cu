@@ -11,6 +11,18 @@ int check_shape(const art_shape* s);  // art_api.cu
 
 constexpr int kMergeBlock = 256;
 
+// Columns 4 ch .. 4 ch + 3 of a finished row.
+template <bool kBF16, int D>
+__device__ __forceinline__ void put_row4(const AttendParams& p, size_t row, int ch, const float4& o, float l) {
+    const float inv = l > 0.f ? 1.f / l : l;  // no key seen: 0; NaN stays
+    if constexpr (kBF16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + ch * 4) =
+            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    else
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D + ch * 4) =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
 // One row's pieces joined: a lane holds one piece's (m, l), up to 32 at a time, then the
 // pieces' columns are read side by side (no load waits for another).
 template <bool kBF16, int D>
@@ -69,15 +81,7 @@ struct MergeRow {
         }
     }
     __device__ __forceinline__ void store(const AttendParams& p, size_t row) {
-        if (lane >= D / 4) return;
-        const float inv = l > 0.f ? 1.f / l : l;  // no key seen: 0; NaN stays
-        if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if constexpr (kBF16)
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + lane * 4) =
-                make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        else
-            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D + lane * 4) =
-                make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (lane < D / 4) put_row4<kBF16, D>(p, row, lane, o, l);
     }
 };
 
@@ -163,24 +167,41 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
     } else {
         MergeRow<kBF16, D> z;
         z.lane = lane;
+        // the items that go over a border between shares: a thread takes four columns of a row
+        __shared__ int s_prow[kAttendCtas];
         for (int c = blockIdx.x; c < p.ctas; c += gridDim.x) {
             const MergeItem it = p.merge[c];
             if (it.np == 0 || (slow && seq_bad(p, it.seq, -1, lane))) continue;
-            const int base = item_cost_base(p, it.nrow), per = item_cost_tile(p, it.nrow);
-            for (int r = blockIdx.y * WPB + w; r < it.nrow; r += gridDim.y * WPB) {
-                MergeRow<kBF16, D> m;
-                m.lane = lane;
-                m.add(p, it.np, [&](int k, int& prow, int& nrow, int& row) {
-                    const int a = k == 0 ? 0 : it.off + (k - 1) * quota;
-                    prow = piece_row_extend(it.c0 + k, k == 0, p.rt);
-                    nrow = it.nrow;
-                    row = r;
-                    const int to = k == it.np - 1 ? it.tiles : tiles_before(it.off + k * quota, base, per, it.tiles);
-                    return to > tiles_before(a, base, per, it.tiles);
-                });
-                const int R = it.r0 + r, t = R / p.G;
-                m.store(p, (size_t)(it.tok0 + t) * p.Hq + it.g * p.G + (R - t * p.G));
+            if (tid < it.np) {  // the pieces' first partial rows, -1 where one is empty
+                const int base = item_cost_base(p, it.nrow), per = item_cost_tile(p, it.nrow);
+                const int from = tid == 0 ? 0 : tiles_before(it.off + (tid - 1) * quota, base, per, it.tiles);
+                const int to = tid == it.np - 1 ? it.tiles : tiles_before(it.off + tid * quota, base, per, it.tiles);
+                s_prow[tid] = to > from ? piece_row_extend(it.c0 + tid, tid == 0, p.rt) : -1;
             }
+            __syncthreads();
+            for (int u = blockIdx.y * kMergeBlock + tid; u < it.nrow * (D / 4); u += gridDim.y * kMergeBlock) {
+                const int r = u / (D / 4), ch = u - r * (D / 4);
+                float m = -INFINITY, l = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                for (int k = 0; k < it.np; ++k) {
+                    const int pr = s_prow[k];
+                    if (pr < 0) continue;
+                    const float2 e = __ldcg(&p.part_ml[pr + r]);
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + (size_t)pr * D) + ch * it.nrow + r);
+                    if (e.y == 0.f) continue;  // saw no key
+                    const float mn = fmaxf(m, e.x), a = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(e.x - mn);
+                    l = l * a + e.y * w;
+                    o.x = o.x * a + v.x * w;
+                    o.y = o.y * a + v.y * w;
+                    o.z = o.z * a + v.z * w;
+                    o.w = o.w * a + v.w * w;
+                    m = mn;
+                }
+                const int R = it.r0 + r, t = R / p.G;
+                put_row4<kBF16, D>(p, (size_t)(it.tok0 + t) * p.Hq + it.g * p.G + (R - t * p.G), ch, o, l);
+            }
+            __syncthreads();
         }
         // sequences without keys, and bad ones: zero
         for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -283,7 +304,7 @@ static int attend_run(AttendParams& p, const art_shape& s, void* workspace, size
     if ((e = bf ? launch_attend_tc(p, st) : launch_attend_simt(p, st)) != cudaSuccess) return cuda_fail(e);
     // the merge kernel's launch overlaps the main kernel's end
     const long long blocks = p.shared ? ((long long)p.B * p.Hq + kMergeBlock / 32 - 1) / (kMergeBlock / 32) : p.ctas;
-    const dim3 grid((unsigned)(blocks < 8LL * p.ctas ? blocks : 8LL * p.ctas), p.shared ? 1 : p.rt / 32);
+    const dim3 grid((unsigned)(blocks < 8LL * p.ctas ? blocks : 8LL * p.ctas), p.shared ? 1 : p.rt / 16);
 #define ART_MERGE(BF, DD)                                                                                    \
     e = p.shared ? launch_after(art_attend_merge_kernel<BF, DD, true>, grid, dim3(kMergeBlock), 0, st, p)   \
                  : launch_after(art_attend_merge_kernel<BF, DD, false>, grid, dim3(kMergeBlock), 0, st, p)

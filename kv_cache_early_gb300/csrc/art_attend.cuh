@@ -37,7 +37,7 @@ constexpr int kRowsTc = 256;       // rows of an item's tile, bf16
 constexpr int kItemRows = 64;      // ... and fp32
 constexpr int kSmallRows = 16;     // rows of an item that the warps take key by key, bf16
 constexpr int kSmallRowsF32 = 8;   // ... and fp32
-constexpr int kSplitSlack = 16;    // dense_extend: a share may grow by 1 / 16 at an end so that an item is not split
+constexpr int kSplitSlack = 32;    // dense_extend: a share may grow by 1 / 32 at an end so that an item is not split
 constexpr int kMaxGroups = 8192;   // groups of a dense_decode_shared call (their offsets are kept in shared memory)
 
 // How far a row sees: all keys of the segment; up to its own token; up to the
