@@ -200,7 +200,7 @@ def kernel_source_hash(path=None):
     for f in sorted(os.listdir(csrc)):
         if not f.endswith((".cu", ".cuh")):
             continue
-        if path is not None and f == "art_select.cu":
+        if path is not None and (f == "art_select.cu" or f.startswith(("art_append", "art_attend"))):
             continue
         if path == "one CTA per item" and f.startswith("art_units"):
             continue

@@ -351,6 +351,8 @@ def art_append_kv(q, k, v, block_table, seq_lens, q_offsets, inv_freq, q_out, k_
                        ", ".join(f"{tuple(t.shape)} {t.dtype} strides {t.stride()}" for t in (q, k, v) if t is not None))
     rope = _ropes.get((rot_dim, interleaved, scale))
     if rope is None:
+        if len(_ropes) >= 64:
+            _ropes.clear()
         rope = _ropes.setdefault((rot_dim, interleaved, scale), ArtRope(int(rot_dim), 1 if interleaved else 0, scale))
     rc = L.art_append_kv(_addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(q_offsets), tokens,
                          _addr(positions), block_table.data_ptr(), seq_lens.data_ptr(), _addr(inv_freq),

@@ -315,8 +315,7 @@ static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 static bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
-// also the checks of art_append.cu and art_attend.cu
-int check_shape(const art_shape* s) {
+static int check_shape(const art_shape* s) {
     if (!s) return ART_ERR_INVALID_ARG;
     if (s->batch < 1 || s->num_q_heads < 1 || s->num_kv_heads < 1 || s->head_dim < 1 || s->page_size < 1 ||
         s->block_size < 1 || s->max_pages_per_seq < 1 || s->max_visit < 1 || s->num_pages_total < 1)

@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kAppendThreads) art_append_kernel(const Append
     }
 }
 
-int check_shape(const art_shape* s);  // art_api.cu
+int check_cache_shape(const art_shape* s);  // art_attend.cu
 
 }  // namespace art
 
@@ -357,7 +357,7 @@ int art_append_kv(const void* q, const void* k, const void* v, int64_t q_stride,
                   const int32_t* q_offsets, int32_t num_tokens, const int32_t* positions, const int32_t* block_table,
                   const int32_t* seq_lens, const float* inv_freq, const art_rope* rope, void* q_out, void* k_cache,
                   void* v_cache, const art_shape* shape, void* workspace, size_t workspace_bytes, void* stream) {
-    const int rc = check_shape(shape);
+    const int rc = check_cache_shape(shape);
     if (rc != ART_OK) return rc;
     const art_shape& s = *shape;
     if (!block_table || !seq_lens || !k_cache || !v_cache || !workspace || !rope) return ART_ERR_INVALID_ARG;

@@ -7,8 +7,6 @@
 
 namespace art {
 
-int check_shape(const art_shape* s);  // art_api.cu
-
 constexpr int kMergeBlock = 256;
 
 // Columns 4 ch .. 4 ch + 3 of a finished row.
@@ -216,6 +214,22 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+int check_cache_shape(const art_shape* s) {
+    if (!s) return ART_ERR_INVALID_ARG;
+    if (s->batch < 1 || s->num_q_heads < 1 || s->num_kv_heads < 1 || s->head_dim < 1 || s->page_size < 1 ||
+        s->block_size < 1 || s->max_pages_per_seq < 1 || s->num_pages_total < 1)
+        return ART_ERR_INVALID_ARG;
+    if (s->num_q_heads % s->num_kv_heads != 0) return ART_ERR_INVALID_ARG;
+    if (s->dtype != ART_DTYPE_BF16 && s->dtype != ART_DTYPE_F32) return ART_ERR_INVALID_ARG;
+    if ((long long)s->batch * s->num_kv_heads > (1LL << 30)) return ART_ERR_UNSUPPORTED;
+    const int G = s->num_q_heads / s->num_kv_heads;
+    if (G != 1 && G != 2 && G != 4 && G != 7 && G != 8) return ART_ERR_UNSUPPORTED;
+    if (s->head_dim != 64 && s->head_dim != 128) return ART_ERR_UNSUPPORTED;
+    if (s->block_size != kBK) return ART_ERR_UNSUPPORTED;
+    if ((s->page_size & (s->page_size - 1)) != 0 || s->page_size < 8 || s->page_size > 4096) return ART_ERR_UNSUPPORTED;
+    return ART_OK;
+}
+
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Sizes and workspace layout of a call; returns the bytes, or 0 where they pass the
@@ -326,7 +340,7 @@ using namespace art;
 extern "C" {
 
 size_t dense_extend_workspace_bytes(const art_shape* shape, int32_t num_tokens) {
-    if (check_shape(shape) != ART_OK || num_tokens < 0) return 0;
+    if (check_cache_shape(shape) != ART_OK || num_tokens < 0) return 0;
     AttendParams p = {};
     fill_shape(p, *shape);
     p.T = num_tokens;
@@ -336,7 +350,7 @@ size_t dense_extend_workspace_bytes(const art_shape* shape, int32_t num_tokens) 
 int dense_extend(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
                  const int32_t* seq_lens, const int32_t* q_offsets, int32_t num_tokens, int32_t causal, void* out,
                  const art_shape* shape, void* workspace, size_t workspace_bytes, void* stream) {
-    const int rc = check_shape(shape);
+    const int rc = check_cache_shape(shape);
     if (rc != ART_OK) return rc;
     if (!k_cache || !v_cache || !block_table || !seq_lens || !q_offsets || !workspace) return ART_ERR_INVALID_ARG;
     if (num_tokens != 0 && (!q || !out)) return ART_ERR_INVALID_ARG;
@@ -358,7 +372,7 @@ int dense_extend(const void* q, const void* k_cache, const void* v_cache, const 
 }
 
 size_t dense_decode_shared_workspace_bytes(const art_shape* shape, int32_t num_groups) {
-    if (check_shape(shape) != ART_OK || num_groups < 0) return 0;
+    if (check_cache_shape(shape) != ART_OK || num_groups < 0) return 0;
     AttendParams p = {};
     fill_shape(p, *shape);
     p.shared = 1;
@@ -370,7 +384,7 @@ int dense_decode_shared(const void* q, const void* k_cache, const void* v_cache,
                         const int32_t* seq_lens, const int32_t* group_offsets, const int32_t* prefix_lens,
                         int32_t num_groups, void* out, const art_shape* shape, void* workspace,
                         size_t workspace_bytes, void* stream) {
-    const int rc = check_shape(shape);
+    const int rc = check_cache_shape(shape);
     if (rc != ART_OK) return rc;
     if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !workspace) return ART_ERR_INVALID_ARG;
     if (num_groups < 0 || (num_groups > 0 && (!group_offsets || !prefix_lens))) return ART_ERR_INVALID_ARG;

@@ -160,6 +160,10 @@ inline cudaError_t launch_after(void (*kernel)(A...), dim3 grid, dim3 block, siz
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The shape checks of art_decode for the calls around the cache (max_visit and
+// num_probe are not used).
+int check_cache_shape(const art_shape* s);
+
 cudaError_t launch_attend_simt(const AttendParams& p, cudaStream_t st);  // fp32
 cudaError_t launch_attend_tc(const AttendParams& p, cudaStream_t st);    // bf16
 
