@@ -273,7 +273,10 @@ static size_t attend_layout(AttendParams& p, unsigned char* base) {
     return up256(o);
 }
 
-// Cost units (about 0.15 us): what segments of each kind take beside their neighbours.
+// Cost units (about 0.15 us): what segments and key tiles of each kind take beside their
+// neighbours, fitted to the CTAs' timelines. They set the shares only. Tiles alone at one
+// cost: chunks of 1-2k tokens 527 us against 358, 128 sequences behind a document 159
+// against 134, 64 behind a prompt 61 against 52.
 constexpr CostRule kCostBf16 = {13, 7, 35, 11, 50, 13}, kCostF32 = {10, 8, 10, 16, 10, 16};
 
 static void fill_shape(AttendParams& p, const art_shape& s) {

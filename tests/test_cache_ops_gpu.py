@@ -154,7 +154,7 @@ def test_append_bad_device_data():
 
 @pytest.mark.parametrize("dtype,rot,interleaved", [("bf16", 64, False), ("f32", 64, True), ("bf16", 22, False)])
 def test_append_many_tokens(dtype, rot, interleaved):
-    """More than 1024 tokens: two to a CTA, whose tokens belong to several sequences, to none, or to one."""
+    """Many tokens: two to a CTA, whose tokens belong to several sequences, to none, or to one."""
     new = [1, 2, 3, 0, 5, 700, 1, 1, 350, 13]
     append_case(11, dtype, 2, 1, 64, 16, new, np.arange(10) * 7, rot, interleaved, fused=True, pad=(3, 5))
 
