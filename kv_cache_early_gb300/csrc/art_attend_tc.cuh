@@ -24,8 +24,9 @@
 // segment's end.
 //
 // Softmax: p = 2^(s c - m) with c = log2(e) / sqrt(d), s and the sums in fp32; m
-// follows the row's maximum only when that has risen by more than 2^8 (p and l stay
-// far from overflow, and O need not be rescaled for each new maximum). p is rounded
+// follows the row's maximum only when that has risen by far (small segments: by more
+// than 2^8; large ones: when 64 weights add up to more than 2^16): p and l stay far
+// from overflow, and O need not be rescaled for each new maximum. p is rounded
 // to bf16 for the product, as V is bf16 and both operands have one type; its sum is
 // taken before the rounding.
 //
@@ -67,7 +68,7 @@ constexpr int kTcConsumers = 8, kTcThreads = (kTcConsumers + 4) * 32;  // three 
 constexpr int kRegConsumer = 192, kRegHelper = 120;
 static_assert(128 * (2 * kRegConsumer + kRegHelper) <= kTcThreads * 168, "no more than the launch's registers");
 constexpr float kRescale = 8.f;  // small segments: log2 units by which a row's maximum may lead its reference
-constexpr float kMaxSum = 1.0995116e12f;  // 2^40, large segments: the sum of a tile's weights from which it moves
+constexpr float kMaxSum = 65536.f;  // large segments: the sum of 64 weights from which it moves
 
 template <int NS>
 struct alignas(16) TcCtrl {

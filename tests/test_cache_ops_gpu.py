@@ -284,7 +284,7 @@ def steep(pool, up):
 @pytest.mark.parametrize("new", [3, 20, 70])
 @pytest.mark.parametrize("up", [True, False])
 def test_extend_maxima_that_move_far(dtype, hq, hkv, d, new, up):
-    """A row's maximum climbs by far more than 2^40 between and inside key tiles, or is met first and everything
+    """A row's maximum climbs by hundreds of powers of two between and inside key tiles, or is met first and everything
     after it underflows; the rows of a tile do so in opposite directions (the sign of q)."""
     rng = np.random.default_rng(33)
     seq = [new + 400]
