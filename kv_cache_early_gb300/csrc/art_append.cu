@@ -224,15 +224,12 @@ __global__ void __launch_bounds__(kAppendThreads) art_append_kernel(const Append
         int b = p.q_offsets ? b0 : t0 + tid, i = 0, n = 1, state = kStateNone, page = -1, s = 0;
         if (p.q_offsets) {
             while (b < p.B && p.q_offsets[b + 1] <= t0 + tid) ++b;
-            if (b < p.B) {
-                const int lo = p.q_offsets[b];
-                i = t0 + tid - lo;
-                n = p.q_offsets[b + 1] - lo;
-            } else {
-                n = 0;  // behind the last sequence
-            }
+            const int lo = b < p.B ? p.q_offsets[b] : 0, hi = b < p.B ? p.q_offsets[b + 1] : 0;
+            const bool fine = lo >= 0 && hi <= p.T;  // flagged by block 0 where not
+            i = t0 + tid - lo;
+            n = fine ? hi - lo : 0;  // 0 too behind the last sequence
         }
-        if (i >= 0 && i < n) {  // offsets that do not hold the token are flagged by block 0
+        if (i >= 0 && i < n) {
             const int len = p.seq_lens[b];
             s = len - n + i;
             if (len >= n && (long long)len <= (long long)p.max_pages * p.Ps) {

@@ -152,6 +152,38 @@ def test_append_bad_device_data():
         assert K.art_read_device_status(ws) & 128
 
 
+@pytest.mark.parametrize("offsets", [[-3, 2, 5, 9], [0, 2, 5, 12]])
+def test_append_skips_the_sequence_with_bad_offsets(offsets):
+    """Only the sequence whose own two offsets lie outside 0 .. num_tokens appends nothing, its q_out rows stay."""
+    rng = np.random.default_rng(12)
+    dtype, hq, hkv, d, page = "bf16", 4, 2, 64, 16
+    T, off = 9, np.array(offsets, np.int32)
+    pool = Pool(rng, dtype, hkv, d, page, [20, 30, 40], fill=False, poison=False)
+    q, k, v = (rounded(rng.standard_normal((T, h, d)), dtype) for h in (hq, hkv, hkv))
+    inv = np.ones(d // 2, np.float32)
+    shape = K.make_shape(**pool.shape(hq))
+    ws = workspace(64)
+    kc, vc = dev(pool.k, dtype), dev(pool.v, dtype)
+    q_out = torch.full((T, hq, d), SENTINEL, dtype=kc.dtype, device="cuda")
+    K.art_append_kv(dev(q, dtype), dev(k, dtype), dev(v, dtype), dev(pool.table), dev(pool.seq_lens), dev(off),
+                    dev(inv), q_out, kc, vc, shape, ws, rot_dim=d)
+    torch.cuda.synchronize()
+    assert K.art_read_device_status(ws) == 128
+    wrong = 0 if offsets[0] < 0 else 2
+    lo, hi = max(0, offsets[wrong]), min(T, offsets[wrong + 1])
+    kept = [b for b in range(3) if b != wrong]
+    rq, rk, rv = q * np.nan, pool.k, pool.v
+    for b in kept:  # one sequence at a time: the oracle knows no bad offsets
+        one, rk, rv = O.append(q, k, v, off[b:b + 2], None, pool.table[b:b + 1], pool.seq_lens[b:b + 1], inv, d, False,
+                               1.0, rk, rv, pool.num_pages)
+        rq[off[b]:off[b + 1]] = one[off[b]:off[b + 1]]
+    assert np.all(np.abs(host(kc) - rk) <= 8.2 * E24 * 13 + U[dtype] * np.abs(rk))
+    assert np.array_equal(host(vc), rv)
+    got, held = host(q_out), np.r_[0:lo, hi:T]
+    assert np.all(np.abs(got - rq)[held] <= 8.2 * E24 * 13 + U[dtype] * np.abs(rq[held]))
+    assert np.all(got[lo:hi] == SENTINEL)
+
+
 @pytest.mark.parametrize("dtype,rot,interleaved", [("bf16", 64, False), ("f32", 64, True), ("bf16", 22, False)])
 def test_append_many_tokens(dtype, rot, interleaved):
     """Many tokens: two to a CTA, whose tokens belong to several sequences, to none, or to one."""
@@ -784,6 +816,38 @@ def test_two_graphs_share_their_workspaces():
             g.replay()
     torch.cuda.synchronize()
     c.check()
+
+
+def test_captured_behind_a_copy_of_another_stream():
+    """The first kernel of a call follows a memory copy and an event of another stream, in a capture and outside."""
+    c = Chain(68)
+    c.run()
+    torch.cuda.synchronize()
+    rows = c.t["prow"].clone()
+    side = torch.cuda.Stream()
+
+    def joined():
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            c.t["prow"].copy_(rows)
+        K.dense_extend(c.t["pq"], c.t["kc"], c.t["vc"], c.t["table"][:1], c.t["len1"], c.t["off1"], c.t["po"], c.s1,
+                       c.ws[1])
+        torch.cuda.current_stream().wait_stream(side)
+        c.run()
+        c.t["po"].zero_()
+        K.dense_extend(c.t["pq"], c.t["kc"], c.t["vc"], c.t["table"][:1], c.t["len1"], c.t["off1"], c.t["po"], c.s1,
+                       c.ws[1])
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        joined()
+    for run in (g.replay, joined, g.replay):
+        c.t["prow"].fill_(float("nan"))
+        for n in ("pq", "po", "sq", "so", "dd"):
+            c.t[n].fill_(SENTINEL)
+        run()
+        torch.cuda.synchronize()
+        c.check()
 
 
 def test_repeated_calls_give_the_same_bits():
