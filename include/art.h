@@ -308,14 +308,15 @@ typedef struct art_rope {
  *   positions  int32 [num_tokens] or NULL
  *   inv_freq   fp32 [rot_dim / 2] (any scaling of the frequencies is in it)
  *   q_out      [num_tokens][num_q_heads][head_dim]; may be q itself where
- *              q_stride is num_q_heads * head_dim
+ *              q_stride is num_q_heads * head_dim; no other overlap with the inputs
  *   k_cache, v_cache: the pool; only the new tokens' rows are written. Two
  *              tokens of a call must not share a cache row.
  *   workspace  art_append_workspace_bytes(shape) bytes: the status word
  * A sequence with a bad length (below its new tokens, or beyond the table)
  * appends nothing and its q_out rows are zero; a token whose page id lies
  * outside the pool is not appended; tokens of a sequence with bad offsets are
- * skipped. One kernel, nothing else on the stream.
+ * skipped. One kernel, nothing else on the stream. Supported: rows of
+ * (num_q_heads + 2 num_kv_heads) * head_dim up to 2^29.
  */
 size_t art_append_workspace_bytes(const art_shape* shape);
 int art_append_kv(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,

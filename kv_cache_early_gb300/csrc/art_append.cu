@@ -380,6 +380,9 @@ int art_append_kv(const void* q, const void* k, const void* v, int64_t q_stride,
     if ((q && (q_stride < (int64_t)s.num_q_heads * s.head_dim || q_stride % chunk)) || k_stride < kvw ||
         k_stride % chunk || v_stride < kvw || v_stride % chunk)
         return ART_ERR_INVALID_ARG;
+    // in place only row by row: another token's row would be overwritten before it is read
+    if (q && q == q_out && num_tokens > 1 && q_stride != (int64_t)s.num_q_heads * s.head_dim) return ART_ERR_INVALID_ARG;
+    if (2 * ((int64_t)s.num_q_heads + 2 * (int64_t)s.num_kv_heads) * s.head_dim > (1LL << 30)) return ART_ERR_UNSUPPORTED;
     if (workspace_bytes < sizeof(WsHeader)) return ART_ERR_WORKSPACE;
 
     AppendParams p;

@@ -107,6 +107,9 @@ BAD, UNS, WS = K.ART_ERR_INVALID_ARG, K.ART_ERR_UNSUPPORTED, K.ART_ERR_WORKSPACE
     (dict(reserved=1), BAD),
     (dict(T=0x7fffffff), UNS),
     (dict(ws_bytes=63), WS),
+    (dict(q=FAKE, q_out=FAKE, qs=1536), BAD),               # in place, but the rows of q are further apart
+    (dict(shape=good_shape(batch=1, num_q_heads=1 << 22, num_kv_heads=1 << 22), off=0, T=1, qs=1 << 29, ks=1 << 29,
+          vs=1 << 29), UNS),
 ])
 def test_append_refusals(lib, case, expect):
     assert call_append(lib, **case) == expect
