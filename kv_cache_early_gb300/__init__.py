@@ -406,7 +406,7 @@ def dense_extend(q, k_cache, v_cache, block_table, seq_lens, q_offsets, out, sha
     device = _attend_checked(q, k_cache, v_cache, block_table, seq_lens, out, shape, workspace, tokens,
                              q_offsets, shape.batch + 1, None, 0)
     rc = L.dense_extend(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                        seq_lens.data_ptr(), q_offsets.data_ptr(), tokens, 1 if causal else 0, out.data_ptr(),
+                        seq_lens.data_ptr(), _addr(q_offsets), tokens, 1 if causal else 0, out.data_ptr(),
                         ctypes.byref(shape), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, device))
     if check and rc != ART_OK:
         _check(rc)

@@ -873,6 +873,8 @@ def test_binding_refuses_what_the_pointers_would_hide():
         bad[i] = wrong
         with pytest.raises(K.ArtError):
             K.dense_decode_shared(*bad)
+    with pytest.raises(K.ArtError):  # the new tokens' offsets are not optional here
+        K.dense_extend(t["pq"], t["kc"], t["vc"], t["table"][:1], t["len1"], None, t["po"], c.s1, c.ws[1])
     row = t["srow"]
     with pytest.raises(K.ArtError):  # heads not side by side
         K.art_append_kv(row[:, 0:16:2], row[:, 8:10], row[:, 10:12], t["table"], t["len2"], None, t["inv"], t["sq"],
