@@ -22,7 +22,7 @@
 // longer of the two and not for their sum. One more CTA (block 0) checks the device
 // data of the call and stores the status word, so that no memset precedes the
 // kernel; every token's CTA checks what it uses by itself. Measured: prompts of 36727
-// tokens (32/8 heads, d 128, bf16) 137 us, 98 % of the copy rate; a step of 1 or 128
+// tokens (32/8 heads, d 128, bf16) 136 us, 99 % of the copy rate; a step of 1 or 128
 // tokens 2.9 us.
 #include "art_common.cuh"
 
@@ -150,9 +150,10 @@ __device__ __forceinline__ float2 turn_of(int pos, float f) {
 }
 
 // kVec: a row is taken in units of two 16-byte chunks: of a rotated row in pairs
-// (j, j + rot_dim / 2) the chunks c and c + npair for c < npair, then the copied chunks
-// two by two; otherwise neighbours. It needs rot_dim / 2 (interleaved: rot_dim) to be a
-// multiple of a chunk's elements; without it a thread takes an element, or a pair.
+// (j, j + rot_dim / 2) the chunks c and c + npair for c < npair; of what is left, and of
+// other rows, a chunk of the first half and its like of the second. It needs rot_dim / 2
+// (interleaved: rot_dim) to be a multiple of a chunk's elements; without it a thread takes
+// an element, or a pair.
 // kTok: tokens of a CTA.
 template <bool kBF16, int D, bool kVec, int kTok>
 __global__ void __launch_bounds__(kAppendThreads) art_append_kernel(const AppendParams p) {
@@ -187,15 +188,13 @@ __global__ void __launch_bounds__(kAppendThreads) art_append_kernel(const Append
         return static_cast<const char*>(p.v) + (t * p.v_stride + (size_t)(r - nq - p.Hkv) * D) * E::kBytes;
     };
     const int c = kVec ? tid % PER : 0;
-    // the unit's chunks (of a rotated row; the values' rows take neighbours)
+    // the unit's chunks; neighbouring threads take neighbouring chunks, so that each access
+    // of a warp is of whole 32-byte sectors (two neighbours a thread: 7 chunks of 1-4000
+    // tokens, interleaved pairs in half a head, 49 us against 45)
     auto chunks = [&](bool turned, int& ca, int& cb) {
-        if (turned && npair > 0 && c < npair) {
-            ca = c;
-            cb = c + npair;
-        } else {
-            ca = 2 * c;  // past the pairs: 2 npair + 2 (c - npair)
-            cb = 2 * c + 1;
-        }
+        const int n = turned ? npair : 0;
+        ca = c < n ? c : c + n;
+        cb = c < n ? c + n : c + PER;
     };
     uint4 a[PF], b2[PF];
     auto load = [&](int R0) {
