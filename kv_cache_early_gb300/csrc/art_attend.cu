@@ -34,48 +34,54 @@ struct MergeRow {
     __device__ __forceinline__ void add(const AttendParams& p, int n, F at) {
         for (int k0 = 0; k0 < n; k0 += 32) {
             int prow = 0, nrow = 1, r = 0;
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (k0 + lane < n && at(k0 + lane, prow, nrow, r)) ml = __ldcg(&p.part_ml[prow + r]);
-            const bool live = ml.y != 0.f;  // saw a key (or a NaN)
-            float top = live ? ml.x : -INFINITY;
-#pragma unroll
-            for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            const float mn = fmaxf(m, top);
-            const float a = m == -INFINITY ? 0.f : exp2f(m - mn);
-            const float w = live ? exp2f(ml.x - mn) : 0.f;
-            float sum = live ? ml.y * w : 0.f;
-#pragma unroll
-            for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-            l = l * a + sum;
-            o.x *= a;
-            o.y *= a;
-            o.z *= a;
-            o.w *= a;
-            m = mn;
-            unsigned todo = __ballot_sync(0xffffffffu, live);
-            while (todo) {
+            const bool some = k0 + lane < n && at(k0 + lane, prow, nrow, r);
+            const float2 ml = some ? __ldcg(&p.part_ml[prow + r]) : make_float2(-INFINITY, 0.f);
+            unsigned todo = __ballot_sync(0xffffffffu, some), saw = 0;
+            float w = 0.f;
+            bool fresh = true;
+            do {
                 float4 v[4];
-                float f[4];
+                int src[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int src = todo ? __ffs(todo) - 1 : 0;
-                    f[u] = __shfl_sync(0xffffffffu, w, src);
-                    const int pr = __shfl_sync(0xffffffffu, prow, src), nr = __shfl_sync(0xffffffffu, nrow, src);
-                    const int rr = __shfl_sync(0xffffffffu, r, src);
-                    v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (!todo) f[u] = 0.f;
-                    else if (lane < D / 4)
+                for (int u = 0; u < 4; ++u) {  // the first columns come beside the (m, l)
+                    src[u] = todo ? __ffs(todo) - 1 : -1;
+                    const int from = src[u] & 31;
+                    const int pr = __shfl_sync(0xffffffffu, prow, from), nr = __shfl_sync(0xffffffffu, nrow, from);
+                    const int rr = __shfl_sync(0xffffffffu, r, from);
+                    if (todo && lane < D / 4)
                         v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (size_t)pr * D) + (size_t)lane * nr + rr);
                     todo &= todo - 1;
                 }
+                if (fresh) {
+                    fresh = false;
+                    const bool live = ml.y != 0.f;  // saw a key (or a NaN)
+                    saw = __ballot_sync(0xffffffffu, live);
+                    float top = live ? ml.x : -INFINITY;
+#pragma unroll
+                    for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    const float mn = fmaxf(m, top);
+                    const float a = m == -INFINITY ? 0.f : exp2f(m - mn);
+                    w = live ? exp2f(ml.x - mn) : 0.f;
+                    float sum = live ? ml.y * w : 0.f;
+#pragma unroll
+                    for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                    l = l * a + sum;
+                    o.x *= a;
+                    o.y *= a;
+                    o.z *= a;
+                    o.w *= a;
+                    m = mn;
+                }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    o.x += v[u].x * f[u];
-                    o.y += v[u].y * f[u];
-                    o.z += v[u].z * f[u];
-                    o.w += v[u].w * f[u];
+                    const float f = __shfl_sync(0xffffffffu, w, src[u] & 31);
+                    if (src[u] < 0 || !(saw >> src[u] & 1)) continue;
+                    o.x += v[u].x * f;
+                    o.y += v[u].y * f;
+                    o.z += v[u].z * f;
+                    o.w += v[u].w * f;
                 }
-            }
+            } while (todo);
         }
     }
     __device__ __forceinline__ void store(const AttendParams& p, size_t row) {
@@ -107,6 +113,7 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
     const int first = kShared ? min(blockIdx.x * WPB + w, p.B * p.Hq - 1) / p.Hq : 0;
     const int j0 = kShared ? p.group_of[first] : -1, lim0 = kShared ? p.row_lim[first] : 0;
     const int quota = p.info->quota, computed = p.info->ok;
+    const MergeItem it0 = p.merge[kShared ? 0 : min((int)blockIdx.x, p.ctas - 1)];
     __shared__ int s_status;
     if (tid == 0) s_status = 0;
     const int mine = tid < p.ctas ? p.cta_status[tid] : 0;
@@ -168,7 +175,7 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
         // the items that go over a border between shares: a thread takes four columns of a row
         __shared__ int s_prow[kAttendCtas];
         for (int c = blockIdx.x; c < p.ctas; c += gridDim.x) {
-            const MergeItem it = p.merge[c];
+            const MergeItem it = c == (int)blockIdx.x ? it0 : p.merge[c];
             if (it.np == 0 || (slow && seq_bad(p, it.seq, -1, lane))) continue;
             if (tid < it.np) {  // the pieces' first partial rows, -1 where one is empty
                 const int base = item_cost_base(p, it.nrow), per = item_cost_tile(p, it.nrow);
