@@ -21,35 +21,36 @@ __device__ __forceinline__ void put_row4(const AttendParams& p, size_t row, int 
             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
 }
 
-// One row's pieces joined: a lane holds one piece's (m, l), up to 32 at a time, then the
-// pieces' columns are read side by side (no load waits for another).
+// One row's pieces joined: a lane holds one piece's (m, l), up to 16 of each of two items
+// at a time, then the pieces' columns are read side by side (no load waits for another).
 template <bool kBF16, int D>
 struct MergeRow {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     int lane;
-    // at(k, prow, nrow, r): piece k's first partial row, its segment's rows, the row's place
-    // among them; false where it is empty
+    int nr, r;  // this half warp's item: its rows, the row's place among them
+    // n: the item's pieces; at(k, prow): piece k's first partial row, false where it is empty
     template <class F>
     __device__ __forceinline__ void add(const AttendParams& p, int n, F at) {
-        for (int k0 = 0; k0 < n; k0 += 32) {
-            int prow = 0, nrow = 1, r = 0;
-            const bool some = k0 + lane < n && at(k0 + lane, prow, nrow, r);
+        const int most = max(n, __shfl_xor_sync(0xffffffffu, n, 16));
+        for (int k0 = 0; k0 < most; k0 += 16) {
+            int prow = 0;
+            const int k = k0 + (lane & 15);
+            const bool some = k < n && at(k, prow);
             const float2 ml = some ? __ldcg(&p.part_ml[prow + r]) : make_float2(-INFINITY, 0.f);
             unsigned todo = __ballot_sync(0xffffffffu, some), saw = 0;
             float w = 0.f;
             bool fresh = true;
             do {
                 float4 v[4];
-                int src[4];
+                unsigned use = todo;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {  // the first columns come beside the (m, l)
-                    src[u] = todo ? __ffs(todo) - 1 : -1;
-                    const int from = src[u] & 31;
-                    const int pr = __shfl_sync(0xffffffffu, prow, from), nr = __shfl_sync(0xffffffffu, nrow, from);
-                    const int rr = __shfl_sync(0xffffffffu, r, from);
+                    const int from = __ffs(todo) - 1;
+                    const int pr = __shfl_sync(0xffffffffu, prow, from);
+                    const int n1 = __shfl_sync(0xffffffffu, nr, from), r1 = __shfl_sync(0xffffffffu, r, from);
                     if (todo && lane < D / 4)
-                        v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (size_t)pr * D) + (size_t)lane * nr + rr);
+                        v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (size_t)pr * D) + (size_t)lane * n1 + r1);
                     todo &= todo - 1;
                 }
                 if (fresh) {
@@ -74,8 +75,10 @@ struct MergeRow {
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const float f = __shfl_sync(0xffffffffu, w, src[u] & 31);
-                    if (src[u] < 0 || !(saw >> src[u] & 1)) continue;
+                    const float f = __shfl_sync(0xffffffffu, w, __ffs(use) - 1);
+                    const bool skip = !(use & -use & saw);
+                    use &= use - 1;
+                    if (skip) continue;
                     o.x += v[u].x * f;
                     o.y += v[u].y * f;
                     o.z += v[u].z * f;
@@ -104,8 +107,12 @@ static __device__ __noinline__ bool seq_bad(const AttendParams& p, int b, int le
     return __any_sync(0xffffffffu, bad);
 }
 
-template <bool kBF16, int D, bool kShared>
-__global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const AttendParams p) {
+// kMany (dense_decode_shared): more rows than three blocks an SM take at once. Four need 64
+// registers, and then a row's first columns wait for its (m, l): 128 x 32 rows 138 us with
+// three blocks against 134 with four; 64 x 32 rows 50.7 against 52.8, 89 x 28 rows 91.1
+// against 93.5. dense_extend at five blocks: drafts 66.7, encoder 30.5; at three 65.5, 31.3.
+template <bool kBF16, int D, bool kShared, bool kMany>
+__global__ void __launch_bounds__(kMergeBlock, !kShared ? 5 : kMany ? 4 : 3) art_attend_merge_kernel(const AttendParams p) {
     constexpr int WPB = kMergeBlock / 32;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -133,38 +140,22 @@ __global__ void __launch_bounds__(kMergeBlock) art_attend_merge_kernel(const Att
             m.lane = lane;
             const int lead = j >= 0 ? p.offsets[j] : -1;
             if (lim >= 0 && !(slow && seq_bad(p, b, lead, lane))) {
-                // the items that hold the row, of its group and its own: their pieces by the
-                // plan's arithmetic, those of the group first
-                struct Pieces {
-                    int x, end, base, per, tiles, c0, np, prow, nrow, r;
-                } it[2];
-                const EntityPlace q[2] = {p.place[lim > 0 ? j : p.NG + b], p.place[p.NG + b]};
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int R = i == 0 ? (b - lead) * p.G + hg : hg, t = R / p.rt;
-                    Pieces& e = it[i];
-                    e.np = 0;
-                    if (q[i].nrows == 0 || (i == 0 && lim <= 0)) continue;
-                    e.nrow = min(p.rt, q[i].nrows - t * p.rt);
-                    e.tiles = tiles_of(p, q[i].k0, q[i].k1);
-                    e.base = item_cost_base(p, e.nrow);
-                    e.per = item_cost_tile(p, e.nrow);
-                    e.x = q[i].start + g * q[i].hc + t * (item_cost_base(p, p.rt) + item_cost_tile(p, p.rt) * e.tiles);
-                    e.end = e.x + e.base + e.per * e.tiles;
-                    e.c0 = e.x / quota;
-                    e.np = (e.end - 1) / quota - e.c0 + 1;
-                    e.prow = q[i].prow + g * q[i].nrows + t * p.rt;
-                    e.r = R - t * p.rt;
-                }
-                m.add(p, it[0].np + it[1].np, [&](int k, int& prow, int& nrow, int& r) {
-                    const bool own = k >= it[0].np;
-                    const Pieces e = own ? it[1] : it[0];
-                    const int c = e.c0 + (own ? k - it[0].np : k);
-                    const int a = max(c * quota, e.x), y = min((c + 1) * quota, e.end);
-                    prow = e.prow + c * p.rt;
-                    nrow = e.nrow;
-                    r = e.r;
-                    return tiles_before(y - e.x, e.base, e.per, e.tiles) > tiles_before(a - e.x, e.base, e.per, e.tiles);
+                // the items that hold the row, of its group (lanes 0 to 15) and its own: their
+                // pieces by the plan's arithmetic
+                const bool own = lane >= 16;
+                const EntityPlace q = p.place[!own && lim > 0 ? j : p.NG + b];
+                const int R = own ? hg : (b - lead) * p.G + hg, t = R / p.rt;
+                const int nrow = min(p.rt, q.nrows - t * p.rt), tiles = tiles_of(p, q.k0, q.k1);
+                const int base = item_cost_base(p, nrow), per = item_cost_tile(p, nrow);
+                const int x = q.start + g * q.hc + t * (item_cost_base(p, p.rt) + item_cost_tile(p, p.rt) * tiles);
+                const int end = x + base + per * tiles, c0 = x / quota;
+                const int np = q.nrows != 0 && (own || lim > 0) ? (end - 1) / quota - c0 + 1 : 0;
+                m.nr = nrow;
+                m.r = R - t * p.rt;
+                m.add(p, np, [&](int k, int& prow) {
+                    const int c = c0 + k, a = max(c * quota, x), y = min((c + 1) * quota, end);
+                    prow = q.prow + g * q.nrows + t * p.rt + c * p.rt;
+                    return tiles_before(y - x, base, per, tiles) > tiles_before(a - x, base, per, tiles);
                 });
             }
             m.store(p, row);
@@ -329,9 +320,11 @@ static int attend_run(AttendParams& p, const art_shape& s, void* workspace, size
     // the merge kernel's launch overlaps the main kernel's end
     const long long blocks = p.shared ? ((long long)p.B * p.Hq + kMergeBlock / 32 - 1) / (kMergeBlock / 32) : p.ctas;
     const dim3 grid((unsigned)(blocks < 8LL * p.ctas ? blocks : 8LL * p.ctas), p.shared ? 1 : p.rt / 16);
-#define ART_MERGE(BF, DD)                                                                                    \
-    e = p.shared ? launch_after(art_attend_merge_kernel<BF, DD, true>, grid, dim3(kMergeBlock), 0, st, p)   \
-                 : launch_after(art_attend_merge_kernel<BF, DD, false>, grid, dim3(kMergeBlock), 0, st, p)
+    const bool many = blocks > 3LL * p.ctas;
+#define ART_MERGE(BF, DD)                                                                                              \
+    e = !p.shared ? launch_after(art_attend_merge_kernel<BF, DD, false, false>, grid, dim3(kMergeBlock), 0, st, p)    \
+        : many    ? launch_after(art_attend_merge_kernel<BF, DD, true, true>, grid, dim3(kMergeBlock), 0, st, p)      \
+                  : launch_after(art_attend_merge_kernel<BF, DD, true, false>, grid, dim3(kMergeBlock), 0, st, p)
     if (bf && p.D == 128) ART_MERGE(true, 128);
     else if (bf) ART_MERGE(true, 64);
     else if (p.D == 128) ART_MERGE(false, 128);

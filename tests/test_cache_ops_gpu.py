@@ -591,6 +591,14 @@ def test_shared_long_prefix_split():
     shared_case(48, "f32", 2, 2, 64, 64, [(5003, [1, 20])], [])
 
 
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 32, 4, 64), ("f32", 32, 8, 64), ("bf16", 28, 4, 128)])
+def test_shared_many_rows(dtype, hq, hkv, d):
+    """More rows than one wave of the merge kernel's blocks, of prefixes cut into many pieces and of short ones."""
+    rng = np.random.default_rng(47)
+    own = lambda n: [int(x) for x in rng.integers(1, 20, n)]
+    shared_case(47, dtype, hq, hkv, d, 16, [(2500, own(90)), (33, own(40)), (0, own(2))], own(8))
+
+
 def test_shared_many_sequences_and_groups():
     """More groups and sequences than the plan takes in one round."""
     groups = [(10 + j % 60, [1 + (j + i) % 5 for i in range(j % 4)]) for j in range(300)]
