@@ -693,12 +693,16 @@ struct TcConsumer {
 #pragma unroll
                         for (int k = 0; k < 64; ++k)
                             if (h + k < lo || h + k >= hi) s[k] = -INFINITY;
+                        if (hi <= h && m == -INFINITY) m = 0.f;  // no key in this stream: any reference will do
                     }
                     // Steady state: no maximum is formed. Weights and their sum are taken against the
-                    // row's reference m; where none is set yet, or the sum passes kMaxSum (or is not a
-                    // number), m moves to these columns' maximum and they are done once more.
+                    // row's reference m. A row that has none yet takes these columns' maximum beforehand
+                    // (again 1); where a sum passes kMaxSum (or is not a number), m moves to it and the
+                    // weights are formed once more (again 2). The sums are looked at after the first pass
+                    // of either kind: a row without a reference must not hold its neighbours'. One
+                    // correction is enough, what it moves has a sum of 64 at most.
                     float rowsum = m == -INFINITY ? INFINITY : 0.f;
-                    for (bool again = __any_sync(0xffffffffu, m == -INFINITY);;) {
+                    for (int again = __any_sync(0xffffffffu, m == -INFINITY);;) {
                         if (again) {
                             const float top = row_max<64>(s) * p.scale_log2;
                             if (!(rowsum <= kMaxSum) && top > m) {
@@ -730,9 +734,12 @@ struct TcConsumer {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) up2(sum[i], a[2 * i], a[2 * i + 1]);
                         rowsum = ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
-                        if (again || !__any_sync(0xffffffffu, !(rowsum <= kMaxSum))) break;
+                        if (again == 2 || !__any_sync(0xffffffffu, !(rowsum <= kMaxSum))) break;
+                        // a row that is not a number stays so: it asks for this once, and has a reference then
+                        if (!__any_sync(0xffffffffu, !(rowsum <= kMaxSum) && l == l)) break;
+                        if (rowsum != rowsum && m == -INFINITY) m = 0.f;
                         tc_wait_st();
-                        again = true;
+                        again = 2;
                     }
                     l += rowsum;
                     if (__any_sync(0xffffffffu, fO != 1.f)) {

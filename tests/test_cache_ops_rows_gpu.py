@@ -1,0 +1,132 @@
+"""GPU tests that the rows of a call do not disturb each other: rows whose scores
+climb by hundreds of powers of two beside rows that see no key of a tile, that see
+none at all, or whose queries are not numbers. fp64 oracle: oracle/cache_ops.py;
+tolerances: cache_ops_harness.py."""
+import numpy as np
+import pytest
+
+from cache_ops_harness import Pool, rounded
+from oracle import cache_ops as O
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import kv_cache_early_gb300 as K  # noqa: E402
+from test_cache_ops_gpu import SENTINEL, attend_close, dev, host, workspace  # noqa: E402
+
+
+def climbing_pool(rng, dtype, hkv, d, lens, first, up):
+    """A pool whose sequence b holds tokens first[b] .. lens[b] - 1 (elsewhere NaN). The keys lie along one direction:
+    their scores with signed_queries climb (or fall) by hundreds of powers of two in steps of 37 keys, over and over,
+    so that a segment of several key tiles meets a rise wherever it starts."""
+    pool = Pool(rng, dtype, hkv, d, 16, lens, fill=False)
+    u = np.zeros(d, np.float32)
+    u[::2] = 1.0
+    for b, n in enumerate(lens):
+        t = np.arange(first[b], n)
+        at = pool.table[b, t // 16], slice(None), t % 16
+        level = (t if up else n - 1 - t) // 37 % 12 - 6
+        pool.k[at] = (level[:, None] * u)[:, None]
+        pool.v[at] = rounded(rng.standard_normal((len(t), hkv, d)), dtype)
+    return pool
+
+
+def signed_queries(n, hq, d):
+    """Queries along the direction of climbing_pool's keys: rising and falling scores, of several sizes."""
+    q = np.zeros((n, hq, d), np.float32)
+    q[..., ::2] = 8.0
+    q[1::2] *= -1.0
+    q[:, ::3] *= 0.125
+    return q
+
+
+def shared_climb(dtype, hq, hkv, d, prefix, lens, up, heads, nan_rows=()):
+    """One group behind a prefix whose scores climb; lens: whole lengths of its members (the first leads); heads:
+    the query heads that are checked; nan_rows: (member, head) of queries that are NaN."""
+    rng = np.random.default_rng(70)
+    pool = climbing_pool(rng, dtype, hkv, d, [max(lens[0], prefix)] + lens[1:], [0] + [prefix] * (len(lens) - 1), up)
+    pool.seq_lens = np.asarray(lens, np.int32)
+    for b in range(1, len(lens)):
+        pool.table[b, :prefix // 16] = -777  # read through the leader's row
+        if lens[b] <= prefix:
+            pool.table[b] = -777
+    q = signed_queries(len(lens), hq, d)
+    for b, h in nan_rows:
+        q[b, h] = np.nan
+    shape = K.make_shape(**pool.shape(hq))
+    ws = workspace(K.dense_decode_shared_workspace_bytes(shape, 1))
+    tq = dev(q, dtype)
+    out = torch.full_like(tq, SENTINEL)
+    K.dense_decode_shared(tq, dev(pool.k, dtype), dev(pool.v, dtype), dev(pool.table), dev(pool.seq_lens),
+                          dev(np.array([0, len(lens)], np.int32)), dev(np.array([prefix], np.int32)), out, shape, ws)
+    torch.cuda.synchronize()
+    assert K.art_read_device_status(ws) == 0
+    got = host(out)
+    lead = {g: [O.gather(c, pool.table[0], max(lens[0], prefix), g) for c in (pool.k, pool.v)]
+            for g in {h // (hq // hkv) for h in heads}}
+
+    def rows_of(b, h):
+        if (b, h) in nan_rows or h not in heads:
+            return None
+        g, p, rows = h // (hq // hkv), min(prefix, lens[b]), []
+        for c, shared in zip((pool.k, pool.v), lead[g]):
+            own = [c[pool.table[b, t // 16], g, t % 16] for t in range(p, lens[b])]
+            rows.append(np.concatenate([shared[:p], np.reshape(own, (-1, d)).astype(np.float64)]))
+        return rows
+
+    attend_close(got, q, rows_of, dtype)
+    for b, h in nan_rows:  # no key seen: zero, whatever the query holds
+        assert np.isnan(got[b, h]).all() if lens[b] > 0 else np.all(got[b, h] == 0), (b, h)
+
+
+# Enough keys and KV heads that a CTA's share of the prefix is several key tiles.
+LONG = 6000
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 32, 8, 128), ("bf16", 16, 8, 64), ("bf16", 28, 4, 128), ("f32", 16, 4, 64)])
+@pytest.mark.parametrize("members", [6, 30, 70])
+def test_shared_short_member_beside_climbing_scores(dtype, hq, hkv, d, members):
+    """A member that sees the first 40 keys of the prefix (nothing of a tile's second half) among members whose
+    scores climb over all of it: rows of one tile, and of more."""
+    lens = [LONG + 1 + 3 * i % 50 for i in range(members)]
+    lens[2] = 40
+    lens[members - 1] = 1
+    shared_climb(dtype, hq, hkv, d, LONG, lens, members != 30, (0, 1, hq - 1))
+
+
+@pytest.mark.parametrize("members", [3, 6, 30, 70])
+@pytest.mark.parametrize("length", [0, LONG + 30])
+def test_shared_nan_query_beside_climbing_scores(members, length):
+    """A query that is NaN, of a padded member without keys and of one with keys."""
+    lens = [LONG + 1 + 3 * i % 50 for i in range(members)]
+    lens[1] = length
+    shared_climb("bf16", 32, 8, 128, LONG, lens, True, (0, 1, 30, 31),
+                 nan_rows=[(1, h) for h in range(0, 32, 3)])
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 32, 4, 128), ("bf16", 8, 4, 64), ("f32", 8, 4, 64)])
+@pytest.mark.parametrize("new", [3, 20, 70])
+@pytest.mark.parametrize("up", [True, False])
+def test_extend_nan_query_beside_climbing_scores(dtype, hq, hkv, d, new, up):
+    rng = np.random.default_rng(71)
+    n = new + LONG
+    pool = climbing_pool(rng, dtype, hkv, d, [n], [0], up)
+    q = signed_queries(new, hq, d)
+    bad = [(t, h) for t in (1, new // 2, new - 1) for h in range(t % 2, hq, 3)]
+    for t, h in bad:
+        q[t, h] = np.nan
+    shape = K.make_shape(**pool.shape(hq))
+    ws = workspace(K.dense_extend_workspace_bytes(shape, new))
+    tq = dev(q, dtype)
+    out = torch.full_like(tq, SENTINEL)
+    K.dense_extend(tq, dev(pool.k, dtype), dev(pool.v, dtype), dev(pool.table), dev(pool.seq_lens),
+                   dev(np.array([0, new], np.int32)), out, shape, ws)
+    torch.cuda.synchronize()
+    assert K.art_read_device_status(ws) == 0
+    got = host(out)
+    group, heads = hq // hkv, (0, 1, hq - 2, hq - 1)
+    rows = {g: [O.gather(c, pool.table[0], n, g) for c in (pool.k, pool.v)] for g in {h // group for h in heads}}
+    attend_close(got, q, lambda t, h: [c[:LONG + 1 + t] for c in rows[h // group]]
+                 if h in heads and (t, h) not in bad else None, dtype)
+    for t, h in bad:
+        assert np.isnan(got[t, h]).all(), (t, h)
