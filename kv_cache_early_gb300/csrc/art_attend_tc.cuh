@@ -1,7 +1,7 @@
 // art_attend_tc.cuh -- the segments of art_attend.cuh for bf16, on the tensor cores.
 //
-// One CTA per SM, 12 warps, and one shared-memory ring that K and V tiles of 128
-// keys stream through without a pause from segment to segment:
+// One CTA per SM, 12 warps (168 registers a thread at most), and one shared-memory ring
+// that K and V tiles of 128 keys stream through without a pause from segment to segment:
 //
 //   producer warp   resolves the tiles' pages (the ids of 32 pages at a time, one
 //                   batch ahead) and copies each page by one tensor copy
@@ -63,10 +63,6 @@ struct TcCfg {
 };
 
 constexpr int kTcConsumers = 8, kTcThreads = (kTcConsumers + 4) * 32;  // three warpgroups
-// Registers: 12 warps at 168 at launch (64512); then the two consumer warpgroups take
-// 192 each and the third keeps 120: 64512.
-constexpr int kRegConsumer = 192, kRegHelper = 120;
-static_assert(128 * (2 * kRegConsumer + kRegHelper) <= kTcThreads * 168, "no more than the launch's registers");
 constexpr float kRescale = 8.f;  // small segments: log2 units by which a row's maximum may lead its reference
 constexpr float kMaxSum = 65536.f;  // large segments: the sum of 64 weights from which it moves
 
@@ -1050,12 +1046,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (s0 >= s1) {
         // nothing to do
     } else if (w >= kTcConsumers) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegHelper));
         if (w == kTcConsumers) tc_producer<D>(p, smem, c, &tk, &tv, s0, s1);
         else if (w == kTcConsumers + 1) tc_issuer<D>(p, smem, c, tmem, s0, s1);
         else if (w == kTcConsumers + 2) tc_edges<D>(p, gen, c, s0, s1);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegConsumer));
         if (!p.stall || wait_tc(&c->stall, 0u, &c->abort, p)) {
             TcConsumer<D> k{p, c, smem, gen, tmem, w, lane};
             k.run(s0, s1);
