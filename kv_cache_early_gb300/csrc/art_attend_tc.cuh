@@ -775,9 +775,13 @@ struct TcConsumer {
                 tc_fence_before();
             }
         } else {
-            // the two halves' results of a row meet; each stream writes half of the columns
+            // the two halves' results of a row meet; each stream writes half of the columns. What a
+            // warp has seen of its own stream's products must hold for the other stream's warps, which
+            // read this O too: the fences on both sides of the barrier.
             (x ? c->ml2 : c->ml)[quad * 32 + lane] = make_float2(m, l);
+            tc_fence_before();
             if (!sync()) return false;
+            tc_fence_after();
             if (live) {
                 const float2 e = c->ml[quad * 32 + lane], d = c->ml2[quad * 32 + lane];
                 const bool he = e.y != 0.f, hd = d.y != 0.f;  // saw a key; otherwise O may hold anything

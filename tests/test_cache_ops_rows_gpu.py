@@ -130,3 +130,29 @@ def test_extend_nan_query_beside_climbing_scores(dtype, hq, hkv, d, new, up):
                  if h in heads and (t, h) not in bad else None, dtype)
     for t, h in bad:
         assert np.isnan(got[t, h]).all(), (t, h)
+
+
+@pytest.mark.parametrize("new,hq,hkv,d", [(5, 32, 8, 128), (32, 8, 2, 64), (16, 8, 1, 128)])
+def test_one_row_tile_joins_both_halves_every_time(new, hq, hkv, d):
+    """17 to 128 rows: the two halves of every key tile are summed apart and each is read by the warps of both.
+    Many calls of many items (whole ones and cut ones), the same bits every time, and right."""
+    rng = np.random.default_rng(72)
+    seq = [200 + 64 * (b % 5) + 37 * b for b in range(24)]
+    pool = Pool(rng, "bf16", hkv, d, 16, seq)
+    off = np.arange(len(seq) + 1, dtype=np.int32) * new
+    q = rounded(rng.standard_normal((int(off[-1]), hq, d)), "bf16")
+    shape = K.make_shape(**pool.shape(hq))
+    ws = workspace(K.dense_extend_workspace_bytes(shape, int(off[-1])))
+    tq = dev(q, "bf16")
+    args = dev(pool.k, "bf16"), dev(pool.v, "bf16"), dev(pool.table), dev(pool.seq_lens), dev(off)
+    outs = torch.full((40,) + tuple(tq.shape), SENTINEL, dtype=tq.dtype, device="cuda")
+    for o in outs:
+        K.dense_extend(tq, *args, o, shape, ws)
+    torch.cuda.synchronize()
+    assert K.art_read_device_status(ws) == 0
+    assert bool((outs == outs[:1]).all())
+    got, heads = host(outs[0]), (0, hq - 1)
+    rows = {(b, g): [O.gather(c, pool.table[b], seq[b], g) for c in (pool.k, pool.v)]
+            for b in range(0, len(seq), 5) for g in {h // (hq // hkv) for h in heads}}
+    attend_close(got, q, lambda t, h: [c[:seq[t // new] - new + t % new + 1] for c in rows[t // new, h // (hq // hkv)]]
+                 if h in heads and t // new % 5 == 0 else None, "bf16")
