@@ -281,8 +281,10 @@ int art_select_blocks(const void* q, const void* k_cache, const int32_t* block_t
  * q_offsets int32 [batch + 1]: the new tokens of sequence b are rows
  * q_offsets[b] .. q_offsets[b+1]-1 of q (and k, v, out), and seq_lens[b] counts
  * them already: they are the last ones of the sequence. 0 <= q_offsets[0] <=
- * ... <= q_offsets[batch] <= num_tokens. Rows that no sequence holds are
- * neither read nor written.
+ * ... <= q_offsets[batch] <= num_tokens. q, k, v and the outputs have
+ * num_tokens rows. Rows that no sequence holds (a padded batch) may hold
+ * anything and are never written; art_append_kv may read them (and drops what
+ * it has read), dense_extend does not.
  */
 
 /* The position rotation of art_append_kv. */

@@ -210,6 +210,8 @@ __global__ void __launch_bounds__(kAppendThreads) art_append_kernel(const Append
             b2[k] = src[cb];
         }
     };
+    // before it is known which sequence holds the tokens, or whether any does: behind the loads of
+    // the first and the last offset, prompts took 139.6 us against 136.2, chunks 46.4 against 44.8
     if constexpr (kVec) load(tid / PER);
 
     // the tokens' sequences, places and pages

@@ -5,7 +5,7 @@ tolerances: cache_ops_harness.py."""
 import numpy as np
 import pytest
 
-from cache_ops_harness import Pool, rounded
+from cache_ops_harness import E24, U, Pool, rounded
 from oracle import cache_ops as O
 
 torch = pytest.importorskip("torch")
@@ -156,3 +156,35 @@ def test_one_row_tile_joins_both_halves_every_time(new, hq, hkv, d):
             for b in range(0, len(seq), 5) for g in {h // (hq // hkv) for h in heads}}
     attend_close(got, q, lambda t, h: [c[:seq[t // new] - new + t % new + 1] for c in rows[t // new, h // (hq // hkv)]]
                  if h in heads and t // new % 5 == 0 else None, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rot", [64, 22])
+@pytest.mark.parametrize("new", [[1, 2, 0, 3], [301, 1, 499]])
+def test_append_rows_of_no_sequence_may_hold_anything(dtype, rot, new):
+    """A batch padded in front and behind with rows that are no numbers: nothing of them is kept, their rows of
+    q_out stay as they were. (Vector and scalar form; one token a CTA and two.)"""
+    rng = np.random.default_rng(73)
+    hq, hkv, d, page = 4, 2, 64, 16
+    pool = Pool(rng, dtype, hkv, d, page, [n + 7 for n in new], fill=False)
+    off = (np.concatenate([[0], np.cumsum(new)]) + 5).astype(np.int32)
+    T = int(off[-1]) + 3
+    q, k, v = (rounded(rng.standard_normal((T, h, d)), dtype) for h in (hq, hkv, hkv))
+    for x in (q, k, v):
+        x[:5], x[off[-1]:] = np.nan, np.inf
+    inv = (10000.0 ** (-np.arange(0, rot, 2) / rot)).astype(np.float32)
+    shape = K.make_shape(**pool.shape(hq))
+    ws = workspace(K.art_append_workspace_bytes(shape))
+    kc, vc = dev(pool.k, dtype), dev(pool.v, dtype)
+    q_out = torch.full((T, hq, d), SENTINEL, dtype=kc.dtype, device="cuda")
+    K.art_append_kv(dev(q, dtype), dev(k, dtype), dev(v, dtype), dev(pool.table), dev(pool.seq_lens), dev(off),
+                    dev(inv), q_out, kc, vc, shape, ws, rot_dim=rot)
+    torch.cuda.synchronize()
+    assert K.art_read_device_status(ws) == 0
+    rq, rk, rv = O.append(q, k, v, off, None, pool.table, pool.seq_lens, inv, rot, False, 1.0, pool.k, pool.v,
+                          pool.num_pages)
+    for got, ref in ((host(kc), rk), (host(vc), rv), (host(q_out)[5:off[-1]], rq[5:off[-1]])):
+        held = ~np.isnan(ref)
+        assert np.array_equal(np.isnan(got), ~held)
+        assert np.all(np.abs(got - ref)[held] <= 8.2 * E24 * 13 + U[dtype] * np.abs(ref[held]))
+    assert np.all(host(q_out)[:5] == SENTINEL) and np.all(host(q_out)[off[-1]:] == SENTINEL)
