@@ -299,8 +299,10 @@ typedef struct art_rope {
  * Appends keys and values to the paged cache and rotates keys and queries to
  * their positions. For new token i (of n) of sequence b, with cache place
  * s = seq_len - n + i and position pos = positions[t], or s where positions is
- * NULL: angle_j = pos * inv_freq[j] (formed in 64 bits), and every pair (x, y)
- * of a query or key head becomes scale * (x cos - y sin, y cos + x sin).
+ * NULL: angle_j = pos * inv_freq[j], and every pair (x, y) of a query or key
+ * head becomes scale * (x cos - y sin, y cos + x sin). The angle is formed and
+ * reduced to a turn with its rounding errors kept (within 2e-14) where pos and
+ * the product are below 2^24 in magnitude, and in 64 bits beyond.
  *   q, k, v    rows of num_q_heads (num_kv_heads) heads of head_dim; token t
  *              starts q_stride (k_stride, v_stride) elements after token t - 1,
  *              so that they may be slices of one projection's rows. Strides are

@@ -188,3 +188,29 @@ def test_append_rows_of_no_sequence_may_hold_anything(dtype, rot, new):
         assert np.array_equal(np.isnan(got), ~held)
         assert np.all(np.abs(got - ref)[held] <= 8.2 * E24 * 13 + U[dtype] * np.abs(ref[held]))
     assert np.all(host(q_out)[:5] == SENTINEL) and np.all(host(q_out)[off[-1]:] == SENTINEL)
+
+
+def test_append_angles_of_both_reductions():
+    """Positions and products on both sides of 2^24, negative ones too, fp32 results: beyond 2^24 the 64-bit
+    product, the turns and 2 pi are each off by 2^-53 of 2^27 at most, 3 2^-26 radians in all."""
+    rng = np.random.default_rng(74)
+    d, T = 64, 24
+    pos = np.array([0, 1, -1, 5, -4097, 99991, (1 << 20) + 1, -(1 << 20) - 3, (1 << 22) - 1, 3 - (1 << 22), 1 << 23,
+                    8388607, (1 << 24) - 1, 1 - (1 << 24), 1 << 24, -(1 << 24), (1 << 24) + 1, (1 << 24) + 7,
+                    -(1 << 24) - 5, 11863283, 2670176, 2670177, 3, 4], np.int32)
+    inv = (10000.0 ** (-np.arange(0, d, 2) / d)).astype(np.float32)
+    inv[1], inv[2], inv[3] = 0.0, 1.0, np.float32(2.0 * np.pi)  # 2 pi: whole turns, products past 2^24 below pos 2^24
+    pool = Pool(rng, "f32", 1, d, 16, [T], fill=False)
+    k, v = (rounded(rng.standard_normal((T, 1, d)), "f32") for _ in range(2))
+    shape = K.make_shape(**pool.shape(1))
+    ws = workspace(K.art_append_workspace_bytes(shape))
+    kc, vc = dev(pool.k, "f32"), dev(pool.v, "f32")
+    K.art_append_kv(None, dev(k, "f32"), dev(v, "f32"), dev(pool.table), dev(pool.seq_lens),
+                    dev(np.array([0, T], np.int32)), dev(inv), None, kc, vc, shape, ws, rot_dim=d, positions=dev(pos))
+    torch.cuda.synchronize()
+    assert K.art_read_device_status(ws) == 0
+    _, rk, _ = O.append(np.zeros((T, 1, d)), k, v, [0, T], pos, pool.table, [T], inv, d, False, 1.0, pool.k, pool.v,
+                        pool.num_pages)
+    got, held = host(kc), ~np.isnan(rk)
+    tol = (8.2 * E24 + 3 * 2.0 ** -26) * 2 * np.abs(k).max() + U["f32"] * np.abs(rk[held])
+    assert np.all(np.abs(got[held] - rk[held]) <= tol), np.abs(got[held] - rk[held]).max()
