@@ -12,7 +12,6 @@ importing works without it, but the first call raises if it is missing.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 import threading
 
@@ -233,7 +232,8 @@ def art_select_blocks(q, k_cache, block_table, seq_lens, top_frac, keep_last, vi
     return rc
 
 
-# The wrappers below check their tensors, since the C ABI takes bare pointers. A decode
+# The wrappers below check their tensors, since the C ABI takes bare pointers: dtype, device
+# and the whole shape, as many elements in another order are other data. A decode
 # step calls them once a layer, so the checks are one condition of attribute reads, and
 # only a failed one goes through the tensors again to say what is wrong.
 _torch = None
@@ -270,7 +270,7 @@ def _refuse(device, want, data, ints):
                 raise ArtError(f"{name} is {t.dtype}, not {dt}")
             if t.device != here:
                 raise ArtError(f"{name} is on {t.device}, not on {here}")
-            if sizes is not None and t.numel() != math.prod(sizes):
+            if sizes is not None and t.shape != sizes:
                 raise ArtError(f"{name} is {tuple(t.shape)}, not {tuple(sizes)}")
             if not t.is_contiguous():
                 raise ArtError(f"{name} is not contiguous")
@@ -307,8 +307,7 @@ def art_append_kv(q, k, v, block_table, seq_lens, q_offsets, inv_freq, q_out, k_
     batch, hq, hkv, d = shape.batch, shape.num_q_heads, shape.num_kv_heads, shape.head_dim
     device = _device_of(k_cache)
     tokens = k.shape[0]
-    pages, ps = shape.num_pages_total, shape.page_size
-    pool, pool_n = (pages, hkv, ps, d), pages * hkv * ps * d
+    pool = (shape.num_pages_total, hkv, shape.page_size, d)
     # a lone row's stride is never used: any whole one
     many = tokens > 1
     qs = 0
@@ -325,20 +324,20 @@ def art_append_kv(q, k, v, block_table, seq_lens, q_offsets, inv_freq, q_out, k_
             k.get_device() == device and v.get_device() == device and
             (tokens == 0 or (sk[2] == 1 and sv[2] == 1 and (hkv == 1 or (sk[1] == d and sv[1] == d)))) and
             torch.cuda.current_device() == device and
-            k_cache.dtype is dt and k_cache.numel() == pool_n and k_cache.is_contiguous() and
-            v_cache.dtype is dt and v_cache.numel() == pool_n and v_cache.is_contiguous() and
+            k_cache.dtype is dt and k_cache.shape == pool and k_cache.is_contiguous() and
+            v_cache.dtype is dt and v_cache.shape == pool and v_cache.is_contiguous() and
             v_cache.get_device() == device and
-            (q_out is None or (q_out.dtype is dt and q_out.numel() == tokens * hq * d and q_out.is_contiguous() and
+            (q_out is None or (q_out.dtype is dt and q_out.shape == (tokens, hq, d) and q_out.is_contiguous() and
                                q_out.get_device() == device)) and
-            block_table.dtype is i32 and block_table.numel() == batch * shape.max_pages_per_seq and
+            block_table.dtype is i32 and block_table.shape == (batch, shape.max_pages_per_seq) and
             block_table.is_contiguous() and block_table.get_device() == device and
-            seq_lens.dtype is i32 and seq_lens.numel() == batch and seq_lens.is_contiguous() and
+            seq_lens.dtype is i32 and seq_lens.shape == (batch,) and seq_lens.is_contiguous() and
             seq_lens.get_device() == device and
-            (q_offsets is None or (q_offsets.dtype is i32 and q_offsets.numel() == batch + 1 and
+            (q_offsets is None or (q_offsets.dtype is i32 and q_offsets.shape == (batch + 1,) and
                                    q_offsets.is_contiguous() and q_offsets.get_device() == device)) and
-            (positions is None or (positions.dtype is i32 and positions.numel() == tokens and
+            (positions is None or (positions.dtype is i32 and positions.shape == (tokens,) and
                                    positions.is_contiguous() and positions.get_device() == device)) and
-            (inv_freq is None or (inv_freq.dtype is torch.float32 and inv_freq.numel() == rot_dim // 2 and
+            (inv_freq is None or (inv_freq.dtype is torch.float32 and inv_freq.shape == (rot_dim // 2,) and
                                   inv_freq.get_device() == device and inv_freq.is_contiguous())) and
             workspace.get_device() == device and workspace.is_contiguous()):
         _refuse(device, dt, (("k_cache", k_cache, pool), ("v_cache", v_cache, pool), ("q_out", q_out, (tokens, hq, d))),
@@ -370,21 +369,20 @@ def _attend_checked(q, k_cache, v_cache, block_table, seq_lens, out, shape, work
     i32, dt = torch.int32, torch.bfloat16 if shape.dtype == ART_DTYPE_BF16 else torch.float32
     batch, d = shape.batch, shape.head_dim
     device = _device_of(k_cache)
-    pages, hkv, ps, hq = shape.num_pages_total, shape.num_kv_heads, shape.page_size, shape.num_q_heads
-    pool, pool_n = (pages, hkv, ps, d), pages * hkv * ps * d
-    rows, rows_n = (tokens, hq, d), tokens * hq * d
+    pool = (shape.num_pages_total, shape.num_kv_heads, shape.page_size, d)
+    rows = (tokens, shape.num_q_heads, d)
     if not (torch.cuda.current_device() == device and
-            q.dtype is dt and q.numel() == rows_n and q.is_contiguous() and q.get_device() == device and
-            out.dtype is dt and out.numel() == rows_n and out.is_contiguous() and out.get_device() == device and
-            k_cache.dtype is dt and k_cache.numel() == pool_n and k_cache.is_contiguous() and
-            v_cache.dtype is dt and v_cache.numel() == pool_n and v_cache.is_contiguous() and
+            q.dtype is dt and q.shape == rows and q.is_contiguous() and q.get_device() == device and
+            out.dtype is dt and out.shape == rows and out.is_contiguous() and out.get_device() == device and
+            k_cache.dtype is dt and k_cache.shape == pool and k_cache.is_contiguous() and
+            v_cache.dtype is dt and v_cache.shape == pool and v_cache.is_contiguous() and
             v_cache.get_device() == device and
-            block_table.dtype is i32 and block_table.numel() == batch * shape.max_pages_per_seq and
+            block_table.dtype is i32 and block_table.shape == (batch, shape.max_pages_per_seq) and
             block_table.is_contiguous() and block_table.get_device() == device and
-            seq_lens.dtype is i32 and seq_lens.numel() == batch and seq_lens.is_contiguous() and
+            seq_lens.dtype is i32 and seq_lens.shape == (batch,) and seq_lens.is_contiguous() and
             seq_lens.get_device() == device and
-            (a is None or (a.dtype is i32 and a.numel() == a_n and a.is_contiguous() and a.get_device() == device)) and
-            (b is None or (b.dtype is i32 and b.numel() == b_n and b.is_contiguous() and b.get_device() == device)) and
+            (a is None or (a.dtype is i32 and a.shape == (a_n,) and a.is_contiguous() and a.get_device() == device)) and
+            (b is None or (b.dtype is i32 and b.shape == (b_n,) and b.is_contiguous() and b.get_device() == device)) and
             workspace.get_device() == device and workspace.is_contiguous()):
         _refuse(device, dt, (("q", q, rows), ("k_cache", k_cache, pool), ("v_cache", v_cache, pool), ("out", out, rows)),
                 (("block_table", block_table, (batch, shape.max_pages_per_seq)), ("seq_lens", seq_lens, (batch,)),

@@ -1,6 +1,6 @@
 """GPU tests that the rows of a call do not disturb each other: rows whose scores
 climb by hundreds of powers of two beside rows that see no key of a tile, that see
-none at all, or whose queries are not numbers. fp64 oracle: oracle/cache_ops.py;
+none at all, or whose queries are not numbers; and of refused shapes. fp64 oracle: oracle/cache_ops.py;
 tolerances: cache_ops_harness.py."""
 import numpy as np
 import pytest
@@ -12,7 +12,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import kv_cache_early_gb300 as K  # noqa: E402
-from test_cache_ops_gpu import SENTINEL, attend_close, dev, host, workspace  # noqa: E402
+from test_cache_ops_gpu import SENTINEL, Chain, attend_close, dev, host, workspace  # noqa: E402
 
 
 def climbing_pool(rng, dtype, hkv, d, lens, first, up):
@@ -214,3 +214,33 @@ def test_append_angles_of_both_reductions():
     got, held = host(kc), ~np.isnan(rk)
     tol = (8.2 * E24 + 3 * 2.0 ** -26) * 2 * np.abs(k).max() + U["f32"] * np.abs(rk[held])
     assert np.all(np.abs(got[held] - rk[held]) <= tol), np.abs(got[held] - rk[held]).max()
+
+
+def test_binding_refuses_as_many_elements_in_another_order():
+    """A tensor with the right number of elements and another shape is other data: [pages, page_size, heads, d]
+    caches, transposed tables, heads behind columns, flat rows."""
+    c = Chain(75)
+    t, row, hq, hkv, d = c.t, c.t["srow"], c.hq, c.hkv, c.d
+    z = lambda *n: torch.zeros(*n, dtype=torch.bfloat16, device="cuda")
+    swapped = z(c.num_pages, c.page, hkv, d)
+    table = t["table"].t().contiguous()
+    shared = [t["sq"], t["kc"], t["vc"], t["table"], t["len2"], t["goff"], t["pre"], t["so"], c.sB, c.ws[3]]
+    extend = [t["pq"], t["kc"], t["vc"], t["table"][:1], t["len1"], t["off1"], t["po"], c.s1, c.ws[1]]
+    append = [row[:, :hq], row[:, hq:hq + hkv], row[:, hq + hkv:], t["table"], t["len2"], None, t["inv"], t["sq"],
+              t["kc"], t["vc"], c.sB, c.ws[2]]
+    for call, good, wrongs in (
+            (K.dense_decode_shared, shared, [(0, z(3, d, hq)), (0, z(3, hq * d)), (1, swapped), (2, swapped), (3, table),
+                                             (4, t["len2"][:, None]), (5, t["goff"][None]), (6, t["pre"][:, None]),
+                                             (7, z(3, d, hq))]),
+            (K.dense_extend, extend, [(0, z(c.prompt, d, hq)), (1, swapped), (2, swapped), (3, table[:, :1]),
+                                      (5, t["off1"][None]), (6, z(c.prompt, hq * d))]),
+            (lambda *a: K.art_append_kv(*a, rot_dim=d), append,
+             [(3, table), (4, t["len2"][None]), (6, t["inv"][None]), (7, z(3, d, hq)), (8, swapped), (9, swapped)])):
+        call(*good)
+        for i, wrong in wrongs:
+            assert wrong.numel() == good[i].numel()
+            bad = list(good)
+            bad[i] = wrong
+            with pytest.raises(K.ArtError):
+                call(*bad)
+    torch.cuda.synchronize()
