@@ -287,7 +287,17 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-_ropes = {}  # by (rot_dim, interleaved, scale): a program has one or two
+_ropes = {}  # by (rot_dim, interleaved, scale), plain numbers: a program has one or two
+
+
+def _rope(rot_dim, interleaved, scale) -> ArtRope:
+    key = int(rot_dim), bool(interleaved), float(scale)  # a tensor as a key would be found by its identity
+    rope = _ropes.get(key)
+    if rope is None:
+        if len(_ropes) >= 64:
+            _ropes.clear()
+        rope = _ropes.setdefault(key, ArtRope(*key))
+    return rope
 
 
 def art_append_workspace_bytes(shape: ArtShape) -> int:
@@ -348,14 +358,9 @@ def art_append_kv(q, k, v, block_table, seq_lens, q_offsets, inv_freq, q_out, k_
         raise ArtError("q, k and v are not [tokens, heads, head_dim] rows of the cache's dtype and device, dense in "
                        "their last two dimensions: " +
                        ", ".join(f"{tuple(t.shape)} {t.dtype} strides {t.stride()}" for t in (q, k, v) if t is not None))
-    rope = _ropes.get((rot_dim, interleaved, scale))
-    if rope is None:
-        if len(_ropes) >= 64:
-            _ropes.clear()
-        rope = _ropes.setdefault((rot_dim, interleaved, scale), ArtRope(int(rot_dim), 1 if interleaved else 0, scale))
     rc = L.art_append_kv(_addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(q_offsets), tokens,
                          _addr(positions), block_table.data_ptr(), seq_lens.data_ptr(), _addr(inv_freq),
-                         ctypes.byref(rope), _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
+                         ctypes.byref(_rope(rot_dim, interleaved, scale)), _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
                          ctypes.byref(shape), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, device))
     if check and rc != ART_OK:
         _check(rc)
