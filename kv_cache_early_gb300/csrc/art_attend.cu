@@ -245,7 +245,6 @@ static size_t attend_layout(AttendParams& p, unsigned char* base) {
     if (rows > (1LL << 30) || items > (1LL << 28) || prows > (1LL << 30) || p.NG > kMaxGroups ||
         (long long)p.max_pages * p.Ps > (1LL << 30))
         return 0;
-    p.part_rows = (int)prows;
     // cost units fit 31 bits, with room for sums of one share beyond the end
     const long long tiles = (((long long)p.max_pages * p.Ps) >> p.kt_log2) + 1;
     const long long per = p.cost.two_tile > p.cost.small_tile ? p.cost.two_tile : p.cost.small_tile;

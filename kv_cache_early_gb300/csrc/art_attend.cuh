@@ -68,10 +68,10 @@ struct Entity {
     int k0, k1;  // keys of the last row
     int lim0, kind;
 };
-// ... and its place in the work, for the merge kernel
+// ... and its place in the work, from which the merge kernel finds the pieces of its rows
 struct alignas(16) EntityPlace {
-    int nrows, k0, k1, item0;  // item0: its first item
-    int start, prow, hc, pad;  // its first cost unit, its first partial row (dense_decode_shared), a KV head's cost
+    int nrows, k0, k1, start;  // start: its first cost unit
+    int prow, hc, pad[2];      // its first partial row (dense_decode_shared), a KV head's cost
 };
 static_assert(sizeof(EntityPlace) == 32, "two 16-byte words");
 
@@ -84,9 +84,8 @@ struct alignas(16) MergeItem {
 };
 
 struct PlanInfo {
-    int quota, total;  // cost units of a share, of the whole work
-    int ok;            // 0: bad offsets, nothing is computed
-    int pad;
+    int quota;  // cost units of a share
+    int ok;     // 0: bad offsets, nothing is computed
 };
 
 // Cost units of an item and of a key tile, by rows.
@@ -105,7 +104,7 @@ struct AttendParams {
     int shared, causal;
     int B, T, NG, NE;  // sequences, query tokens, groups, entities
     int Hq, Hkv, G, D, Ps, max_pages, num_pages;
-    int rt, ctas, part_rows;
+    int rt, ctas;
     int kt_log2, small_rows;  // keys of a tile; rows of a small item
     CostRule cost;
     float scale_log2;  // log2(e) / sqrt(d)
@@ -123,7 +122,7 @@ struct AttendParams {
     MergeItem* merge;    // per CTA: the item that its share starts inside of, by the first CTA it goes on in
     Seg* seg;            // segment of item i in CTA c: i + c
     float* part_o;       // partial results of a segment: [D / 4][nrow][4], D floats a row
-    float2* part_ml;     // [part_rows]: (m, l)
+    float2* part_ml;     // of each partial row: (m, l)
 };
 
 __device__ __forceinline__ int item_cost_tile(const AttendParams& p, int nrow) {

@@ -280,11 +280,10 @@ __device__ void plan_share(const AttendParams& p, PlanScratch* s, int& s0, int& 
             pl.nrows = q.nrt > 0 ? q.en.nrows : 0;
             pl.k0 = q.en.k0;
             pl.k1 = q.en.k1;
-            pl.item0 = q.item0;
             pl.start = q.start;
             pl.prow = q.prow;
             pl.hc = q.hc;
-            pl.pad = 0;
+            pl.pad[0] = pl.pad[1] = 0;
             p.place[e] = pl;
         }
         if (q.nrt > 0 && q.start < hi && q.start + q.hc * p.Hkv > lo) s->list[atomicAdd(&s->listed, 1)] = q;
@@ -304,7 +303,6 @@ __device__ void plan_share(const AttendParams& p, PlanScratch* s, int& s0, int& 
         p.cta_segs[c] = make_int2(s0, s1);
         if (c == 0) {
             p.info->quota = quota;
-            p.info->total = W;
             p.info->ok = 1;
         }
     }
