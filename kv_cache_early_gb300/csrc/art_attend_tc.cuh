@@ -599,7 +599,8 @@ struct TcConsumer {
         }
     }
 
-    // The row's 64 weights at t, and its D sums at t, times f (seldom).
+    // The row's 64 weights at t, and its D sums at t, times f (seldom). References are integers,
+    // so f is a power of two and the weights are not rounded a second time.
     __device__ __noinline__ static void scale_weights(uint32_t t, float f) {
 #pragma unroll 1
         for (int k = 0; k < 32; k += 16) {
@@ -700,7 +701,7 @@ struct TcConsumer {
                     float rowsum = m == -INFINITY ? INFINITY : 0.f;
                     for (int again = __any_sync(0xffffffffu, m == -INFINITY);;) {
                         if (again) {
-                            const float top = row_max<64>(s) * p.scale_log2;
+                            const float top = ceilf(row_max<64>(s) * p.scale_log2);  // an integer: scale_weights
                             if (!(rowsum <= kMaxSum) && top > m) {
                                 // a row that had a reference: what it has summed is scaled down
                                 const float f = ex2(m - top);

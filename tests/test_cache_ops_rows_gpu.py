@@ -244,3 +244,39 @@ def test_binding_refuses_as_many_elements_in_another_order():
             with pytest.raises(K.ArtError):
                 call(*bad)
     torch.cuda.synchronize()
+
+
+def test_weights_are_rounded_once():
+    """bf16, more than 128 rows: the maximum of the second half of a key tile moves the reference of weights that are
+    rounded already. Their scaling must not round them again. Weights against an integer reference (in log2) have the
+    same bits whatever it is, so the oracle rounds its own: out = bf16(p_a2) v / (p_a1 + p_a2 + p_b), to the output's
+    rounding and the fp32 scores' 2^-15. Rows whose p_a2 lies within 2^-13 of a tie are left out."""
+    rng = np.random.default_rng(76)
+    d, rows, n, a1, a2, b = 64, 160, 128, 5, 40, 100
+    pool = Pool(rng, "bf16", 1, d, 16, [n], fill=False)
+    k, v = np.zeros((n, d), np.float32), np.zeros((n, d), np.float32)
+    k[:, 0] = -4.0  # weights below 2^-60 of the others
+    k[a1, 0], k[a2, 0], k[b, 0] = 1.0, 1.0, 2.0
+    k[a2, 1:8] = rounded(rng.standard_normal(7), "bf16")
+    v[a2] = 2.0 ** 17 * rounded(1.0 + rng.random(d), "bf16")
+    at = pool.table[0, np.arange(n) // 16], 0, np.arange(n) % 16
+    pool.k[at], pool.v[at] = k, v
+    q = np.zeros((rows, 1, d), np.float32)
+    q[:, 0, 0] = 100.0 + rng.integers(0, 32, rows)  # b leads a1 by 18 to 24 powers of two
+    q[:, 0, 1:8] = rounded(rng.standard_normal((rows, 7)) - 1.5 * np.sign(k[a2, 1:8]), "bf16")  # a2 stays below a1
+    shape = K.make_shape(**pool.shape(1))
+    ws = workspace(K.dense_extend_workspace_bytes(shape, rows))
+    tq = dev(q, "bf16")
+    out = torch.full_like(tq, SENTINEL)
+    K.dense_extend(tq, dev(pool.k, "bf16"), dev(pool.v, "bf16"), dev(pool.table), dev(pool.seq_lens),
+                   dev(np.array([0, rows], np.int32)), out, shape, ws, causal=False)
+    torch.cuda.synchronize()
+    assert K.art_read_device_status(ws) == 0
+    s = q[:, 0].astype(np.float64) @ k.astype(np.float64).T / np.sqrt(d) / np.log(2.0)
+    p = 2.0 ** (s - np.ceil(s[:, b:b + 1]))
+    frac, _ = np.frexp(p[:, a2])          # bf16 keeps 8 bits: steps of 2^-8 of frac in [0.5, 1)
+    near = np.abs(frac * 256 - np.floor(frac * 256) - 0.5) < 256 * 2.0 ** -13
+    once = rounded(p[:, a2], "bf16").astype(np.float64)
+    ref = (once / p.sum(1))[:, None] * v[a2].astype(np.float64)
+    err = np.abs(host(out)[:, 0] - ref) / ref
+    assert (~near).sum() > rows / 2 and np.all(err[~near] <= U["bf16"] + 2.0 ** -15), err[~near].max() / U["bf16"]
