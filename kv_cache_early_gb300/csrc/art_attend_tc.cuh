@@ -26,9 +26,18 @@
 // Softmax: p = 2^(s c - m) with c = log2(e) / sqrt(d), s and the sums in fp32; m
 // follows the row's maximum only when that has risen by far (small segments: by more
 // than 2^8; large ones: when 64 weights add up to more than 2^16): p and l stay far
-// from overflow, and O need not be rescaled for each new maximum. p is rounded
-// to bf16 for the product, as V is bf16 and both operands have one type; its sum is
-// taken before the rounding.
+// from overflow, and O need not be rescaled for each new maximum.
+//
+// V is bf16 and both operands have one type, so p enters the product in bf16; its sum is
+// taken before. With eight rows or fewer (a sequence's one token, a few drafted ones)
+// what the rounding left of p takes the product's eight rows of padding: about 16 bits of p,
+// as in the decode kernel, at no product more (64 sequences of one row 175.8 us without
+// and 175.7 with it, 16 x 3-4 drafts 62.9 and 63.1). With more rows p is rounded once: a
+// second product for 9 to 16 rows took 2 to 6 % (d 64, 2 to 16 rows: 50.1 us without, 51.1
+// unrolled, 53.2 in a loop), for large segments 35 % on chunks of 1-2k tokens (360 and
+// 488 us) and 18 % on a 32k prefix for 128 sequences (136 and 161). Against 64 bits on
+// random data a result's error (rms, relative) is then 2.0e-3 to 2.3e-3; the output's own
+// rounding alone makes 1.65e-3.
 //
 // Layout: a page's copy lands as [8-row group][64-column half][8 rows][128 bytes],
 // 128B-swizzled. So 8-row groups follow one another at d * 16 bytes whatever the
@@ -40,12 +49,12 @@
 //
 // Every wait is bounded (AttendParams::wait_ns); see wait_tc.
 //
-// Measured on a GB300: chunks of 1-2k tokens behind 0-8k (32/8 heads, d 128) 359 us a
+// Measured on a GB300: chunks of 1-2k tokens behind 0-8k (32/8 heads, d 128) 362 us a
 // call, the tensor pipe 59 % active: a stream's chain softmax (1580 cycles) -> P V and
 // Q K^T (1024) -> hand-overs (300) is 2900 cycles a tile of two streams, whose products
-// take 2048. A 32k prefix for 128 sequences with 64-2047 own tokens each: 134 us,
+// take 2048. A 32k prefix for 128 sequences with 64-2047 own tokens each: 136 us,
 // 5.5 TB/s over the main kernel. Drafts of 5 tokens for 16 sequences behind 1k-8k:
-// 68 us, 5.7 TB/s while it streams.
+// 67 us, 5.7 TB/s while it streams.
 #pragma once
 
 #include "art_attend_plan.cuh"
@@ -829,6 +838,7 @@ struct TcConsumer {
 #pragma unroll
         for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         const int mat = lane >> 3, mr = lane & 7;
+        const bool few = sg.nrow <= 8;  // the product's rows 8 to 15 hold what the weights' rounding left
 #pragma unroll 1
         for (int j = 0; j < nt; ++j) {
             const int kb = (t0 + j) * kKeyTile + w * 16;  // first key of this warp's slice
@@ -871,7 +881,7 @@ struct TcConsumer {
                 const bool ua = ta > ma + kRescale || (ma == -INFINITY && ta > ma);
                 const bool ub = tb > mb + kRescale || (mb == -INFINITY && tb > mb);
                 if (__any_sync(0xffffffffu, ua || ub)) {
-                    const float fa = ua ? ex2(ma - ta) : 1.f, fb = ub ? ex2(mb - tb) : 1.f;
+                    const float fa = ua ? ex2(ma - ta) : 1.f, fb = few ? fa : ub ? ex2(mb - tb) : 1.f;
                     if (ua) ma = ta;
                     if (ub) mb = tb;
                     suma *= fa;
@@ -892,6 +902,8 @@ struct TcConsumer {
                     sumb += e2 + e3;
                     pa[2 * n] = pack_bf16(e0, e1);
                     pa[2 * n + 1] = pack_bf16(e2, e3);
+                    const uint32_t rest = pack_bf16(e0 - bf16_lo_f(pa[2 * n]), e1 - bf16_hi_f(pa[2 * n]));
+                    if (few) pa[2 * n + 1] = rest;
                 }
             }
             if (!wait(&c->full[st.s], st.ph)) return false;
@@ -935,6 +947,10 @@ struct TcConsumer {
         }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
+            if (few) {
+                o[i][0] += o[i][2];
+                o[i][1] += o[i][3];
+            }
             if (ra < sg.nrow) *reinterpret_cast<float2*>(ex + ra * D + i * 8 + cq) = make_float2(o[i][0], o[i][1]);
             if (rb < sg.nrow) *reinterpret_cast<float2*>(ex + rb * D + i * 8 + cq) = make_float2(o[i][2], o[i][3]);
         }

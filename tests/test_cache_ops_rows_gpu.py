@@ -5,7 +5,7 @@ tolerances: cache_ops_harness.py."""
 import numpy as np
 import pytest
 
-from cache_ops_harness import E24, U, Pool, rounded
+from cache_ops_harness import E24, U, Pool, attend_tol, rounded
 from oracle import cache_ops as O
 
 torch = pytest.importorskip("torch")
@@ -280,3 +280,56 @@ def test_weights_are_rounded_once():
     ref = (once / p.sum(1))[:, None] * v[a2].astype(np.float64)
     err = np.abs(host(out)[:, 0] - ref) / ref
     assert (~near).sum() > rows / 2 and np.all(err[~near] <= U["bf16"] + 2.0 ** -15), err[~near].max() / U["bf16"]
+
+
+def close_to_two_parts(got, q, rows_of):
+    """bf16 with the weights in two bf16 parts: the rounding of the second leaves u^2 of a weight (u = 2^-8)."""
+    for t in range(q.shape[0]):
+        for h in range(q.shape[1]):
+            k, v = rows_of(t, h)
+            qd = q[t, h].astype(np.float64)
+            ref, ref_abs = O.attend(qd, k, v), O.attend(qd, k, np.abs(v))
+            tol = attend_tol(ref, ref_abs, (np.abs(k) @ np.abs(qd)).max() / np.sqrt(q.shape[2]), len(k), q.shape[2],
+                             np.abs(v).max(), "bf16") - U["bf16"] * (1 - U["bf16"]) * ref_abs
+            assert np.all(np.abs(got[t, h] - ref) <= tol), (t, h, len(k))
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (8, 8, 64), (14, 2, 64), (8, 1, 128)])
+def test_few_rows_keep_the_weights_of_dense_decode(hq, hkv, d):
+    """Eight rows or fewer: sequences without groups, few samples of one prompt, few drafted tokens."""
+    rng = np.random.default_rng(77)
+    g = hq // hkv
+    seq = [1, 17, 130, 700, 701, 702]
+    pool = Pool(rng, "bf16", hkv, d, 16, seq)
+    shape = K.make_shape(**pool.shape(hq))
+    kc, vc, lens = dev(pool.k, "bf16"), dev(pool.v, "bf16"), dev(pool.seq_lens)
+    rows = {(b, x): [O.gather(c, pool.table[b], seq[b], x) for c in (pool.k, pool.v)]
+            for b in range(len(seq)) for x in range(hkv)}
+    q = rounded(rng.standard_normal((len(seq), hq, d)), "bf16")
+    tq = dev(q, "bf16")
+    ws = workspace(K.dense_decode_shared_workspace_bytes(shape, 1))
+    out = torch.full_like(tq, SENTINEL)
+    K.dense_decode_shared(tq, kc, vc, dev(pool.table), lens, None, None, out, shape, ws)
+    torch.cuda.synchronize()
+    assert K.art_read_device_status(ws) == 0
+    close_to_two_parts(host(out), q, lambda b, h: rows[b, h // g])
+    # the last members as samples of one prompt: their first 640 tokens are sequence `lead`'s
+    members, pre = min(3, 8 // g), 640
+    lead = len(seq) - members
+    K.dense_decode_shared(tq, kc, vc, dev(pool.table), lens, dev(np.array([lead, len(seq)], np.int32)),
+                          dev(np.array([pre], np.int32)), out, shape, ws)
+    torch.cuda.synchronize()
+    assert K.art_read_device_status(ws) == 0
+    close_to_two_parts(host(out), q, lambda b, h: rows[b, h // g] if b < lead else
+                       [np.concatenate([s[:pre], o[pre:]]) for s, o in zip(rows[lead, h // g], rows[b, h // g])])
+    n = 8 // g
+    off = np.array([0, 1, 2, 2 + n, 2 + 2 * n, 3 + 2 * n, 3 + 3 * n], np.int32)
+    q = rounded(rng.standard_normal((int(off[-1]), hq, d)), "bf16")
+    ws = workspace(K.dense_extend_workspace_bytes(shape, int(off[-1])))
+    tq = dev(q, "bf16")
+    out = torch.full_like(tq, SENTINEL)
+    K.dense_extend(tq, kc, vc, dev(pool.table), lens, dev(off), out, shape, ws)
+    torch.cuda.synchronize()
+    assert K.art_read_device_status(ws) == 0
+    of = np.searchsorted(off, np.arange(off[-1]), side="right") - 1
+    close_to_two_parts(host(out), q, lambda t, h: [c[:seq[of[t]] - (off[of[t] + 1] - t) + 1] for c in rows[of[t], h // g]])
