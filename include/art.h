@@ -273,7 +273,8 @@ int art_select_blocks(const void* q, const void* k_cache, const int32_t* block_t
  * The cache's other side: writing new tokens, attending with several of them,
  * and decoding a batch that shares a prefix. (Additions of this library: the
  * ART paper reads a cache that a serving engine has filled.) They take the
- * shape of art_decode (its checks apply; max_visit and num_probe are not used),
+ * shape of art_decode (its checks apply, the group sizes among them; max_visit and
+ * num_probe are not used),
  * its cache and block-table layout, its workspace and status rules: bad device
  * data never faults, sets a bit of the status word and leaves the results
  * described below. Sequences of one call are independent of each other.
@@ -338,14 +339,20 @@ int art_append_kv(const void* q, const void* k, const void* v, int64_t q_stride,
  *   causal 0: every new token sees all seq_len keys, whatever n is
  *   q, out    [num_tokens][num_q_heads][head_dim]
  *   workspace dense_extend_workspace_bytes(shape, num_tokens) bytes (0: sizes
- *             beyond the supported range)
+ *             beyond the supported range); partial results for 160 CTAs are most
+ *             of it, 42 MB at head_dim 128 in bf16 for any num_tokens
+ * Rounding (bf16): scores, softmax statistics and sums are fp32. The weights
+ * enter the product with the values in bf16; of a sequence whose new tokens * G
+ * are 8 at most, with their remainder as a second bf16 part. A random result's
+ * error is the output's own rounding there and about 1.4 times as much elsewhere.
  * A token that sees no key, and every token of a sequence with a bad length or
  * page, gets a zero output. With bad offsets no output is written. Keys and
  * values outside a sequence's length may hold anything, NaN included; a value
  * that some new tokens of a sequence see must be finite for the others too.
  * Supported: num_tokens * G and a table row's tokens up to 2^30, and
- * (num_tokens * G / rows + batch) * num_kv_heads * (a table row's tokens / keys)
- * up to 2^30, with rows = 256 and keys = 128 for bf16, both 64 for fp32.
+ * (num_tokens * G / rows + batch) * num_kv_heads * (a table row's tokens / keys + 1)
+ * up to 2^30 (its first two factors up to 2^28), with rows = 256 and keys = 128 for
+ * bf16, both 64 for fp32.
  */
 size_t dense_extend_workspace_bytes(const art_shape* shape, int32_t num_tokens);
 int dense_extend(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
@@ -369,11 +376,14 @@ int dense_extend(const void* q, const void* k_cache, const void* v_cache, const 
  *                 padded batch) nothing: zero output.
  *   num_groups 0: group_offsets and prefix_lens may be NULL
  *   workspace     dense_decode_shared_workspace_bytes(shape, num_groups) bytes
+ * Rounding (bf16): as dense_extend. A sequence's own tokens keep both parts, a
+ * prefix where its group's members * G <= 8; beyond, a result that a caller
+ * takes from here has somewhat fewer bits than dense_decode's.
  * A sequence with a bad length or page gets a zero output; a bad prefix length
  * or prefix page gives the whole group zero outputs; with bad offsets no output
  * is written. Values that some members see must be finite for the others too.
  * Supported: as dense_extend, with batch query tokens and num_groups more
- * sequences; num_groups up to 8192.
+ * sequences; num_groups up to 8192, batch * num_q_heads below 2^29 - 2^15.
  */
 size_t dense_decode_shared_workspace_bytes(const art_shape* shape, int32_t num_groups);
 int dense_decode_shared(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,

@@ -271,9 +271,12 @@ static size_t attend_layout(AttendParams& p, unsigned char* base) {
 }
 
 // Cost units (about 0.15 us): what segments and key tiles of each kind take beside their
-// neighbours, fitted to the CTAs' timelines. They set the shares only. Tiles alone at one
-// cost: chunks of 1-2k tokens 527 us against 358, 128 sequences behind a document 159
-// against 134, 64 behind a prompt 61 against 52.
+// neighbours, fitted to the CTAs' timelines at head_dim 128. They set the shares only. Tiles
+// alone at one cost: chunks of 1-2k tokens 527 us against 362, 128 sequences behind a
+// document 159 against 134, 64 behind a prompt 61 against 52. At head_dim 64, where a tile has half the
+// bytes and products, the same numbers hold: with tiles at {4, 7, 9} instead of {7, 11, 13}
+// chunks 299 us against 297, a document 125 against 116, a mixed batch 62.2 against 60.8; with
+// items at {9, 20, 30} instead of {13, 35, 50} chunks 315, a document 117, mixed 60.7.
 constexpr CostRule kCostBf16 = {13, 7, 35, 11, 50, 13}, kCostF32 = {10, 8, 10, 16, 10, 16};
 
 static void fill_shape(AttendParams& p, const art_shape& s) {
