@@ -337,7 +337,7 @@ int art_append_kv(const void* q, const void* k, const void* v, int64_t q_stride,
  *   causal 1: new token i of n sees the keys below seq_len - n + i + 1 (the new
  *             tokens' own keys are in the cache already); seq_len >= n
  *   causal 0: every new token sees all seq_len keys, whatever n is
- *   q, out    [num_tokens][num_q_heads][head_dim]
+ *   q, out    [num_tokens][num_q_heads][head_dim]; out may be q
  *   workspace dense_extend_workspace_bytes(shape, num_tokens) bytes (0: sizes
  *             beyond the supported range); partial results for 160 CTAs are most
  *             of it, 42 MB at head_dim 128 in bf16 for any num_tokens
@@ -375,6 +375,7 @@ int dense_extend(const void* q, const void* k_cache, const void* v_cache, const 
  *                 prefix sees only its own length of it, one of length 0 (a
  *                 padded batch) nothing: zero output.
  *   num_groups 0: group_offsets and prefix_lens may be NULL
+ *   out may be q
  *   workspace     dense_decode_shared_workspace_bytes(shape, num_groups) bytes
  * Rounding (bf16): as dense_extend. A sequence's own tokens keep both parts, a
  * prefix where its group's members * G <= 8; beyond, a result that a caller

@@ -23,7 +23,8 @@
 // the main one and the memset that its counters would need. A page id is checked where
 // it is used; a bad one marks its segment, and the merge kernel zeroes the rows of the
 // sequences that have such a segment. So a call is two kernels and nothing is zeroed
-// beforehand.
+// beforehand. A row's query is read, by whatever CTAs, before its result is written (by the
+// one CTA that had the whole item, after its last key, or by the merge kernel): out may be q.
 #pragma once
 
 #include "art_common.cuh"

@@ -333,3 +333,108 @@ def test_few_rows_keep_the_weights_of_dense_decode(hq, hkv, d):
     assert K.art_read_device_status(ws) == 0
     of = np.searchsorted(off, np.arange(off[-1]), side="right") - 1
     close_to_two_parts(host(out), q, lambda t, h: [c[:seq[of[t]] - (off[of[t] + 1] - t) + 1] for c in rows[of[t], h // g]])
+
+
+# ----------------------------------------------------------------------------
+# calls that the documentation allows
+# ----------------------------------------------------------------------------
+def test_stream_given_as_object_and_as_handle():
+    c = Chain(78)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):  # the copies between the calls go there too
+        c.run(stream=side)
+    torch.cuda.synchronize()
+    c.check()
+    for n in ("pq", "po", "sq", "so", "dd"):
+        c.t[n].fill_(SENTINEL)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        c.run(stream=side.cuda_stream)
+    side.synchronize()
+    c.check()
+
+
+def test_return_codes_without_check():
+    c = Chain(79)
+    t = c.t
+    small = c.ws[1][:32]
+    args = (t["pq"], t["kc"], t["vc"], t["table"][:1], t["len1"], t["off1"], t["po"], c.s1)
+    assert K.dense_extend(*args, small, check=False) == K.ART_ERR_WORKSPACE
+    with pytest.raises(K.ArtError):
+        K.dense_extend(*args, small)
+    assert K.dense_decode_shared(t["sq"], t["kc"], t["vc"], t["table"], t["len2"], t["goff"], t["pre"], t["so"], c.sB,
+                                 c.ws[3][8:], check=False) == K.ART_ERR_INVALID_ARG  # not 16-byte aligned
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_results_in_place_of_the_queries(dtype):
+    """out may be q: whole items and cut ones, rows of one tile, of several, and few."""
+    rng = np.random.default_rng(80)
+    hq, hkv, d = 8, 2, 64
+    new, seq = [1, 40, 0, 150, 3], [3000, 90, 10, 2150, 700]
+    pool = Pool(rng, dtype, hkv, d, 16, seq)
+    off = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    shape = K.make_shape(**pool.shape(hq))
+    q = rounded(rng.standard_normal((int(off[-1]), hq, d)), dtype)
+    q1 = rounded(rng.standard_normal((len(seq), hq, d)), dtype)
+    cache = dev(pool.k, dtype), dev(pool.v, dtype), dev(pool.table), dev(pool.seq_lens)
+    we = workspace(K.dense_extend_workspace_bytes(shape, int(off[-1])))
+    wd = workspace(K.dense_decode_shared_workspace_bytes(shape, 0))
+    for causal in (True, False):
+        a, b = dev(q, dtype), torch.full((len(q), hq, d), SENTINEL, device="cuda").to(dev(q[:1], dtype).dtype)
+        K.dense_extend(a, *cache, dev(off), b, shape, we, causal=causal)
+        K.dense_extend(a, *cache, dev(off), a, shape, we, causal=causal)
+        torch.cuda.synchronize()
+        assert torch.equal(a, b)
+    a = dev(q1, dtype)
+    b = torch.empty_like(a)
+    K.dense_decode_shared(a, *cache, None, None, b, shape, wd)
+    K.dense_decode_shared(a, *cache, None, None, a, shape, wd)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+
+
+def test_replay_with_other_lengths_offsets_and_tables():
+    """A captured call reads its lengths, offsets, prefixes and tables at the replay."""
+    rng = np.random.default_rng(81)
+    hq, hkv, d, T, B, cols = 8, 2, 64, 64, 4, 80
+    one = dict(num_q_heads=hq, num_kv_heads=hkv, head_dim=d, page_size=16, block_size=64, max_pages_per_seq=cols,
+               max_visit=1, num_probe=1, num_pages_total=B * cols, dtype=0, batch=B)
+    shape = K.make_shape(**one)
+    kv = [rounded(np.clip(rng.standard_normal((B * cols, hkv, 16, d)), -3.9, 3.9), "bf16") for _ in range(2)]
+    q, q1 = (rounded(rng.standard_normal((n, hq, d)), "bf16") for n in (T, B))
+    kc, vc, tq, tq1 = (dev(x, "bf16") for x in (*kv, q, q1))
+    table, lens, off, goff, pre = (torch.zeros(n, dtype=torch.int32, device="cuda")
+                                   for n in ((B, cols), B, B + 1, 3, 2))
+    out, dec = torch.empty_like(tq), torch.empty_like(tq1)
+    we, wd = (workspace(n) for n in (K.dense_extend_workspace_bytes(shape, T),
+                                     K.dense_decode_shared_workspace_bytes(shape, 2)))
+
+    def run():
+        K.dense_extend(tq, kc, vc, table, lens, off, out, shape, we)
+        K.dense_decode_shared(tq1, kc, vc, table, lens, goff, pre, dec, shape, wd)
+
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for hlens, hoff, hgoff, hpre in (([64, 1200, 7, 300], [0, 1, 40, 40, 64], [0, 2, 4], [50, 7]),
+                                     ([0, 0, 0, 0], [5, 5, 5, 5, 5], [0, 0, 0], [0, 0]),
+                                     ([1280, 33, 1280, 1], [0, 30, 63, 64, 64], [1, 1, 4], [9, 33])):
+        htable = rng.permutation(B * cols).reshape(B, cols).astype(np.int32)
+        for x, h in ((table, htable), (lens, hlens), (off, hoff), (goff, hgoff), (pre, hpre)):
+            x.copy_(dev(np.asarray(h, np.int32)))
+        out.fill_(SENTINEL)
+        dec.fill_(SENTINEL)
+        g.replay()
+        torch.cuda.synchronize()
+        assert K.art_read_device_status(we) == 0 and K.art_read_device_status(wd) == 0
+        ref = O.extend(q, kv[0], kv[1], htable, hlens, hoff, True)
+        got, held = host(out), ~np.isnan(ref)
+        assert np.all(got[~held] == SENTINEL)
+        assert np.all(np.abs(got - ref)[held] <= 8 * U["bf16"])  # |v| < 4: u |out| + u sum(p |v|)
+        ref = O.decode_shared(q1, kv[0], kv[1], htable, hlens, hgoff, hpre)
+        assert np.abs(host(dec) - ref).max() <= 8 * U["bf16"]
