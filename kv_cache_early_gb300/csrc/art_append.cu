@@ -22,7 +22,7 @@
 // longer of the two and not for their sum. One more CTA (block 0) checks the device
 // data of the call and stores the status word, so that no memset precedes the
 // kernel; every token's CTA checks what it uses by itself. Measured: prompts of 36727
-// tokens (32/8 heads, d 128, bf16) 136 us, 99 % of the copy rate; a step of 1 or 128
+// tokens (32/8 heads, d 128, bf16) 136 us, 98 % of the copy rate; a step of 1 or 128
 // tokens 2.9 us.
 #include "art_common.cuh"
 
