@@ -392,6 +392,88 @@ int dense_decode_shared(const void* q, const void* k_cache, const void* v_cache,
                         int32_t num_groups, void* out, const art_shape* shape, void* workspace,
                         size_t workspace_bytes, void* stream);
 
+/*
+ * A cache in 4 bits: writing it, reading it back, attending over it. (Additions
+ * of this library.) The calls take the shape, block tables, status and workspace
+ * rules of the calls above; what they name k_cache and v_cache is one array here:
+ *
+ *   cache  bytes [num_pages_total][num_kv_heads][art_kv4_page_bytes(shape, group)],
+ *          16-byte aligned. A page of a head has page_size * (d + 8 d / group)
+ *          bytes: slabs of S = min(page_size, 64) tokens, each with
+ *            keys' codes    [S / 8][d / 32][8 tokens][16 bytes], two columns a byte,
+ *                           the lower column in the lower four bits
+ *            values' codes  the same
+ *            keys' scales   [S / 8][d / group][8 tokens] pairs of bf16: step, lowest
+ *            values' scales the same
+ *   group  columns that share a scale: 32, 64 or 128, head_dim at most; others are
+ *          ART_ERR_UNSUPPORTED
+ *
+ * A column's value is lowest + step * code. Written are, of the values x of a
+ * token's group of columns, lowest: the largest bf16 that is no larger than min x;
+ * step: the bf16 nearest to (max x - lowest) / 15, zero below 2^-100; code: the
+ * whole number nearest to (x - lowest) / step, 15 at most, 0 where step is 0.
+ * All as in exact arithmetic, with ties to even. A group that holds a NaN or an
+ * infinity, or spans 15 * 2^100 or more, becomes NaN as a whole (step 0, lowest NaN).
+ */
+size_t art_kv4_page_bytes(const art_shape* shape, int32_t group); /* 0: unsupported */
+
+/*
+ * art_append_kv into such a cache: same arguments, same rules. A key is rotated
+ * as in exact arithmetic (angles below 2^24; beyond, as in 64 bits) and rounded to the dtype, then
+ * quantised; q_out is as art_append_kv's. The bytes of other tokens stay as they are.
+ *   workspace  art_append_kv4_workspace_bytes(shape) bytes: the status word
+ */
+size_t art_append_kv4_workspace_bytes(const art_shape* shape);
+int art_append_kv4(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                   const int32_t* q_offsets, int32_t num_tokens, const int32_t* positions,
+                   const int32_t* block_table, const int32_t* seq_lens, const float* inv_freq,
+                   const art_rope* rope, void* q_out, void* cache, int32_t group, const art_shape* shape,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Reads cached keys and values back, as fp32 (lowest + step * code rounded once)
+ * or that rounded to bf16, by the dtype.
+ *   out_table NULL: rows. k_out, v_out [num_tokens][num_kv_heads][head_dim]; token i of
+ *              the n of sequence b (q_offsets as above) is its place seq_len - n + i:
+ *              what art_append_kv4 with these offsets has written. q_offsets NULL:
+ *              the last token of each sequence, num_tokens = batch. out_pages 0.
+ *              Rows of a sequence with a bad length are zero, a token's whose page
+ *              id lies outside the pool too; of one with bad offsets, and those
+ *              that no sequence holds, are left as they are (with bad offsets of
+ *              one sequence no row is written).
+ *   out_table int32 [batch][max_pages_per_seq]: pages of a plain cache, k_out, v_out
+ *              [out_pages][num_kv_heads][page_size][head_dim], as every other call
+ *              reads it. All tokens of each sequence; q_offsets NULL, num_tokens 0.
+ *              A sequence with a bad length writes nothing, a page with a bad id in
+ *              out_table is skipped, one with a bad id in block_table reads as zero.
+ *              Two sequences must not share a page of the output.
+ *   workspace  art_read_kv4_workspace_bytes(shape) bytes: the status word
+ * One kernel. Supported: a table row's tokens up to 2^30.
+ */
+size_t art_read_kv4_workspace_bytes(const art_shape* shape);
+int art_read_kv4(const void* cache, int32_t group, const int32_t* block_table, const int32_t* seq_lens,
+                 const int32_t* q_offsets, int32_t num_tokens, const int32_t* out_table, int32_t out_pages,
+                 void* k_out, void* v_out, const art_shape* shape, void* workspace, size_t workspace_bytes,
+                 void* stream);
+
+/*
+ * dense_extend over such a cache. q_offsets NULL: one new token for each sequence,
+ * which sees all of its keys (a decode step), num_tokens = batch.
+ *   workspace  dense_extend_kv4_workspace_bytes(shape, num_tokens, group) bytes
+ *              (0: sizes beyond the supported range)
+ * Rounding: codes enter the products as they are; queries exactly (bf16) or to
+ * about 22 bits (fp32), weights times step to 11 bits (bf16) or about 22 (fp32);
+ * everything else is fp32. Queries below 2^100 in magnitude.
+ * A token that sees no key, and every token of a sequence with a bad length or
+ * page, gets a zero output. With bad offsets no output is written. What lies
+ * outside a row's keys may be anything, a group of NaN that another row sees too.
+ * Supported: as dense_extend, with rows = 32 and keys = 128.
+ */
+size_t dense_extend_kv4_workspace_bytes(const art_shape* shape, int32_t num_tokens, int32_t group);
+int dense_extend_kv4(const void* q, const void* cache, int32_t group, const int32_t* block_table,
+                     const int32_t* seq_lens, const int32_t* q_offsets, int32_t num_tokens, int32_t causal,
+                     void* out, const art_shape* shape, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Copies the device status word out of `workspace` (a blocking copy; call it
  * after the stream has finished the call of interest). Returns ART_OK or
  * ART_ERR_INVALID_ARG / ART_ERR_LAUNCH. */

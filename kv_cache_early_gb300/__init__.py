@@ -3,7 +3,7 @@
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels of libart.so. The names follow the C ABI: `art_decode`,
 `dense_decode`, `art_append_kv`, `dense_extend`, `dense_decode_shared`,
-`art_workspace_bytes`, `art_read_device_status`.
+`art_append_kv4`, `art_read_kv4`, `dense_extend_kv4`, `art_workspace_bytes`, `art_read_device_status`.
 Tensors are torch CUDA tensors; PyTorch supplies device memory and streams.
 
 The library must have been built (`kv_cache_early_gb300.build.build()`);
@@ -29,7 +29,10 @@ EXPORTS = ("art_workspace_bytes", "art_decode_path", "dense_decode_path", "art_d
            "art_status_string", "art_last_cuda_error", "art_set_timing_events",
            "art_select_workspace_bytes", "art_select_blocks",
            "art_append_workspace_bytes", "art_append_kv", "dense_extend_workspace_bytes", "dense_extend",
-           "dense_decode_shared_workspace_bytes", "dense_decode_shared")
+           "dense_decode_shared_workspace_bytes", "dense_decode_shared",
+           "art_kv4_page_bytes", "art_append_kv4_workspace_bytes", "art_append_kv4",
+           "art_read_kv4_workspace_bytes", "art_read_kv4",
+           "dense_extend_kv4_workspace_bytes", "dense_extend_kv4")
 
 
 class ArtShape(ctypes.Structure):
@@ -108,6 +111,20 @@ def lib(path: str = LIB_PATH) -> ctypes.CDLL:
             L.dense_decode_shared_workspace_bytes.restype = SZ
             L.dense_decode_shared.argtypes = [P, P, P, P, P, P, P, I32, P, SP, P, SZ, P]
             L.dense_decode_shared.restype = ctypes.c_int
+            L.art_kv4_page_bytes.argtypes = [SP, I32]
+            L.art_kv4_page_bytes.restype = SZ
+            L.art_append_kv4_workspace_bytes.argtypes = [SP]
+            L.art_append_kv4_workspace_bytes.restype = SZ
+            L.art_append_kv4.argtypes = [P, P, P, I64, I64, I64, P, I32, P, P, P, P, RP, P, P, I32, SP, P, SZ, P]
+            L.art_append_kv4.restype = ctypes.c_int
+            L.art_read_kv4_workspace_bytes.argtypes = [SP]
+            L.art_read_kv4_workspace_bytes.restype = SZ
+            L.art_read_kv4.argtypes = [P, I32, P, P, P, I32, P, I32, P, P, SP, P, SZ, P]
+            L.art_read_kv4.restype = ctypes.c_int
+            L.dense_extend_kv4_workspace_bytes.argtypes = [SP, I32, I32]
+            L.dense_extend_kv4_workspace_bytes.restype = SZ
+            L.dense_extend_kv4.argtypes = [P, P, I32, P, P, P, I32, I32, P, SP, P, SZ, P]
+            L.dense_extend_kv4.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -432,6 +449,178 @@ def dense_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offset
                                seq_lens.data_ptr(), _addr(group_offsets), _addr(prefix_lens), groups,
                                out.data_ptr(), ctypes.byref(shape), workspace.data_ptr(), workspace.nbytes,
                                _raw_stream(stream, device))
+    if check and rc != ART_OK:
+        _check(rc)
+    return rc
+
+
+def _append_checked(q, k, v, block_table, seq_lens, q_offsets, inv_freq, q_out, shape, workspace, rot_dim, positions,
+                    device):
+    """Checks the tensors of an append into a cache in 4 bits; returns the strides of q, k and v."""
+    torch = _t()
+    i32, dt = torch.int32, torch.bfloat16 if shape.dtype == ART_DTYPE_BF16 else torch.float32
+    batch, hq, hkv, d = shape.batch, shape.num_q_heads, shape.num_kv_heads, shape.head_dim
+    tokens = k.shape[0]
+    # a lone row's stride is never used: any whole one
+    many = tokens > 1
+    qs = 0
+    dense = True
+    if q is not None:
+        st = q.stride()
+        qs = st[0] if many else hq * d
+        dense = (q.dtype is dt and q.get_device() == device and q.shape == (tokens, hq, d) and
+                 (tokens == 0 or (st[2] == 1 and (hq == 1 or st[1] == d))))
+    sk, sv = k.stride(), v.stride()
+    ks, vs = (sk[0], sv[0]) if many else (hkv * d, hkv * d)
+    rows = (tokens, hkv, d)
+    if not (dense and k.dtype is dt and v.dtype is dt and k.shape == rows and v.shape == rows and
+            k.get_device() == device and v.get_device() == device and
+            (tokens == 0 or (sk[2] == 1 and sv[2] == 1 and (hkv == 1 or (sk[1] == d and sv[1] == d)))) and
+            (q_out is None or (q_out.dtype is dt and q_out.shape == (tokens, hq, d) and q_out.is_contiguous() and
+                               q_out.get_device() == device)) and
+            block_table.dtype is i32 and block_table.shape == (batch, shape.max_pages_per_seq) and
+            block_table.is_contiguous() and block_table.get_device() == device and
+            seq_lens.dtype is i32 and seq_lens.shape == (batch,) and seq_lens.is_contiguous() and
+            seq_lens.get_device() == device and
+            (q_offsets is None or (q_offsets.dtype is i32 and q_offsets.shape == (batch + 1,) and
+                                   q_offsets.is_contiguous() and q_offsets.get_device() == device)) and
+            (positions is None or (positions.dtype is i32 and positions.shape == (tokens,) and
+                                   positions.is_contiguous() and positions.get_device() == device)) and
+            (inv_freq is None or (inv_freq.dtype is torch.float32 and inv_freq.shape == (rot_dim // 2,) and
+                                  inv_freq.get_device() == device and inv_freq.is_contiguous())) and
+            workspace.get_device() == device and workspace.is_contiguous()):
+        _refuse(device, dt, (("q_out", q_out, (tokens, hq, d)),),
+                (("block_table", block_table, (batch, shape.max_pages_per_seq)), ("seq_lens", seq_lens, (batch,)),
+                 ("q_offsets", q_offsets, (batch + 1,)), ("positions", positions, (tokens,))))
+        _refuse(device, torch.float32, (("inv_freq", inv_freq, (rot_dim // 2,)),), ())
+        _refuse(device, workspace.dtype, (("workspace", workspace, None),), ())
+        raise ArtError("q, k and v are not [tokens, heads, head_dim] rows of the shape's dtype on the cache's device, "
+                       "dense in their last two dimensions: " +
+                       ", ".join(f"{tuple(t.shape)} {t.dtype} strides {t.stride()}" for t in (q, k, v) if t is not None))
+    return qs, ks, vs
+
+
+def art_kv4_page_bytes(shape: ArtShape, group: int) -> int:
+    """Bytes of one page of one KV head of a cache in 4 bits; raises where the sizes are not supported."""
+    n = int(lib().art_kv4_page_bytes(ctypes.byref(shape), int(group)))
+    if n == 0:
+        raise ArtError(f"no cache in 4 bits for this shape with groups of {group} columns")
+    return n
+
+
+_page_bytes = {}  # by (head_dim, page_size, group): a program has one or two
+
+
+def _kv4_cache(cache, shape, group):
+    """Checks the cache tensor's type and sizes; returns the device."""
+    key = shape.head_dim, shape.page_size, int(group)
+    n = _page_bytes.get(key)
+    if n is None:
+        if len(_page_bytes) >= 64:
+            _page_bytes.clear()
+        n = _page_bytes.setdefault(key, art_kv4_page_bytes(shape, group))
+    torch = _t()
+    device = _device_of(cache)
+    sizes = (shape.num_pages_total, shape.num_kv_heads, n)
+    if not (cache.dtype is torch.uint8 and cache.shape == sizes and cache.is_contiguous() and
+            torch.cuda.current_device() == device):
+        _refuse(device, torch.uint8, (("cache", cache, sizes),), ())
+    return device
+
+
+def art_append_kv4_workspace_bytes(shape: ArtShape) -> int:
+    return int(lib().art_append_kv4_workspace_bytes(ctypes.byref(shape)))
+
+
+def art_append_kv4(q, k, v, block_table, seq_lens, q_offsets, inv_freq, q_out, cache, shape: ArtShape, workspace,
+                   group: int, rot_dim: int, interleaved: bool = False, scale: float = 1.0, positions=None, stream=None,
+                   check: bool = True) -> int:
+    """art_append_kv into a cache held in 4 bits (see include/art.h): cache is uint8
+    [num_pages_total, num_kv_heads, art_kv4_page_bytes(shape, group)]."""
+    L = _lib or lib()
+    device = _kv4_cache(cache, shape, group)
+    qs, ks, vs = _append_checked(q, k, v, block_table, seq_lens, q_offsets, inv_freq, q_out, shape, workspace, rot_dim,
+                                 positions, device)
+    rc = L.art_append_kv4(_addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(q_offsets), k.shape[0],
+                          _addr(positions), block_table.data_ptr(), seq_lens.data_ptr(), _addr(inv_freq),
+                          ctypes.byref(_rope(rot_dim, interleaved, scale)), _addr(q_out), cache.data_ptr(), int(group),
+                          ctypes.byref(shape), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, device))
+    if check and rc != ART_OK:
+        _check(rc)
+    return rc
+
+
+def art_read_kv4_workspace_bytes(shape: ArtShape) -> int:
+    return int(lib().art_read_kv4_workspace_bytes(ctypes.byref(shape)))
+
+
+def art_read_kv4(cache, block_table, seq_lens, q_offsets, k_out, v_out, shape: ArtShape, workspace, group: int,
+                 out_table=None, stream=None, check: bool = True) -> int:
+    """Read cached keys and values back from 4 bits (see include/art.h). out_table None: rows
+    [tokens, num_kv_heads, head_dim] of the last tokens of each sequence (q_offsets None: of the
+    last one); with out_table, all tokens into the pages of a plain cache."""
+    L = _lib or lib()
+    torch = _t()
+    i32, dt = torch.int32, torch.bfloat16 if shape.dtype == ART_DTYPE_BF16 else torch.float32
+    device = _kv4_cache(cache, shape, group)
+    batch, hkv, d = shape.batch, shape.num_kv_heads, shape.head_dim
+    table = (batch, shape.max_pages_per_seq)
+    n = k_out.shape[0]
+    rows = (n, hkv, d) if out_table is None else (n, hkv, shape.page_size, d)
+    if not (k_out.dtype is dt and k_out.shape == rows and k_out.is_contiguous() and k_out.get_device() == device and
+            v_out.dtype is dt and v_out.shape == rows and v_out.is_contiguous() and v_out.get_device() == device and
+            block_table.dtype is i32 and block_table.shape == table and block_table.is_contiguous() and
+            block_table.get_device() == device and
+            seq_lens.dtype is i32 and seq_lens.shape == (batch,) and seq_lens.is_contiguous() and
+            seq_lens.get_device() == device and
+            (q_offsets is None or (q_offsets.dtype is i32 and q_offsets.shape == (batch + 1,) and
+                                   q_offsets.is_contiguous() and q_offsets.get_device() == device)) and
+            (out_table is None or (out_table.dtype is i32 and out_table.shape == table and
+                                   out_table.is_contiguous() and out_table.get_device() == device)) and
+            workspace.get_device() == device and workspace.is_contiguous()):
+        _refuse(device, dt, (("k_out", k_out, rows), ("v_out", v_out, rows)),
+                (("block_table", block_table, table), ("seq_lens", seq_lens, (batch,)),
+                 ("q_offsets", q_offsets, (batch + 1,)), ("out_table", out_table, table)))
+        _refuse(device, workspace.dtype, (("workspace", workspace, None),), ())
+    rc = L.art_read_kv4(cache.data_ptr(), int(group), block_table.data_ptr(), seq_lens.data_ptr(), _addr(q_offsets),
+                        n if out_table is None else 0, _addr(out_table), 0 if out_table is None else n,
+                        k_out.data_ptr(), v_out.data_ptr(), ctypes.byref(shape), workspace.data_ptr(),
+                        workspace.nbytes, _raw_stream(stream, device))
+    if check and rc != ART_OK:
+        _check(rc)
+    return rc
+
+
+def dense_extend_kv4_workspace_bytes(shape: ArtShape, num_tokens: int, group: int) -> int:
+    return int(lib().dense_extend_kv4_workspace_bytes(ctypes.byref(shape), int(num_tokens), int(group)))
+
+
+def dense_extend_kv4(q, cache, block_table, seq_lens, q_offsets, out, shape: ArtShape, workspace, group: int,
+                     causal: bool = True, stream=None, check: bool = True) -> int:
+    """dense_extend over a cache held in 4 bits (see include/art.h); q_offsets None: one new token for
+    each sequence (a decode step)."""
+    L = _lib or lib()
+    torch = _t()
+    i32, dt = torch.int32, torch.bfloat16 if shape.dtype == ART_DTYPE_BF16 else torch.float32
+    device = _kv4_cache(cache, shape, group)
+    batch, tokens = shape.batch, q.shape[0]
+    rows, table = (tokens, shape.num_q_heads, shape.head_dim), (batch, shape.max_pages_per_seq)
+    if not (q.dtype is dt and q.shape == rows and q.is_contiguous() and q.get_device() == device and
+            out.dtype is dt and out.shape == rows and out.is_contiguous() and out.get_device() == device and
+            block_table.dtype is i32 and block_table.shape == table and block_table.is_contiguous() and
+            block_table.get_device() == device and
+            seq_lens.dtype is i32 and seq_lens.shape == (batch,) and seq_lens.is_contiguous() and
+            seq_lens.get_device() == device and
+            (q_offsets is None or (q_offsets.dtype is i32 and q_offsets.shape == (batch + 1,) and
+                                   q_offsets.is_contiguous() and q_offsets.get_device() == device)) and
+            workspace.get_device() == device and workspace.is_contiguous()):
+        _refuse(device, dt, (("q", q, rows), ("out", out, rows)),
+                (("block_table", block_table, table), ("seq_lens", seq_lens, (batch,)),
+                 ("q_offsets", q_offsets, (batch + 1,))))
+        _refuse(device, workspace.dtype, (("workspace", workspace, None),), ())
+    rc = L.dense_extend_kv4(q.data_ptr(), cache.data_ptr(), int(group), block_table.data_ptr(), seq_lens.data_ptr(),
+                            _addr(q_offsets), tokens, 1 if causal else 0, out.data_ptr(), ctypes.byref(shape),
+                            workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, device))
     if check and rc != ART_OK:
         _check(rc)
     return rc

@@ -1,0 +1,386 @@
+// art_append_kv4.cu -- appending new tokens to a cache that is held in 4 bits: rotation,
+// quantisation and the write in one kernel.
+//
+// Keys and queries are turned as in art_append.cu. A turned key is rounded to the cache's type;
+// then, of the values x of a token's group of columns of a key or value head,
+//     lowest = the largest bf16 that is no larger than min x
+//     step   = the bf16 nearest to (max x - lowest) / 15
+//     code   = the whole number nearest to (x - lowest) / step, 15 at most
+// with ties to even, all as in exact arithmetic. So the cache holds the same bits on any machine
+// and a test can ask for equality; a border between two codes moves by nothing. What that takes:
+//   - the angle's sine and cosine as sums of two fp32 numbers (turn_exact, within 1e-11), the
+//     products x cos and y sin with their rounding errors (by the fused product) and the sum with
+//     its own (Knuth's two-sum): the turned key's rounding to fp32, and from there to bf16, is
+//     then the exact one's but for about one value in 10^8;
+//   - x - lowest with its rounding error, and where the quotient by the rounded 1 / step comes
+//     near a border, the sign of (x - lowest) - border * step, whose terms are exact (a border is
+//     a half-integer up to 15, step has 8 bits).
+// bf16 inputs meet ties often, since step and x lie on grids, so this is no rare matter.
+//
+// One kernel. Block 0 checks the call's device data and stores the status word. The next blocks
+// rotate queries (append_rows of art_append.cuh, without keys and values), the last ones take
+// tiles of tokens' keys and values: a thread has 8 columns of a row, the lanes of a group of
+// columns find its least and largest value by shuffles, and the eight codes are one 32-bit store.
+// Neighbouring threads take the same columns of neighbouring tokens' rows, so that the stores of
+// a tile fill whole 128-byte units of the cache.
+#include "art_append.cuh"
+#include "art_kv4.cuh"
+
+namespace art {
+
+// Up to these many tokens a CTA takes one token's keys and values, beyond it kKvTile's.
+constexpr int kFewTokensKv4 = 608;
+constexpr int kKvTile = 8;
+
+struct AppendKv4Params {
+    AppendParams a;
+    unsigned char* cache;
+    int slab, slab_bytes, page_bytes;
+    int q_blocks;  // blocks that rotate queries
+};
+
+// sin(n pi / 32), n = 0 .. 16, as a sum of two fp32 numbers.
+__device__ const float2 kSin32[17] = {
+    {0.0f, 0.0f},
+    {0x1.917a6cp-4f, -0x1.eb25eap-31f},
+    {0x1.8f8b84p-3f, -0x1.cb2cfap-30f},
+    {0x1.294062p-2f, 0x1.dab3e0p-27f},
+    {0x1.87de2ap-2f, 0x1.abaa58p-28f},
+    {0x1.e2b5d4p-2f, -0x1.fe4272p-28f},
+    {0x1.1c73b4p-1f, -0x1.9465cep-27f},
+    {0x1.44cf32p-1f, 0x1.424776p-27f},
+    {0x1.6a09e6p-1f, 0x1.9fcef4p-27f},
+    {0x1.8bc806p-1f, 0x1.62a2e8p-26f},
+    {0x1.a9b662p-1f, 0x1.21d434p-26f},
+    {0x1.c38b30p-1f, -0x1.cfe84ap-26f},
+    {0x1.d906bcp-1f, 0x1.e651a8p-26f},
+    {0x1.e9f416p-1f, -0x1.273a44p-26f},
+    {0x1.f6297cp-1f, 0x1.feeb96p-26f},
+    {0x1.fd88dap-1f, 0x1.e89292p-28f},
+    {1.0f, 0.0f}};
+
+// sin(n pi / 32), n >= 0
+__device__ __forceinline__ float2 sin32(int n) {
+    const int m = n & 31;
+    const float2 v = kSin32[m <= 16 ? m : 32 - m];
+    return n & 32 ? make_float2(-v.x, -v.y) : v;
+}
+
+// a b + c d (+ low) as a sum of two fp32 numbers
+__device__ __forceinline__ float2 dot2(float a, float b, float c, float d, float low) {
+    const float p = __fmul_rn(a, b), pe = fmaf(a, b, -p), q = __fmul_rn(c, d), qe = fmaf(c, d, -q);
+    const float s = __fadd_rn(p, q), t = __fadd_rn(s, -p);
+    const float se = __fadd_rn(__fadd_rn(p, -__fadd_rn(s, -t)), __fadd_rn(q, -t));
+    const float e = se + ((pe + qe) + low), h = __fadd_rn(s, e);
+    return make_float2(h, __fadd_rn(__fadd_rn(s, -h), e));
+}
+
+// Cosine and sine of pos * f times `scale`, each as a sum of two fp32 numbers (cos, cos low, sin,
+// sin low). The turn r + low is n steps of pi / 32 and a rest t + tail with |t| < 0.05; n C1 is exact
+// (C1 has 17 bits), and so is r - n C1. cos and sin of the rest by their series, what is above
+// 2^-40 of them with its rounding errors, then the sums of angles with table values.
+__device__ __forceinline__ float4 turn_exact(int pos, float f, float scale) {
+    constexpr float C1 = 0x1.921fp-4f, C2 = 0x1.6a8886p-21f;  // pi / 32 = C1 + C2 - 1.03e-14
+    float r, low;
+    turn_reduce(pos, f, r, low);
+    const bool neg = r < 0.f;
+    r = fabsf(r);
+    low = neg ? -low : low;
+    const float k = rintf(r * 10.185916f);
+    const int n = (int)k;  // turn_reduce may leave a little more than half a turn
+    const float t1 = fmaf(-k, C1, r), m = __fmul_rn(k, C2), ml = fmaf(k, C2, -m);
+    const float t = __fadd_rn(t1, -m), tb = __fadd_rn(t, -t1);
+    const float tail = (__fadd_rn(__fadd_rn(t1, -__fadd_rn(t, -tb)), -__fadd_rn(m, tb)) - ml) + low;
+    const float z = __fmul_rn(t, t), zl = fmaf(t, t, -z);
+    // sin(t + tail) = t + sl, cos(t + tail) = 1 + a + al
+    const float sl = fmaf(tail, 1.f - 0.5f * z, t * z * (-1.6666667e-1f + z * (8.3333333e-3f - z * 1.9841270e-4f)));
+    const float a = -0.5f * z, al = fmaf(z * z, 4.1666667e-2f - z * 1.3888889e-3f, -0.5f * zl) - tail * t;
+    const float2 S = sin32(n), C = sin32(n + 16);
+    // C cos - S sin = C + (C a - S t + ...), S cos + C sin = S + (S a + C t + ...)
+    const float2 dc = dot2(C.x, a, -S.x, t, C.x * al - S.x * sl + fmaf(C.y, a, C.y) - S.y * t);
+    const float2 ds = dot2(S.x, a, C.x, t, S.x * al + C.x * sl + fmaf(S.y, a, S.y) + C.y * t);
+    auto sum = [](float h, float2 d) {  // |h| may be smaller than |d.x|
+        const float s = __fadd_rn(h, d.x), b = __fadd_rn(s, -h);
+        const float e = __fadd_rn(__fadd_rn(h, -__fadd_rn(s, -b)), __fadd_rn(d.x, -b)) + d.y;
+        return make_float2(s, e);
+    };
+    float2 c = sum(C.x, dc), s = sum(S.x, ds);
+    if (neg) s = make_float2(-s.x, -s.y);
+    if (scale != 1.f) {
+        auto times = [&](float2 x) {
+            const float h = __fmul_rn(x.x, scale);
+            return make_float2(h, fmaf(x.y, scale, fmaf(x.x, scale, -h)));
+        };
+        c = times(c);
+        s = times(s);
+    }
+    return make_float4(c.x, c.y, s.x, s.y);
+}
+
+// x cos + y sin, rounded to the cache's type. Where its fp32 rounding is the middle between two
+// bf16 numbers, what that rounding left decides.
+template <bool kBF16>
+__device__ __forceinline__ float turned(float x, float y, const float4& cs) {
+    const float2 v = dot2(x, cs.x, y, cs.z, fmaf(x, cs.y, y * cs.w));
+    if constexpr (!kBF16) return v.x;
+    uint32_t u = __float_as_uint(v.x);
+    if ((u & 0xffffu) == 0x8000u && v.y != 0.f) u += (v.y > 0.f) == (v.x > 0.f) ? 1 : -1;
+    return bf16_lo_f(pack_bf16(__uint_as_float(u), 0.f));
+}
+
+// The larger and the smaller number; not a number where one of them is none.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+constexpr float kMaxRange = 0x1.ep103f;   // 15 * 2^100: groups of such a range, and those with an infinity or NaN, become NaN
+constexpr float kMinStep = 0x1p-100f;     // smaller steps are zero
+
+// The largest bf16 number that is no larger than x.
+__device__ __forceinline__ float floor_bf16(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const uint32_t up = (u >> 31) & ((u & 0xffffu) != 0u);
+    return __uint_as_float((u & 0xffff0000u) + (up << 16));
+}
+
+// The codes of the thread's 8 values, the first in the lowest bits, and (step, lowest) of its
+// group of `kLanes` threads (consecutive lanes from a multiple of kLanes).
+template <int kLanes>
+__device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& scales) {
+    float mn = x[0], mx = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        mn = min_nan(mn, x[i]);
+        mx = max_nan(mx, x[i]);
+    }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) {
+        mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    }
+    const float low = floor_bf16(mn);
+    const float d = __fadd_rn(mx, -low);
+    if (!(d < kMaxRange)) {
+        scales = 0x7fc00000u;
+        return 0u;
+    }
+    // (d + de) / 15 = q + rest
+    const float b = __fadd_rn(d, -mx);
+    const float de = __fadd_rn(__fadd_rn(mx, -__fadd_rn(d, -b)), -__fadd_rn(low, b));
+    const float q = __fdiv_rn(d, 15.f), rest = fmaf(-15.f, q, d) + de;
+    uint32_t u = __float_as_uint(q);
+    if ((u & 0xffffu) == 0x8000u && rest != 0.f) u += rest > 0.f ? 1 : -1;
+    float step = bf16_lo_f(pack_bf16(__uint_as_float(u), 0.f));
+    if (step < kMinStep) step = 0.f;
+    scales = (__float_as_uint(step) >> 16) | __float_as_uint(low);
+    const float inv = step > 0.f ? __frcp_rn(step) : 0.f;
+    uint32_t codes = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = __fadd_rn(x[i], -low), v = t * inv;
+        const float m = __fadd_rn(v, 12582912.f);  // 1.5 * 2^23: to the nearest whole number, even at ties
+        uint32_t c = __float_as_uint(m) & 31u;
+        const float off = __fadd_rn(v, -__fadd_rn(m, -12582912.f));
+        if (fabsf(off) > 0.49998f) {  // v is within 16 * 3 * 2^-24 of x - low over step
+            const float h = floorf(v) + 0.5f, hs = h * step;  // the border; exact
+            const float bb = __fadd_rn(t, -x[i]);
+            const float te = __fadd_rn(__fadd_rn(x[i], -__fadd_rn(t, -bb)), -__fadd_rn(low, bb));
+            const float side = __fadd_rn(__fadd_rn(t, -hs), te);
+            const uint32_t f = (uint32_t)(int)h;
+            c = side > 0.f ? f + 1 : side < 0.f ? f : f + (f & 1u);
+        }
+        codes |= min(c, 15u) << (4 * i);
+    }
+    return codes;
+}
+
+// Keys and values of tokens kTok * tile ..
+// kVec: columns turn in whole units of 8 (rot_dim, or its half where the pairs are (j, j + rot_dim / 2)).
+template <bool kBF16, int D, int NG, bool kVec, int kTok>
+__device__ __forceinline__ void append_kv4_tile(const AppendKv4Params& pp, int tile) {
+    const AppendParams& p = pp.a;
+    constexpr int PER = D / 8;                       // units of a row
+    constexpr int RPS = kAppendThreads / PER;        // rows of a step of the CTA
+    constexpr int N = kBF16 ? 1 : 2;                 // 16-byte chunks of a unit
+    __shared__ float4 s_cs[kTok][8][kMaxRotHalf / 8 + 1];  // of frequency j: [j % 8][j / 8], neighbouring units in other banks
+    __shared__ int s_place[kTok], s_page[kTok], s_state[kTok];
+    const int t0 = tile * kTok, tid = threadIdx.x, ntok = min(kTok, p.T - t0), half = p.rot / 2;
+    const int ch = tid % PER, e0 = ch * 8;
+    const bool turns = e0 < p.rot;
+    // row R: keys, then values; of a head, the tokens side by side
+    auto split = [&](int R, int& tok, int& g, bool& key) {
+        tok = R % kTok;
+        const int h = R / kTok;
+        key = h < p.Hkv;
+        g = key ? h : h - p.Hkv;
+    };
+    auto row_of = [&](int tok, int g, bool key) -> const char* {
+        const size_t t = (size_t)(t0 + tok);
+        return static_cast<const char*>(key ? p.k : p.v) +
+               (t * (size_t)(key ? p.k_stride : p.v_stride) + (size_t)g * D) * (kBF16 ? 2 : 4);
+    };
+    const int partner = p.interleaved ? e0 : e0 < half ? e0 + half : e0 - half;  // kVec: of the unit's first column
+    uint4 a[N], b[N];
+    auto load = [&](int R) {
+        int tok, g;
+        bool key;
+        split(R, tok, g, key);
+        if (R >= 2 * p.Hkv * kTok || tok >= ntok) return;
+        const char* row = row_of(tok, g, key);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            a[i] = reinterpret_cast<const uint4*>(row)[ch * N + i];
+            if (kVec && key && turns && !p.interleaved) b[i] = reinterpret_cast<const uint4*>(row)[partner / 8 * N + i];
+        }
+    };
+    load(tid / PER);
+    append_places<kTok>(p, t0, ntok, s_place, s_page, s_state);
+    for (int x = tid; x < ntok * half; x += kAppendThreads) {
+        const int tok = x / half, j = x - tok * half;
+        s_cs[tok][j & 7][j >> 3] = turn_exact(p.positions ? p.positions[t0 + tok] : s_place[tok], p.inv_freq[j], p.scale);
+    }
+    __syncthreads();
+    for (int R0 = 0; R0 < 2 * p.Hkv * kTok; R0 += RPS) {  // whole warps: the lanes of a row exchange values
+        const int R = R0 + tid / PER;
+        if (R0 > 0) load(R);
+        int tok, g;
+        bool key;
+        split(R, tok, g, key);
+        const bool live = R < 2 * p.Hkv * kTok && tok < ntok && s_state[tok] == kStateOk && s_page[tok] >= 0;
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+        if (live) {
+            auto unpack = [&](const uint4 (&u)[N], float (&o)[8]) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const Vec16<kBF16> v(u[i]);
+#pragma unroll
+                    for (int e = 0; e < Vec16<kBF16>::N; ++e) o[i * Vec16<kBF16>::N + e] = v.x[e];
+                }
+            };
+            unpack(a, x);
+            if (key && turns) {
+                float y[8], o[8];
+                if constexpr (kVec) {
+                    unpack(b, y);
+                    const int jb = p.interleaved ? e0 / 2 : e0 < half ? e0 : e0 - half;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int j = p.interleaved ? jb + e / 2 : jb + e;
+                        const float4 cs = s_cs[tok][j & 7][j >> 3];
+                        const bool second = p.interleaved ? e & 1 : e0 >= half;
+                        const float other = p.interleaved ? x[e ^ 1] : y[e];
+                        o[e] = turned<kBF16>(x[e], second ? other : -other, cs);
+                    }
+                } else {
+                    const char* row = row_of(tok, g, key);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int c = e0 + e;
+                        o[e] = x[e];
+                        if (c >= p.rot) continue;
+                        const int j = p.interleaved ? c / 2 : c < half ? c : c - half;
+                        const bool second = p.interleaved ? c & 1 : c >= half;
+                        const int other = p.interleaved ? c ^ 1 : second ? c - half : c + half;
+                        float v;
+                        if constexpr (kBF16) v = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[other] << 16);
+                        else v = reinterpret_cast<const float*>(row)[other];
+                        o[e] = turned<kBF16>(x[e], second ? v : -v, s_cs[tok][j & 7][j >> 3]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = o[e];
+            }
+        }
+        uint32_t scales;
+        const uint32_t codes = quantise<D / NG / 8>(x, scales);
+        if (!live) continue;
+        const int in_page = s_place[tok] & (p.Ps - 1), u = in_page & (pp.slab - 1);
+        unsigned char* slab = pp.cache + ((size_t)s_page[tok] * p.Hkv + g) * (size_t)pp.page_bytes +
+                              (size_t)(in_page / pp.slab) * pp.slab_bytes;
+        *reinterpret_cast<uint32_t*>(slab + (key ? 0 : pp.slab * (D / 2)) + kv4_code_at<D>(u, ch >> 2) + (ch & 3) * 4) = codes;
+        if (ch % (PER / NG) == 0)
+            *reinterpret_cast<uint32_t*>(slab + pp.slab * (D + (key ? 0 : 4 * NG)) + kv4_scale_at<NG>(u, ch / (PER / NG))) = scales;
+    }
+}
+
+// kVecQ: append_rows takes queries in whole chunks; kVec: append_kv4_tile its units.
+template <bool kBF16, int D, int NG, bool kVecQ, bool kVec, int kTokQ, int kTok>
+__global__ void __launch_bounds__(kAppendThreads) art_append_kv4_kernel(const AppendKv4Params p) {
+    if (blockIdx.x == 0) append_check(p.a);
+    else if ((int)blockIdx.x <= p.q_blocks) append_rows<kBF16, D, kVecQ, kTokQ>(p.a, 0, blockIdx.x - 1);
+    else append_kv4_tile<kBF16, D, NG, kVec, kTok>(p, blockIdx.x - 1 - p.q_blocks);
+}
+
+template <bool kBF16, int D, int NG>
+static void launch_append_kv4(AppendKv4Params& p, cudaStream_t st) {
+    const int turn = p.a.interleaved ? p.a.rot : p.a.rot / 2;
+    const bool vec = turn % 8 == 0, vec_q = turn % (kBF16 ? 8 : 4) == 0;
+    const bool few = p.a.T <= kFewTokensKv4;
+    const int tq = few ? 1 : 2, tk = few ? 1 : kKvTile;
+    p.q_blocks = p.a.q ? (p.a.T + tq - 1) / tq : 0;
+    const unsigned grid = 1u + (unsigned)p.q_blocks + (unsigned)((p.a.T + tk - 1) / tk);
+#define ART_APPEND4(VQ, V)                                                                                       \
+    (few ? art_append_kv4_kernel<kBF16, D, NG, VQ, V, 1, 1><<<grid, kAppendThreads, 0, st>>>(p)                 \
+         : art_append_kv4_kernel<kBF16, D, NG, VQ, V, 2, kKvTile><<<grid, kAppendThreads, 0, st>>>(p))
+    if (vec) ART_APPEND4(true, true);
+    else if (vec_q) ART_APPEND4(true, false);
+    else ART_APPEND4(false, false);
+#undef ART_APPEND4
+}
+
+}  // namespace art
+
+using namespace art;
+
+extern "C" {
+
+size_t art_kv4_page_bytes(const art_shape* shape, int32_t group) {
+    if (check_cache_shape(shape) != ART_OK || !kv4_group_ok(shape->head_dim, group)) return 0;
+    return (size_t)kv4_layout(shape->page_size, shape->head_dim, group).page_bytes;
+}
+
+size_t art_append_kv4_workspace_bytes(const art_shape* shape) { return shape ? sizeof(WsHeader) : 0; }
+
+int art_append_kv4(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                   const int32_t* q_offsets, int32_t num_tokens, const int32_t* positions, const int32_t* block_table,
+                   const int32_t* seq_lens, const float* inv_freq, const art_rope* rope, void* q_out, void* cache,
+                   int32_t group, const art_shape* shape, void* workspace, size_t workspace_bytes, void* stream) {
+    AppendKv4Params p;
+    const int rc = append_setup(p.a, q, k, v, q_stride, k_stride, v_stride, q_offsets, num_tokens, positions, block_table,
+                                seq_lens, inv_freq, rope, q_out, cache, cache, shape, workspace, workspace_bytes);
+    if (rc == ART_OK || rc == ART_ERR_WORKSPACE)
+        if (!kv4_group_ok(shape->head_dim, group)) return ART_ERR_UNSUPPORTED;
+    if (rc != ART_OK) return rc;
+    // blocks for queries and for keys and values
+    if (num_tokens > 0x3fffffff) return ART_ERR_UNSUPPORTED;
+    const art_shape& s = *shape;
+    p.cache = static_cast<unsigned char*>(cache);
+    const Kv4Layout l = kv4_layout(s.page_size, s.head_dim, group);
+    p.slab = l.slab;
+    p.slab_bytes = l.slab_bytes;
+    p.page_bytes = l.page_bytes;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int ng = s.head_dim / group;
+    const bool bf = s.dtype == ART_DTYPE_BF16;
+    if (s.head_dim == 128) {
+        if (ng == 1) bf ? launch_append_kv4<true, 128, 1>(p, st) : launch_append_kv4<false, 128, 1>(p, st);
+        else if (ng == 2) bf ? launch_append_kv4<true, 128, 2>(p, st) : launch_append_kv4<false, 128, 2>(p, st);
+        else bf ? launch_append_kv4<true, 128, 4>(p, st) : launch_append_kv4<false, 128, 4>(p, st);
+    } else {
+        if (ng == 1) bf ? launch_append_kv4<true, 64, 1>(p, st) : launch_append_kv4<false, 64, 1>(p, st);
+        else bf ? launch_append_kv4<true, 64, 2>(p, st) : launch_append_kv4<false, 64, 2>(p, st);
+    }
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? ART_OK : cuda_fail(e);
+}
+
+}  // extern "C"

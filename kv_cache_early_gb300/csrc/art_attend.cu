@@ -230,9 +230,7 @@ int check_cache_shape(const art_shape* s) {
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Sizes and workspace layout of a call; returns the bytes, or 0 where they pass the
-// supported range. `base` null: only the bytes.
-static size_t attend_layout(AttendParams& p, unsigned char* base) {
+size_t attend_layout(AttendParams& p, unsigned char* base) {
     p.G = p.Hq / p.Hkv;
     p.NE = p.shared ? p.NG + p.B : p.B;
     const long long rows = (long long)(p.shared ? p.B : p.T) * p.G;  // of one KV head
@@ -279,7 +277,7 @@ static size_t attend_layout(AttendParams& p, unsigned char* base) {
 // items at {9, 20, 30} instead of {13, 35, 50} chunks 315, a document 117, mixed 60.7.
 constexpr CostRule kCostBf16 = {13, 7, 35, 11, 50, 13}, kCostF32 = {10, 8, 10, 16, 10, 16};
 
-static void fill_shape(AttendParams& p, const art_shape& s) {
+void attend_shape(AttendParams& p, const art_shape& s) {
     p.B = s.batch;
     p.Hq = s.num_q_heads;
     p.Hkv = s.num_kv_heads;
@@ -297,7 +295,8 @@ static void fill_shape(AttendParams& p, const art_shape& s) {
     p.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)s.head_dim));
 }
 
-static int attend_run(AttendParams& p, const art_shape& s, void* workspace, size_t workspace_bytes, cudaStream_t st) {
+int attend_run(AttendParams& p, const art_shape& s, void* workspace, size_t workspace_bytes, cudaStream_t st,
+               AttendLaunch launch, const void* more) {
     const size_t need = attend_layout(p, nullptr);
     if (need == 0) return ART_ERR_UNSUPPORTED;
     if (workspace_bytes < need) return ART_ERR_WORKSPACE;
@@ -318,7 +317,9 @@ static int attend_run(AttendParams& p, const art_shape& s, void* workspace, size
         }
     }
     const bool bf = s.dtype == ART_DTYPE_BF16;
-    if ((e = bf ? launch_attend_tc(p, st) : launch_attend_simt(p, st)) != cudaSuccess) return cuda_fail(e);
+    if (launch) e = launch(p, more, st);
+    else e = bf ? launch_attend_tc(p, st) : launch_attend_simt(p, st);
+    if (e != cudaSuccess) return cuda_fail(e);
     // the merge kernel's launch overlaps the main kernel's end
     const long long blocks = p.shared ? ((long long)p.B * p.Hq + kMergeBlock / 32 - 1) / (kMergeBlock / 32) : p.ctas;
     const dim3 grid((unsigned)(blocks < 8LL * p.ctas ? blocks : 8LL * p.ctas), p.shared ? 1 : p.rt / 16);
@@ -347,7 +348,7 @@ extern "C" {
 size_t dense_extend_workspace_bytes(const art_shape* shape, int32_t num_tokens) {
     if (check_cache_shape(shape) != ART_OK || num_tokens < 0) return 0;
     AttendParams p = {};
-    fill_shape(p, *shape);
+    attend_shape(p, *shape);
     p.T = num_tokens;
     return attend_layout(p, nullptr);
 }
@@ -363,7 +364,7 @@ int dense_extend(const void* q, const void* k_cache, const void* v_cache, const 
         return ART_ERR_INVALID_ARG;
     if (num_tokens < 0 || (causal != 0 && causal != 1)) return ART_ERR_INVALID_ARG;
     AttendParams p = {};
-    fill_shape(p, *shape);
+    attend_shape(p, *shape);
     p.q = q;
     p.k = k_cache;
     p.v = v_cache;
@@ -379,7 +380,7 @@ int dense_extend(const void* q, const void* k_cache, const void* v_cache, const 
 size_t dense_decode_shared_workspace_bytes(const art_shape* shape, int32_t num_groups) {
     if (check_cache_shape(shape) != ART_OK || num_groups < 0) return 0;
     AttendParams p = {};
-    fill_shape(p, *shape);
+    attend_shape(p, *shape);
     p.shared = 1;
     p.NG = num_groups;
     return attend_layout(p, nullptr);
@@ -396,7 +397,7 @@ int dense_decode_shared(const void* q, const void* k_cache, const void* v_cache,
     if (misaligned(q) || misaligned(k_cache) || misaligned(v_cache) || misaligned(out) || misaligned(workspace))
         return ART_ERR_INVALID_ARG;
     AttendParams p = {};
-    fill_shape(p, *shape);
+    attend_shape(p, *shape);
     p.shared = 1;
     p.q = q;
     p.k = k_cache;

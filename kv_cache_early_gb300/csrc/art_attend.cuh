@@ -172,6 +172,16 @@ inline cudaError_t launch_after(void (*kernel)(A...), dim3 grid, dim3 block, siz
 // num_probe are not used).
 int check_cache_shape(const art_shape* s);
 
+// Sizes and costs of a call by its shape (bf16, fp32 caches).
+void attend_shape(AttendParams& p, const art_shape& s);
+// Sizes and workspace layout of a call; returns the bytes, or 0 where they pass the
+// supported range. `base` null: only the bytes.
+size_t attend_layout(AttendParams& p, unsigned char* base);
+// The main kernel (`launch`, given `more`; null: the one of the shape's type) and the merge kernel.
+using AttendLaunch = cudaError_t (*)(const AttendParams& p, const void* more, cudaStream_t st);
+int attend_run(AttendParams& p, const art_shape& s, void* workspace, size_t workspace_bytes, cudaStream_t st,
+               AttendLaunch launch = nullptr, const void* more = nullptr);
+
 cudaError_t launch_attend_simt(const AttendParams& p, cudaStream_t st);  // fp32
 cudaError_t launch_attend_tc(const AttendParams& p, cudaStream_t st);    // bf16
 
