@@ -6,7 +6,7 @@
 namespace art {
 
 // Cost units of items and of their tiles of 128 keys, by rows (8, more).
-constexpr CostRule kCostKv4 = {13, 5, 13, 9, 13, 9};
+constexpr CostRule kCostKv4 = {13, 5, 13, 8, 13, 8};
 
 static void kv4_shape(AttendParams& p, const art_shape& s) {
     attend_shape(p, s);

@@ -3,10 +3,15 @@
 // With K = low + step c in each group of columns (c the codes) the products need the codes only:
 //     q . k_t = sum_g step_tg (sum_{j in g} q_j c_tj) + low_tg (sum_{j in g} q_j)
 //     o_j     = sum_t (p_t step_tg) c_tj + p_t low_tg
-// so codes are never turned into values: they enter the matrix product as fp16, where the four
-// bits of a code, moved to the lowest bits, ARE the number code * 2^-24 (a denormal), and moved to
-// the next four code * 2^-20. Eight codes of a 32-bit word become four operand registers by four
-// masks and one shift; 2^24 and the 16 of the odd ones go into queries and results.
+// so codes are never turned into values: they enter the matrix product as fp16. Four bits moved to
+// the lowest ones ARE the number code * 2^-24 (a denormal), moved to the next four code * 2^-20, so
+// eight codes of a 32-bit word become four operand registers by four masks and a shift: the keys'
+// of bf16 calls; 2^24 and the 16 of the odd ones go into queries and results. The products'
+// sums take a denormal's place for that of 2^-14 and cut off what lies 2^24 below, which leaves
+// about 17 bits. The values' codes, and fp32 calls' keys', are taken less 8 (and low more by 8 step)
+// by one more fp16 sum: all of one sign, their sums over many tokens are far larger than what is
+// left of them (an fp32 decode of 100 to 4000 tokens was 3.9e-5 from the exact result without it,
+// 8e-6 with denormals less 8, NNN so).
 //
 // S^T = C Q^T and O^T = C^T W^T, keys or columns in the 16 rows of mma.sync 16 x 8 x 16, up to
 // eight query rows in its columns, so no row of the product is padding where eight rows attend
@@ -20,11 +25,16 @@
 // stays within fp16's range whatever the values' scales are, and the row's sum l is brought to
 // [1, 2) before parts meet. Queries are scaled by a power of two to fp16's range.
 //
-// One CTA per SM: a producer warp (page ids 32 at a time, one bulk copy for each slab of a page,
-// art_kv4.cuh) fills a ring of tiles of 128 keys; 8 consumer warps in two groups of four take
-// alternate tiles, a warp 32 keys of each. Up to 8 rows: 32 keys at a time, two chains of
-// products; up to 16: two column tiles. 17 to 32 rows: the groups take 16 rows each, and every tile.
-// Each warp has its own reference, sums and O; they meet at the segment's end.
+// One CTA per SM, 12 warps, which meet at barriers in shared memory only:
+//   producer   page ids 32 at a time, one bulk copy for each slab of a page (art_kv4.cuh), into a ring of
+//              tiles of 128 keys
+//   queries    turns the next segment's queries into operands, in shared memory
+//   8 consumers in two groups of four that take alternate tiles, a warp 32 keys of each, with a
+//              reference, sums and O of its own. Up to 8 rows: 32 keys at a time, two chains of products
+//              and the queries in registers; up to 24: 16 keys at a time and two or three column tiles, for
+//              which the codes are taken apart once
+//   2 mergers  join the consumers' parts of a segment, eight rows at a time, and store them, while the
+//              consumers are at the next one
 //
 // Keys and values outside a segment's keys may be anything: codes are always finite numbers, and
 // scales of keys that a row does not see are not used for it.
@@ -35,11 +45,14 @@
 
 namespace art {
 
-constexpr int kRowsKv4 = 32;  // rows of an item's tile
-constexpr int kKv4Consumers = 8, kKv4Threads = (kKv4Consumers + 1) * 32;
+constexpr int kRowsKv4 = 24;  // rows of an item's tile
+constexpr int kKv4Consumers = 8, kKv4Mergers = 2, kKv4Threads = (kKv4Consumers + kKv4Mergers + 2) * 32;
 // A row's reference is set so that its largest weight times step is about 2^kKv4Lift, and moves when
 // one passes 2^kKv4Most: fp16 holds 11 bits of whatever is within 2^-19 of the largest.
 constexpr float kKv4Lift = 5.f, kKv4Most = 14.f;
+constexpr uint32_t kMostWeight = 0x74007400u;  // 2^14, twice
+constexpr float kMostSum = 0x1p100f;           // of weights without steps, which may be as small as 2^-80
+constexpr float kNoReference = -1e30f;  // of a row that has seen no key: any key's weight passes the limit
 
 struct AttendKv4Params {
     AttendParams a;
@@ -47,26 +60,35 @@ struct AttendKv4Params {
     int slab, slab_bytes, page_bytes, bf16;
 };
 
-template <int D, int NG>
+template <bool kBF16, int D, int NG>
 struct Kv4Cfg {
+    static constexpr int NC = D / 32;                     // 32-column chunks
+    static constexpr int KP = kBF16 ? 1 : 2;              // fp16 parts of a query and of a weight
     static constexpr int TILE = kKeyTile * (D + 8 * NG);  // bytes of a tile
     static constexpr int EXROW = D + 4;                   // floats of a row in the exchange area
     static constexpr int EX = kKv4Consumers * 8 * EXROW * 4;
-    static constexpr int NS = (220 * 1024 - EX) / TILE < 16 ? (220 * 1024 - EX) / TILE : 16;  // ring stages
-    static constexpr int EXOFF = NS * TILE;
-    static constexpr int CTRL = EXOFF + EX;
+    static constexpr int QTILE = KP * NC * 512;           // bytes of the operands of 8 rows
+    static constexpr int Q = 3 * QTILE;
+    static constexpr int NS0 = (224 * 1024 - EX - 2 * Q) / TILE;
+    static constexpr int NS = NS0 < 16 ? NS0 : 16;        // ring stages
+    static constexpr int EXOFF = NS * TILE, QOFF = EXOFF + EX, CTRL = QOFF + 2 * Q;
 };
 
-template <int NS>
+template <int NS, int NG>
 struct alignas(16) Kv4Ctrl {
-    uint64_t full[NS], empty[NS], cons, stall;
+    uint64_t full[NS], empty[NS], q_full[2], q_free[2], ex_full, ex_free, stall;
+    struct Rows {  // of a segment's queries: factor of the products, the groups' sums, limit
+        float f[kRowsKv4], sum[NG][kRowsKv4];
+        int lim[kRowsKv4];
+    } rows[2];
     float2 ml[kKv4Consumers][8];
     int abort, seg0, seg1;
 };
 
-template <int D, int NG>
+template <bool kBF16, int D, int NG>
 constexpr size_t kv4_smem() {
-    return (size_t)Kv4Cfg<D, NG>::CTRL + sizeof(Kv4Ctrl<Kv4Cfg<D, NG>::NS>);
+    using C = Kv4Cfg<kBF16, D, NG>;
+    return (size_t)C::CTRL + sizeof(Kv4Ctrl<C::NS, NG>);
 }
 
 // d[0..3] += A(16x16 fp16, row) * B(16x8 fp16, col)
@@ -90,8 +112,30 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t v) {
         : "r"(v));
     return make_float2(lo, hi);
 }
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
+__device__ __forceinline__ uint32_t add_f16(uint32_t a, uint32_t c) {  // two sums
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_f16(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ bool any_above(uint32_t a, uint32_t limit) {  // of two fp16 numbers
+    uint32_t r;
+    asm("{\n\t.reg .pred p, q;\n\tsetp.gt.f16x2 p|q, %1, %2;\n\tor.pred p, p, q;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(limit));
+    return r != 0;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ void lds128(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
 // 2^e for -126 <= e <= 127
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
@@ -99,9 +143,10 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t
 // ---------------------------------------------------------------------------
 // producer warp
 // ---------------------------------------------------------------------------
-template <int D, int NG>
-__device__ void kv4_producer(const AttendKv4Params& pp, unsigned char* gen, Kv4Ctrl<Kv4Cfg<D, NG>::NS>* c, int s0, int s1) {
-    using C = Kv4Cfg<D, NG>;
+template <bool kBF16, int D, int NG>
+__device__ void kv4_producer(const AttendKv4Params& pp, unsigned char* gen, Kv4Ctrl<Kv4Cfg<kBF16, D, NG>::NS, NG>* c, int s0,
+                             int s1) {
+    using C = Kv4Cfg<kBF16, D, NG>;
     const AttendParams& p = pp.a;
     const int lane = threadIdx.x & 31;
     const int ppt = kKeyTile / pp.slab;  // slabs of a tile (2 .. 16)
@@ -175,66 +220,25 @@ __device__ void kv4_producer(const AttendKv4Params& pp, unsigned char* gen, Kv4C
 }
 
 // ---------------------------------------------------------------------------
-// consumer warps
+// query warp
 // ---------------------------------------------------------------------------
 template <bool kBF16, int D, int NG>
-struct Kv4Consumer {
-    using C = Kv4Cfg<D, NG>;
-    static constexpr int NC = D / 32;       // 32-column chunks
-    static constexpr int CPG = NC / NG;     // ... of a group
-    static constexpr int KP = kBF16 ? 1 : 2;  // fp16 parts of a query and of a weight
-    const AttendKv4Params& pp;
-    const AttendParams& p;
-    Kv4Ctrl<C::NS>* c;
-    uint32_t smem;
-    unsigned char* gen;
-    int w, lane;
-    uint32_t ph_c = 0;
-    int odd = 0;  // which group of warps takes the next tile
-    Stage<C::NS> st;
-
-    __device__ __forceinline__ bool wait(uint64_t* b, uint32_t ph) { return wait_tc(b, ph, &c->abort, p); }
-    __device__ __forceinline__ bool sync() {  // all consumer warps
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->cons);
-        const bool ok = wait(&c->cons, ph_c);
-        ph_c ^= 1u;
-        return ok;
-    }
-    // codes of 8 tokens: a word a chunk of 32 columns. `o`: offset in shared memory of the octets' codes
-    template <bool kTrans>
-    __device__ __forceinline__ void codes(uint32_t oa, uint32_t ob, uint32_t (&wa)[NC], uint32_t (&wb)[NC]) const {
-        if constexpr (NC == 4) {
-            if constexpr (kTrans) {
-                ldsm_x4_t(oa + lane * 16, wa[0], wa[1], wa[2], wa[3]);
-                ldsm_x4_t(ob + lane * 16, wb[0], wb[1], wb[2], wb[3]);
-            } else {
-                ldsm_x4(oa + lane * 16, wa[0], wa[1], wa[2], wa[3]);
-                ldsm_x4(ob + lane * 16, wb[0], wb[1], wb[2], wb[3]);
-            }
-        } else {
-            const uint32_t o = lane < 16 ? oa + lane * 16 : ob + (lane - 16) * 16;
-            if constexpr (kTrans) ldsm_x4_t(o, wa[0], wa[1], wb[0], wb[1]);
-            else ldsm_x4(o, wa[0], wa[1], wb[0], wb[1]);
-        }
-    }
-
-    // The rows r0 .. r0 + 8 NT - 1 of a segment, by this warp, over its tiles. dual: the other group
-    // of warps has other rows and takes every tile, too. KM: steps of 16 keys taken together.
-    template <int NT, int KM>
-    __device__ bool rows(const Seg& sg, int r0, bool dual, int t0, int nt) {
-        const int gq = lane >> 2, tq = lane & 3;
-        const int grp = w >> 2, sub = w & 3;
-        constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
-
-        // queries: lane (gq, tq) has row gq of each column tile, columns 32 chunk + 8 tq ..
-        uint32_t qb[KP][NT][NC][4];
-        uint64_t F2[NT], qs2[NT][NG];  // of rows 2 tq and 2 tq + 1: factor of the products, the groups' sums of q
-        int lim[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
+__device__ void kv4_queries(const AttendParams& p, unsigned char* gen, Kv4Ctrl<Kv4Cfg<kBF16, D, NG>::NS, NG>* c, int s0, int s1) {
+    using C = Kv4Cfg<kBF16, D, NG>;
+    constexpr int NC = C::NC, CPG = NC / NG;
+    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+    int k = 0;
+    for (int si = s0; si < s1; ++si) {
+        const Seg sg = load_seg(&p.seg[si]);
+        if (sg.nrow == 0) continue;
+        const int buf = k & 1;
+        if (k >= 2 && !wait_tc(&c->q_free[buf], (uint32_t)((k >> 1) - 1) & 1u, &c->abort, p)) return;
+        ++k;
+#pragma unroll 1
+        for (int n = 0; n * 8 < sg.nrow; ++n) {
+            // lane (gq, tq): row gq of the tile, columns 32 chunk + 8 tq ..
             float x[NC][8];
-            const size_t row = row_index(p, sg, min(r0 + n * 8 + gq, sg.nrow - 1));
+            const size_t row = row_index(p, sg, min(n * 8 + gq, sg.nrow - 1));
 #pragma unroll
             for (int ch = 0; ch < NC; ++ch) {
                 if constexpr (kBF16) {
@@ -248,8 +252,8 @@ struct Kv4Consumer {
                 } else {
                     const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + row * D + ch * 32) + 2 * tq;
                     const float4 u = __ldg(q), v = __ldg(q + 1);
-                    x[ch][0] = u.x; x[ch][1] = u.y; x[ch][2] = u.z; x[ch][3] = u.w;
-                    x[ch][4] = v.x; x[ch][5] = v.y; x[ch][6] = v.z; x[ch][7] = v.w;
+                    x[ch][0] = u.x, x[ch][1] = u.y, x[ch][2] = u.z, x[ch][3] = u.w;
+                    x[ch][4] = v.x, x[ch][5] = v.y, x[ch][6] = v.z, x[ch][7] = v.w;
                 }
             }
             float qs[NG], top = 0.f;
@@ -263,45 +267,188 @@ struct Kv4Consumer {
                     top = fmaxf(top, fabsf(x[ch][e]));
                 }
 #pragma unroll
-            for (int k = 1; k <= 2; k <<= 1) {
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+            for (int o = 1; o <= 2; o <<= 1) {
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll
-                for (int g = 0; g < NG; ++g) qs[g] += __shfl_xor_sync(0xffffffffu, qs[g], k);
+                for (int g = 0; g < NG; ++g) qs[g] += __shfl_xor_sync(0xffffffffu, qs[g], o);
             }
             // the row times 2^-e lies below 2^14
             const int e = min(max((int)(__float_as_uint(top) >> 23) - 127 - 13, -100), 113);
-            const float down = pow2i(-e), F = pow2i(e) * p.scale_log2;
+            const float down = pow2i(-e);
+            uint4* dst = reinterpret_cast<uint4*>(gen + C::QOFF + buf * C::Q + n * C::QTILE) + lane;
 #pragma unroll
-            for (int ch = 0; ch < NC; ++ch)
+            for (int ch = 0; ch < NC; ++ch) {
+                uint32_t u[C::KP][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {  // columns i and i + 4; the odd ones meet codes times 16
                     const float f = i & 1 ? down * 0.0625f : down;
                     const float a = x[ch][i] * f, b = x[ch][i + 4] * f;
-                    qb[0][n][ch][i] = pack_f16(a, b);
-                    if constexpr (KP == 2) {
-                        const float2 h = unpack_f16(qb[0][n][ch][i]);
-                        qb[1][n][ch][i] = pack_f16(a - h.x, b - h.y);
+                    u[0][i] = pack_f16(a, b);
+                    if constexpr (C::KP == 2) {
+                        const float2 h = unpack_f16(u[0][i]);
+                        u[1][i] = pack_f16(a - h.x, b - h.y);
                     }
                 }
-            // what the lanes of the results need: rows 2 tq, 2 tq + 1 (lanes 8 tq and 8 tq + 4 have them)
-            F2[n] = pk2(__shfl_sync(0xffffffffu, F, 8 * tq) * 16777216.f, __shfl_sync(0xffffffffu, F, 8 * tq + 4) * 16777216.f);
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const float s = qs[g] * p.scale_log2;
-                qs2[n][g] = pk2(__shfl_sync(0xffffffffu, s, 8 * tq), __shfl_sync(0xffffffffu, s, 8 * tq + 4));
+                for (int i = 0; i < C::KP; ++i) dst[(i * NC + ch) * 32] = make_uint4(u[i][0], u[i][1], u[i][2], u[i][3]);
             }
-            lim[n][0] = row_limit(p, sg, r0 + n * 8 + 2 * tq);
-            lim[n][1] = row_limit(p, sg, r0 + n * 8 + 2 * tq + 1);
-        }
-        // keys beyond khi nobody sees; below klo + 1 everybody (of the rows that are there)
-        int khi = sg.k0, klo = sg.k1;
+            if (tq == 0) {
+                const int r = n * 8 + gq;
+                c->rows[buf].f[r] = pow2i(e) * p.scale_log2 * (kBF16 ? 16777216.f : 1.f);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+                for (int g = 0; g < NG; ++g) c->rows[buf].sum[g][r] = qs[g] * p.scale_log2;
+                c->rows[buf].lim[r] = row_limit(p, sg, r);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->q_full[buf]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// merger warps
+// ---------------------------------------------------------------------------
+template <bool kBF16, int D, int NG>
+__device__ void kv4_mergers(const AttendParams& p, unsigned char* gen, Kv4Ctrl<Kv4Cfg<kBF16, D, NG>::NS, NG>* c, int s0, int s1) {
+    using C = Kv4Cfg<kBF16, D, NG>;
+    const int lane = threadIdx.x & 31, tid = threadIdx.x - kKv4Consumers * 32;
+    const float* ex = reinterpret_cast<const float*>(gen + C::EXOFF);
+    uint32_t ph = 0;
+    Seg nx = load_seg(&p.seg[s0]);
+    for (int si = s0; si < s1; ++si) {
+        const Seg sg = nx;
+        if (si + 1 < s1) nx = load_seg(&p.seg[si + 1]);
+#pragma unroll 1
+        for (int n = 0; n * 8 < sg.nrow; ++n) {
+            if (!wait_tc(&c->ex_full, ph, &c->abort, p)) return;
+            ph ^= 1u;
+            const int rows = min(8, sg.nrow - n * 8);
+#pragma unroll 1
+            for (int u = tid; u < rows * (D / 4); u += kKv4Mergers * 32) {
+                const int r = u / (D / 4), col = (u - r * (D / 4)) * 4, rr = n * 8 + r;
+                float2 ml[kKv4Consumers];
+                float mm = -INFINITY, ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < kKv4Consumers; ++k) {
+                    ml[k] = c->ml[k][r];
+                    mm = fmaxf(mm, ml[k].x);
+                }
+#pragma unroll
+                for (int k = 0; k < kKv4Consumers; ++k) {
+                    const float f = ml[k].y == 0.f ? 0.f : ex2(ml[k].x - mm);  // saw no key: its sums are zero
+                    const float4 v = *reinterpret_cast<const float4*>(ex + (k * 8 + r) * C::EXROW + col);
+                    ll = fmaf(ml[k].y, f, ll);
+                    acc[0] = fmaf(v.x, f, acc[0]);
+                    acc[1] = fmaf(v.y, f, acc[1]);
+                    acc[2] = fmaf(v.z, f, acc[2]);
+                    acc[3] = fmaf(v.w, f, acc[3]);
+                }
+                if (sg.prow >= 0) {
+                    *reinterpret_cast<float4*>(part_at(p, sg, rr, col)) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                    if (col == 0) p.part_ml[sg.prow + rr] = make_float2(mm, ll);
+                    continue;
+                }
+                const float inv = ll > 0.f ? 1.f / ll : ll;  // no key seen: 0; NaN stays
+                const size_t at = row_index(p, sg, rr) * D + col;
+                if constexpr (kBF16)
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+                        make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+                else
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
+                        make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->ex_free);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// consumer warps
+// ---------------------------------------------------------------------------
+template <bool kBF16, int D, int NG>
+struct Kv4Consumer {
+    using C = Kv4Cfg<kBF16, D, NG>;
+    static constexpr int NC = C::NC, CPG = NC / NG, KP = C::KP;
+    const AttendKv4Params& pp;
+    const AttendParams& p;
+    Kv4Ctrl<C::NS, NG>* c;
+    uint32_t smem;
+    unsigned char* gen;
+    int w, lane;
+    uint32_t ph_ex = 0;
+    int odd = 0;    // which group of warps takes the next tile
+    int segs = 0;   // segments so far
+    bool ex_used = false;
+    Stage<C::NS> st;
+
+    __device__ __forceinline__ bool wait(uint64_t* b, uint32_t ph) { return wait_tc(b, ph, &c->abort, p); }
+
+    // codes of two octets of tokens: a word a chunk of 32 columns. `oa`, `ob`: shared-memory addresses, this lane's
+    // 16 bytes of each (head_dim 64: of one of them)
+    template <bool kTrans>
+    __device__ __forceinline__ static void codes(uint32_t oa, uint32_t ob, uint32_t (&wa)[NC], uint32_t (&wb)[NC]) {
+        if constexpr (NC == 4) {
+            if constexpr (kTrans) {
+                ldsm_x4_t(oa, wa[0], wa[1], wa[2], wa[3]);
+                ldsm_x4_t(ob, wb[0], wb[1], wb[2], wb[3]);
+            } else {
+                ldsm_x4(oa, wa[0], wa[1], wa[2], wa[3]);
+                ldsm_x4(ob, wb[0], wb[1], wb[2], wb[3]);
+            }
+        } else {
+            const uint32_t o = (threadIdx.x & 16) ? ob : oa;
+            if constexpr (kTrans) ldsm_x4_t(o, wa[0], wa[1], wb[0], wb[1]);
+            else ldsm_x4(o, wa[0], wa[1], wb[0], wb[1]);
+        }
+    }
+    // the operand registers of a chunk: codes 0 | 1 (times 16) of octets a, b, then codes 2 | 3, as code * 2^-24, or
+    // (kLess) less 8: 2^10 + code, by its bits, less 2^10 + 8
+    template <bool kLess>
+    __device__ __forceinline__ static void apart(uint32_t wa, uint32_t wb, uint32_t (&a0)[4], uint32_t (&a1)[4]) {
+        constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u, K = kLess ? 0x64006400u : 0u;
+        const uint32_t ua = wa >> 8, ub = wb >> 8;
+        a0[0] = wa & M0 | K, a0[1] = wa & M1 | K, a0[2] = wb & M0 | K, a0[3] = wb & M1 | K;
+        a1[0] = ua & M0 | K, a1[1] = ua & M1 | K, a1[2] = ub & M0 | K, a1[3] = ub & M1 | K;
+        if constexpr (kLess)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a0[i] = add_f16(a0[i], i & 1 ? 0xe480e480u : 0xe408e408u);  // -1152, -1032
+                a1[i] = add_f16(a1[i], i & 1 ? 0xe480e480u : 0xe408e408u);
+            }
+    }
+
+    // A segment's rows, eight to each of NT tiles, by this warp over its keys. KM: steps of 16 keys taken together.
+    template <int NT, int KM>
+    __device__ bool rows(const Seg& sg, int t0, int nt) {
+        const int gq = lane >> 2, tq = lane & 3, grp = w >> 2, sub = w & 3;
+        const int buf = segs & 1;
+        if (!wait(&c->q_full[buf], (uint32_t)(segs >> 1) & 1u)) return false;
+        const uint32_t qaddr = smem + C::QOFF + buf * C::Q + lane * 16;
+        constexpr bool kQRegs = NT == 1;  // the queries stay in registers
+        uint32_t qr[kQRegs ? KP : 1][kQRegs ? NC : 1][4];
+        if constexpr (kQRegs)
+#pragma unroll
+            for (int k = 0; k < KP; ++k)
+#pragma unroll
+                for (int ch = 0; ch < NC; ++ch) lds128(qaddr + (k * NC + ch) * 512, qr[k][ch]);
+        uint64_t F2[NT], qs2[NT][NG];  // of rows 2 tq and 2 tq + 1
+        int lim[NT][2], khi = sg.k0, klo = sg.k1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = n * 8 + 2 * tq;
+            F2[n] = *reinterpret_cast<const uint64_t*>(&c->rows[buf].f[r]);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) qs2[n][g] = *reinterpret_cast<const uint64_t*>(&c->rows[buf].sum[g][r]);
+            lim[n][0] = c->rows[buf].lim[r];
+            lim[n][1] = c->rows[buf].lim[r + 1];
+            // keys from khi on nobody sees; those below klo everybody (of the rows that are there)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 khi = max(khi, lim[n][i]);
-                if (r0 + n * 8 + 2 * tq + i < sg.nrow) klo = min(klo, lim[n][i]);
+                if (r + i < sg.nrow) klo = min(klo, lim[n][i]);
             }
+        }
         khi = __reduce_max_sync(0xffffffffu, khi);
         klo = __reduce_min_sync(0xffffffffu, klo);
 
@@ -310,7 +457,7 @@ struct Kv4Consumer {
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                R[n][i] = -INFINITY;
+                R[n][i] = kNoReference;
                 l[n][i] = 0.f;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) L[n][g][i] = 0.f;
@@ -318,21 +465,19 @@ struct Kv4Consumer {
 #pragma unroll
             for (int k = 0; k < 2 * NC; ++k) o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
         }
-        // the octets of this warp's 32 keys in a tile
-        uint32_t at[4];
-        {
-            const int per = pp.slab >> 3;
+        // the octets of this warp's 32 keys in a tile: its bytes of the keys' codes, and its keys' scales
+        uint32_t kc[4], sc[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int oct = sub * 4 + k;
-                at[k] = (uint32_t)(oct / per * pp.slab_bytes) | ((uint32_t)(oct % per) << 20);
-            }
+        for (int k = 0; k < 4; ++k) {
+            const int per = pp.slab >> 3, oct = sub * 4 + k, slab = oct / per, in = oct - slab * per;
+            kc[k] = smem + slab * pp.slab_bytes + in * (4 * D) + (NC == 4 ? lane : lane & 15) * 16;
+            sc[k] = smem + slab * pp.slab_bytes + pp.slab * D + in * (32 * NG) + gq * 4;
         }
-        const uint32_t v_codes = pp.slab * (D / 2), scales = pp.slab * D, v_scales = pp.slab * 4 * NG;
+        const uint32_t v_codes = pp.slab * (D / 2), v_scales = pp.slab * 4 * NG;
 
 #pragma unroll 1
         for (int j = 0; j < nt; ++j) {
-            const bool own = dual || odd == grp;
+            const bool own = odd == grp;
             odd ^= 1;
             if (!own) {
                 st.next();
@@ -349,50 +494,59 @@ struct Kv4Consumer {
                 float s[KM][NT][4];
                 uint32_t pv[KM][2][NG];  // (step, lowest) of the values of keys gq and gq + 8
                 bool vis[KM][NT][4];
-                uint32_t base_a[KM], base_b[KM];
 #pragma unroll
                 for (int m = 0; m < KM; ++m) {
-                    // octets 2 (h + m) and 2 (h + m) + 1 of the slice
-                    const uint32_t xa = KM == 2 ? at[2 * m] : h ? at[2] : at[0], xb = KM == 2 ? at[2 * m + 1] : h ? at[3] : at[1];
-                    const uint32_t sa = smem + tile + (xa & 0xfffffu), sb = smem + tile + (xb & 0xfffffu);
-                    const uint32_t ia = xa >> 20, ib = xb >> 20;
-                    base_a[m] = sa + ia * (8 * D / 2);
-                    base_b[m] = sb + ib * (8 * D / 2);
-                    uint32_t pk[2][NG];
+                    const uint32_t ka = tile + (KM == 2 ? kc[2 * m] : h ? kc[2] : kc[0]), kb2 = tile + (KM == 2 ? kc[2 * m + 1] : h ? kc[3] : kc[1]);
+                    const uint32_t sa = tile + (KM == 2 ? sc[2 * m] : h ? sc[2] : sc[0]), sb = tile + (KM == 2 ? sc[2 * m + 1] : h ? sc[3] : sc[1]);
+                    uint32_t pk[2][NG], wa[NC], wb[NC];
+                    codes<false>(ka, kb2, wa, wb);
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
-                        const uint32_t ka = sa + scales + (ia * NG + g) * 32 + gq * 4, kb2 = sb + scales + (ib * NG + g) * 32 + gq * 4;
-                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(pk[0][g]) : "r"(ka));
-                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(pk[1][g]) : "r"(kb2));
-                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(pv[m][0][g]) : "r"(ka + v_scales));
-                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(pv[m][1][g]) : "r"(kb2 + v_scales));
+                        pk[0][g] = lds32(sa + g * 32);
+                        pk[1][g] = lds32(sb + g * 32);
+                        pv[m][0][g] = lds32(sa + v_scales + g * 32);
+                        pv[m][1][g] = lds32(sb + v_scales + g * 32);
                     }
-                    uint32_t wa[NC], wb[NC];
-                    codes<false>(base_a[m], base_b[m], wa, wb);
                     uint64_t tot[NT][2], lo2[NT][2];  // of keys gq, gq + 8: rows 2 tq, 2 tq + 1
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
-                        float acc[NT][4];
+                        float acc[KP][NT][4];  // the parts apart: sums of the second are far smaller
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+                        for (int k = 0; k < KP; ++k)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) acc[k][n][0] = acc[k][n][1] = acc[k][n][2] = acc[k][n][3] = 0.f;
 #pragma unroll
                         for (int ch = g * CPG; ch < (g + 1) * CPG; ++ch) {
-                            const uint32_t ua = wa[ch] >> 8, ub = wb[ch] >> 8;
+                            uint32_t a0[4], a1[4];
+                            apart<!kBF16>(wa[ch], wb[ch], a0, a1);
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
 #pragma unroll
                                 for (int k = 0; k < KP; ++k) {
-                                    mma_f16(acc[n], wa[ch] & M0, wb[ch] & M0, wa[ch] & M1, wb[ch] & M1, qb[k][n][ch][0], qb[k][n][ch][1]);
-                                    mma_f16(acc[n], ua & M0, ub & M0, ua & M1, ub & M1, qb[k][n][ch][2], qb[k][n][ch][3]);
+                                    uint32_t q4[4];
+                                    if constexpr (kQRegs) {
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) q4[i] = qr[k][ch][i];
+                                    } else {
+                                        lds128(qaddr + n * C::QTILE + (k * NC + ch) * 512, q4);
+                                    }
+                                    mma_f16(acc[k][n], a0[0], a0[2], a0[1], a0[3], q4[0], q4[1]);
+                                    mma_f16(acc[k][n], a1[0], a1[2], a1[1], a1[3], q4[2], q4[3]);
                                 }
                         }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float step = bf16_lo_f(pk[i][g]), low = bf16_hi_f(pk[i][g]);
+                            const float step = bf16_lo_f(pk[i][g]);
+                            const float low = kBF16 ? bf16_hi_f(pk[i][g]) : fmaf(8.f, step, bf16_hi_f(pk[i][g]));
                             const uint64_t step2 = pk2(step, step), low2 = pk2(low, low);
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                const uint64_t a2 = pk2(acc[n][2 * i], acc[n][2 * i + 1]);
+                                float x = acc[0][n][2 * i], y = acc[0][n][2 * i + 1];
+                                if constexpr (KP == 2) {
+                                    x += acc[1][n][2 * i];
+                                    y += acc[1][n][2 * i + 1];
+                                }
+                                const uint64_t a2 = pk2(x, y);
                                 tot[n][i] = g == 0 ? mul2(a2, step2) : fma2(a2, step2, tot[n][i]);
                                 lo2[n][i] = g == 0 ? mul2(low2, qs2[n][g]) : fma2(low2, qs2[n][g], lo2[n][i]);
                             }
@@ -416,24 +570,59 @@ struct Kv4Consumer {
                         }
                     }
                 }
-                // references: above score + log2 of the values' step (the largest of the groups')
-                bool rise = false;
-                float ev[KM][2];
+                // Weights against the references as they are; where a weight times its step, or a row's sum, goes
+                // too far, the references move and they are formed once more.
+                float pr[KM][NT][4], ln[NT][2];
+                uint32_t wf[KP][KM][NT][NG][2];
+#pragma unroll 1
+                for (bool again = false;; again = true) {
+                    uint32_t most = 0;
+                    bool far = false;
 #pragma unroll
-                for (int m = 0; m < KM; ++m)
+                    for (int n = 0; n < NT; ++n) {
+                        ln[n][0] = l[n][0];
+                        ln[n][1] = l[n][1];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t x = pv[m][i][0] & 0x7f80u;
+                        for (int m = 0; m < KM; ++m)
 #pragma unroll
-                        for (int g = 1; g < NG; ++g) x = max(x, pv[m][i][g] & 0x7f80u);
-                        x = min(max(x >> 7, 27u), 227u);  // 2^-100 .. 2^100
-                        ev[m][i] = __uint_as_float(0x4b000000u | x) - (8388608.f + 127.f);
+                            for (int i = 0; i < 2; ++i) {
+                                const float p0 = ex2(s[m][n][2 * i] - R[n][0]), p1 = ex2(s[m][n][2 * i + 1] - R[n][1]);
+                                pr[m][n][2 * i] = p0;
+                                pr[m][n][2 * i + 1] = p1;
+                                ln[n][0] += p0;
+                                ln[n][1] += p1;
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) rise |= s[m][n][2 * i + e] + ev[m][i] > R[n][e] + kKv4Most;
+                                for (int g = 0; g < NG; ++g) {
+                                    const float step = bf16_lo_f(pv[m][i][g]);
+                                    float w0 = p0 * step, w1 = p1 * step;
+                                    if (!whole) {  // scales that a row does not see may be no numbers
+                                        if (!vis[m][n][2 * i]) w0 = 0.f;
+                                        if (!vis[m][n][2 * i + 1]) w1 = 0.f;
+                                    }
+                                    const uint32_t u = pack_f16(w0, w1);
+                                    wf[0][m][n][g][i] = u;
+                                    most = max_f16(most, u);
+                                    if constexpr (KP == 2) {
+                                        const float2 hi = unpack_f16(u);
+                                        wf[1][m][n][g][i] = pack_f16(w0 - hi.x, w1 - hi.y);
+                                    }
+                                }
+                            }
+                        far |= fmaxf(ln[n][0], ln[n][1]) > kMostSum;
                     }
-                if (__any_sync(0xffffffffu, rise)) {
+                    if (again || !__any_sync(0xffffffffu, far || any_above(most, kMostWeight))) break;
+                    // up to the maximum of score + log2 of the values' step (the largest of the groups')
+                    float ev[KM][2];
+#pragma unroll
+                    for (int m = 0; m < KM; ++m)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t x = pv[m][i][0] & 0x7f80u;
+#pragma unroll
+                            for (int g = 1; g < NG; ++g) x = max(x, pv[m][i][g] & 0x7f80u);
+                            x = min(max(x >> 7, 47u), 227u);  // 2^-80 .. 2^100
+                            ev[m][i] = __uint_as_float(0x4b000000u | x) - (8388608.f + 127.f);
+                        }
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -444,7 +633,7 @@ struct Kv4Consumer {
                                 top = fmaxf(top, fmaxf(s[m][n][e] + ev[m][0], s[m][n][2 + e] + ev[m][1]));
 #pragma unroll
                             for (int k = 4; k <= 16; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-                            if (top > R[n][e] + kKv4Most) {  // the same for all lanes of the row
+                            if (top > R[n][e] + (kKv4Most - 1.f)) {  // the same for all lanes of the row
                                 top = ceilf(top) - kKv4Lift;
                                 const float f = ex2(R[n][e] - top);
                                 R[n][e] = top;
@@ -459,144 +648,117 @@ struct Kv4Consumer {
                             }
                         }
                 }
-                // weights, and the products with the values' codes
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    l[n][0] = ln[n][0];
+                    l[n][1] = ln[n][1];
+                }
+                // what is multiplied by low, and the products with the values' codes
 #pragma unroll
                 for (int m = 0; m < KM; ++m) {
-                    uint32_t wf[KP][NT][NG][2];
+                    uint32_t wa[NC], wb[NC];
+                    codes<true>(tile + v_codes + (KM == 2 ? kc[2 * m] : h ? kc[2] : kc[0]),
+                                tile + v_codes + (KM == 2 ? kc[2 * m + 1] : h ? kc[3] : kc[1]), wa, wb);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float xr0 = R[n][0] == -INFINITY ? 0.f : R[n][0], xr1 = R[n][1] == -INFINITY ? 0.f : R[n][1];
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float p0 = ex2(s[m][n][2 * i] - xr0), p1 = ex2(s[m][n][2 * i + 1] - xr1);
-                            l[n][0] += p0;
-                            l[n][1] += p1;
+                        for (int g = 0; g < NG; ++g) {
+                            const float low = fmaf(8.f, bf16_lo_f(pv[m][i][g]), bf16_hi_f(pv[m][i][g]));
 #pragma unroll
-                            for (int g = 0; g < NG; ++g) {
-                                const float step = bf16_lo_f(pv[m][i][g]), low = bf16_hi_f(pv[m][i][g]);
-                                float w0 = p0 * step, w1 = p1 * step;
-                                if (whole) {
-                                    L[n][g][0] = fmaf(p0, low, L[n][g][0]);
-                                    L[n][g][1] = fmaf(p1, low, L[n][g][1]);
-                                } else {  // scales that a row does not see may be no numbers
-                                    if (vis[m][n][2 * i]) L[n][g][0] = fmaf(p0, low, L[n][g][0]);
-                                    else w0 = 0.f;
-                                    if (vis[m][n][2 * i + 1]) L[n][g][1] = fmaf(p1, low, L[n][g][1]);
-                                    else w1 = 0.f;
-                                }
-                                const uint32_t u = pack_f16(w0, w1);
-                                wf[0][n][g][i] = movm_t(u);
-                                if constexpr (KP == 2) {
-                                    const float2 hi = unpack_f16(u);
-                                    wf[1][n][g][i] = movm_t(pack_f16(w0 - hi.x, w1 - hi.y));
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (whole || vis[m][n][2 * i + e]) L[n][g][e] = fmaf(pr[m][n][2 * i + e], low, L[n][g][e]);
+                        }
+#pragma unroll
+                    for (int k = 0; k < KP; ++k)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) wf[k][m][n][g][i] = movm_t(wf[k][m][n][g][i]);
+#pragma unroll
+                    for (int ch = 0; ch < NC; ++ch) {
+                        uint32_t a0[4], a1[4];
+                        apart<true>(wa[ch], wb[ch], a0, a1);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const uint32_t(&b)[2] = wf[0][m][n][ch / CPG];
+                            mma_f16(o[n][2 * ch], a0[0], a0[1], a0[2], a0[3], b[0], b[1]);
+                            mma_f16(o[n][2 * ch + 1], a1[0], a1[1], a1[2], a1[3], b[0], b[1]);
+                            if constexpr (KP == 2) {  // apart, as above
+                                const uint32_t(&b2)[2] = wf[KP - 1][m][n][ch / CPG];
+                                float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma_f16(x, a0[0], a0[1], a0[2], a0[3], b2[0], b2[1]);
+                                mma_f16(y, a1[0], a1[1], a1[2], a1[3], b2[0], b2[1]);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    o[n][2 * ch][i] += x[i];
+                                    o[n][2 * ch + 1][i] += y[i];
                                 }
                             }
                         }
                     }
-                    uint32_t wa[NC], wb[NC];
-                    codes<true>(base_a[m] + v_codes, base_b[m] + v_codes, wa, wb);
-#pragma unroll
-                    for (int ch = 0; ch < NC; ++ch) {
-                        const uint32_t ua = wa[ch] >> 8, ub = wb[ch] >> 8;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int k = 0; k < KP; ++k) {
-                                const uint32_t b0 = wf[k][n][ch / CPG][0], b1 = wf[k][n][ch / CPG][1];
-                                mma_f16(o[n][2 * ch], wa[ch] & M0, wa[ch] & M1, wb[ch] & M0, wb[ch] & M1, b0, b1);
-                                mma_f16(o[n][2 * ch + 1], ua & M0, ua & M1, ub & M0, ub & M1, b0, b1);
-                            }
-                    }
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive_n(&c->empty[st.s], dual ? 1 : 2);
+            if (lane == 0) mbar_arrive(&c->empty[st.s]);
             st.next();
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->q_free[buf]);
+        ++segs;
 
-        // the warps' parts meet, eight rows at a time
-        float* ex = reinterpret_cast<float*>(gen + C::EXOFF);
-#pragma unroll 1
+        // this warp's part, eight rows at a time
+#pragma unroll
         for (int n = 0; n < NT; ++n) {
-            if (!sync()) return false;  // the exchange area is free
+            if (n * 8 >= sg.nrow) break;
+            float fa[2], fb[2];
 #pragma unroll
-            for (int n2 = 0; n2 < NT; ++n2) {
-                if (n2 != n) continue;
-                uint64_t f2[2];
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[n][e];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float sum = l[n2][e];
+                for (int k = 4; k <= 16; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+                // sums of any size come to [1, 2)
+                const int k = min(max((int)((__float_as_uint(sum) >> 23) & 255u) - 127, -100), 120);
+                const float f = sum > 0.f ? pow2i(-k) : 1.f;
+                fa[e] = f;
+                fb[e] = f * 0.0625f;
+                l[n][e] = sum * f;
+                R[n][e] += sum > 0.f ? (float)k : 0.f;
 #pragma unroll
-                    for (int k = 4; k <= 16; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-                    // sums of any size come to [1, 2)
-                    const int k = min(max((int)((__float_as_uint(sum) >> 23) & 255u) - 127, -100), 120);
-                    const float f = sum > 0.f ? pow2i(-k) : 1.f;
-                    f2[e] = pk2(f * 16777216.f, f * 1048576.f);
-                    if (gq == 0) c->ml[w][2 * tq + e] = make_float2(sum > 0.f ? R[n2][e] + (float)k : R[n2][e], sum * f);
+                for (int g = 0; g < NG; ++g) {
+                    float x = L[n][g][e];
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        float x = L[n2][g][e];
-#pragma unroll
-                        for (int k2 = 4; k2 <= 16; k2 <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k2);
-                        L[n2][g][e] = x * f;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float fa, fb;
-                    up2(f2[e], fa, fb);
-                    float* row = ex + (w * 8 + 2 * tq + e) * C::EXROW + gq * 4;
-#pragma unroll
-                    for (int ch = 0; ch < NC; ++ch) {
-                        const float lw = L[n2][ch / CPG][e];
-                        *reinterpret_cast<float4*>(row + ch * 32) =
-                            make_float4(fmaf(o[n2][2 * ch][e], fa, lw), fmaf(o[n2][2 * ch][2 + e], fb, lw),
-                                        fmaf(o[n2][2 * ch + 1][e], fa, lw), fmaf(o[n2][2 * ch + 1][2 + e], fb, lw));
-                    }
+                    for (int k2 = 4; k2 <= 16; k2 <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k2);
+                    L[n][g][e] = x * f;
                 }
             }
-            if (!sync()) return false;
-            // dual: the rows of each group are its own
-            const int wa = dual ? grp * 4 : 0, wn = dual ? 4 : kKv4Consumers;
-            const int tid = (w - wa) * 32 + lane;
-            for (int u = tid; u < 8 * (D / 4); u += wn * 32) {
-                const int r = u / (D / 4), col = (u - r * (D / 4)) * 4, rr = r0 + n * 8 + r;
-                if (rr >= sg.nrow) continue;
-                float mm = -INFINITY, ll = 0.f;
-                for (int k = wa; k < wa + wn; ++k) mm = fmaxf(mm, c->ml[k][r].x);
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                for (int k = wa; k < wa + wn; ++k) {
-                    const float2 e = c->ml[k][r];
-                    if (e.y == 0.f) continue;  // saw no key
-                    const float f = e.x == mm ? 1.f : ex2(e.x - mm);
-                    const float4 v = *reinterpret_cast<const float4*>(ex + (k * 8 + r) * C::EXROW + col);
-                    ll += e.y * f;
-                    acc[0] += v.x * f;
-                    acc[1] += v.y * f;
-                    acc[2] += v.z * f;
-                    acc[3] += v.w * f;
-                }
-                put4(sg, rr, col, acc, ll);
-                if (col == 0 && sg.prow >= 0) p.part_ml[sg.prow + rr] = make_float2(mm, ll);
+            if (ex_used) {
+                if (!wait(&c->ex_free, ph_ex)) return false;
+                ph_ex ^= 1u;
             }
+            ex_used = true;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (gq == 0) c->ml[w][2 * tq + e] = make_float2(R[n][e], l[n][e]);
+                float* row = reinterpret_cast<float*>(gen + C::EXOFF) + (w * 8 + 2 * tq + e) * C::EXROW + gq * 4;
+#pragma unroll
+                for (int ch = 0; ch < NC; ++ch) {
+                    const float lw = L[n][ch / CPG][e];
+                    *reinterpret_cast<float4*>(row + ch * 32) =
+                        make_float4(fmaf(o[n][2 * ch][e], fa[e], lw), fmaf(o[n][2 * ch][2 + e], fb[e], lw),
+                                    fmaf(o[n][2 * ch + 1][e], fa[e], lw), fmaf(o[n][2 * ch + 1][2 + e], fb[e], lw));
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->ex_full);
         }
         return true;
     }
 
-    __device__ __forceinline__ void put4(const Seg& sg, int r, int col, const float* o, float l) {
-        if (sg.prow >= 0) {
-            *reinterpret_cast<float4*>(part_at(p, sg, r, col)) = make_float4(o[0], o[1], o[2], o[3]);
-            return;
-        }
-        const float inv = l > 0.f ? 1.f / l : l;  // no key seen: 0; NaN stays
-        const size_t at = row_index(p, sg, r) * D + col;
-        if constexpr (kBF16)
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
-                make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
-        else
-            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-    }
-
+    template <bool kDecode>
     __device__ void run(int s0, int s1) {
         Seg nx = load_seg(&p.seg[s0]);
         for (int si = s0; si < s1; ++si) {
@@ -605,26 +767,32 @@ struct Kv4Consumer {
             if (sg.nrow == 0) continue;
             const int t0 = sg.k0 / kKeyTile, nt = (sg.k1 + kKeyTile - 1) / kKeyTile - t0;
             bool ok;
-            if (sg.nrow <= 8) ok = rows<1, 2>(sg, 0, false, t0, nt);
-            else ok = rows<2, 1>(sg, sg.nrow > 16 ? (w >> 2) * 16 : 0, sg.nrow > 16, t0, nt);
+            if (kDecode || sg.nrow <= 8) ok = rows<1, 2>(sg, t0, nt);
+            else if constexpr (!kDecode) ok = sg.nrow <= 16 ? rows<2, 1>(sg, t0, nt) : rows<3, 1>(sg, t0, nt);
             if (!ok) return;
         }
     }
 };
 
-template <bool kBF16, int D, int NG>
+// kDecode: one token of each sequence, so no item has more than 8 rows.
+template <bool kBF16, int D, int NG, bool kDecode>
 __global__ void __launch_bounds__(kKv4Threads, 1) art_attend_kv4_kernel(const __grid_constant__ AttendKv4Params pp) {
-    using C = Kv4Cfg<D, NG>;
+    using C = Kv4Cfg<kBF16, D, NG>;
     extern __shared__ __align__(1024) unsigned char gen[];
     const AttendParams& p = pp.a;
-    Kv4Ctrl<C::NS>* c = reinterpret_cast<Kv4Ctrl<C::NS>*>(gen + C::CTRL);
+    auto* c = reinterpret_cast<Kv4Ctrl<C::NS, NG>*>(gen + C::CTRL);
     const int w = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NS; ++i) {
             mbar_init(&c->full[i], 1);
-            mbar_init(&c->empty[i], kKv4Consumers);
+            mbar_init(&c->empty[i], kKv4Consumers / 2);
         }
-        mbar_init(&c->cons, kKv4Consumers);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c->q_full[i], 1);
+            mbar_init(&c->q_free[i], kKv4Consumers);
+        }
+        mbar_init(&c->ex_full, kKv4Consumers);
+        mbar_init(&c->ex_free, kKv4Mergers);
         mbar_init(&c->stall, 1);
         c->abort = 0;
         fence_mbar_init();
@@ -644,19 +812,24 @@ __global__ void __launch_bounds__(kKv4Threads, 1) art_attend_kv4_kernel(const __
     asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel may be set up; it waits for this grid's end
     const int s0 = c->seg0, s1 = c->seg1;
     if (s0 >= s1) return;
-    if (w == kKv4Consumers) {
-        kv4_producer<D, NG>(pp, gen, c, s0, s1);
-    } else if (!p.stall || wait_tc(&c->stall, 0u, &c->abort, p)) {
+    if (w < kKv4Consumers) {
+        if (p.stall && !wait_tc(&c->stall, 0u, &c->abort, p)) return;
         Kv4Consumer<kBF16, D, NG> k{pp, p, c, smem_addr(gen), gen, w, lane};
-        k.run(s0, s1);
+        k.template run<kDecode>(s0, s1);
+    } else if (w < kKv4Consumers + kKv4Mergers) {
+        kv4_mergers<kBF16, D, NG>(p, gen, c, s0, s1);
+    } else if (w == kKv4Consumers + kKv4Mergers) {
+        kv4_queries<kBF16, D, NG>(p, gen, c, s0, s1);
+    } else {
+        kv4_producer<kBF16, D, NG>(pp, gen, c, s0, s1);
     }
 }
 
 template <bool kBF16, int D, int NG>
 cudaError_t launch_kv4(const AttendKv4Params& p, cudaStream_t st) {
-    constexpr size_t smem = kv4_smem<D, NG>();
+    constexpr size_t smem = kv4_smem<kBF16, D, NG>();
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-    auto kernel = art_attend_kv4_kernel<kBF16, D, NG>;
+    auto kernel = p.a.shared ? art_attend_kv4_kernel<kBF16, D, NG, true> : art_attend_kv4_kernel<kBF16, D, NG, false>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_after(kernel, dim3(p.a.ctas), dim3(kKv4Threads), smem, st, p);
