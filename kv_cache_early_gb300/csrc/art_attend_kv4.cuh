@@ -46,7 +46,11 @@
 namespace art {
 
 constexpr int kRowsKv4 = 24;  // rows of an item's tile
-constexpr int kKv4Consumers = 8, kKv4Mergers = 2, kKv4Threads = (kKv4Consumers + kKv4Mergers + 2) * 32;
+#ifndef KV4_PROD
+#define KV4_PROD 2
+#define KV4_MERG 1
+#endif
+constexpr int kKv4Mergers = KV4_MERG, kKv4Producers = KV4_PROD;
 // A row's reference is set so that its largest weight times step is about 2^kKv4Lift, and moves when
 // one passes 2^kKv4Most: fp16 holds 11 bits of whatever is within 2^-19 of the largest.
 constexpr float kKv4Lift = 5.f, kKv4Most = 14.f;
@@ -60,35 +64,39 @@ struct AttendKv4Params {
     int slab, slab_bytes, page_bytes, bf16;
 };
 
-template <bool kBF16, int D, int NG>
+// kCons: consumer warps.
+template <bool kBF16, int D, int NG, int kCons>
 struct Kv4Cfg {
+    static constexpr int THREADS = (kCons + kKv4Mergers + kKv4Producers + 1) * 32;
     static constexpr int NC = D / 32;                     // 32-column chunks
     static constexpr int KP = kBF16 ? 1 : 2;              // fp16 parts of a query and of a weight
     static constexpr int TILE = kKeyTile * (D + 8 * NG);  // bytes of a tile
     static constexpr int EXROW = D + 4;                   // floats of a row in the exchange area
-    static constexpr int EX = kKv4Consumers * 8 * EXROW * 4;
+    static constexpr int EX = kCons * 8 * EXROW * 4;
     static constexpr int QTILE = KP * NC * 512;           // bytes of the operands of 8 rows
     static constexpr int Q = 3 * QTILE;
     static constexpr int NS0 = (224 * 1024 - EX - 2 * Q) / TILE;
-    static constexpr int NS = NS0 < 16 ? NS0 : 16;        // ring stages
+    // Ring stages: a multiple of the groups, so that a group of warps always has the same stages. Copies land out
+    // of order; a group that saw every other use of a stage would take the one before for its own.
+    static constexpr int GROUPS = kCons / 4, NS = (NS0 < 16 ? NS0 : 16) / GROUPS * GROUPS;
     static constexpr int EXOFF = NS * TILE, QOFF = EXOFF + EX, CTRL = QOFF + 2 * Q;
 };
 
-template <int NS, int NG>
+template <int NS, int NG, int kCons>
 struct alignas(16) Kv4Ctrl {
     uint64_t full[NS], empty[NS], q_full[2], q_free[2], ex_full, ex_free, stall;
     struct Rows {  // of a segment's queries: factor of the products, the groups' sums, limit
         float f[kRowsKv4], sum[NG][kRowsKv4];
         int lim[kRowsKv4];
     } rows[2];
-    float2 ml[kKv4Consumers][8];
+    float2 ml[kCons][8];
     int abort, seg0, seg1;
 };
 
-template <bool kBF16, int D, int NG>
+template <bool kBF16, int D, int NG, int kCons>
 constexpr size_t kv4_smem() {
-    using C = Kv4Cfg<kBF16, D, NG>;
-    return (size_t)C::CTRL + sizeof(Kv4Ctrl<C::NS, NG>);
+    using C = Kv4Cfg<kBF16, D, NG, kCons>;
+    return (size_t)C::CTRL + sizeof(Kv4Ctrl<C::NS, NG, kCons>);
 }
 
 // d[0..3] += A(16x16 fp16, row) * B(16x8 fp16, col)
@@ -143,17 +151,18 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t
 // ---------------------------------------------------------------------------
 // producer warp
 // ---------------------------------------------------------------------------
-template <bool kBF16, int D, int NG>
-__device__ void kv4_producer(const AttendKv4Params& pp, unsigned char* gen, Kv4Ctrl<Kv4Cfg<kBF16, D, NG>::NS, NG>* c, int s0,
-                             int s1) {
-    using C = Kv4Cfg<kBF16, D, NG>;
+template <bool kBF16, int D, int NG, int kCons>
+__device__ void kv4_producer(const AttendKv4Params& pp, unsigned char* gen, Kv4Ctrl<Kv4Cfg<kBF16, D, NG, kCons>::NS, NG, kCons>* c, int s0,
+                             int s1, int which) {
+    using C = Kv4Cfg<kBF16, D, NG, kCons>;
     const AttendParams& p = pp.a;
     const int lane = threadIdx.x & 31;
     const int ppt = kKeyTile / pp.slab;  // slabs of a tile (2 .. 16)
+    const bool share = lane % kKv4Producers == which;  // each producer warp issues its share of a tile's copies
     const int tpb = 32 / ppt;            // tiles whose page ids the warp holds
     auto ids_of = [&](const Seg& sg, int bt) -> int {  // of this lane's slab of batch bt, -1 where it has none
         const int key = (sg.k0 / kKeyTile + bt * tpb) * kKeyTile + lane * pp.slab;
-        if (sg.nrow == 0 || key >= sg.k1 || key + pp.slab <= sg.k0) return -1;
+        if (!share || sg.nrow == 0 || key >= sg.k1 || key + pp.slab <= sg.k0) return -1;
         const int pg = __ldg(&p.block_table[(size_t)sg.table_row * p.max_pages + key / p.Ps]);
         return pg < 0 || pg >= p.num_pages ? -2 : pg;
     };
@@ -222,9 +231,9 @@ __device__ void kv4_producer(const AttendKv4Params& pp, unsigned char* gen, Kv4C
 // ---------------------------------------------------------------------------
 // query warp
 // ---------------------------------------------------------------------------
-template <bool kBF16, int D, int NG>
-__device__ void kv4_queries(const AttendParams& p, unsigned char* gen, Kv4Ctrl<Kv4Cfg<kBF16, D, NG>::NS, NG>* c, int s0, int s1) {
-    using C = Kv4Cfg<kBF16, D, NG>;
+template <bool kBF16, int D, int NG, int kCons>
+__device__ void kv4_queries(const AttendParams& p, unsigned char* gen, Kv4Ctrl<Kv4Cfg<kBF16, D, NG, kCons>::NS, NG, kCons>* c, int s0, int s1) {
+    using C = Kv4Cfg<kBF16, D, NG, kCons>;
     constexpr int NC = C::NC, CPG = NC / NG;
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
     int k = 0;
@@ -308,10 +317,10 @@ __device__ void kv4_queries(const AttendParams& p, unsigned char* gen, Kv4Ctrl<K
 // ---------------------------------------------------------------------------
 // merger warps
 // ---------------------------------------------------------------------------
-template <bool kBF16, int D, int NG>
-__device__ void kv4_mergers(const AttendParams& p, unsigned char* gen, Kv4Ctrl<Kv4Cfg<kBF16, D, NG>::NS, NG>* c, int s0, int s1) {
-    using C = Kv4Cfg<kBF16, D, NG>;
-    const int lane = threadIdx.x & 31, tid = threadIdx.x - kKv4Consumers * 32;
+template <bool kBF16, int D, int NG, int kCons>
+__device__ void kv4_mergers(const AttendParams& p, unsigned char* gen, Kv4Ctrl<Kv4Cfg<kBF16, D, NG, kCons>::NS, NG, kCons>* c, int s0, int s1) {
+    using C = Kv4Cfg<kBF16, D, NG, kCons>;
+    const int lane = threadIdx.x & 31, tid = threadIdx.x - kCons * 32;
     const float* ex = reinterpret_cast<const float*>(gen + C::EXOFF);
     uint32_t ph = 0;
     Seg nx = load_seg(&p.seg[s0]);
@@ -326,15 +335,15 @@ __device__ void kv4_mergers(const AttendParams& p, unsigned char* gen, Kv4Ctrl<K
 #pragma unroll 1
             for (int u = tid; u < rows * (D / 4); u += kKv4Mergers * 32) {
                 const int r = u / (D / 4), col = (u - r * (D / 4)) * 4, rr = n * 8 + r;
-                float2 ml[kKv4Consumers];
+                float2 ml[kCons];
                 float mm = -INFINITY, ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < kKv4Consumers; ++k) {
+                for (int k = 0; k < kCons; ++k) {
                     ml[k] = c->ml[k][r];
                     mm = fmaxf(mm, ml[k].x);
                 }
 #pragma unroll
-                for (int k = 0; k < kKv4Consumers; ++k) {
+                for (int k = 0; k < kCons; ++k) {
                     const float f = ml[k].y == 0.f ? 0.f : ex2(ml[k].x - mm);  // saw no key: its sums are zero
                     const float4 v = *reinterpret_cast<const float4*>(ex + (k * 8 + r) * C::EXROW + col);
                     ll = fmaf(ml[k].y, f, ll);
@@ -366,18 +375,18 @@ __device__ void kv4_mergers(const AttendParams& p, unsigned char* gen, Kv4Ctrl<K
 // ---------------------------------------------------------------------------
 // consumer warps
 // ---------------------------------------------------------------------------
-template <bool kBF16, int D, int NG>
+template <bool kBF16, int D, int NG, int kCons>
 struct Kv4Consumer {
-    using C = Kv4Cfg<kBF16, D, NG>;
+    using C = Kv4Cfg<kBF16, D, NG, kCons>;
     static constexpr int NC = C::NC, CPG = NC / NG, KP = C::KP;
     const AttendKv4Params& pp;
     const AttendParams& p;
-    Kv4Ctrl<C::NS, NG>* c;
+    Kv4Ctrl<C::NS, NG, kCons>* c;
     uint32_t smem;
     unsigned char* gen;
     int w, lane;
     uint32_t ph_ex = 0;
-    int odd = 0;    // which group of warps takes the next tile
+    int turn = 0;   // which group of four warps takes the next tile
     int segs = 0;   // segments so far
     bool ex_used = false;
     Stage<C::NS> st;
@@ -477,8 +486,8 @@ struct Kv4Consumer {
 
 #pragma unroll 1
         for (int j = 0; j < nt; ++j) {
-            const bool own = odd == grp;
-            odd ^= 1;
+            const bool own = turn == grp;
+            turn = turn == kCons / 4 - 1 ? 0 : turn + 1;
             if (!own) {
                 st.next();
                 continue;
@@ -758,7 +767,7 @@ struct Kv4Consumer {
         return true;
     }
 
-    template <bool kDecode>
+    template <int KM, bool kDecode>
     __device__ void run(int s0, int s1) {
         Seg nx = load_seg(&p.seg[s0]);
         for (int si = s0; si < s1; ++si) {
@@ -767,7 +776,7 @@ struct Kv4Consumer {
             if (sg.nrow == 0) continue;
             const int t0 = sg.k0 / kKeyTile, nt = (sg.k1 + kKeyTile - 1) / kKeyTile - t0;
             bool ok;
-            if (kDecode || sg.nrow <= 8) ok = rows<1, 2>(sg, t0, nt);
+            if (kDecode || sg.nrow <= 8) ok = rows<1, KM>(sg, t0, nt);
             else if constexpr (!kDecode) ok = sg.nrow <= 16 ? rows<2, 1>(sg, t0, nt) : rows<3, 1>(sg, t0, nt);
             if (!ok) return;
         }
@@ -775,23 +784,23 @@ struct Kv4Consumer {
 };
 
 // kDecode: one token of each sequence, so no item has more than 8 rows.
-template <bool kBF16, int D, int NG, bool kDecode>
-__global__ void __launch_bounds__(kKv4Threads, 1) art_attend_kv4_kernel(const __grid_constant__ AttendKv4Params pp) {
-    using C = Kv4Cfg<kBF16, D, NG>;
+template <bool kBF16, int D, int NG, int kCons, int KM, bool kDecode>
+__global__ void __launch_bounds__((kCons + kKv4Mergers + kKv4Producers + 1) * 32, 1) art_attend_kv4_kernel(const __grid_constant__ AttendKv4Params pp) {
+    using C = Kv4Cfg<kBF16, D, NG, kCons>;
     extern __shared__ __align__(1024) unsigned char gen[];
     const AttendParams& p = pp.a;
-    auto* c = reinterpret_cast<Kv4Ctrl<C::NS, NG>*>(gen + C::CTRL);
+    auto* c = reinterpret_cast<Kv4Ctrl<C::NS, NG, kCons>*>(gen + C::CTRL);
     const int w = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NS; ++i) {
-            mbar_init(&c->full[i], 1);
-            mbar_init(&c->empty[i], kKv4Consumers / 2);
+            mbar_init(&c->full[i], kKv4Producers);
+            mbar_init(&c->empty[i], 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c->q_full[i], 1);
-            mbar_init(&c->q_free[i], kKv4Consumers);
+            mbar_init(&c->q_free[i], kCons);
         }
-        mbar_init(&c->ex_full, kKv4Consumers);
+        mbar_init(&c->ex_full, kCons);
         mbar_init(&c->ex_free, kKv4Mergers);
         mbar_init(&c->stall, 1);
         c->abort = 0;
@@ -799,9 +808,9 @@ __global__ void __launch_bounds__(kKv4Threads, 1) art_attend_kv4_kernel(const __
     }
     static_assert(sizeof(PlanScratch) <= C::CTRL, "the scratch lies in the tiles");
     asm volatile("griddepcontrol.wait;" ::: "memory");  // what ran before on the stream has ended
-    if (w < kKv4Consumers) {
+    if (w < 8) {
         int a, z;
-        plan_share<kKv4Consumers * 32>(p, reinterpret_cast<PlanScratch*>(gen), a, z);
+        plan_share<256>(p, reinterpret_cast<PlanScratch*>(gen), a, z);
         if (threadIdx.x == 0) {
             c->seg0 = a;
             c->seg1 = z;
@@ -812,27 +821,36 @@ __global__ void __launch_bounds__(kKv4Threads, 1) art_attend_kv4_kernel(const __
     asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel may be set up; it waits for this grid's end
     const int s0 = c->seg0, s1 = c->seg1;
     if (s0 >= s1) return;
-    if (w < kKv4Consumers) {
+    if (w < kCons) {
         if (p.stall && !wait_tc(&c->stall, 0u, &c->abort, p)) return;
-        Kv4Consumer<kBF16, D, NG> k{pp, p, c, smem_addr(gen), gen, w, lane};
-        k.template run<kDecode>(s0, s1);
-    } else if (w < kKv4Consumers + kKv4Mergers) {
-        kv4_mergers<kBF16, D, NG>(p, gen, c, s0, s1);
-    } else if (w == kKv4Consumers + kKv4Mergers) {
-        kv4_queries<kBF16, D, NG>(p, gen, c, s0, s1);
+        Kv4Consumer<kBF16, D, NG, kCons> k{pp, p, c, smem_addr(gen), gen, w, lane};
+        k.template run<KM, kDecode>(s0, s1);
+    } else if (w < kCons + kKv4Mergers) {
+        kv4_mergers<kBF16, D, NG, kCons>(p, gen, c, s0, s1);
+    } else if (w == kCons + kKv4Mergers) {
+        kv4_queries<kBF16, D, NG, kCons>(p, gen, c, s0, s1);
     } else {
-        kv4_producer<kBF16, D, NG>(pp, gen, c, s0, s1);
+        kv4_producer<kBF16, D, NG, kCons>(pp, gen, c, s0, s1, w - kCons - kKv4Mergers - 1);
     }
 }
 
-template <bool kBF16, int D, int NG>
-cudaError_t launch_kv4(const AttendKv4Params& p, cudaStream_t st) {
-    constexpr size_t smem = kv4_smem<kBF16, D, NG>();
+template <bool kBF16, int D, int NG, int kCons, int KM, bool kDecode>
+cudaError_t launch_kv4_as(const AttendKv4Params& p, cudaStream_t st) {
+    using C = Kv4Cfg<kBF16, D, NG, kCons>;
+    constexpr size_t smem = kv4_smem<kBF16, D, NG, kCons>();
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-    auto kernel = p.a.shared ? art_attend_kv4_kernel<kBF16, D, NG, true> : art_attend_kv4_kernel<kBF16, D, NG, false>;
+    auto kernel = art_attend_kv4_kernel<kBF16, D, NG, kCons, KM, kDecode>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_after(kernel, dim3(p.a.ctas), dim3(kKv4Threads), smem, st, p);
+    return launch_after(kernel, dim3(p.a.ctas), dim3(C::THREADS), smem, st, p);
+}
+#ifndef KV4_CONS
+#define KV4_CONS 12
+#define KV4_KM 1
+#endif
+template <bool kBF16, int D, int NG>
+cudaError_t launch_kv4(const AttendKv4Params& p, cudaStream_t st) {
+    return p.a.shared ? launch_kv4_as<kBF16, D, NG, KV4_CONS, KV4_KM, true>(p, st) : launch_kv4_as<kBF16, D, NG, 8, 2, false>(p, st);
 }
 
 // One translation unit for each head_dim and type.
