@@ -46,11 +46,7 @@
 namespace art {
 
 constexpr int kRowsKv4 = 24;  // rows of an item's tile
-#ifndef KV4_PROD
-#define KV4_PROD 2
-#define KV4_MERG 1
-#endif
-constexpr int kKv4Mergers = KV4_MERG, kKv4Producers = KV4_PROD;
+constexpr int kKv4Mergers = 2;
 // A row's reference is set so that its largest weight times step is about 2^kKv4Lift, and moves when
 // one passes 2^kKv4Most: fp16 holds 11 bits of whatever is within 2^-19 of the largest.
 constexpr float kKv4Lift = 5.f, kKv4Most = 14.f;
@@ -67,7 +63,7 @@ struct AttendKv4Params {
 // kCons: consumer warps.
 template <bool kBF16, int D, int NG, int kCons>
 struct Kv4Cfg {
-    static constexpr int THREADS = (kCons + kKv4Mergers + kKv4Producers + 1) * 32;
+    static constexpr int THREADS = (kCons + kKv4Mergers + 2) * 32;
     static constexpr int NC = D / 32;                     // 32-column chunks
     static constexpr int KP = kBF16 ? 1 : 2;              // fp16 parts of a query and of a weight
     static constexpr int TILE = kKeyTile * (D + 8 * NG);  // bytes of a tile
@@ -151,23 +147,27 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t
 // ---------------------------------------------------------------------------
 // producer warp
 // ---------------------------------------------------------------------------
+// A lane has a slab of a batch of tiles: it waits for its tile's stage and issues its copy, side by side
+// with the others. (One tile after the other, a warp of few instructions, each waiting for the one
+// before, was what bound the kernel: 0.4 us a tile alone, 0.7 beside busy consumers.)
 template <bool kBF16, int D, int NG, int kCons>
-__device__ void kv4_producer(const AttendKv4Params& pp, unsigned char* gen, Kv4Ctrl<Kv4Cfg<kBF16, D, NG, kCons>::NS, NG, kCons>* c, int s0,
-                             int s1, int which) {
+__device__ void kv4_producer(const AttendKv4Params& pp, unsigned char* gen, Kv4Ctrl<Kv4Cfg<kBF16, D, NG, kCons>::NS, NG, kCons>* c,
+                             int s0, int s1) {
     using C = Kv4Cfg<kBF16, D, NG, kCons>;
     const AttendParams& p = pp.a;
     const int lane = threadIdx.x & 31;
-    const int ppt = kKeyTile / pp.slab;  // slabs of a tile (2 .. 16)
-    const bool share = lane % kKv4Producers == which;  // each producer warp issues its share of a tile's copies
-    const int tpb = 32 / ppt;            // tiles whose page ids the warp holds
-    auto ids_of = [&](const Seg& sg, int bt) -> int {  // of this lane's slab of batch bt, -1 where it has none
+    const int ppt = kKeyTile / pp.slab;         // slabs of a tile (2 .. 16)
+    const int tpb = min(32 / ppt, C::NS);       // tiles of a batch: no two of them in one stage
+    const int t = lane / ppt, in_tile = lane - t * ppt;  // this lane's tile of a batch, its slab of the tile
+    const uint32_t dst0 = in_tile * pp.slab_bytes;
+    auto ids_of = [&](const Seg& sg, int bt) -> int {  // page of this lane's slab of batch bt, -1 where it has none
         const int key = (sg.k0 / kKeyTile + bt * tpb) * kKeyTile + lane * pp.slab;
-        if (!share || sg.nrow == 0 || key >= sg.k1 || key + pp.slab <= sg.k0) return -1;
+        if (t >= tpb || sg.nrow == 0 || key >= sg.k1 || key + pp.slab <= sg.k0) return -1;
         const int pg = __ldg(&p.block_table[(size_t)sg.table_row * p.max_pages + key / p.Ps]);
         return pg < 0 || pg >= p.num_pages ? -2 : pg;
     };
-    Stage<C::NS> st;
-    uint32_t used = 0, ph = 0, filled_ph = 0;  // per stage: filled once; parity to wait for
+    int stage = 0, use = 0, tiles = 0;  // of the batch's first tile
+    unsigned issued = 0;                // lanes that issued copies of a batch that was given up
     Seg sg = load_seg(&p.seg[s0]);
     int ids = ids_of(sg, 0);
     bool ok = true;
@@ -191,41 +191,65 @@ __device__ void kv4_producer(const AttendKv4Params& pp, unsigned char* gen, Kv4C
                 }
                 if (ids == -2) ids = 0;
             }
-            for (int t = 0; t < nb; ++t) {
-                const bool mine = lane / ppt == t && ids >= 0;
-                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * pp.slab_bytes;
-                const int in_tile = lane - t * ppt;  // this lane's slab in the tile
-                const int key = (t0 + bt * tpb + t) * kKeyTile + in_tile * pp.slab;
-                const uint32_t bit = 1u << st.s;
-                if (used & bit) {
-                    if (!wait_tc(&c->empty[st.s], (ph & bit) ? 1u : 0u, &c->abort, p)) {
+            int s = stage + t, u = use;
+            if (s >= C::NS) {
+                s -= C::NS;
+                ++u;
+            }
+            const int key = (t0 + bt * tpb + t) * kKeyTile + in_tile * pp.slab;
+            const unsigned char* src = pp.cache + ((size_t)max(ids, 0) * p.Hkv + sg.g) * (size_t)pp.page_bytes +
+                                       (size_t)((key & (p.Ps - 1)) / pp.slab) * pp.slab_bytes;
+            bool todo = t < nb;
+            for (int polls = 0;;) {
+                // the lanes of a tile go by what the first of them sees: all of a tile's copies are issued, or none
+                const bool mine = u == 0 || mbar_test_wait(&c->empty[s], (uint32_t)(u - 1) & 1u);
+                const bool room = __shfl_sync(0xffffffffu, (int)mine, t * ppt) != 0;
+                if (todo && room) {
+                    if (ids >= 0) {
+                        mbar_arrive_expect_tx(&c->full[s], (uint32_t)pp.slab_bytes);
+                        bulk_g2s(gen + s * C::TILE + dst0, src, (uint32_t)pp.slab_bytes, &c->full[s]);
+                    } else {
+                        mbar_arrive(&c->full[s]);  // no key of the segment in this slab
+                    }
+                    todo = false;
+                }
+                const unsigned left = __ballot_sync(0xffffffffu, todo);
+                if (!left) break;
+                if (++polls == 64) {  // the long wait, by the whole warp for one lane's stage
+                    polls = 0;
+                    const int from = __ffs(left) - 1;
+                    const int ls = __shfl_sync(0xffffffffu, s, from), lu = __shfl_sync(0xffffffffu, u, from);
+                    if (!wait_tc(&c->empty[ls], (uint32_t)(lu - 1) & 1u, &c->abort, p)) {
                         ok = false;
+                        issued = __ballot_sync(0xffffffffu, t < nb && !todo);
                         break;
                     }
-                    ph ^= bit;
                 }
-                used |= bit;
-                filled_ph = st.ph ? filled_ph | bit : filled_ph & ~bit;
-                if (lane == 0) mbar_arrive_expect_tx(&c->full[st.s], bytes);
-                __syncwarp();
-                if (mine)
-                    bulk_g2s(gen + st.s * C::TILE + in_tile * pp.slab_bytes,
-                             pp.cache + ((size_t)ids * p.Hkv + sg.g) * (size_t)pp.page_bytes +
-                                 (size_t)((key & (p.Ps - 1)) / pp.slab) * pp.slab_bytes,
-                             (uint32_t)pp.slab_bytes, &c->full[st.s]);
-                st.next();
+            }
+            if (!ok) break;
+            tiles += nb;
+            stage += nb;
+            if (stage >= C::NS) {
+                stage -= C::NS;
+                ++use;
             }
             ids = more;
         }
         sg = nx;
     }
-    // no copy of this CTA may be in flight when it ends
-    for (int s = 0; s < C::NS; ++s)
-        if (used & (1u << s)) {
-            const unsigned long long w0 = global_ns();
-            while (!__all_sync(0xffffffffu, mbar_try_wait(&c->full[s], (filled_ph >> s) & 1u)))
-                if (__any_sync(0xffffffffu, lane == 0 && global_ns() - w0 > kWaitLimitNs)) break;
+    // no copy of this CTA may be in flight when it ends: a lane waits for the last tile of its stage
+    {
+        const int back = (stage - 1 - lane + 2 * C::NS) % C::NS;  // tiles between the stage's last whole one and the last
+        int k = tiles - 1 - back;
+        const int given = (lane - stage + C::NS) % C::NS;  // its tile of the batch that was given up
+        if (given < tpb && (issued >> (given * ppt) & 1u)) k = tiles + given;
+        bool open = lane < C::NS && k >= 0;
+        const unsigned long long w0 = global_ns();
+        while (__any_sync(0xffffffffu, open)) {
+            if (open && mbar_test_wait(&c->full[lane], (uint32_t)(k / C::NS) & 1u)) open = false;
+            if (__any_sync(0xffffffffu, lane == 0 && global_ns() - w0 > kWaitLimitNs)) break;
         }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -434,6 +458,10 @@ struct Kv4Consumer {
         const int buf = segs & 1;
         if (!wait(&c->q_full[buf], (uint32_t)(segs >> 1) & 1u)) return false;
         const uint32_t qaddr = smem + C::QOFF + buf * C::Q + lane * 16;
+#ifndef KV4_SPLIT
+#define KV4_SPLIT 1
+#endif
+        constexpr int SPL = KV4_SPLIT;
         constexpr bool kQRegs = NT == 1;  // the queries stay in registers
         uint32_t qr[kQRegs ? KP : 1][kQRegs ? NC : 1][4];
         if constexpr (kQRegs)
@@ -519,11 +547,13 @@ struct Kv4Consumer {
                     uint64_t tot[NT][2], lo2[NT][2];  // of keys gq, gq + 8: rows 2 tq, 2 tq + 1
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
-                        float acc[KP][NT][4];  // the parts apart: sums of the second are far smaller
+                        float acc[KP][NT][SPL][4];  // the parts apart: sums of the second are far smaller
 #pragma unroll
                         for (int k = 0; k < KP; ++k)
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) acc[k][n][0] = acc[k][n][1] = acc[k][n][2] = acc[k][n][3] = 0.f;
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int x = 0; x < SPL; ++x) acc[k][n][x][0] = acc[k][n][x][1] = acc[k][n][x][2] = acc[k][n][x][3] = 0.f;
 #pragma unroll
                         for (int ch = g * CPG; ch < (g + 1) * CPG; ++ch) {
                             uint32_t a0[4], a1[4];
@@ -539,8 +569,8 @@ struct Kv4Consumer {
                                     } else {
                                         lds128(qaddr + n * C::QTILE + (k * NC + ch) * 512, q4);
                                     }
-                                    mma_f16(acc[k][n], a0[0], a0[2], a0[1], a0[3], q4[0], q4[1]);
-                                    mma_f16(acc[k][n], a1[0], a1[2], a1[1], a1[3], q4[2], q4[3]);
+                                    mma_f16(acc[k][n][0], a0[0], a0[2], a0[1], a0[3], q4[0], q4[1]);
+                                    mma_f16(acc[k][n][SPL - 1], a1[0], a1[2], a1[1], a1[3], q4[2], q4[3]);
                                 }
                         }
 #pragma unroll
@@ -550,10 +580,11 @@ struct Kv4Consumer {
                             const uint64_t step2 = pk2(step, step), low2 = pk2(low, low);
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                float x = acc[0][n][2 * i], y = acc[0][n][2 * i + 1];
-                                if constexpr (KP == 2) {
-                                    x += acc[1][n][2 * i];
-                                    y += acc[1][n][2 * i + 1];
+                                float x = acc[0][n][0][2 * i], y = acc[0][n][0][2 * i + 1];
+#pragma unroll
+                                for (int k = 1; k < KP * SPL; ++k) {
+                                    x += acc[k / SPL][n][k % SPL][2 * i];
+                                    y += acc[k / SPL][n][k % SPL][2 * i + 1];
                                 }
                                 const uint64_t a2 = pk2(x, y);
                                 tot[n][i] = g == 0 ? mul2(a2, step2) : fma2(a2, step2, tot[n][i]);
@@ -785,7 +816,7 @@ struct Kv4Consumer {
 
 // kDecode: one token of each sequence, so no item has more than 8 rows.
 template <bool kBF16, int D, int NG, int kCons, int KM, bool kDecode>
-__global__ void __launch_bounds__((kCons + kKv4Mergers + kKv4Producers + 1) * 32, 1) art_attend_kv4_kernel(const __grid_constant__ AttendKv4Params pp) {
+__global__ void __launch_bounds__((kCons + kKv4Mergers + 2) * 32, 1) art_attend_kv4_kernel(const __grid_constant__ AttendKv4Params pp) {
     using C = Kv4Cfg<kBF16, D, NG, kCons>;
     extern __shared__ __align__(1024) unsigned char gen[];
     const AttendParams& p = pp.a;
@@ -793,7 +824,7 @@ __global__ void __launch_bounds__((kCons + kKv4Mergers + kKv4Producers + 1) * 32
     const int w = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NS; ++i) {
-            mbar_init(&c->full[i], kKv4Producers);
+            mbar_init(&c->full[i], kKeyTile / pp.slab);
             mbar_init(&c->empty[i], 4);
         }
         for (int i = 0; i < 2; ++i) {
@@ -830,7 +861,7 @@ __global__ void __launch_bounds__((kCons + kKv4Mergers + kKv4Producers + 1) * 32
     } else if (w == kCons + kKv4Mergers) {
         kv4_queries<kBF16, D, NG, kCons>(p, gen, c, s0, s1);
     } else {
-        kv4_producer<kBF16, D, NG, kCons>(pp, gen, c, s0, s1, w - kCons - kKv4Mergers - 1);
+        kv4_producer<kBF16, D, NG, kCons>(pp, gen, c, s0, s1);
     }
 }
 
