@@ -65,6 +65,7 @@ int dense_extend_kv4(const void* q, const void* cache, int32_t group, const int3
     pp.slab_bytes = l.slab_bytes;
     pp.page_bytes = l.page_bytes;
     pp.bf16 = s.dtype == ART_DTYPE_BF16;
+    pp.f16_1024 = 0x64006400u;
     AttendParams p = {};
     kv4_shape(p, s);
     p.q = q;

@@ -31,8 +31,8 @@
 //   queries    turns the next segment's queries into operands, in shared memory
 //   8 consumers in two groups of four that take alternate tiles, a warp 32 keys of each, with a
 //              reference, sums and O of its own. Up to 8 rows: 32 keys at a time, two chains of products
-//              and the queries in registers; up to 24: 16 keys at a time and two or three column tiles, for
-//              which the codes are taken apart once
+//              and the queries in registers; up to 16: 16 keys at a time and two column tiles, for which the
+//              codes are taken apart once
 //   2 mergers  join the consumers' parts of a segment, eight rows at a time, and store them, while the
 //              consumers are at the next one
 //
@@ -40,17 +40,19 @@
 // scales of keys that a row does not see are not used for it.
 #pragma once
 
+#include <type_traits>
+
 #include "art_attend_tc.cuh"
 #include "art_kv4.cuh"
 
 namespace art {
 
-constexpr int kRowsKv4 = 24;  // rows of an item's tile
+constexpr int kRowsKv4 = 16;  // rows of an item's tile
 constexpr int kKv4Mergers = 2;
 // A row's reference is set so that its largest weight times step is about 2^kKv4Lift, and moves when
 // one passes 2^kKv4Most: fp16 holds 11 bits of whatever is within 2^-19 of the largest.
 constexpr float kKv4Lift = 5.f, kKv4Most = 14.f;
-constexpr uint32_t kMostWeight = 0x74007400u;  // 2^14, twice
+constexpr float kMostWeight = 0x1p14f;
 constexpr float kMostSum = 0x1p100f;           // of weights without steps, which may be as small as 2^-80
 constexpr float kNoReference = -1e30f;  // of a row that has seen no key: any key's weight passes the limit
 
@@ -58,6 +60,7 @@ struct AttendKv4Params {
     AttendParams a;
     const unsigned char* cache;
     int slab, slab_bytes, page_bytes, bf16;
+    uint32_t f16_1024;  // 2^10 in fp16, twice
 };
 
 // kCons: consumer warps.
@@ -70,7 +73,7 @@ struct Kv4Cfg {
     static constexpr int EXROW = D + 4;                   // floats of a row in the exchange area
     static constexpr int EX = kCons * 8 * EXROW * 4;
     static constexpr int QTILE = KP * NC * 512;           // bytes of the operands of 8 rows
-    static constexpr int Q = 3 * QTILE;
+    static constexpr int Q = kRowsKv4 / 8 * QTILE;
     static constexpr int NS0 = (224 * 1024 - EX - 2 * Q) / TILE;
     // Ring stages: a multiple of the groups, so that a group of warps always has the same stages. Copies land out
     // of order; a group that saw every other use of a stage would take the one before for its own.
@@ -121,18 +124,6 @@ __device__ __forceinline__ uint32_t add_f16(uint32_t a, uint32_t c) {  // two su
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(c));
     return r;
 }
-__device__ __forceinline__ uint32_t max_f16(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ bool any_above(uint32_t a, uint32_t limit) {  // of two fp16 numbers
-    uint32_t r;
-    asm("{\n\t.reg .pred p, q;\n\tsetp.gt.f16x2 p|q, %1, %2;\n\tor.pred p, p, q;\n\tselp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"(a), "r"(limit));
-    return r != 0;
-}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t r;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a));
@@ -140,6 +131,26 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 }
 __device__ __forceinline__ void lds128(uint32_t a, uint32_t (&r)[4]) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+// wait_tc for warps that mostly wait: asleep between the looks, so that they leave the issue slots to others (with
+// wait_tc's looks, a fifth of the kernel's instructions were theirs).
+static __device__ __noinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, int* abort, unsigned long long wait_ns, int* status) {
+    const unsigned long long t0 = global_ns();
+    for (;;) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 20000u))) return true;
+        const bool late = (threadIdx.x & 31) == 0 && global_ns() - t0 > wait_ns;
+        if (__any_sync(0xffffffffu, late)) {
+            if ((threadIdx.x & 31) == 0) {
+                st_volatile_shared(abort, 1);
+                atomicOr(status, ART_STATUS_TIMEOUT);
+            }
+            return false;
+        }
+        if (__any_sync(0xffffffffu, ld_volatile_shared(abort) != 0)) return false;
+    }
+}
+__device__ __forceinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, int* abort, const AttendParams& p) {
+    return wait_asleep(bar, parity, abort, p.wait_ns, &p.cta_status[blockIdx.x]);
 }
 // 2^e for -126 <= e <= 127
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
@@ -215,11 +226,11 @@ __device__ void kv4_producer(const AttendKv4Params& pp, unsigned char* gen, Kv4C
                 }
                 const unsigned left = __ballot_sync(0xffffffffu, todo);
                 if (!left) break;
-                if (++polls == 64) {  // the long wait, by the whole warp for one lane's stage
+                if (++polls == 2) {  // the long wait, by the whole warp for one lane's stage
                     polls = 0;
                     const int from = __ffs(left) - 1;
                     const int ls = __shfl_sync(0xffffffffu, s, from), lu = __shfl_sync(0xffffffffu, u, from);
-                    if (!wait_tc(&c->empty[ls], (uint32_t)(lu - 1) & 1u, &c->abort, p)) {
+                    if (!wait_asleep(&c->empty[ls], (uint32_t)(lu - 1) & 1u, &c->abort, p)) {
                         ok = false;
                         issued = __ballot_sync(0xffffffffu, t < nb && !todo);
                         break;
@@ -265,7 +276,7 @@ __device__ void kv4_queries(const AttendParams& p, unsigned char* gen, Kv4Ctrl<K
         const Seg sg = load_seg(&p.seg[si]);
         if (sg.nrow == 0) continue;
         const int buf = k & 1;
-        if (k >= 2 && !wait_tc(&c->q_free[buf], (uint32_t)((k >> 1) - 1) & 1u, &c->abort, p)) return;
+        if (k >= 2 && !wait_asleep(&c->q_free[buf], (uint32_t)((k >> 1) - 1) & 1u, &c->abort, p)) return;
         ++k;
 #pragma unroll 1
         for (int n = 0; n * 8 < sg.nrow; ++n) {
@@ -353,7 +364,7 @@ __device__ void kv4_mergers(const AttendParams& p, unsigned char* gen, Kv4Ctrl<K
         if (si + 1 < s1) nx = load_seg(&p.seg[si + 1]);
 #pragma unroll 1
         for (int n = 0; n * 8 < sg.nrow; ++n) {
-            if (!wait_tc(&c->ex_full, ph, &c->abort, p)) return;
+            if (!wait_asleep(&c->ex_full, ph, &c->abort, p)) return;
             ph ^= 1u;
             const int rows = min(8, sg.nrow - n * 8);
 #pragma unroll 1
@@ -409,6 +420,7 @@ struct Kv4Consumer {
     uint32_t smem;
     unsigned char* gen;
     int w, lane;
+    uint32_t k1024;
     uint32_t ph_ex = 0;
     int turn = 0;   // which group of four warps takes the next tile
     int segs = 0;   // segments so far
@@ -436,11 +448,12 @@ struct Kv4Consumer {
         }
     }
     // the operand registers of a chunk: codes 0 | 1 (times 16) of octets a, b, then codes 2 | 3, as code * 2^-24, or
-    // (kLess) less 8: 2^10 + code, by its bits, less 2^10 + 8
+    // (kLess) less 8: 2^10 + code, by its bits, less 2^10 + 8. The bits of 2^10 come from a register (of the call's
+    // parameters), since an instruction holds one constant only: a mask and they would be two.
     template <bool kLess>
-    __device__ __forceinline__ static void apart(uint32_t wa, uint32_t wb, uint32_t (&a0)[4], uint32_t (&a1)[4]) {
-        constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u, K = kLess ? 0x64006400u : 0u;
-        const uint32_t ua = wa >> 8, ub = wb >> 8;
+    __device__ __forceinline__ void apart(uint32_t wa, uint32_t wb, uint32_t (&a0)[4], uint32_t (&a1)[4]) const {
+        constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
+        const uint32_t ua = wa >> 8, ub = wb >> 8, K = kLess ? k1024 : 0u;
         a0[0] = wa & M0 | K, a0[1] = wa & M1 | K, a0[2] = wb & M0 | K, a0[3] = wb & M1 | K;
         a1[0] = ua & M0 | K, a1[1] = ua & M1 | K, a1[2] = ub & M0 | K, a1[3] = ub & M1 | K;
         if constexpr (kLess)
@@ -458,10 +471,6 @@ struct Kv4Consumer {
         const int buf = segs & 1;
         if (!wait(&c->q_full[buf], (uint32_t)(segs >> 1) & 1u)) return false;
         const uint32_t qaddr = smem + C::QOFF + buf * C::Q + lane * 16;
-#ifndef KV4_SPLIT
-#define KV4_SPLIT 1
-#endif
-        constexpr int SPL = KV4_SPLIT;
         constexpr bool kQRegs = NT == 1;  // the queries stay in registers
         uint32_t qr[kQRegs ? KP : 1][kQRegs ? NC : 1][4];
         if constexpr (kQRegs)
@@ -502,15 +511,228 @@ struct Kv4Consumer {
 #pragma unroll
             for (int k = 0; k < 2 * NC; ++k) o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
         }
-        // the octets of this warp's 32 keys in a tile: its bytes of the keys' codes, and its keys' scales
-        uint32_t kc[4], sc[4];
+        // the octets of this warp's 32 keys in a tile, two to each 16 keys: its bytes of the keys' codes, and its
+        // keys' scales; the second 16 keys lie dk, ds bytes on whatever the slab
+        uint32_t kc[2], sc[2], dk, ds;
+        {
+            const int per = pp.slab >> 3;
+            auto codes_at = [&](int oct) { return oct / per * pp.slab_bytes + oct % per * (4 * D); };
+            auto scales_at = [&](int oct) { return oct / per * pp.slab_bytes + oct % per * (32 * NG); };
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int per = pp.slab >> 3, oct = sub * 4 + k, slab = oct / per, in = oct - slab * per;
-            kc[k] = smem + slab * pp.slab_bytes + in * (4 * D) + (NC == 4 ? lane : lane & 15) * 16;
-            sc[k] = smem + slab * pp.slab_bytes + pp.slab * D + in * (32 * NG) + gq * 4;
+            for (int i = 0; i < 2; ++i) {
+                kc[i] = smem + codes_at(sub * 4 + i) + (NC == 4 ? lane : lane & 15) * 16;
+                sc[i] = smem + pp.slab * D + scales_at(sub * 4 + i) + gq * 4;
+            }
+            dk = codes_at(sub * 4 + 2) - codes_at(sub * 4);
+            ds = scales_at(sub * 4 + 2) - scales_at(sub * 4);
         }
         const uint32_t v_codes = pp.slab * (D / 2), v_scales = pp.slab * 4 * NG;
+
+        // 16 KM keys from kb on. whole: every row sees all of them. ka .. sb: addresses of their first octets
+        auto step = [&](auto whole_, int kb, const uint32_t ka0, const uint32_t kb0, const uint32_t sa0, const uint32_t sb0) {
+            constexpr bool whole = decltype(whole_)::value;
+            float s[KM][NT][4];
+            uint32_t pv[KM][2][NG];  // (step, lowest) of the values of keys gq and gq + 8
+            bool vis[KM][NT][4];
+#pragma unroll
+            for (int m = 0; m < KM; ++m) {
+                const uint32_t ka = ka0 + m * dk, kb2 = kb0 + m * dk, sa = sa0 + m * ds, sb = sb0 + m * ds;
+                uint32_t pk[2][NG], wa[NC], wb[NC];
+                codes<false>(ka, kb2, wa, wb);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    pk[0][g] = lds32(sa + g * 32);
+                    pk[1][g] = lds32(sb + g * 32);
+                    pv[m][0][g] = lds32(sa + v_scales + g * 32);
+                    pv[m][1][g] = lds32(sb + v_scales + g * 32);
+                }
+                uint64_t tot[NT][2], lo2[NT][2];  // of keys gq, gq + 8: rows 2 tq, 2 tq + 1
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    float acc[KP][NT][4];  // the parts apart: sums of the second are far smaller
+#pragma unroll
+                    for (int k = 0; k < KP; ++k)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            acc[k][n][0] = acc[k][n][1] = acc[k][n][2] = acc[k][n][3] = 0.f;
+#pragma unroll
+                    for (int ch = g * CPG; ch < (g + 1) * CPG; ++ch) {
+                        uint32_t a0[4], a1[4];
+                        apart<!kBF16>(wa[ch], wb[ch], a0, a1);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int k = 0; k < KP; ++k) {
+                                uint32_t q4[4];
+                                if constexpr (kQRegs) {
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) q4[i] = qr[k][ch][i];
+                                } else {
+                                    lds128(qaddr + n * C::QTILE + (k * NC + ch) * 512, q4);
+                                }
+                                mma_f16(acc[k][n], a0[0], a0[2], a0[1], a0[3], q4[0], q4[1]);
+                                mma_f16(acc[k][n], a1[0], a1[2], a1[1], a1[3], q4[2], q4[3]);
+                            }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float step = bf16_lo_f(pk[i][g]);
+                        const float low = kBF16 ? bf16_hi_f(pk[i][g]) : fmaf(8.f, step, bf16_hi_f(pk[i][g]));
+                        const uint64_t step2 = pk2(step, step), low2 = pk2(low, low);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            float x = acc[0][n][2 * i], y = acc[0][n][2 * i + 1];
+                            if constexpr (KP == 2) {
+                                x += acc[1][n][2 * i];
+                                y += acc[1][n][2 * i + 1];
+                            }
+                            const uint64_t a2 = pk2(x, y);
+                            tot[n][i] = g == 0 ? mul2(a2, step2) : fma2(a2, step2, tot[n][i]);
+                            lo2[n][i] = g == 0 ? mul2(low2, qs2[n][g]) : fma2(low2, qs2[n][g], lo2[n][i]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) up2(fma2(tot[n][i], F2[n], lo2[n][i]), s[m][n][2 * i], s[m][n][2 * i + 1]);
+                if constexpr (!whole) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int key = kb + m * 16 + i * 8 + gq;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                vis[m][n][2 * i + e] = key >= sg.k0 && key < lim[n][e];
+                                if (!vis[m][n][2 * i + e]) s[m][n][2 * i + e] = -INFINITY;
+                            }
+                    }
+                }
+            }
+            // Weights against the references as they are; where a weight times its step, or a row's sum, goes
+            // too far, the references move and they are formed once more.
+            float pr[KM][NT][4], ln[NT][2], most_step[KM][2];
+#pragma unroll
+            for (int m = 0; m < KM; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {  // the largest of the groups'
+                    uint32_t x = pv[m][i][0] << 16;
+#pragma unroll
+                    for (int g = 1; g < NG; ++g) x = max(x, pv[m][i][g] << 16);
+                    most_step[m][i] = __uint_as_float(x);
+                }
+#pragma unroll 1
+            for (bool again = false;; again = true) {
+                float most = 0.f;
+                bool far = false;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    ln[n][0] = l[n][0];
+                    ln[n][1] = l[n][1];
+#pragma unroll
+                    for (int m = 0; m < KM; ++m)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float p0 = ex2(s[m][n][2 * i] - R[n][0]), p1 = ex2(s[m][n][2 * i + 1] - R[n][1]);
+                            pr[m][n][2 * i] = p0;
+                            pr[m][n][2 * i + 1] = p1;
+                            ln[n][0] += p0;
+                            ln[n][1] += p1;
+                            most = max3(most, p0 * most_step[m][i], p1 * most_step[m][i]);  // no number: left out
+                        }
+                    far |= fmaxf(ln[n][0], ln[n][1]) > kMostSum;
+                }
+                if (again || !__any_sync(0xffffffffu, far || most > kMostWeight)) break;
+                // up to the maximum of score + log2 of the values' step (the largest of the groups')
+                float ev[KM][2];
+#pragma unroll
+                for (int m = 0; m < KM; ++m)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t x = min(max(__float_as_uint(most_step[m][i]) >> 23 & 255u, 47u), 227u);  // 2^-80 .. 2^100
+                        ev[m][i] = __uint_as_float(0x4b000000u | x) - (8388608.f + 127.f);
+                    }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int m = 0; m < KM; ++m)
+                            top = fmaxf(top, fmaxf(s[m][n][e] + ev[m][0], s[m][n][2 + e] + ev[m][1]));
+#pragma unroll
+                        for (int k = 4; k <= 16; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+                        if (top > R[n][e] + (kKv4Most - 1.f)) {  // the same for all lanes of the row
+                            top = ceilf(top) - kKv4Lift;
+                            const float f = ex2(R[n][e] - top);
+                            R[n][e] = top;
+                            l[n][e] *= f;
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) L[n][g][e] *= f;
+#pragma unroll
+                            for (int k = 0; k < 2 * NC; ++k) {
+                                o[n][k][e] *= f;
+                                o[n][k][2 + e] *= f;
+                            }
+                        }
+                    }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                l[n][0] = ln[n][0];
+                l[n][1] = ln[n][1];
+            }
+            // what is multiplied by low, and the products with the values' codes
+#pragma unroll
+            for (int m = 0; m < KM; ++m) {
+                uint32_t wa[NC], wb[NC];
+                codes<true>(ka0 + m * dk + v_codes, kb0 + m * dk + v_codes, wa, wb);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    uint32_t wf[KP][NT][2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float step = bf16_lo_f(pv[m][i][g]), low = fmaf(8.f, step, bf16_hi_f(pv[m][i][g]));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            float w0 = pr[m][n][2 * i] * step, w1 = pr[m][n][2 * i + 1] * step;
+                            // scales that a row does not see may be no numbers
+                            if (whole || vis[m][n][2 * i]) L[n][g][0] = fmaf(pr[m][n][2 * i], low, L[n][g][0]);
+                            else w0 = 0.f;
+                            if (whole || vis[m][n][2 * i + 1]) L[n][g][1] = fmaf(pr[m][n][2 * i + 1], low, L[n][g][1]);
+                            else w1 = 0.f;
+                            const uint32_t u = pack_f16(w0, w1);
+                            wf[0][n][i] = movm_t(u);
+                            if constexpr (KP == 2) {
+                                const float2 hi = unpack_f16(u);
+                                wf[KP - 1][n][i] = movm_t(pack_f16(w0 - hi.x, w1 - hi.y));
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int ch = g * CPG; ch < (g + 1) * CPG; ++ch) {
+                        uint32_t a0[4], a1[4];
+                        apart<true>(wa[ch], wb[ch], a0, a1);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma_f16(o[n][2 * ch], a0[0], a0[1], a0[2], a0[3], wf[0][n][0], wf[0][n][1]);
+                            mma_f16(o[n][2 * ch + 1], a1[0], a1[1], a1[2], a1[3], wf[0][n][0], wf[0][n][1]);
+                            if constexpr (KP == 2) {  // apart, as above
+                                float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma_f16(x, a0[0], a0[1], a0[2], a0[3], wf[KP - 1][n][0], wf[KP - 1][n][1]);
+                                mma_f16(y, a1[0], a1[1], a1[2], a1[3], wf[KP - 1][n][0], wf[KP - 1][n][1]);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    o[n][2 * ch][i] += x[i];
+                                    o[n][2 * ch + 1][i] += y[i];
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+        };
 
 #pragma unroll 1
         for (int j = 0; j < nt; ++j) {
@@ -527,220 +749,9 @@ struct Kv4Consumer {
             for (int h = 0; h < 2; h += KM) {
                 const int kb = kw + h * 16;
                 if (kb >= khi || kb + 16 * KM <= sg.k0) continue;
-                const bool whole = kb >= sg.k0 && kb + 16 * KM <= klo;
-                float s[KM][NT][4];
-                uint32_t pv[KM][2][NG];  // (step, lowest) of the values of keys gq and gq + 8
-                bool vis[KM][NT][4];
-#pragma unroll
-                for (int m = 0; m < KM; ++m) {
-                    const uint32_t ka = tile + (KM == 2 ? kc[2 * m] : h ? kc[2] : kc[0]), kb2 = tile + (KM == 2 ? kc[2 * m + 1] : h ? kc[3] : kc[1]);
-                    const uint32_t sa = tile + (KM == 2 ? sc[2 * m] : h ? sc[2] : sc[0]), sb = tile + (KM == 2 ? sc[2 * m + 1] : h ? sc[3] : sc[1]);
-                    uint32_t pk[2][NG], wa[NC], wb[NC];
-                    codes<false>(ka, kb2, wa, wb);
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        pk[0][g] = lds32(sa + g * 32);
-                        pk[1][g] = lds32(sb + g * 32);
-                        pv[m][0][g] = lds32(sa + v_scales + g * 32);
-                        pv[m][1][g] = lds32(sb + v_scales + g * 32);
-                    }
-                    uint64_t tot[NT][2], lo2[NT][2];  // of keys gq, gq + 8: rows 2 tq, 2 tq + 1
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        float acc[KP][NT][SPL][4];  // the parts apart: sums of the second are far smaller
-#pragma unroll
-                        for (int k = 0; k < KP; ++k)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int x = 0; x < SPL; ++x) acc[k][n][x][0] = acc[k][n][x][1] = acc[k][n][x][2] = acc[k][n][x][3] = 0.f;
-#pragma unroll
-                        for (int ch = g * CPG; ch < (g + 1) * CPG; ++ch) {
-                            uint32_t a0[4], a1[4];
-                            apart<!kBF16>(wa[ch], wb[ch], a0, a1);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int k = 0; k < KP; ++k) {
-                                    uint32_t q4[4];
-                                    if constexpr (kQRegs) {
-#pragma unroll
-                                        for (int i = 0; i < 4; ++i) q4[i] = qr[k][ch][i];
-                                    } else {
-                                        lds128(qaddr + n * C::QTILE + (k * NC + ch) * 512, q4);
-                                    }
-                                    mma_f16(acc[k][n][0], a0[0], a0[2], a0[1], a0[3], q4[0], q4[1]);
-                                    mma_f16(acc[k][n][SPL - 1], a1[0], a1[2], a1[1], a1[3], q4[2], q4[3]);
-                                }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float step = bf16_lo_f(pk[i][g]);
-                            const float low = kBF16 ? bf16_hi_f(pk[i][g]) : fmaf(8.f, step, bf16_hi_f(pk[i][g]));
-                            const uint64_t step2 = pk2(step, step), low2 = pk2(low, low);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                float x = acc[0][n][0][2 * i], y = acc[0][n][0][2 * i + 1];
-#pragma unroll
-                                for (int k = 1; k < KP * SPL; ++k) {
-                                    x += acc[k / SPL][n][k % SPL][2 * i];
-                                    y += acc[k / SPL][n][k % SPL][2 * i + 1];
-                                }
-                                const uint64_t a2 = pk2(x, y);
-                                tot[n][i] = g == 0 ? mul2(a2, step2) : fma2(a2, step2, tot[n][i]);
-                                lo2[n][i] = g == 0 ? mul2(low2, qs2[n][g]) : fma2(low2, qs2[n][g], lo2[n][i]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) up2(fma2(tot[n][i], F2[n], lo2[n][i]), s[m][n][2 * i], s[m][n][2 * i + 1]);
-                    if (!whole) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int key = kb + m * 16 + i * 8 + gq;
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    vis[m][n][2 * i + e] = key >= sg.k0 && key < lim[n][e];
-                                    if (!vis[m][n][2 * i + e]) s[m][n][2 * i + e] = -INFINITY;
-                                }
-                        }
-                    }
-                }
-                // Weights against the references as they are; where a weight times its step, or a row's sum, goes
-                // too far, the references move and they are formed once more.
-                float pr[KM][NT][4], ln[NT][2];
-                uint32_t wf[KP][KM][NT][NG][2];
-#pragma unroll 1
-                for (bool again = false;; again = true) {
-                    uint32_t most = 0;
-                    bool far = false;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        ln[n][0] = l[n][0];
-                        ln[n][1] = l[n][1];
-#pragma unroll
-                        for (int m = 0; m < KM; ++m)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const float p0 = ex2(s[m][n][2 * i] - R[n][0]), p1 = ex2(s[m][n][2 * i + 1] - R[n][1]);
-                                pr[m][n][2 * i] = p0;
-                                pr[m][n][2 * i + 1] = p1;
-                                ln[n][0] += p0;
-                                ln[n][1] += p1;
-#pragma unroll
-                                for (int g = 0; g < NG; ++g) {
-                                    const float step = bf16_lo_f(pv[m][i][g]);
-                                    float w0 = p0 * step, w1 = p1 * step;
-                                    if (!whole) {  // scales that a row does not see may be no numbers
-                                        if (!vis[m][n][2 * i]) w0 = 0.f;
-                                        if (!vis[m][n][2 * i + 1]) w1 = 0.f;
-                                    }
-                                    const uint32_t u = pack_f16(w0, w1);
-                                    wf[0][m][n][g][i] = u;
-                                    most = max_f16(most, u);
-                                    if constexpr (KP == 2) {
-                                        const float2 hi = unpack_f16(u);
-                                        wf[1][m][n][g][i] = pack_f16(w0 - hi.x, w1 - hi.y);
-                                    }
-                                }
-                            }
-                        far |= fmaxf(ln[n][0], ln[n][1]) > kMostSum;
-                    }
-                    if (again || !__any_sync(0xffffffffu, far || any_above(most, kMostWeight))) break;
-                    // up to the maximum of score + log2 of the values' step (the largest of the groups')
-                    float ev[KM][2];
-#pragma unroll
-                    for (int m = 0; m < KM; ++m)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t x = pv[m][i][0] & 0x7f80u;
-#pragma unroll
-                            for (int g = 1; g < NG; ++g) x = max(x, pv[m][i][g] & 0x7f80u);
-                            x = min(max(x >> 7, 47u), 227u);  // 2^-80 .. 2^100
-                            ev[m][i] = __uint_as_float(0x4b000000u | x) - (8388608.f + 127.f);
-                        }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float top = -INFINITY;
-#pragma unroll
-                            for (int m = 0; m < KM; ++m)
-                                top = fmaxf(top, fmaxf(s[m][n][e] + ev[m][0], s[m][n][2 + e] + ev[m][1]));
-#pragma unroll
-                            for (int k = 4; k <= 16; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-                            if (top > R[n][e] + (kKv4Most - 1.f)) {  // the same for all lanes of the row
-                                top = ceilf(top) - kKv4Lift;
-                                const float f = ex2(R[n][e] - top);
-                                R[n][e] = top;
-                                l[n][e] *= f;
-#pragma unroll
-                                for (int g = 0; g < NG; ++g) L[n][g][e] *= f;
-#pragma unroll
-                                for (int k = 0; k < 2 * NC; ++k) {
-                                    o[n][k][e] *= f;
-                                    o[n][k][2 + e] *= f;
-                                }
-                            }
-                        }
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    l[n][0] = ln[n][0];
-                    l[n][1] = ln[n][1];
-                }
-                // what is multiplied by low, and the products with the values' codes
-#pragma unroll
-                for (int m = 0; m < KM; ++m) {
-                    uint32_t wa[NC], wb[NC];
-                    codes<true>(tile + v_codes + (KM == 2 ? kc[2 * m] : h ? kc[2] : kc[0]),
-                                tile + v_codes + (KM == 2 ? kc[2 * m + 1] : h ? kc[3] : kc[1]), wa, wb);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            const float low = fmaf(8.f, bf16_lo_f(pv[m][i][g]), bf16_hi_f(pv[m][i][g]));
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    if (whole || vis[m][n][2 * i + e]) L[n][g][e] = fmaf(pr[m][n][2 * i + e], low, L[n][g][e]);
-                        }
-#pragma unroll
-                    for (int k = 0; k < KP; ++k)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int g = 0; g < NG; ++g)
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) wf[k][m][n][g][i] = movm_t(wf[k][m][n][g][i]);
-#pragma unroll
-                    for (int ch = 0; ch < NC; ++ch) {
-                        uint32_t a0[4], a1[4];
-                        apart<true>(wa[ch], wb[ch], a0, a1);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            const uint32_t(&b)[2] = wf[0][m][n][ch / CPG];
-                            mma_f16(o[n][2 * ch], a0[0], a0[1], a0[2], a0[3], b[0], b[1]);
-                            mma_f16(o[n][2 * ch + 1], a1[0], a1[1], a1[2], a1[3], b[0], b[1]);
-                            if constexpr (KP == 2) {  // apart, as above
-                                const uint32_t(&b2)[2] = wf[KP - 1][m][n][ch / CPG];
-                                float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma_f16(x, a0[0], a0[1], a0[2], a0[3], b2[0], b2[1]);
-                                mma_f16(y, a1[0], a1[1], a1[2], a1[3], b2[0], b2[1]);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    o[n][2 * ch][i] += x[i];
-                                    o[n][2 * ch + 1][i] += y[i];
-                                }
-                            }
-                        }
-                    }
-                }
+                const uint32_t ok = tile + h * dk, os = tile + h * ds;
+                if (kb >= sg.k0 && kb + 16 * KM <= klo) step(std::true_type(), kb, kc[0] + ok, kc[1] + ok, sc[0] + os, sc[1] + os);
+                else step(std::false_type(), kb, kc[0] + ok, kc[1] + ok, sc[0] + os, sc[1] + os);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->empty[st.s]);
@@ -808,7 +819,7 @@ struct Kv4Consumer {
             const int t0 = sg.k0 / kKeyTile, nt = (sg.k1 + kKeyTile - 1) / kKeyTile - t0;
             bool ok;
             if (kDecode || sg.nrow <= 8) ok = rows<1, KM>(sg, t0, nt);
-            else if constexpr (!kDecode) ok = sg.nrow <= 16 ? rows<2, 1>(sg, t0, nt) : rows<3, 1>(sg, t0, nt);
+            else if constexpr (!kDecode) ok = rows<2, 1>(sg, t0, nt);
             if (!ok) return;
         }
     }
@@ -854,7 +865,7 @@ __global__ void __launch_bounds__((kCons + kKv4Mergers + 2) * 32, 1) art_attend_
     if (s0 >= s1) return;
     if (w < kCons) {
         if (p.stall && !wait_tc(&c->stall, 0u, &c->abort, p)) return;
-        Kv4Consumer<kBF16, D, NG, kCons> k{pp, p, c, smem_addr(gen), gen, w, lane};
+        Kv4Consumer<kBF16, D, NG, kCons> k{pp, p, c, smem_addr(gen), gen, w, lane, pp.f16_1024};
         k.template run<KM, kDecode>(s0, s1);
     } else if (w < kCons + kKv4Mergers) {
         kv4_mergers<kBF16, D, NG, kCons>(p, gen, c, s0, s1);
@@ -875,13 +886,9 @@ cudaError_t launch_kv4_as(const AttendKv4Params& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     return launch_after(kernel, dim3(p.a.ctas), dim3(C::THREADS), smem, st, p);
 }
-#ifndef KV4_CONS
-#define KV4_CONS 12
-#define KV4_KM 1
-#endif
 template <bool kBF16, int D, int NG>
 cudaError_t launch_kv4(const AttendKv4Params& p, cudaStream_t st) {
-    return p.a.shared ? launch_kv4_as<kBF16, D, NG, KV4_CONS, KV4_KM, true>(p, st) : launch_kv4_as<kBF16, D, NG, 8, 2, false>(p, st);
+    return p.a.shared ? launch_kv4_as<kBF16, D, NG, 12, 1, true>(p, st) : launch_kv4_as<kBF16, D, NG, 8, 2, false>(p, st);
 }
 
 // One translation unit for each head_dim and type.
