@@ -461,15 +461,25 @@ int art_read_kv4(const void* cache, int32_t group, const int32_t* block_table, c
  * which sees all of its keys (a decode step), num_tokens = batch.
  *   workspace  dense_extend_kv4_workspace_bytes(shape, num_tokens, group) bytes
  *              (0: sizes beyond the supported range)
- * Rounding: codes enter the products as they are; queries exactly (bf16) or to
+ * Paths (dense_extend_kv4_path): 0 attends over the codes; 1, for prompt chunks in
+ * bf16 (with q_offsets, num_tokens * G of 96 * batch and num_tokens * num_q_heads of
+ * 2048 or more), reads the cache of the sequences with new tokens back into the workspace, as art_read_kv4 does, and
+ * runs dense_extend's kernels on it. Path 1 is offered where batch * max_pages_per_seq
+ * pages of keys and values take 4 GiB at most, and taken where the workspace holds
+ * them; one of dense_extend_kv4_min_workspace_bytes keeps every call on path 0.
+ * Rounding. Path 0: codes enter the products as they are; queries exactly (bf16) or to
  * about 22 bits (fp32), weights times step to 11 bits (bf16) or about 22 (fp32);
- * everything else is fp32. Queries below 2^100 in magnitude.
+ * everything else is fp32. Path 1: keys and values are rounded to bf16, and the rest is
+ * as dense_extend; a value that some new tokens of a sequence see must be finite for
+ * the others too. Steps must not be negative, queries be below 2^100 in magnitude.
  * A token that sees no key, and every token of a sequence with a bad length or
  * page, gets a zero output. With bad offsets no output is written. What lies
- * outside a row's keys may be anything, a group of NaN that another row sees too.
- * Supported: as dense_extend, with rows = 32 and keys = 128.
+ * outside a row's keys may be anything, on path 0 a group of NaN that another row sees too.
+ * Supported: as dense_extend, with rows = 16 and keys = 128.
  */
+int dense_extend_kv4_path(const art_shape* shape, int32_t num_tokens, int32_t group, size_t workspace_bytes);
 size_t dense_extend_kv4_workspace_bytes(const art_shape* shape, int32_t num_tokens, int32_t group);
+size_t dense_extend_kv4_min_workspace_bytes(const art_shape* shape, int32_t num_tokens, int32_t group);
 int dense_extend_kv4(const void* q, const void* cache, int32_t group, const int32_t* block_table,
                      const int32_t* seq_lens, const int32_t* q_offsets, int32_t num_tokens, int32_t causal,
                      void* out, const art_shape* shape, void* workspace, size_t workspace_bytes, void* stream);

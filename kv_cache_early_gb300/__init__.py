@@ -32,7 +32,7 @@ EXPORTS = ("art_workspace_bytes", "art_decode_path", "dense_decode_path", "art_d
            "dense_decode_shared_workspace_bytes", "dense_decode_shared",
            "art_kv4_page_bytes", "art_append_kv4_workspace_bytes", "art_append_kv4",
            "art_read_kv4_workspace_bytes", "art_read_kv4",
-           "dense_extend_kv4_workspace_bytes", "dense_extend_kv4")
+           "dense_extend_kv4_workspace_bytes", "dense_extend_kv4_min_workspace_bytes", "dense_extend_kv4_path", "dense_extend_kv4")
 
 
 class ArtShape(ctypes.Structure):
@@ -123,6 +123,10 @@ def lib(path: str = LIB_PATH) -> ctypes.CDLL:
             L.art_read_kv4.restype = ctypes.c_int
             L.dense_extend_kv4_workspace_bytes.argtypes = [SP, I32, I32]
             L.dense_extend_kv4_workspace_bytes.restype = SZ
+            L.dense_extend_kv4_min_workspace_bytes.argtypes = [SP, I32, I32]
+            L.dense_extend_kv4_min_workspace_bytes.restype = SZ
+            L.dense_extend_kv4_path.argtypes = [SP, I32, I32, SZ]
+            L.dense_extend_kv4_path.restype = ctypes.c_int
             L.dense_extend_kv4.argtypes = [P, P, I32, P, P, P, I32, I32, P, SP, P, SZ, P]
             L.dense_extend_kv4.restype = ctypes.c_int
             _lib = L
@@ -593,6 +597,16 @@ def art_read_kv4(cache, block_table, seq_lens, q_offsets, k_out, v_out, shape: A
 
 def dense_extend_kv4_workspace_bytes(shape: ArtShape, num_tokens: int, group: int) -> int:
     return int(lib().dense_extend_kv4_workspace_bytes(ctypes.byref(shape), int(num_tokens), int(group)))
+
+
+def dense_extend_kv4_min_workspace_bytes(shape: ArtShape, num_tokens: int, group: int) -> int:
+    """The least that a call takes; with it every call attends over the codes (see include/art.h)."""
+    return int(lib().dense_extend_kv4_min_workspace_bytes(ctypes.byref(shape), int(num_tokens), int(group)))
+
+
+def dense_extend_kv4_path(shape: ArtShape, num_tokens: int, group: int, workspace_bytes: int) -> int:
+    """The path a call with offsets takes: 0 over the codes, 1 reads the cache back first (see include/art.h)."""
+    return int(lib().dense_extend_kv4_path(ctypes.byref(shape), int(num_tokens), int(group), int(workspace_bytes)))
 
 
 def dense_extend_kv4(q, cache, block_table, seq_lens, q_offsets, out, shape: ArtShape, workspace, group: int,

@@ -1,4 +1,9 @@
-// art_attend_kv4.cu -- dense_extend_kv4: argument checks and the choice of the kernel.
+// art_attend_kv4.cu -- dense_extend_kv4: argument checks and the choice of the kernels.
+//
+// Two paths. Path 0 attends over the codes (art_attend_kv4.cuh): 16 rows of queries at a time, bound by the
+// cache's bytes for few rows and by the taking apart of codes and the small products for many. Path 1, for prompt chunks
+// in bf16, reads the cache back to bf16 in the workspace and calls the tensor-memory kernel of dense_extend
+// on it, whose products are several times faster.
 #include <cmath>
 
 #include "art_attend_kv4.cuh"
@@ -26,6 +31,45 @@ static cudaError_t launch_attend_kv4(const AttendParams& p, const void* more, cu
 }
 
 static bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Rows of a key head and sequence, in the mean, and rows of all heads together, from which the cache is read back.
+// Measured, codes against read back (us; 32/8 heads, d 128, context 2048, 8 sequences): 64 rows 48 / 50, 96 rows
+// 62 / 54, 256 rows 127 / 69; context 4096, 32 sequences: 64 rows 217 / 239, 96 rows 313 / 243. One sequence of
+// 8192 tokens leaves most SMs idle on path 1's large tiles: 192 rows (1536 in all) 57 / 74, 256 (2048) 69 / 73,
+// 384 92 / 62. 8/8 heads, d 64, 8 sequences of 8192: 64 rows 69 / 86, 96 rows 97 / 87.
+constexpr int kReadBackRows = 96, kReadBackAll = 2048;
+constexpr size_t kReadBackMost = 4ull << 30;  // bytes of a pool at most
+
+// What a call needs of the workspace, by its path. Path 1: dense_extend's part, the pool's block table, the pool.
+struct Kv4Workspace {
+    size_t codes;  // path 0; 0 where its sizes are not supported
+    size_t table, pool, whole;  // path 1: offsets of the last two and the bytes, whole 0 where it is not offered
+};
+static Kv4Workspace kv4_workspace(const art_shape& s, int num_tokens, bool offsets) {
+    Kv4Workspace w = {};
+    AttendParams p = {};
+    kv4_shape(p, s);
+    p.T = num_tokens;
+    p.shared = !offsets;
+    w.codes = attend_layout(p, nullptr);
+    const int G = s.num_q_heads / s.num_kv_heads;
+    if (!offsets || s.dtype != ART_DTYPE_BF16 || (long long)num_tokens * G < (long long)kReadBackRows * s.batch ||
+        (long long)num_tokens * s.num_q_heads < kReadBackAll)
+        return w;
+    const unsigned long long pages = (unsigned long long)s.batch * s.max_pages_per_seq;
+    const unsigned long long page = 2ull * s.num_kv_heads * s.page_size * s.head_dim;  // of keys, or values
+    if (pages > 0x7fffffffull || pages * page > kReadBackMost / 2) return w;
+    AttendParams t = {};
+    attend_shape(t, s);
+    t.T = num_tokens;
+    const size_t need = attend_layout(t, nullptr);
+    if (need == 0) return w;
+    w.table = up256(need > w.codes ? need : w.codes);
+    w.pool = up256(w.table + pages * sizeof(int32_t));
+    w.whole = w.pool + 2 * pages * page;
+    return w;
+}
 
 }  // namespace art
 
@@ -33,18 +77,31 @@ using namespace art;
 
 extern "C" {
 
-size_t dense_extend_kv4_workspace_bytes(const art_shape* shape, int32_t num_tokens, int32_t group) {
+static size_t kv4_bytes(const art_shape* shape, int32_t num_tokens, int32_t group, bool least) {
     if (check_cache_shape(shape) != ART_OK || num_tokens < 0 || !kv4_group_ok(shape->head_dim, group)) return 0;
-    // a call without offsets, and one with them
-    AttendParams p = {}, d = {};
-    kv4_shape(p, *shape);
-    p.T = num_tokens;
-    const size_t with = attend_layout(p, nullptr);
-    if (num_tokens != shape->batch) return with;
-    kv4_shape(d, *shape);
-    d.shared = 1;
-    const size_t without = attend_layout(d, nullptr);
-    return with == 0 || without == 0 ? 0 : with > without ? with : without;
+    Kv4Workspace w = kv4_workspace(*shape, num_tokens, true);
+    if (w.codes == 0) return 0;
+    size_t need = !least && w.whole > w.codes ? w.whole : w.codes;
+    if (num_tokens == shape->batch) {  // a call without offsets
+        w = kv4_workspace(*shape, num_tokens, false);
+        if (w.codes == 0) return 0;
+        if (w.codes > need) need = w.codes;
+    }
+    return need;
+}
+
+size_t dense_extend_kv4_workspace_bytes(const art_shape* shape, int32_t num_tokens, int32_t group) {
+    return kv4_bytes(shape, num_tokens, group, false);
+}
+
+size_t dense_extend_kv4_min_workspace_bytes(const art_shape* shape, int32_t num_tokens, int32_t group) {
+    return kv4_bytes(shape, num_tokens, group, true);
+}
+
+int dense_extend_kv4_path(const art_shape* shape, int32_t num_tokens, int32_t group, size_t workspace_bytes) {
+    if (check_cache_shape(shape) != ART_OK || num_tokens < 0 || !kv4_group_ok(shape->head_dim, group)) return 0;
+    const Kv4Workspace w = kv4_workspace(*shape, num_tokens, true);
+    return w.whole != 0 && workspace_bytes >= w.whole;
 }
 
 int dense_extend_kv4(const void* q, const void* cache, int32_t group, const int32_t* block_table, const int32_t* seq_lens,
@@ -66,7 +123,35 @@ int dense_extend_kv4(const void* q, const void* cache, int32_t group, const int3
     pp.page_bytes = l.page_bytes;
     pp.bf16 = s.dtype == ART_DTYPE_BF16;
     pp.f16_1024 = 0x64006400u;
+    const Kv4Workspace w = kv4_workspace(s, num_tokens, q_offsets != nullptr);
+    if (w.codes == 0) return ART_ERR_UNSUPPORTED;
+    if (workspace_bytes < w.codes) return ART_ERR_WORKSPACE;
     AttendParams p = {};
+    if (w.whole != 0 && workspace_bytes >= w.whole) {
+        int dev = 0, sms = 0;
+        cudaError_t e;
+        if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e);
+        if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return cuda_fail(e);
+        unsigned char* ws = static_cast<unsigned char*>(workspace);
+        int32_t* map = reinterpret_cast<int32_t*>(ws + w.table);
+        unsigned char *k = ws + w.pool, *v = k + (w.whole - w.pool) / 2;
+        e = read_kv4_pool(s, group, cache, block_table, seq_lens, q_offsets, map, k, v, sms, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return cuda_fail(e);
+        art_shape plain = s;
+        plain.num_pages_total = s.batch * s.max_pages_per_seq;
+        attend_shape(p, plain);
+        p.num_pages = plain.num_pages_total;
+        p.k = k;
+        p.v = v;
+        p.q = q;
+        p.out = out;
+        p.block_table = map;
+        p.seq_lens = seq_lens;
+        p.offsets = q_offsets;
+        p.causal = causal;
+        p.T = num_tokens;
+        return attend_run(p, plain, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+    }
     kv4_shape(p, s);
     p.q = q;
     p.out = out;

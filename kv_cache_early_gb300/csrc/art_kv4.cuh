@@ -31,6 +31,12 @@ inline bool kv4_group_ok(int head_dim, int group) {
     return (group == 32 || group == 64 || group == 128) && group <= head_dim;
 }
 
+// Reads the whole cache of the sequences that have new tokens (by q_offsets) into a pool of max_pages_per_seq pages for
+// each, whose block table `map` it writes: -1 for a page outside the cache (art_read_kv4.cu).
+cudaError_t read_kv4_pool(const art_shape& s, int group, const void* cache, const int32_t* block_table,
+                          const int32_t* seq_lens, const int32_t* q_offsets, int32_t* map, void* k_out, void* v_out,
+                          int sms, cudaStream_t st);
+
 // Place of a token in its slab's arrays: u is its number in the slab.
 template <int D>
 __device__ __forceinline__ int kv4_code_at(int u, int chunk) {  // 16 bytes: columns 32 chunk ..

@@ -21,6 +21,9 @@ struct ReadKv4Params {
     const int32_t *block_table, *seq_lens;
     const int32_t* q_offsets;  // null: every token, or (one) the last one of each sequence
     const int32_t* out_table;  // null: rows
+    // a pool with max_pages pages for each sequence, and its block table, which is written, -1 for bad pages; the
+    // sequences with new tokens by q_offsets only
+    int32_t* map;
     void *k_out, *v_out;
     WsHeader* hdr;
     int B, T, Hkv, Ps, max_pages, num_pages, out_pages;
@@ -32,7 +35,9 @@ __device__ __forceinline__ bool read_span(const ReadKv4Params& p, int b, int& lo
     const int len = p.seq_lens[b];
     lo = hi = row0 = 0;
     int n = len;
-    if (!p.out_table) {
+    if (p.map) {
+        if (p.q_offsets[b] == p.q_offsets[b + 1]) return false;
+    } else if (!p.out_table) {
         const int a = p.q_offsets ? p.q_offsets[b] : b, z = p.q_offsets ? p.q_offsets[b + 1] : b + 1;
         if (a < 0 || z < a || z > p.T) {
             err |= ART_STATUS_BAD_OFFSETS;
@@ -44,7 +49,7 @@ __device__ __forceinline__ bool read_span(const ReadKv4Params& p, int b, int& lo
     if (len < 0 || len < n || (long long)len > (long long)p.max_pages * p.Ps) {
         err |= ART_STATUS_BAD_SEQLEN;
         // its rows are zero
-        hi = p.out_table ? 0 : n;
+        hi = p.out_table || p.map ? 0 : n;
         return false;
     }
     lo = len - n;
@@ -106,7 +111,11 @@ __device__ __forceinline__ void read_unit(const ReadKv4Params& p, const ReadRun&
     const bool good = page >= 0 && page < p.num_pages;
     size_t row = 0;
     bool to = here;
-    if (p.out_table) {
+    if (p.map) {
+        row = (at * p.Hkv + g) * p.Ps + in_page;
+        to = good;
+        if (here && g == 0 && w == 0) p.map[at] = good ? (int)at : -1;
+    } else if (p.out_table) {
         const int o = here ? p.out_table[at] : -1;
         to = o >= 0 && o < p.out_pages;
         row = ((size_t)(to ? o : 0) * p.Hkv + g) * p.Ps + in_page;
@@ -156,7 +165,7 @@ __device__ __forceinline__ void read_unit(const ReadKv4Params& p, const ReadRun&
 template <bool kBF16, int D, int NG>
 __global__ void __launch_bounds__(kReadThreads) art_read_kv4_kernel(const ReadKv4Params p) {
     if (blockIdx.x == 0) {
-        read_check(p);
+        if (!p.map) read_check(p);
         return;
     }
     constexpr int WARPS = kReadThreads / 32;
@@ -224,6 +233,50 @@ __global__ void __launch_bounds__(kReadThreads) art_read_kv4_kernel(const ReadKv
     }
 }
 
+static void launch_read_kv4(const ReadKv4Params& p, const art_shape& s, int group, unsigned grid, cudaStream_t st) {
+    const int ng = s.head_dim / group;
+    const bool bf = s.dtype == ART_DTYPE_BF16;
+#define ART_READ4(DD, NN)                                                              \
+    (bf ? art_read_kv4_kernel<true, DD, NN><<<grid, kReadThreads, 0, st>>>(p)          \
+        : art_read_kv4_kernel<false, DD, NN><<<grid, kReadThreads, 0, st>>>(p))
+    if (s.head_dim == 128) {
+        if (ng == 1) ART_READ4(128, 1);
+        else if (ng == 2) ART_READ4(128, 2);
+        else ART_READ4(128, 4);
+    } else {
+        if (ng == 1) ART_READ4(64, 1);
+        else ART_READ4(64, 2);
+    }
+#undef ART_READ4
+}
+
+static void read_params(ReadKv4Params& p, const art_shape& s, int group) {
+    p.B = s.batch;
+    p.Hkv = s.num_kv_heads;
+    p.Ps = s.page_size;
+    p.max_pages = s.max_pages_per_seq;
+    p.num_pages = s.num_pages_total;
+    const Kv4Layout l = kv4_layout(s.page_size, s.head_dim, group);
+    p.slab = l.slab;
+    p.slab_bytes = l.slab_bytes;
+    p.page_bytes = l.page_bytes;
+}
+
+cudaError_t read_kv4_pool(const art_shape& s, int group, const void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* q_offsets, int32_t* map, void* k_out, void* v_out, int sms, cudaStream_t st) {
+    ReadKv4Params p = {};
+    read_params(p, s, group);
+    p.cache = static_cast<const unsigned char*>(cache);
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.q_offsets = q_offsets;
+    p.map = map;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    launch_read_kv4(p, s, group, (unsigned)(kReadCtas * sms) + 1u, st);
+    return cudaGetLastError();
+}
+
 int check_cache_shape(const art_shape* s);  // art_attend.cu
 
 }  // namespace art
@@ -253,26 +306,18 @@ int art_read_kv4(const void* cache, int32_t group, const int32_t* block_table, c
     cudaError_t e;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e);
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return cuda_fail(e);
-    ReadKv4Params p;
+    ReadKv4Params p = {};
+    read_params(p, s, group);
     p.cache = static_cast<const unsigned char*>(cache);
     p.block_table = block_table;
     p.seq_lens = seq_lens;
     p.q_offsets = q_offsets;
     p.out_table = out_table;
+    p.out_pages = out_pages;
     p.k_out = k_out;
     p.v_out = v_out;
     p.hdr = static_cast<WsHeader*>(workspace);
-    p.B = s.batch;
     p.T = num_tokens;
-    p.Hkv = s.num_kv_heads;
-    p.Ps = s.page_size;
-    p.max_pages = s.max_pages_per_seq;
-    p.num_pages = s.num_pages_total;
-    p.out_pages = out_pages;
-    const Kv4Layout l = kv4_layout(s.page_size, s.head_dim, group);
-    p.slab = l.slab;
-    p.slab_bytes = l.slab_bytes;
-    p.page_bytes = l.page_bytes;
     // no more CTAs than there may be units of rows
     long long ctas = (long long)kReadCtas * sms;
     if (!out_table) {
@@ -280,21 +325,7 @@ int art_read_kv4(const void* cache, int32_t group, const int32_t* block_table, c
         if (units < ctas) ctas = units > 0 ? units : 1;
     }
     const unsigned grid = (unsigned)ctas + 1u;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int ng = s.head_dim / group;
-    const bool bf = s.dtype == ART_DTYPE_BF16;
-#define ART_READ4(DD, NN)                                                              \
-    (bf ? art_read_kv4_kernel<true, DD, NN><<<grid, kReadThreads, 0, st>>>(p)          \
-        : art_read_kv4_kernel<false, DD, NN><<<grid, kReadThreads, 0, st>>>(p))
-    if (s.head_dim == 128) {
-        if (ng == 1) ART_READ4(128, 1);
-        else if (ng == 2) ART_READ4(128, 2);
-        else ART_READ4(128, 4);
-    } else {
-        if (ng == 1) ART_READ4(64, 1);
-        else ART_READ4(64, 2);
-    }
-#undef ART_READ4
+    launch_read_kv4(p, s, group, grid, static_cast<cudaStream_t>(stream));
     e = cudaGetLastError();
     return e == cudaSuccess ? ART_OK : cuda_fail(e);
 }

@@ -334,11 +334,13 @@ def test_read_bad_device_data():
 # ----------------------------------------------------------------------------
 # dense_extend_kv4
 # ----------------------------------------------------------------------------
-def run_extend(pool, q, off, causal, hq, offsets=True, table=None, lens=None, in_place=False, ws=None):
+def run_extend(pool, q, off, causal, hq, offsets=True, table=None, lens=None, in_place=False, path=0):
+    """path 0: a workspace that keeps every call on the codes."""
     dtype = pool.dtype
     shape = K.make_shape(**pool.shape(hq))
     T = q.shape[0]
-    ws = workspace(K.dense_extend_kv4_workspace_bytes(shape, T, pool.group)) if ws is None else ws
+    size = K.dense_extend_kv4_workspace_bytes if path else K.dense_extend_kv4_min_workspace_bytes
+    ws = workspace(size(shape, T, pool.group))
     tq = dev(q, dtype)
     out = tq if in_place else torch.full(q.shape, SENTINEL, dtype=tq.dtype, device="cuda")
     K.dense_extend_kv4(tq, dev(pool.bytes), dev(pool.table if table is None else table),
@@ -546,6 +548,72 @@ def test_no_tokens():
 
 
 # ----------------------------------------------------------------------------
+# prompt chunks: the cache read back in the workspace
+# ----------------------------------------------------------------------------
+def plain_rows(pool, b, kv):
+    """What art_read_kv4 gives of a sequence, [heads, tokens, d]."""
+    n = int(pool.seq_lens[b])
+    out = []
+    for g in range(pool.hkv):
+        c, s, z = Q.held(pool.bytes, pool.table[b], n, g, pool.page, pool.d, pool.group, kv)
+        out.append(rounded((z + s * c).astype(np.float32), "bf16").astype(np.float64))
+    return out
+
+
+@pytest.mark.parametrize("heads,page,group", [((8, 2, 128), 16, 64), ((8, 1, 64), 8, 32), ((14, 2, 128), 256, 128)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_chunks(heads, page, group, causal):
+    """Against attention over the values rounded to bf16, with dense_extend's tolerances (cache_ops_harness)."""
+    import cache_ops_harness as H
+    rng = np.random.default_rng(80)
+    hq, hkv, d = heads
+    new, lens = [200, 0, 90, 3], [200, 40, 240, 131]
+    pool = Pool4(rng, "bf16", hkv, d, page, group, lens).fill(rng)
+    pool.table[1] = -7  # a sequence without new tokens is not read
+    off = offsets_of(new, 1)
+    T = int(off[-1]) + 2
+    q = rounded(rng.standard_normal((T, hq, d)), "bf16")
+    shape = K.make_shape(**pool.shape(hq))
+    n = K.dense_extend_kv4_workspace_bytes(shape, T, group)
+    assert K.dense_extend_kv4_path(shape, T, group, n) == 1 and K.dense_extend_kv4_path(shape, T, group, n - 1) == 0
+    got, status = run_extend(pool, q, off, causal, hq, path=1)
+    assert status == 0
+    for b, (m, s) in enumerate(zip(new, lens)):
+        if m == 0:
+            continue
+        k, v = plain_rows(pool, b, 0), plain_rows(pool, b, 1)
+        for h in range(hq):
+            g = h // (hq // hkv)
+            for i in range(m):
+                seen = s - m + i + 1 if causal else s
+                x, kk, vv = q[off[b] + i, h], k[g][:seen], v[g][:seen]
+                ref, ref_abs = O.attend(x, kk, vv), O.attend(x, kk, np.abs(vv))
+                score = (np.abs(kk) @ np.abs(x)).max() / np.sqrt(d)
+                tol = H.attend_tol(ref, ref_abs, score, seen, d, np.abs(vv).max(), "bf16")
+                assert np.all(np.abs(got[off[b] + i, h] - ref) <= tol), (b, h, i)
+    assert (got[:1] == SENTINEL).all() and (got[T - 2:] == SENTINEL).all()
+
+
+def test_prompt_chunks_bad_device_data():
+    rng = np.random.default_rng(81)
+    new, lens = [90, 100, 80, 130], [90, 100, 150, 300]
+    pool = Pool4(rng, "bf16", 2, 64, 16, 32, lens).fill(rng)
+    off = offsets_of(new)
+    q = rounded(rng.standard_normal((int(off[-1]), 8, 64)), "bf16")
+    good, status = run_extend(pool, q, off, True, 8, path=1)
+    assert status == 0 and np.isfinite(good).all()
+    bad_lens, table = pool.seq_lens.copy(), pool.table.copy()
+    bad_lens[0] = 89                    # fewer than its new tokens
+    bad_lens[2] = pool.table.shape[1] * 16 + 1
+    table[3, 7] = pool.num_pages
+    got, status = run_extend(pool, q, off, True, 8, table=table, lens=bad_lens, path=1)
+    assert status == 4 | 8
+    assert not got[:90].any() and not got[190:].any() and np.array_equal(got[90:190], good[90:190])
+    got, status = run_extend(pool, q, np.array([0, 90, 80, 270, 400], np.int32), True, 8, path=1)
+    assert status & 128 and (got == SENTINEL).all()
+
+
+# ----------------------------------------------------------------------------
 # together
 # ----------------------------------------------------------------------------
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -561,11 +629,11 @@ def test_serving_run(dtype):
     table = torch.randperm(B * cap, device="cuda").to(torch.int32).reshape(B, cap)
     cache = torch.randint(0, 256, (B * cap, hkv, K.art_kv4_page_bytes(shape, group)), dtype=torch.uint8, device="cuda")
     inv = (10000.0 ** (-torch.arange(0, d, 2, device="cuda", dtype=torch.float64) / d)).float()
-    lens = torch.tensor([37, 1, 130], dtype=torch.int32, device="cuda")
-    off = torch.tensor([0, 37, 38, 168], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([37, 1, 230], dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 37, 38, 268], dtype=torch.int32, device="cuda")
     ws = [workspace(K.art_append_kv4_workspace_bytes(shape)), workspace(K.art_read_kv4_workspace_bytes(shape))]
-    T = 168
-    ws_e = workspace(K.dense_extend_kv4_workspace_bytes(shape, T, group))
+    T = 268
+    ws_e = workspace(K.dense_extend_kv4_min_workspace_bytes(shape, T, group))  # over the codes
     qkv = torch.randn(T, hq + 2 * hkv, d, device="cuda").to(dt)
     q_rot, out = torch.empty(T, hq, d, dtype=dt, device="cuda"), torch.empty(T, hq, d, dtype=dt, device="cuda")
     K.art_append_kv4(qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], table, lens, off, inv, q_rot, cache, shape, ws[0],
@@ -596,13 +664,20 @@ def test_serving_run(dtype):
         tol = (2.0 ** -8 * ref.abs() + 2.0 ** -12 * 12) if dtype == "bf16" else 2.0 ** -24 * (8 * 12 * 40 + 8 * 15 + 16) * 12 + 0 * ref
         assert (((got.double() - ref).abs() <= tol)).all(), float((got.double() - ref).abs().max())
 
-    near(out, reference(q_rot, [37, 1, 130]))
+    near(out, reference(q_rot, [37, 1, 230]))
     # the same cache through the plain calls: pages read back, dense_extend over them
     kc, vc = (torch.full((B * cap, hkv, page, d), float("nan"), dtype=dt, device="cuda") for _ in range(2))
     K.art_read_kv4(cache, table, lens, None, kc, vc, shape, ws[1], group=group, out_table=table)
     plain = torch.empty_like(out)
     ws_p = workspace(K.dense_extend_workspace_bytes(shape, T))
     K.dense_extend(q_rot, kc, vc, table, lens, off, plain, shape, ws_p)
+    # ... as dense_extend_kv4 does by itself where the workspace holds the pages: the same bits
+    if dtype == "bf16":
+        n = K.dense_extend_kv4_workspace_bytes(shape, T, group)
+        assert K.dense_extend_kv4_path(shape, T, group, n) == 1
+        back, ws_b = torch.empty_like(out), workspace(n)
+        K.dense_extend_kv4(q_rot, cache, table, lens, off, back, shape, ws_b, group=group)
+        assert torch.equal(back, plain) and K.art_read_device_status(ws_b) == 0
     # there keys and values are rounded to bf16: 2^-8 of scores (|q . k| / sqrt(d) < 40) and of values, on both sides
     tol = 2.0 ** -8 * (2 * 40 + 2) * 6 if dtype == "bf16" else 1e-3
     assert float((plain.double() - out.double()).abs().max()) <= tol

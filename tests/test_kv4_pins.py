@@ -154,6 +154,22 @@ def test_sizes(lib):
     assert lib.dense_extend_kv4_workspace_bytes(None, 4, 64) == 0
 
 
+def test_paths(lib):
+    """Path 1, in bf16 from 96 rows a sequence and 2048 rows in all on, where the pages fit 4 GiB and the workspace has room for them."""
+    s = good_shape(batch=2)  # 4 heads a key head
+    assert K.dense_extend_kv4_path(good_shape(batch=40), 959, 64, 1 << 40) == 0
+    assert K.dense_extend_kv4_path(good_shape(batch=40), 960, 64, 1 << 40) == 1
+    for tokens, path in ((255, 0), (256, 1), (1000, 1)):
+        full, least = (f(s, tokens, 64) for f in (K.dense_extend_kv4_workspace_bytes, K.dense_extend_kv4_min_workspace_bytes))
+        assert K.dense_extend_kv4_path(s, tokens, 64, full) == path and (full > least) == (path == 1)
+        assert K.dense_extend_kv4_path(s, tokens, 64, full - 1) == 0
+    assert full - least > 2 * 2 * 8 * 16 * 2 * 128 * 2  # keys and values of every page of the table
+    assert K.dense_extend_kv4_path(good_shape(batch=2, dtype=1), 1000, 64, 1 << 40) == 0
+    # 2 * 1 << 20 pages of 16 tokens x 2 heads x 128 columns x 2 bytes, keys and values: 32 GiB
+    assert K.dense_extend_kv4_path(good_shape(batch=2, max_pages_per_seq=1 << 20), 1000, 64, 1 << 40) == 0
+    assert K.dense_extend_kv4_path(s, -1, 64, 1 << 40) == K.dense_extend_kv4_path(s, 1000, 7, 1 << 40) == 0
+
+
 def test_binding_refuses_tensors_on_the_host():
     torch = pytest.importorskip("torch")
     s = good_shape()
