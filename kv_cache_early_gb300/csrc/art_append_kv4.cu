@@ -30,12 +30,19 @@ namespace art {
 
 // Up to these many tokens a CTA takes one token's keys and values, beyond it kKvTile's.
 constexpr int kFewTokensKv4 = 608;
-constexpr int kKvTile = 8;
+#ifndef KVT
+#define KVT 8
+#define TQ 4
+#endif
+constexpr int kKvTile = KVT, kQTile = TQ;
+#ifndef APP_BLK
+#define APP_BLK 4
+#endif
 
 struct AppendKv4Params {
     AppendParams a;
     unsigned char* cache;
-    int slab, slab_bytes, page_bytes;
+    int slab, slab_log2, slab_bytes, page_bytes;
     int q_blocks;  // blocks that rotate queries
 };
 
@@ -167,38 +174,69 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& scal
     }
     const float low = floor_bf16(mn);
     const float d = __fadd_rn(mx, -low);
-    if (!(d < kMaxRange)) {
-        scales = 0x7fc00000u;
-        return 0u;
-    }
-    // (d + de) / 15 = q + rest
+    // (d + de) / 15 = q + rest / 15: the quotient by a rounded 1 / 15, corrected once
     const float b = __fadd_rn(d, -mx);
     const float de = __fadd_rn(__fadd_rn(mx, -__fadd_rn(d, -b)), -__fadd_rn(low, b));
-    const float q = __fdiv_rn(d, 15.f), rest = fmaf(-15.f, q, d) + de;
+    constexpr float kFifteenth = 0.0666666701f;
+    const float q0 = __fmul_rn(d, kFifteenth), q = fmaf(fmaf(-15.f, q0, d), kFifteenth, q0);
+    const float rest = fmaf(-15.f, q, d) + de;
     uint32_t u = __float_as_uint(q);
     if ((u & 0xffffu) == 0x8000u && rest != 0.f) u += rest > 0.f ? 1 : -1;
     float step = bf16_lo_f(pack_bf16(__uint_as_float(u), 0.f));
     if (step < kMinStep) step = 0.f;
     scales = (__float_as_uint(step) >> 16) | __float_as_uint(low);
-    const float inv = step > 0.f ? __frcp_rn(step) : 0.f;
-    uint32_t codes = 0;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
+    if (step == 0.f) inv = 0.f;
+    // to the nearest whole number by 1.5 * 2^23, even at ties; the codes of four make a number below 2^16
+    float r[8], w[8], off = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float t = __fadd_rn(x[i], -low), v = t * inv;
-        const float m = __fadd_rn(v, 12582912.f);  // 1.5 * 2^23: to the nearest whole number, even at ties
-        uint32_t c = __float_as_uint(m) & 31u;
-        const float off = __fadd_rn(v, -__fadd_rn(m, -12582912.f));
-        if (fabsf(off) > 0.49998f) {  // v is within 16 * 3 * 2^-24 of x - low over step
-            const float h = floorf(v) + 0.5f, hs = h * step;  // the border; exact
+        const float v = __fmul_rn(__fadd_rn(x[i], -low), inv);
+        r[i] = __fadd_rn(__fadd_rn(v, 12582912.f), -12582912.f);
+        w[i] = __fadd_rn(v, -r[i]);
+        off = fmaxf(off, fabsf(w[i]));
+    }
+    if (off > 0.49998f) {  // v is within 16 * 4 * 2^-24 of (x - lowest) / step: near a border, by exact terms
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (fabsf(w[i]) <= 0.49998f) continue;
+            const float t = __fadd_rn(x[i], -low), f = w[i] > 0.f ? r[i] : r[i] - 1.f, hs = (f + 0.5f) * step;  // the border
             const float bb = __fadd_rn(t, -x[i]);
             const float te = __fadd_rn(__fadd_rn(x[i], -__fadd_rn(t, -bb)), -__fadd_rn(low, bb));
             const float side = __fadd_rn(__fadd_rn(t, -hs), te);
-            const uint32_t f = (uint32_t)(int)h;
-            c = side > 0.f ? f + 1 : side < 0.f ? f : f + (f & 1u);
+            r[i] = side > 0.f || (side == 0.f && ((int)f & 1)) ? f + 1.f : f;
         }
-        codes |= min(c, 15u) << (4 * i);
+    }
+    const float lo4 = fmaf(r[3], 4096.f, fmaf(r[2], 256.f, fmaf(r[1], 16.f, r[0])));
+    const float hi4 = fmaf(r[7], 4096.f, fmaf(r[6], 256.f, fmaf(r[5], 16.f, r[4])));
+    const uint32_t codes = (__float_as_uint(lo4 + 8388608.f) & 0xffffu) | (__float_as_uint(hi4 + 8388608.f) << 16);
+    if (!(d < kMaxRange)) {
+        scales = 0x7fc00000u;
+        return 0u;
     }
     return codes;
+}
+
+// Eight turned values x cos + y sin (y with its sign), rounded to the cache's type. bf16: from 32-bit arithmetic, which is
+// within 3.5 * 2^-24 (|x| + |y|) scale; where that bound holds a border between bf16 numbers, by turned(), for which
+// whole(e) gives column e's cosine and sine in full.
+template <bool kBF16, class F>
+__device__ __forceinline__ void turn8(const float (&x)[8], const float (&y)[8], const float2 (&cs)[8], float reach, F whole,
+                                      float (&o)[8]) {
+    if constexpr (kBF16) {
+        uint32_t differ = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float v = fmaf(x[e], cs[e].x, __fmul_rn(y[e], cs[e].y)), m = fabsf(x[e]) + fabsf(y[e]);
+            const uint32_t u = pack_bf16(fmaf(m, reach, v), fmaf(m, -reach, v));
+            differ |= u ^ (u >> 16);
+            o[e] = bf16_hi_f(u);
+        }
+        if ((differ & 0xffffu) == 0) return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = turned<kBF16>(x[e], y[e], whole(e));
 }
 
 // Keys and values of tokens kTok * tile ..
@@ -212,109 +250,143 @@ __device__ __forceinline__ void append_kv4_tile(const AppendKv4Params& pp, int t
     __shared__ float4 s_cs[kTok][8][kMaxRotHalf / 8 + 1];  // of frequency j: [j % 8][j / 8], neighbouring units in other banks
     __shared__ int s_place[kTok], s_page[kTok], s_state[kTok];
     const int t0 = tile * kTok, tid = threadIdx.x, ntok = min(kTok, p.T - t0), half = p.rot / 2;
-    const int ch = tid % PER, e0 = ch * 8;
-    const bool turns = e0 < p.rot;
-    // row R: keys, then values; of a head, the tokens side by side
-    auto split = [&](int R, int& tok, int& g, bool& key) {
-        tok = R % kTok;
-        const int h = R / kTok;
-        key = h < p.Hkv;
-        g = key ? h : h - p.Hkv;
-    };
-    auto row_of = [&](int tok, int g, bool key) -> const char* {
-        const size_t t = (size_t)(t0 + tok);
-        return static_cast<const char*>(key ? p.k : p.v) +
-               (t * (size_t)(key ? p.k_stride : p.v_stride) + (size_t)g * D) * (kBF16 ? 2 : 4);
-    };
-    const int partner = p.interleaved ? e0 : e0 < half ? e0 + half : e0 - half;  // kVec: of the unit's first column
-    uint4 a[N], b[N];
-    auto load = [&](int R) {
-        int tok, g;
-        bool key;
-        split(R, tok, g, key);
-        if (R >= 2 * p.Hkv * kTok || tok >= ntok) return;
-        const char* row = row_of(tok, g, key);
+    // A thread keeps its columns and its token; from step to step it has other heads (keys', then values').
+    static_assert(RPS % kTok == 0, "a step takes whole heads of the tile");
+    constexpr int HSTEP = RPS / kTok;
+    const int ch = tid % PER, e0 = ch * 8, tok = tid / PER % kTok, h0 = tid / PER / kTok, heads = 2 * p.Hkv;
+    const bool turns = e0 < p.rot, second = e0 >= half;
+    constexpr int ELT = kBF16 ? 2 : 4;
+    const size_t t = (size_t)(t0 + tok);
+    const char* k_row = static_cast<const char*>(p.k) + (t * (size_t)p.k_stride + e0) * ELT;
+    const char* v_row = static_cast<const char*>(p.v) + (t * (size_t)p.v_stride + e0) * ELT;
+    const int partner = (second ? -half : half) * ELT;  // kVec, pairs (j, j + rot_dim / 2): bytes to the unit's partners
+    const bool paired = kVec && turns && !p.interleaved;
+    uint4 a[N] = {}, b[N] = {};  // threads without a row work on what is here, and store nothing
+    auto load = [&](bool key, const char* row) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            a[i] = reinterpret_cast<const uint4*>(row)[ch * N + i];
-            if (kVec && key && turns && !p.interleaved) b[i] = reinterpret_cast<const uint4*>(row)[partner / 8 * N + i];
+            a[i] = reinterpret_cast<const uint4*>(row)[i];
+            if (key && paired) b[i] = reinterpret_cast<const uint4*>(row + partner)[i];
         }
     };
-    load(tid / PER);
+    // the first row's bytes before the chain offsets -> length -> page
+    if (tok < ntok && h0 < heads) {
+        if (h0 < p.Hkv) load(true, k_row + (size_t)h0 * (D * ELT));
+        else load(false, v_row + (size_t)(h0 - p.Hkv) * (D * ELT));
+    }
     append_places<kTok>(p, t0, ntok, s_place, s_page, s_state);
     for (int x = tid; x < ntok * half; x += kAppendThreads) {
-        const int tok = x / half, j = x - tok * half;
-        s_cs[tok][j & 7][j >> 3] = turn_exact(p.positions ? p.positions[t0 + tok] : s_place[tok], p.inv_freq[j], p.scale);
+        const int tk = x / half, j = x - tk * half;
+        s_cs[tk][j & 7][j >> 3] = turn_exact(p.positions ? p.positions[t0 + tk] : s_place[tk], p.inv_freq[j], p.scale);
     }
     __syncthreads();
-    for (int R0 = 0; R0 < 2 * p.Hkv * kTok; R0 += RPS) {  // whole warps: the lanes of a row exchange values
-        const int R = R0 + tid / PER;
-        if (R0 > 0) load(R);
-        int tok, g;
-        bool key;
-        split(R, tok, g, key);
-        const bool live = R < 2 * p.Hkv * kTok && tok < ntok && s_state[tok] == kStateOk && s_page[tok] >= 0;
-        float x[8];
+    const bool held = tok < ntok && s_state[tok] == kStateOk && s_page[tok] >= 0;
+    const float reach = 0x1p-22f * fabsf(p.scale);
+    // Cosine and sine of the unit's column e; the sine with the sign that the column's partner has. The high parts
+    // stay in registers.
+    auto whole = [&](int e) {
+        const int c = e0 + e, j = min(p.interleaved ? c / 2 : c < half ? c : c - half, kMaxRotHalf - 1);
+        float4 v = s_cs[tok][j & 7][j >> 3];
+        if (p.interleaved ? !(c & 1) : c < half) {
+            v.z = -v.z;
+            v.w = -v.w;
+        }
+        return v;
+    };
+    float2 cs[8];
+    if (kBF16 && kVec && turns) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.f;
-        if (live) {
-            auto unpack = [&](const uint4 (&u)[N], float (&o)[8]) {
+        for (int e = 0; e < 8; ++e) {
+            const float4 v = whole(e);
+            cs[e] = make_float2(v.x, v.z);
+        }
+    }
+    const int in_page = s_place[tok] & (p.Ps - 1), u = in_page & (pp.slab - 1);
+    unsigned char* dst = pp.cache + (size_t)(held ? s_page[tok] : 0) * p.Hkv * (size_t)pp.page_bytes +
+                         (size_t)(in_page >> pp.slab_log2) * pp.slab_bytes;
+    const int code_at = kv4_code_at<D>(u, ch >> 2) + (ch & 3) * 4;
+    const int scale_at = pp.slab * D + kv4_scale_at<NG>(u, ch / (PER / NG));
+    const int v_codes = pp.slab * (D / 2), v_scales = pp.slab * 4 * NG;
+    // The unit in a and b, of a row whose columns begin at `row`, into the head's page at `page`; `live`: it is stored.
+    // Whole warps: the lanes of a group of columns exchange values.
+    auto unit = [&](bool key, const char* row, unsigned char* page, bool live) {
+        auto unpack = [&](const uint4 (&w)[N], float (&o)[8]) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const Vec16<kBF16> v(u[i]);
+            for (int i = 0; i < N; ++i) {
+                const Vec16<kBF16> v(w[i]);
 #pragma unroll
-                    for (int e = 0; e < Vec16<kBF16>::N; ++e) o[i * Vec16<kBF16>::N + e] = v.x[e];
-                }
-            };
-            unpack(a, x);
-            if (key && turns) {
-                float y[8], o[8];
-                if constexpr (kVec) {
-                    unpack(b, y);
-                    const int jb = p.interleaved ? e0 / 2 : e0 < half ? e0 : e0 - half;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int j = p.interleaved ? jb + e / 2 : jb + e;
-                        const float4 cs = s_cs[tok][j & 7][j >> 3];
-                        const bool second = p.interleaved ? e & 1 : e0 >= half;
-                        const float other = p.interleaved ? x[e ^ 1] : y[e];
-                        o[e] = turned<kBF16>(x[e], second ? other : -other, cs);
-                    }
-                } else {
-                    const char* row = row_of(tok, g, key);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int c = e0 + e;
-                        o[e] = x[e];
-                        if (c >= p.rot) continue;
-                        const int j = p.interleaved ? c / 2 : c < half ? c : c - half;
-                        const bool second = p.interleaved ? c & 1 : c >= half;
-                        const int other = p.interleaved ? c ^ 1 : second ? c - half : c + half;
-                        float v;
-                        if constexpr (kBF16) v = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[other] << 16);
-                        else v = reinterpret_cast<const float*>(row)[other];
-                        o[e] = turned<kBF16>(x[e], second ? v : -v, s_cs[tok][j & 7][j >> 3]);
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = o[e];
+                for (int e = 0; e < Vec16<kBF16>::N; ++e) o[i * Vec16<kBF16>::N + e] = v.x[e];
             }
+        };
+        float x[8];
+        unpack(a, x);
+        if (key && turns) {
+            float y[8], o[8];
+            if constexpr (kVec) {
+                if (p.interleaved) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
+                } else {
+                    unpack(b, y);
+                }
+                turn8<kBF16>(x, y, cs, reach, whole, o);
+            } else {
+                const char* first = row - e0 * ELT;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int c = e0 + e;
+                    o[e] = x[e];
+                    if (c >= p.rot || !live) continue;
+                    const int other = p.interleaved ? c ^ 1 : c >= half ? c - half : c + half;
+                    float v;
+                    if constexpr (kBF16) v = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(first)[other] << 16);
+                    else v = reinterpret_cast<const float*>(first)[other];
+                    o[e] = turned<kBF16>(x[e], v, whole(e));
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = o[e];
         }
         uint32_t scales;
         const uint32_t codes = quantise<D / NG / 8>(x, scales);
-        if (!live) continue;
-        const int in_page = s_place[tok] & (p.Ps - 1), u = in_page & (pp.slab - 1);
-        unsigned char* slab = pp.cache + ((size_t)s_page[tok] * p.Hkv + g) * (size_t)pp.page_bytes +
-                              (size_t)(in_page / pp.slab) * pp.slab_bytes;
-        *reinterpret_cast<uint32_t*>(slab + (key ? 0 : pp.slab * (D / 2)) + kv4_code_at<D>(u, ch >> 2) + (ch & 3) * 4) = codes;
-        if (ch % (PER / NG) == 0)
-            *reinterpret_cast<uint32_t*>(slab + pp.slab * (D + (key ? 0 : 4 * NG)) + kv4_scale_at<NG>(u, ch / (PER / NG))) = scales;
+        if (!live) return;
+        *reinterpret_cast<uint32_t*>(page + code_at + (key ? 0 : v_codes)) = codes;
+        if (ch % (PER / NG) == 0) *reinterpret_cast<uint32_t*>(page + scale_at + (key ? 0 : v_scales)) = scales;
+    };
+    const size_t row_step = HSTEP * D * ELT, page_step = (size_t)HSTEP * pp.page_bytes;
+    if constexpr (kTok == 1) {  // keys and values side by side: a step of one token is one round of the block
+        const char* row = h0 < p.Hkv ? k_row + (size_t)h0 * (D * ELT) : v_row + (size_t)(h0 - p.Hkv) * (D * ELT);
+#pragma unroll 1
+        for (int hb = 0; hb < heads; hb += HSTEP) {
+            const int h = hb + h0, g = h < p.Hkv ? h : h - p.Hkv;
+            const bool key = h < p.Hkv;
+            if (hb > 0 && h < heads) {
+                row = (key ? k_row : v_row) + (size_t)g * (D * ELT);
+                load(key, row);
+            }
+            unit(key, row, dst + (size_t)g * pp.page_bytes, held && h < heads);
+        }
+    } else {
+        auto half_of = [&](bool key, const char* base, bool loaded) {
+            const char* row = base + (size_t)h0 * (D * ELT);
+            unsigned char* page = dst + (size_t)h0 * pp.page_bytes;
+#pragma unroll 1
+            for (int hb = 0; hb < p.Hkv; hb += HSTEP) {
+                const bool live = held && hb + h0 < p.Hkv;
+                if (live && (!loaded || hb > 0)) load(key, row);
+                unit(key, row, page, live);
+                row += row_step;
+                page += page_step;
+            }
+        };
+        half_of(true, k_row, h0 < p.Hkv);
+        half_of(false, v_row, false);
     }
 }
 
 // kVecQ: append_rows takes queries in whole chunks; kVec: append_kv4_tile its units.
 template <bool kBF16, int D, int NG, bool kVecQ, bool kVec, int kTokQ, int kTok>
-__global__ void __launch_bounds__(kAppendThreads) art_append_kv4_kernel(const AppendKv4Params p) {
+__global__ void __launch_bounds__(kAppendThreads, APP_BLK) art_append_kv4_kernel(const AppendKv4Params p) {
     if (blockIdx.x == 0) append_check(p.a);
     else if ((int)blockIdx.x <= p.q_blocks) append_rows<kBF16, D, kVecQ, kTokQ>(p.a, 0, blockIdx.x - 1);
     else append_kv4_tile<kBF16, D, NG, kVec, kTok>(p, blockIdx.x - 1 - p.q_blocks);
@@ -325,12 +397,12 @@ static void launch_append_kv4(AppendKv4Params& p, cudaStream_t st) {
     const int turn = p.a.interleaved ? p.a.rot : p.a.rot / 2;
     const bool vec = turn % 8 == 0, vec_q = turn % (kBF16 ? 8 : 4) == 0;
     const bool few = p.a.T <= kFewTokensKv4;
-    const int tq = few ? 1 : 2, tk = few ? 1 : kKvTile;
+    const int tq = few ? 1 : kQTile, tk = few ? 1 : kKvTile;
     p.q_blocks = p.a.q ? (p.a.T + tq - 1) / tq : 0;
     const unsigned grid = 1u + (unsigned)p.q_blocks + (unsigned)((p.a.T + tk - 1) / tk);
 #define ART_APPEND4(VQ, V)                                                                                       \
     (few ? art_append_kv4_kernel<kBF16, D, NG, VQ, V, 1, 1><<<grid, kAppendThreads, 0, st>>>(p)                 \
-         : art_append_kv4_kernel<kBF16, D, NG, VQ, V, 2, kKvTile><<<grid, kAppendThreads, 0, st>>>(p))
+         : art_append_kv4_kernel<kBF16, D, NG, VQ, V, kQTile, kKvTile><<<grid, kAppendThreads, 0, st>>>(p))
     if (vec) ART_APPEND4(true, true);
     else if (vec_q) ART_APPEND4(true, false);
     else ART_APPEND4(false, false);
@@ -366,6 +438,7 @@ int art_append_kv4(const void* q, const void* k, const void* v, int64_t q_stride
     p.cache = static_cast<unsigned char*>(cache);
     const Kv4Layout l = kv4_layout(s.page_size, s.head_dim, group);
     p.slab = l.slab;
+    p.slab_log2 = l.slab_log2;
     p.slab_bytes = l.slab_bytes;
     p.page_bytes = l.page_bytes;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -16,13 +16,15 @@ namespace art {
 constexpr int kSlabTokens = 64;  // tokens of a slab at most
 
 struct Kv4Layout {
-    int slab;        // tokens of a slab
+    int slab, slab_log2;  // tokens of a slab
     int slab_bytes, page_bytes;
 };
 inline Kv4Layout kv4_layout(int page_size, int head_dim, int group) {
     Kv4Layout l;
     const int token = head_dim + 8 * (head_dim / group);
     l.slab = page_size < kSlabTokens ? page_size : kSlabTokens;
+    l.slab_log2 = 0;
+    while (1 << l.slab_log2 < l.slab) ++l.slab_log2;
     l.slab_bytes = l.slab * token;
     l.page_bytes = page_size * token;
     return l;

@@ -27,7 +27,7 @@ struct ReadKv4Params {
     void *k_out, *v_out;
     WsHeader* hdr;
     int B, T, Hkv, Ps, max_pages, num_pages, out_pages;
-    int slab, slab_bytes, page_bytes;
+    int slab, slab_log2, page_log2, slab_bytes, page_bytes;
 };
 
 // Sequence b: its places [lo, hi) to read; false where its offsets or its length are bad.
@@ -105,7 +105,7 @@ __device__ __forceinline__ void read_unit(const ReadKv4Params& p, const ReadRun&
     constexpr int NC = D / 32, ROWB = D * (kBF16 ? 2 : 4);
     const int i = lane >> 2, w = lane & 3, place = oct * 8 + i;
     const int in_page = place & (p.Ps - 1);
-    const size_t at = (size_t)r.b * p.max_pages + place / p.Ps;
+    const size_t at = (size_t)r.b * p.max_pages + (place >> p.page_log2);
     const bool here = place >= r.lo && place < r.hi;
     const int page = r.ok && here ? p.block_table[at] : -1;
     const bool good = page >= 0 && page < p.num_pages;
@@ -123,7 +123,7 @@ __device__ __forceinline__ void read_unit(const ReadKv4Params& p, const ReadRun&
         row = (size_t)(r.row0 + place - r.lo) * p.Hkv + g;
     }
     const unsigned char* slab = p.cache + ((size_t)(good ? page : 0) * p.Hkv + g) * (size_t)p.page_bytes +
-                                (size_t)(in_page / p.slab) * p.slab_bytes;
+                                (size_t)(in_page >> p.slab_log2) * p.slab_bytes;
     const int u = in_page & (p.slab - 1);
     uint32_t code[2][NC], scale[2][NG];
 #pragma unroll
@@ -258,6 +258,9 @@ static void read_params(ReadKv4Params& p, const art_shape& s, int group) {
     p.num_pages = s.num_pages_total;
     const Kv4Layout l = kv4_layout(s.page_size, s.head_dim, group);
     p.slab = l.slab;
+    p.slab_log2 = l.slab_log2;
+    p.page_log2 = 0;
+    while (1 << p.page_log2 < s.page_size) ++p.page_log2;
     p.slab_bytes = l.slab_bytes;
     p.page_bytes = l.page_bytes;
 }
