@@ -31,19 +31,19 @@ namespace art {
 // Up to these many tokens a CTA takes one token's keys and values, beyond it kKvTile's.
 constexpr int kFewTokensKv4 = 608;
 #ifndef KVT
-#define KVT 8
+#define KVT 16
 #define TQ 4
 #endif
 constexpr int kKvTile = KVT, kQTile = TQ;
 #ifndef APP_BLK
-#define APP_BLK 4
+#define APP_BLK 3
 #endif
 
 struct AppendKv4Params {
     AppendParams a;
     unsigned char* cache;
     int slab, slab_log2, slab_bytes, page_bytes;
-    int q_blocks;  // blocks that rotate queries
+    int per;  // blocks of a group: one tile of keys and values, then the tiles of the same tokens' queries
 };
 
 // sin(n pi / 32), n = 0 .. 16, as a sum of two fp32 numbers.
@@ -309,7 +309,7 @@ __device__ __forceinline__ void append_kv4_tile(const AppendKv4Params& pp, int t
     const int v_codes = pp.slab * (D / 2), v_scales = pp.slab * 4 * NG;
     // The unit in a and b, of a row whose columns begin at `row`, into the head's page at `page`; `live`: it is stored.
     // Whole warps: the lanes of a group of columns exchange values.
-    auto unit = [&](bool key, const char* row, unsigned char* page, bool live) {
+    auto unit = [&](bool key, const char* row, unsigned char* page, bool live, auto next) {
         auto unpack = [&](const uint4 (&w)[N], float (&o)[8]) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -318,17 +318,20 @@ __device__ __forceinline__ void append_kv4_tile(const AppendKv4Params& pp, int t
                 for (int e = 0; e < Vec16<kBF16>::N; ++e) o[i * Vec16<kBF16>::N + e] = v.x[e];
             }
         };
-        float x[8];
+        float x[8], y[8];
         unpack(a, x);
-        if (key && turns) {
-            float y[8], o[8];
-            if constexpr (kVec) {
-                if (p.interleaved) {
+        if (key && turns && kVec) {
+            if (p.interleaved) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
-                } else {
-                    unpack(b, y);
-                }
+                for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
+            } else {
+                unpack(b, y);
+            }
+        }
+        next();  // the next unit's loads, under way while this one is worked on
+        if (key && turns) {
+            float o[8];
+            if constexpr (kVec) {
                 turn8<kBF16>(x, y, cs, reach, whole, o);
             } else {
                 const char* first = row - e0 * ELT;
@@ -364,32 +367,127 @@ __device__ __forceinline__ void append_kv4_tile(const AppendKv4Params& pp, int t
                 row = (key ? k_row : v_row) + (size_t)g * (D * ELT);
                 load(key, row);
             }
-            unit(key, row, dst + (size_t)g * pp.page_bytes, held && h < heads);
+            unit(key, row, dst + (size_t)g * pp.page_bytes, held && h < heads, [] {});
         }
     } else {
-        auto half_of = [&](bool key, const char* base, bool loaded) {
+        auto half_of = [&](bool key, const char* base) {
             const char* row = base + (size_t)h0 * (D * ELT);
             unsigned char* page = dst + (size_t)h0 * pp.page_bytes;
 #pragma unroll 1
-            for (int hb = 0; hb < p.Hkv; hb += HSTEP) {
-                const bool live = held && hb + h0 < p.Hkv;
-                if (live && (!loaded || hb > 0)) load(key, row);
-                unit(key, row, page, live);
+            for (int h = h0; h < p.Hkv + h0; h += HSTEP) {  // as often for every thread
+                unit(key, row, page, held && h < p.Hkv, [&] {
+                    if (held && h + HSTEP < p.Hkv) load(key, row + row_step);
+                    else if (key && held && h0 < p.Hkv && h + HSTEP >= p.Hkv && h < p.Hkv) load(false, v_row + (size_t)h0 * (D * ELT));
+                });
                 row += row_step;
                 page += page_step;
             }
         };
-        half_of(true, k_row, h0 < p.Hkv);
-        half_of(false, v_row, false);
+        half_of(true, k_row);
+        half_of(false, v_row);
     }
 }
 
-// kVecQ: append_rows takes queries in whole chunks; kVec: append_kv4_tile its units.
+// Queries of tokens kTok * tile .. whose columns turn in whole 16-byte chunks. A thread keeps a token and two chunks, c and
+// c + rot_dim / 2 where they turn with one another, and walks the heads with their cosines and sines in registers.
+template <bool kBF16, int D, int kTok>
+__device__ __forceinline__ void rotate_tile(const AppendParams& p, int tile) {
+    constexpr int N = Vec16<kBF16>::N, PER = D / N / 2, ELT = kBF16 ? 2 : 4;
+    constexpr int HSTEP = kAppendThreads / PER / kTok;  // heads of a step
+    constexpr int PF = 4;                               // steps whose loads are under way
+    static_assert(HSTEP * PER * kTok == kAppendThreads, "a step takes whole heads of the tile");
+    __shared__ float2 s_cs[kTok * kMaxRotHalf];
+    __shared__ int s_place[kTok], s_page[kTok], s_state[kTok];
+    const int t0 = tile * kTok, tid = threadIdx.x, ntok = min(kTok, p.T - t0), half = p.rot / 2;
+    const int c = tid % PER, tok = tid / PER % kTok, h0 = tid / PER / kTok, npair = p.interleaved ? 0 : half / N;
+    const int ca = c < npair ? c : c + npair, cb = c < npair ? c + npair : c + PER;
+    const size_t t = (size_t)(t0 + tok);
+    const char* src = static_cast<const char*>(p.q) + (t * (size_t)p.q_stride + (size_t)h0 * D) * ELT;
+    char* dst = static_cast<char*>(p.q_out) + ((t * p.Hq + h0) * D) * ELT;
+    uint4 a[PF], b[PF];
+    auto load = [&](int hb) {
+#pragma unroll
+        for (int k = 0; k < PF; ++k)
+            if (tok < ntok && hb + k * HSTEP + h0 < p.Hq) {
+                const uint4* row = reinterpret_cast<const uint4*>(src + (size_t)(hb + k * HSTEP) * (D * ELT));
+                a[k] = row[ca];
+                b[k] = row[cb];
+            }
+    };
+    load(0);
+    append_places<kTok>(p, t0, ntok, s_place, s_page, s_state);
+    for (int x = tid; x < ntok * half; x += kAppendThreads) {
+        const int tk = x / half, j = x - tk * half;
+        const float2 cs = turn_of(p.positions ? p.positions[t0 + tk] : s_place[tk], p.inv_freq[j]);
+        s_cs[tk * kMaxRotHalf + j] = make_float2(cs.x * p.scale, cs.y * p.scale);
+    }
+    __syncthreads();
+    const int state = tok < ntok ? s_state[tok] : kStateNone;
+    if (state == kStateNone) return;  // no barrier follows
+    const bool pairs = c < npair, in_a = p.interleaved && ca * N < p.rot, in_b = p.interleaved && cb * N < p.rot;
+    float2 cs[N];  // pairs: of pair c N + e; interleaved: of chunk ca's N / 2 pairs, then of cb's
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const int j = p.interleaved ? (e < N / 2 ? ca * (N / 2) + e : cb * (N / 2) + e - N / 2) : c * N + e;
+        cs[e] = pairs || (e < N / 2 ? in_a : in_b) ? s_cs[tok * kMaxRotHalf + j] : make_float2(1.f, 0.f);
+    }
+#pragma unroll 1
+    for (int hb = 0; hb < p.Hq; hb += PF * HSTEP) {
+        if (hb > 0) load(hb);
+#pragma unroll
+        for (int k = 0; k < PF; ++k) {
+            if (hb + k * HSTEP + h0 >= p.Hq) continue;
+            uint4 u = a[k], v = b[k];
+            if (state == kStateBad) {  // no position: queries of a bad sequence are zero
+                u = v = make_uint4(0u, 0u, 0u, 0u);
+            } else if (pairs) {
+                Vec16<kBF16> x(u), y(v);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float xe = x.x[e], ye = y.x[e];
+                    x.x[e] = xe * cs[e].x - ye * cs[e].y;
+                    y.x[e] = ye * cs[e].x + xe * cs[e].y;
+                }
+                u = x.pack();
+                v = y.pack();
+            } else if (p.interleaved) {
+                auto inside = [&](uint4& w, int e0) {
+                    Vec16<kBF16> x(w);
+#pragma unroll
+                    for (int e = 0; e < N; e += 2) {
+                        const float2 z = cs[e0 + e / 2];
+                        const float xe = x.x[e], ye = x.x[e + 1];
+                        x.x[e] = xe * z.x - ye * z.y;
+                        x.x[e + 1] = ye * z.x + xe * z.y;
+                    }
+                    w = x.pack();
+                };
+                if (in_a) inside(u, 0);
+                if (in_b) inside(v, N / 2);
+            }
+            uint4* row = reinterpret_cast<uint4*>(dst + (size_t)(hb + k * HSTEP) * (D * ELT));
+            row[ca] = u;
+            row[cb] = v;
+        }
+    }
+}
+
+// kVecQ: rotate_tile takes the queries; kVec: append_kv4_tile its units.
 template <bool kBF16, int D, int NG, bool kVecQ, bool kVec, int kTokQ, int kTok>
 __global__ void __launch_bounds__(kAppendThreads, APP_BLK) art_append_kv4_kernel(const AppendKv4Params p) {
-    if (blockIdx.x == 0) append_check(p.a);
-    else if ((int)blockIdx.x <= p.q_blocks) append_rows<kBF16, D, kVecQ, kTokQ>(p.a, 0, blockIdx.x - 1);
-    else append_kv4_tile<kBF16, D, NG, kVec, kTok>(p, blockIdx.x - 1 - p.q_blocks);
+    if (blockIdx.x == 0) {
+        append_check(p.a);
+        return;
+    }
+    const int group = (int)(blockIdx.x - 1) / p.per, i = (int)(blockIdx.x - 1) - group * p.per;
+    if (i == 0) {
+        append_kv4_tile<kBF16, D, NG, kVec, kTok>(p, group);
+        return;
+    }
+    const int tile = group * (p.per - 1) + i - 1;
+    if (tile * kTokQ >= p.a.T) return;
+    if constexpr (kVecQ) rotate_tile<kBF16, D, kTokQ>(p.a, tile);
+    else append_rows<kBF16, D, false, kTokQ>(p.a, 0, tile);
 }
 
 template <bool kBF16, int D, int NG>
@@ -397,9 +495,9 @@ static void launch_append_kv4(AppendKv4Params& p, cudaStream_t st) {
     const int turn = p.a.interleaved ? p.a.rot : p.a.rot / 2;
     const bool vec = turn % 8 == 0, vec_q = turn % (kBF16 ? 8 : 4) == 0;
     const bool few = p.a.T <= kFewTokensKv4;
-    const int tq = few ? 1 : kQTile, tk = few ? 1 : kKvTile;
-    p.q_blocks = p.a.q ? (p.a.T + tq - 1) / tq : 0;
-    const unsigned grid = 1u + (unsigned)p.q_blocks + (unsigned)((p.a.T + tk - 1) / tk);
+    const int tk = few ? 1 : kKvTile;
+    p.per = p.a.q ? 1 + (few ? 1 : kKvTile / kQTile) : 1;
+    const unsigned grid = 1u + (unsigned)((p.a.T + tk - 1) / tk) * (unsigned)p.per;
 #define ART_APPEND4(VQ, V)                                                                                       \
     (few ? art_append_kv4_kernel<kBF16, D, NG, VQ, V, 1, 1><<<grid, kAppendThreads, 0, st>>>(p)                 \
          : art_append_kv4_kernel<kBF16, D, NG, VQ, V, kQTile, kKvTile><<<grid, kAppendThreads, 0, st>>>(p))
