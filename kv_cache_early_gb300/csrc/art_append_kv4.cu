@@ -17,12 +17,16 @@
 //     a half-integer up to 15, step has 8 bits).
 // bf16 inputs meet ties often, since step and x lie on grids, so this is no rare matter.
 //
-// One kernel. Block 0 checks the call's device data and stores the status word. The next blocks
-// rotate queries (append_rows of art_append.cuh, without keys and values), the last ones take
-// tiles of tokens' keys and values: a thread has 8 columns of a row, the lanes of a group of
-// columns find its least and largest value by shuffles, and the eight codes are one 32-bit store.
-// Neighbouring threads take the same columns of neighbouring tokens' rows, so that the stores of
-// a tile fill whole 128-byte units of the cache.
+// One kernel. Block 0 checks the call's device data and stores the status word. A tile of 8 tokens is a block's: it turns
+// their queries (RotateQueries), then quantises keys and values (append_kv4_tile). A thread keeps its token and columns and
+// walks the heads; the lanes of a group of columns find its least and largest value by shuffles; eight codes are one
+// 32-bit store, and neighbouring lanes store to neighbouring tokens, so that a tile fills whole 128-byte units.
+//
+// Bound by instructions: 36,864 tokens (32/8 heads, d 128, bf16) take 178 us where their bytes take 117. Eight values of a
+// row are about 150 instructions (without rotation and queries 80 us), the rotation as in exact arithmetic 43 us more; what
+// brought it from 265: 32-bit arithmetic with a bound that decides nearly always, ties resolved where they occur
+// only, fixed columns a thread (the general tile of art_append.cuh spends most on addresses), places and angles of
+// 8 tokens at a time.
 #include "art_append.cuh"
 #include "art_kv4.cuh"
 
@@ -30,20 +34,14 @@ namespace art {
 
 // Up to these many tokens a CTA takes one token's keys and values, beyond it kKvTile's.
 constexpr int kFewTokensKv4 = 608;
-#ifndef KVT
-#define KVT 16
-#define TQ 4
-#endif
-constexpr int kKvTile = KVT, kQTile = TQ;
-#ifndef APP_BLK
-#define APP_BLK 3
-#endif
+// Tokens of a tile, and blocks an SM. 36,864 tokens (32/8 heads, d 128, groups of 64): 8 tokens 178 us, 16 183; two
+// blocks 195 (of 16 tokens), four 210, whose 64 registers spill.
+constexpr int kKvTile = 8, kKvBlocks = 3;
 
 struct AppendKv4Params {
     AppendParams a;
     unsigned char* cache;
     int slab, slab_log2, slab_bytes, page_bytes;
-    int per;  // blocks of a group: one tile of keys and values, then the tiles of the same tokens' queries
 };
 
 // sin(n pi / 32), n = 0 .. 16, as a sum of two fp32 numbers.
@@ -239,9 +237,113 @@ __device__ __forceinline__ void turn8(const float (&x)[8], const float (&y)[8], 
     for (int e = 0; e < 8; ++e) o[e] = turned<kBF16>(x[e], y[e], whole(e));
 }
 
-// Keys and values of tokens kTok * tile ..
+// The queries of a block's kTok tokens from t0 on, whose columns turn in whole 16-byte chunks. A thread keeps a token and
+// two chunks, c and c + rot_dim / 2 where they turn with one another, and walks the heads with their cosines and sines
+// (angle(token, j)) in registers. load: the first heads' chunks, before the angles are there.
+template <bool kBF16, int D, int kTok>
+struct RotateQueries {
+    static constexpr int N = Vec16<kBF16>::N, PER = D / N / 2, ELT = kBF16 ? 2 : 4;
+    static constexpr int HSTEP = kAppendThreads / PER / kTok;  // heads of a step
+    static constexpr int PF = 4;                               // steps whose loads are under way
+    static_assert(HSTEP * PER * kTok == kAppendThreads, "a step takes whole heads of the tile");
+    const AppendParams& p;
+    const char* src;
+    char* dst;
+    int tok, h0, c, ca, cb;
+    bool here;
+    uint4 a[PF], b[PF];
+    __device__ __forceinline__ RotateQueries(const AppendParams& p_, int t0, int ntok) : p(p_) {
+        const int tid = threadIdx.x, npair = p.interleaved ? 0 : p.rot / 2 / N;
+        c = tid % PER;
+        tok = tid / PER % kTok;
+        h0 = tid / PER / kTok;
+        ca = c < npair ? c : c + npair;
+        cb = c < npair ? c + npair : c + PER;
+        here = tok < ntok;
+        const size_t t = (size_t)(t0 + tok);
+        src = static_cast<const char*>(p.q) + (t * (size_t)p.q_stride + (size_t)h0 * D) * ELT;
+        dst = static_cast<char*>(p.q_out) + ((t * p.Hq + h0) * D) * ELT;
+    }
+    __device__ __forceinline__ void load(int hb) {
+#pragma unroll
+        for (int k = 0; k < PF; ++k)
+            if (here && hb + k * HSTEP + h0 < p.Hq) {
+                const uint4* row = reinterpret_cast<const uint4*>(src + (size_t)(hb + k * HSTEP) * (D * ELT));
+                a[k] = row[ca];
+                b[k] = row[cb];
+            }
+    }
+    template <class F>
+    __device__ __forceinline__ void run(int state, F angle) {
+        if (state == kStateNone) return;
+        const bool pairs = !p.interleaved && c < p.rot / 2 / N, in_a = p.interleaved && ca * N < p.rot, in_b = p.interleaved && cb * N < p.rot;
+        float2 cs[N];  // pairs: of pair c N + e; interleaved: of chunk ca's N / 2 pairs, then of cb's
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int j = p.interleaved ? (e < N / 2 ? ca * (N / 2) + e : cb * (N / 2) + e - N / 2) : c * N + e;
+            cs[e] = pairs || (e < N / 2 ? in_a : in_b) ? angle(tok, j) : make_float2(1.f, 0.f);
+        }
+#pragma unroll 1
+        for (int hb = 0; hb < p.Hq; hb += PF * HSTEP) {
+            if (hb > 0) load(hb);
+#pragma unroll
+            for (int k = 0; k < PF; ++k) {
+                if (hb + k * HSTEP + h0 >= p.Hq) continue;
+                uint4 u = a[k], v = b[k];
+                if (state == kStateBad) {  // no position: queries of a bad sequence are zero
+                    u = v = make_uint4(0u, 0u, 0u, 0u);
+                } else if (pairs) {
+                    Vec16<kBF16> x(u), y(v);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const float xe = x.x[e], ye = y.x[e];
+                        x.x[e] = xe * cs[e].x - ye * cs[e].y;
+                        y.x[e] = ye * cs[e].x + xe * cs[e].y;
+                    }
+                    u = x.pack();
+                    v = y.pack();
+                } else if (p.interleaved) {
+                    auto inside = [&](uint4& w, int e0) {
+                        Vec16<kBF16> x(w);
+#pragma unroll
+                        for (int e = 0; e < N; e += 2) {
+                            const float2 z = cs[e0 + e / 2];
+                            const float xe = x.x[e], ye = x.x[e + 1];
+                            x.x[e] = xe * z.x - ye * z.y;
+                            x.x[e + 1] = ye * z.x + xe * z.y;
+                        }
+                        w = x.pack();
+                    };
+                    if (in_a) inside(u, 0);
+                    if (in_b) inside(v, N / 2);
+                }
+                uint4* row = reinterpret_cast<uint4*>(dst + (size_t)(hb + k * HSTEP) * (D * ELT));
+                row[ca] = u;
+                row[cb] = v;
+            }
+        }
+    }
+};
+
+// One token's queries in a block of their own.
+template <bool kBF16, int D>
+__device__ __forceinline__ void rotate_token(const AppendParams& p, int t0) {
+    __shared__ float2 s_cs[kMaxRotHalf];
+    __shared__ int s_place[1], s_page[1], s_state[1];
+    RotateQueries<kBF16, D, 1> q(p, t0, 1);
+    q.load(0);
+    append_places<1>(p, t0, 1, s_place, s_page, s_state);
+    for (int j = threadIdx.x; j < p.rot / 2; j += kAppendThreads) {
+        const float2 cs = turn_of(p.positions ? p.positions[t0] : s_place[0], p.inv_freq[j]);
+        s_cs[j] = make_float2(cs.x * p.scale, cs.y * p.scale);
+    }
+    __syncthreads();
+    q.run(s_state[0], [&](int, int j) { return s_cs[j]; });
+}
+
+// Keys and values of tokens kTok * tile .., and (kQueries) their queries.
 // kVec: columns turn in whole units of 8 (rot_dim, or its half where the pairs are (j, j + rot_dim / 2)).
-template <bool kBF16, int D, int NG, bool kVec, int kTok>
+template <bool kBF16, int D, int NG, bool kVec, bool kQueries, int kTok>
 __device__ __forceinline__ void append_kv4_tile(const AppendKv4Params& pp, int tile) {
     const AppendParams& p = pp.a;
     constexpr int PER = D / 8;                       // units of a row
@@ -280,6 +382,16 @@ __device__ __forceinline__ void append_kv4_tile(const AppendKv4Params& pp, int t
         s_cs[tk][j & 7][j >> 3] = turn_exact(p.positions ? p.positions[t0 + tk] : s_place[tk], p.inv_freq[j], p.scale);
     }
     __syncthreads();
+    if constexpr (kQueries) {
+        if (p.q) {
+            RotateQueries<kBF16, D, kTok> q(p, t0, ntok);
+            q.load(0);
+            q.run(q.here ? s_state[q.tok] : kStateNone, [&](int tk, int j) {
+                const float4 v = s_cs[tk][j & 7][j >> 3];
+                return make_float2(v.x, v.z);
+            });
+        }
+    }
     const bool held = tok < ntok && s_state[tok] == kStateOk && s_page[tok] >= 0;
     const float reach = 0x1p-22f * fabsf(p.scale);
     // Cosine and sine of the unit's column e; the sine with the sign that the column's partner has. The high parts
@@ -388,119 +500,43 @@ __device__ __forceinline__ void append_kv4_tile(const AppendKv4Params& pp, int t
     }
 }
 
-// Queries of tokens kTok * tile .. whose columns turn in whole 16-byte chunks. A thread keeps a token and two chunks, c and
-// c + rot_dim / 2 where they turn with one another, and walks the heads with their cosines and sines in registers.
-template <bool kBF16, int D, int kTok>
-__device__ __forceinline__ void rotate_tile(const AppendParams& p, int tile) {
-    constexpr int N = Vec16<kBF16>::N, PER = D / N / 2, ELT = kBF16 ? 2 : 4;
-    constexpr int HSTEP = kAppendThreads / PER / kTok;  // heads of a step
-    constexpr int PF = 4;                               // steps whose loads are under way
-    static_assert(HSTEP * PER * kTok == kAppendThreads, "a step takes whole heads of the tile");
-    __shared__ float2 s_cs[kTok * kMaxRotHalf];
-    __shared__ int s_place[kTok], s_page[kTok], s_state[kTok];
-    const int t0 = tile * kTok, tid = threadIdx.x, ntok = min(kTok, p.T - t0), half = p.rot / 2;
-    const int c = tid % PER, tok = tid / PER % kTok, h0 = tid / PER / kTok, npair = p.interleaved ? 0 : half / N;
-    const int ca = c < npair ? c : c + npair, cb = c < npair ? c + npair : c + PER;
-    const size_t t = (size_t)(t0 + tok);
-    const char* src = static_cast<const char*>(p.q) + (t * (size_t)p.q_stride + (size_t)h0 * D) * ELT;
-    char* dst = static_cast<char*>(p.q_out) + ((t * p.Hq + h0) * D) * ELT;
-    uint4 a[PF], b[PF];
-    auto load = [&](int hb) {
-#pragma unroll
-        for (int k = 0; k < PF; ++k)
-            if (tok < ntok && hb + k * HSTEP + h0 < p.Hq) {
-                const uint4* row = reinterpret_cast<const uint4*>(src + (size_t)(hb + k * HSTEP) * (D * ELT));
-                a[k] = row[ca];
-                b[k] = row[cb];
-            }
-    };
-    load(0);
-    append_places<kTok>(p, t0, ntok, s_place, s_page, s_state);
-    for (int x = tid; x < ntok * half; x += kAppendThreads) {
-        const int tk = x / half, j = x - tk * half;
-        const float2 cs = turn_of(p.positions ? p.positions[t0 + tk] : s_place[tk], p.inv_freq[j]);
-        s_cs[tk * kMaxRotHalf + j] = make_float2(cs.x * p.scale, cs.y * p.scale);
-    }
-    __syncthreads();
-    const int state = tok < ntok ? s_state[tok] : kStateNone;
-    if (state == kStateNone) return;  // no barrier follows
-    const bool pairs = c < npair, in_a = p.interleaved && ca * N < p.rot, in_b = p.interleaved && cb * N < p.rot;
-    float2 cs[N];  // pairs: of pair c N + e; interleaved: of chunk ca's N / 2 pairs, then of cb's
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-        const int j = p.interleaved ? (e < N / 2 ? ca * (N / 2) + e : cb * (N / 2) + e - N / 2) : c * N + e;
-        cs[e] = pairs || (e < N / 2 ? in_a : in_b) ? s_cs[tok * kMaxRotHalf + j] : make_float2(1.f, 0.f);
-    }
-#pragma unroll 1
-    for (int hb = 0; hb < p.Hq; hb += PF * HSTEP) {
-        if (hb > 0) load(hb);
-#pragma unroll
-        for (int k = 0; k < PF; ++k) {
-            if (hb + k * HSTEP + h0 >= p.Hq) continue;
-            uint4 u = a[k], v = b[k];
-            if (state == kStateBad) {  // no position: queries of a bad sequence are zero
-                u = v = make_uint4(0u, 0u, 0u, 0u);
-            } else if (pairs) {
-                Vec16<kBF16> x(u), y(v);
-#pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const float xe = x.x[e], ye = y.x[e];
-                    x.x[e] = xe * cs[e].x - ye * cs[e].y;
-                    y.x[e] = ye * cs[e].x + xe * cs[e].y;
-                }
-                u = x.pack();
-                v = y.pack();
-            } else if (p.interleaved) {
-                auto inside = [&](uint4& w, int e0) {
-                    Vec16<kBF16> x(w);
-#pragma unroll
-                    for (int e = 0; e < N; e += 2) {
-                        const float2 z = cs[e0 + e / 2];
-                        const float xe = x.x[e], ye = x.x[e + 1];
-                        x.x[e] = xe * z.x - ye * z.y;
-                        x.x[e + 1] = ye * z.x + xe * z.y;
-                    }
-                    w = x.pack();
-                };
-                if (in_a) inside(u, 0);
-                if (in_b) inside(v, N / 2);
-            }
-            uint4* row = reinterpret_cast<uint4*>(dst + (size_t)(hb + k * HSTEP) * (D * ELT));
-            row[ca] = u;
-            row[cb] = v;
-        }
-    }
-}
-
-// kVecQ: rotate_tile takes the queries; kVec: append_kv4_tile its units.
-template <bool kBF16, int D, int NG, bool kVecQ, bool kVec, int kTokQ, int kTok>
-__global__ void __launch_bounds__(kAppendThreads, APP_BLK) art_append_kv4_kernel(const AppendKv4Params p) {
+// Few tokens: a token's keys and values in one block, its queries in the next, so that a step waits for the longer of the
+// two. Beyond: tiles of kKvTile tokens with their queries, which share places and angles (36,864 tokens apart, in tiles
+// of 16 tokens and 8 of queries, 198 us against 183).
+template <bool kBF16, int D, int NG, bool kVecQ, bool kVec>
+__global__ void __launch_bounds__(kAppendThreads, kKvBlocks) art_append_kv4_few_kernel(const AppendKv4Params p) {
     if (blockIdx.x == 0) {
         append_check(p.a);
         return;
     }
-    const int group = (int)(blockIdx.x - 1) / p.per, i = (int)(blockIdx.x - 1) - group * p.per;
-    if (i == 0) {
-        append_kv4_tile<kBF16, D, NG, kVec, kTok>(p, group);
+    const int i = blockIdx.x - 1;
+    if (i < p.a.T) append_kv4_tile<kBF16, D, NG, kVec, false, 1>(p, i);
+    else if constexpr (kVecQ) rotate_token<kBF16, D>(p.a, i - p.a.T);
+    else append_rows<kBF16, D, false, 1>(p.a, 0, i - p.a.T);
+}
+// kVecQ: queries turn in whole chunks; else they are taken two tokens at a time by the blocks behind the tiles'.
+template <bool kBF16, int D, int NG, bool kVecQ, bool kVec>
+__global__ void __launch_bounds__(kAppendThreads, kKvBlocks) art_append_kv4_kernel(const AppendKv4Params p) {
+    if (blockIdx.x == 0) {
+        append_check(p.a);
         return;
     }
-    const int tile = group * (p.per - 1) + i - 1;
-    if (tile * kTokQ >= p.a.T) return;
-    if constexpr (kVecQ) rotate_tile<kBF16, D, kTokQ>(p.a, tile);
-    else append_rows<kBF16, D, false, kTokQ>(p.a, 0, tile);
+    const int i = blockIdx.x - 1, tiles = (p.a.T + kKvTile - 1) / kKvTile;
+    if (kVecQ || i < tiles) append_kv4_tile<kBF16, D, NG, kVec, kVecQ, kKvTile>(p, i);
+    else if constexpr (!kVecQ) append_rows<kBF16, D, false, 2>(p.a, 0, i - tiles);
 }
 
 template <bool kBF16, int D, int NG>
-static void launch_append_kv4(AppendKv4Params& p, cudaStream_t st) {
+static void launch_append_kv4(const AppendKv4Params& p, cudaStream_t st) {
     const int turn = p.a.interleaved ? p.a.rot : p.a.rot / 2;
-    const bool vec = turn % 8 == 0, vec_q = turn % (kBF16 ? 8 : 4) == 0;
+    const bool vec = turn % 8 == 0, vec_q = turn % (kBF16 ? 8 : 4) == 0, q = p.a.q != nullptr;
     const bool few = p.a.T <= kFewTokensKv4;
-    const int tk = few ? 1 : kKvTile;
-    p.per = p.a.q ? 1 + (few ? 1 : kKvTile / kQTile) : 1;
-    const unsigned grid = 1u + (unsigned)((p.a.T + tk - 1) / tk) * (unsigned)p.per;
-#define ART_APPEND4(VQ, V)                                                                                       \
-    (few ? art_append_kv4_kernel<kBF16, D, NG, VQ, V, 1, 1><<<grid, kAppendThreads, 0, st>>>(p)                 \
-         : art_append_kv4_kernel<kBF16, D, NG, VQ, V, kQTile, kKvTile><<<grid, kAppendThreads, 0, st>>>(p))
+    unsigned grid = 1u;
+    if (few) grid += (unsigned)p.a.T * (q ? 2u : 1u);
+    else grid += (unsigned)((p.a.T + kKvTile - 1) / kKvTile) + (q && !vec_q ? (unsigned)((p.a.T + 1) / 2) : 0u);
+#define ART_APPEND4(VQ, V)                                                                              \
+    (few ? art_append_kv4_few_kernel<kBF16, D, NG, VQ, V><<<grid, kAppendThreads, 0, st>>>(p)           \
+         : art_append_kv4_kernel<kBF16, D, NG, VQ, V><<<grid, kAppendThreads, 0, st>>>(p))
     if (vec) ART_APPEND4(true, true);
     else if (vec_q) ART_APPEND4(true, false);
     else ART_APPEND4(false, false);
