@@ -134,10 +134,13 @@ __device__ __forceinline__ void lds128(uint32_t a, uint32_t (&r)[4]) {
 }
 // wait_tc for warps that mostly wait: asleep between the looks, so that they leave the issue slots to others (with
 // wait_tc's looks, a fifth of the kernel's instructions were theirs).
-static __device__ __noinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, int* abort, unsigned long long wait_ns, int* status) {
+static __device__ __noinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, int* abort, unsigned most, unsigned long long wait_ns,
+                                                int* status) {
     const unsigned long long t0 = global_ns();
-    for (;;) {
-        if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 20000u))) return true;
+    for (unsigned nap = 32;;) {
+        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+        __nanosleep(nap);
+        nap = min(nap * 2, most);
         const bool late = (threadIdx.x & 31) == 0 && global_ns() - t0 > wait_ns;
         if (__any_sync(0xffffffffu, late)) {
             if ((threadIdx.x & 31) == 0) {
@@ -149,8 +152,8 @@ static __device__ __noinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, 
         if (__any_sync(0xffffffffu, ld_volatile_shared(abort) != 0)) return false;
     }
 }
-__device__ __forceinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, int* abort, const AttendParams& p) {
-    return wait_asleep(bar, parity, abort, p.wait_ns, &p.cta_status[blockIdx.x]);
+__device__ __forceinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, int* abort, unsigned most, const AttendParams& p) {
+    return wait_asleep(bar, parity, abort, most, p.wait_ns, &p.cta_status[blockIdx.x]);
 }
 // 2^e for -126 <= e <= 127
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
@@ -230,7 +233,7 @@ __device__ void kv4_producer(const AttendKv4Params& pp, unsigned char* gen, Kv4C
                     polls = 0;
                     const int from = __ffs(left) - 1;
                     const int ls = __shfl_sync(0xffffffffu, s, from), lu = __shfl_sync(0xffffffffu, u, from);
-                    if (!wait_asleep(&c->empty[ls], (uint32_t)(lu - 1) & 1u, &c->abort, p)) {
+                    if (!wait_asleep(&c->empty[ls], (uint32_t)(lu - 1) & 1u, &c->abort, 64u, p)) {
                         ok = false;
                         issued = __ballot_sync(0xffffffffu, t < nb && !todo);
                         break;
@@ -276,7 +279,7 @@ __device__ void kv4_queries(const AttendParams& p, unsigned char* gen, Kv4Ctrl<K
         const Seg sg = load_seg(&p.seg[si]);
         if (sg.nrow == 0) continue;
         const int buf = k & 1;
-        if (k >= 2 && !wait_asleep(&c->q_free[buf], (uint32_t)((k >> 1) - 1) & 1u, &c->abort, p)) return;
+        if (k >= 2 && !wait_asleep(&c->q_free[buf], (uint32_t)((k >> 1) - 1) & 1u, &c->abort, 128u, p)) return;
         ++k;
 #pragma unroll 1
         for (int n = 0; n * 8 < sg.nrow; ++n) {
@@ -364,7 +367,7 @@ __device__ void kv4_mergers(const AttendParams& p, unsigned char* gen, Kv4Ctrl<K
         if (si + 1 < s1) nx = load_seg(&p.seg[si + 1]);
 #pragma unroll 1
         for (int n = 0; n * 8 < sg.nrow; ++n) {
-            if (!wait_asleep(&c->ex_full, ph, &c->abort, p)) return;
+            if (!wait_asleep(&c->ex_full, ph, &c->abort, 128u, p)) return;
             ph ^= 1u;
             const int rows = min(8, sg.nrow - n * 8);
 #pragma unroll 1
@@ -734,29 +737,41 @@ struct Kv4Consumer {
             }
         };
 
+        // this group's tiles of the segment
+        constexpr int GROUPS = C::GROUPS;
+        int j = grp - turn + (grp < turn ? GROUPS : 0);
+        Stage<C::NS> at = st;
+        at.skip(j);
 #pragma unroll 1
-        for (int j = 0; j < nt; ++j) {
-            const bool own = turn == grp;
-            turn = turn == kCons / 4 - 1 ? 0 : turn + 1;
-            if (!own) {
-                st.next();
-                continue;
-            }
-            if (!wait(&c->full[st.s], st.ph)) return false;
-            const uint32_t tile = st.s * C::TILE;
+        for (; j < nt; j += GROUPS) {
+            if (!wait(&c->full[at.s], at.ph)) return false;
+            const uint32_t tile = at.s * C::TILE;
             const int kw = (t0 + j) * kKeyTile + sub * 32;  // first key of this warp's slice
+            if (kw >= sg.k0 && kw + 32 <= klo) {
 #pragma unroll 1
-            for (int h = 0; h < 2; h += KM) {
-                const int kb = kw + h * 16;
-                if (kb >= khi || kb + 16 * KM <= sg.k0) continue;
-                const uint32_t ok = tile + h * dk, os = tile + h * ds;
-                if (kb >= sg.k0 && kb + 16 * KM <= klo) step(std::true_type(), kb, kc[0] + ok, kc[1] + ok, sc[0] + os, sc[1] + os);
-                else step(std::false_type(), kb, kc[0] + ok, kc[1] + ok, sc[0] + os, sc[1] + os);
+                for (int h = 0; h < 2; h += KM) {
+                    const uint32_t ok = tile + h * dk, os = tile + h * ds;
+                    step(std::true_type(), 0, kc[0] + ok, kc[1] + ok, sc[0] + os, sc[1] + os);
+                }
+            } else {
+#pragma unroll 1
+                for (int h = 0; h < 2; h += KM) {
+                    const int kb = kw + h * 16;
+                    if (kb >= khi || kb + 16 * KM <= sg.k0) continue;
+                    const uint32_t ok = tile + h * dk, os = tile + h * ds;
+                    step(std::false_type(), kb, kc[0] + ok, kc[1] + ok, sc[0] + os, sc[1] + os);
+                }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c->empty[st.s]);
-            st.next();
+            if (lane == 0) mbar_arrive(&c->empty[at.s]);
+            at.s += GROUPS;
+            if (at.s >= C::NS) {
+                at.s -= C::NS;
+                at.ph ^= 1u;
+            }
         }
+        st.skip(nt);
+        turn = (turn + nt) % GROUPS;
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->q_free[buf]);
         ++segs;
