@@ -25,15 +25,14 @@
 // stays within fp16's range whatever the values' scales are, and the row's sum l is brought to
 // [1, 2) before parts meet. Queries are scaled by a power of two to fp16's range.
 //
-// One CTA per SM, 12 warps, which meet at barriers in shared memory only:
-//   producer   page ids 32 at a time, one bulk copy for each slab of a page (art_kv4.cuh), into a ring of
+// One CTA per SM, of 16 (decode) or 12 warps, which meet at barriers in shared memory only:
+//   2 producers page ids 32 at a time, one bulk copy for each slab of a page (art_kv4.cuh), into a ring of
 //              tiles of 128 keys
 //   queries    turns the next segment's queries into operands, in shared memory
-//   8 consumers in two groups of four that take alternate tiles, a warp 32 keys of each, with a
-//              reference, sums and O of its own. Up to 8 rows: 32 keys at a time, two chains of products
-//              and the queries in registers; up to 16: 16 keys at a time and two column tiles, for which the
-//              codes are taken apart once
-//   2 mergers  join the consumers' parts of a segment, eight rows at a time, and store them, while the
+//   consumers  12 (decode) or 8, in groups of four that take the tiles in turn, a warp 32 keys of each, with a
+//              reference, sums and O of its own. Up to 8 rows: the queries in registers; up to 16: two column
+//              tiles, for which the codes are taken apart once
+//   a merger   joins the consumers' parts of a segment, eight rows at a time, and stores them, while the
 //              consumers are at the next one
 //
 // Keys and values outside a segment's keys may be anything: codes are always finite numbers, and
@@ -48,7 +47,7 @@
 namespace art {
 
 constexpr int kRowsKv4 = 16;  // rows of an item's tile
-constexpr int kKv4Mergers = 2;
+constexpr int kKv4Mergers = 1, kKv4Producers = 2;
 // A row's reference is set so that its largest weight times step is about 2^kKv4Lift, and moves when
 // one passes 2^kKv4Most: fp16 holds 11 bits of whatever is within 2^-19 of the largest.
 constexpr float kKv4Lift = 5.f, kKv4Most = 14.f;
@@ -66,7 +65,7 @@ struct AttendKv4Params {
 // kCons: consumer warps.
 template <bool kBF16, int D, int NG, int kCons>
 struct Kv4Cfg {
-    static constexpr int THREADS = (kCons + kKv4Mergers + 2) * 32;
+    static constexpr int THREADS = (kCons + kKv4Mergers + kKv4Producers + 1) * 32;
     static constexpr int NC = D / 32;                     // 32-column chunks
     static constexpr int KP = kBF16 ? 1 : 2;              // fp16 parts of a query and of a weight
     static constexpr int TILE = kKeyTile * (D + 8 * NG);  // bytes of a tile
@@ -163,19 +162,22 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t
 // ---------------------------------------------------------------------------
 // A lane has a slab of a batch of tiles: it waits for its tile's stage and issues its copy, side by side
 // with the others. (One tile after the other, a warp of few instructions, each waiting for the one
-// before, was what bound the kernel: 0.4 us a tile alone, 0.7 beside busy consumers.)
+// before, was what bound the kernel: 0.4 us a tile alone, 0.7 beside busy consumers.) The copies of a warp are issued one
+// after the other all the same, so kKv4Producers warps share a tile's: with pages of 16 tokens, eight copies a
+// tile, 64 sequences of 4096 tokens took 76 us with
+// one warp and 66 with two.
 template <bool kBF16, int D, int NG, int kCons>
 __device__ void kv4_producer(const AttendKv4Params& pp, unsigned char* gen, Kv4Ctrl<Kv4Cfg<kBF16, D, NG, kCons>::NS, NG, kCons>* c,
-                             int s0, int s1) {
+                             int s0, int s1, int which) {
     using C = Kv4Cfg<kBF16, D, NG, kCons>;
     const AttendParams& p = pp.a;
     const int lane = threadIdx.x & 31;
-    const int ppt = kKeyTile / pp.slab;         // slabs of a tile (2 .. 16)
-    const int tpb = min(32 / ppt, C::NS);       // tiles of a batch: no two of them in one stage
-    const int t = lane / ppt, in_tile = lane - t * ppt;  // this lane's tile of a batch, its slab of the tile
+    const int ppt = kKeyTile / pp.slab / kKv4Producers;  // slabs of a tile that are this warp's (1 .. 8)
+    const int tpb = min(32 / ppt, C::NS);                // tiles of a batch: no two of them in one stage
+    const int t = lane / ppt, in_tile = (lane - t * ppt) * kKv4Producers + which;  // this lane's tile of a batch, its slab of the tile
     const uint32_t dst0 = in_tile * pp.slab_bytes;
     auto ids_of = [&](const Seg& sg, int bt) -> int {  // page of this lane's slab of batch bt, -1 where it has none
-        const int key = (sg.k0 / kKeyTile + bt * tpb) * kKeyTile + lane * pp.slab;
+        const int key = (sg.k0 / kKeyTile + bt * tpb + t) * kKeyTile + in_tile * pp.slab;
         if (t >= tpb || sg.nrow == 0 || key >= sg.k1 || key + pp.slab <= sg.k0) return -1;
         const int pg = __ldg(&p.block_table[(size_t)sg.table_row * p.max_pages + key / p.Ps]);
         return pg < 0 || pg >= p.num_pages ? -2 : pg;
@@ -216,7 +218,7 @@ __device__ void kv4_producer(const AttendKv4Params& pp, unsigned char* gen, Kv4C
             bool todo = t < nb;
             for (int polls = 0;;) {
                 // the lanes of a tile go by what the first of them sees: all of a tile's copies are issued, or none
-                const bool mine = u == 0 || mbar_test_wait(&c->empty[s], (uint32_t)(u - 1) & 1u);
+                const bool mine = t < nb && (u == 0 || mbar_test_wait(&c->empty[s], (uint32_t)(u - 1) & 1u));  // no stage else
                 const bool room = __shfl_sync(0xffffffffu, (int)mine, t * ppt) != 0;
                 if (todo && room) {
                     if (ids >= 0) {
@@ -842,7 +844,7 @@ struct Kv4Consumer {
 
 // kDecode: one token of each sequence, so no item has more than 8 rows.
 template <bool kBF16, int D, int NG, int kCons, int KM, bool kDecode>
-__global__ void __launch_bounds__((kCons + kKv4Mergers + 2) * 32, 1) art_attend_kv4_kernel(const __grid_constant__ AttendKv4Params pp) {
+__global__ void __launch_bounds__((kCons + kKv4Mergers + kKv4Producers + 1) * 32, 1) art_attend_kv4_kernel(const __grid_constant__ AttendKv4Params pp) {
     using C = Kv4Cfg<kBF16, D, NG, kCons>;
     extern __shared__ __align__(1024) unsigned char gen[];
     const AttendParams& p = pp.a;
@@ -887,7 +889,7 @@ __global__ void __launch_bounds__((kCons + kKv4Mergers + 2) * 32, 1) art_attend_
     } else if (w == kCons + kKv4Mergers) {
         kv4_queries<kBF16, D, NG, kCons>(p, gen, c, s0, s1);
     } else {
-        kv4_producer<kBF16, D, NG, kCons>(pp, gen, c, s0, s1);
+        kv4_producer<kBF16, D, NG, kCons>(pp, gen, c, s0, s1, w - kCons - kKv4Mergers - 1);
     }
 }
 
