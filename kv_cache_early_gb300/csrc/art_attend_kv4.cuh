@@ -47,7 +47,7 @@
 namespace art {
 
 constexpr int kRowsKv4 = 16;  // rows of an item's tile
-constexpr int kKv4Mergers = 1, kKv4Producers = 2;
+constexpr int kKv4Producers = 2;
 // A row's reference is set so that its largest weight times step is about 2^kKv4Lift, and moves when
 // one passes 2^kKv4Most: fp16 holds 11 bits of whatever is within 2^-19 of the largest.
 constexpr float kKv4Lift = 5.f, kKv4Most = 14.f;
@@ -65,7 +65,7 @@ struct AttendKv4Params {
 // kCons: consumer warps.
 template <bool kBF16, int D, int NG, int kCons>
 struct Kv4Cfg {
-    static constexpr int THREADS = (kCons + kKv4Mergers + kKv4Producers + 1) * 32;
+    static constexpr int THREADS = (kCons + 2 + kKv4Producers) * 32;
     static constexpr int NC = D / 32;                     // 32-column chunks
     static constexpr int KP = kBF16 ? 1 : 2;              // fp16 parts of a query and of a weight
     static constexpr int TILE = kKeyTile * (D + 8 * NG);  // bytes of a tile
@@ -355,13 +355,15 @@ __device__ void kv4_queries(const AttendParams& p, unsigned char* gen, Kv4Ctrl<K
 }
 
 // ---------------------------------------------------------------------------
-// merger warps
+// merger warp
 // ---------------------------------------------------------------------------
 template <bool kBF16, int D, int NG, int kCons>
-__device__ void kv4_mergers(const AttendParams& p, unsigned char* gen, Kv4Ctrl<Kv4Cfg<kBF16, D, NG, kCons>::NS, NG, kCons>* c, int s0, int s1) {
+__device__ void kv4_merger(const AttendParams& p, unsigned char* gen, Kv4Ctrl<Kv4Cfg<kBF16, D, NG, kCons>::NS, NG, kCons>* c, int s0, int s1) {
     using C = Kv4Cfg<kBF16, D, NG, kCons>;
-    const int lane = threadIdx.x & 31, tid = threadIdx.x - kCons * 32;
-    const float* ex = reinterpret_cast<const float*>(gen + C::EXOFF);
+    // A lane has a row and every fourth four columns (every eighth, where there are four rows or fewer): the eight lanes
+    // that read side by side have the same columns of eight rows, which lie in different banks, and store 128 bytes
+    // of a partial result.
+    const int lane = threadIdx.x & 31;
     uint32_t ph = 0;
     Seg nx = load_seg(&p.seg[s0]);
     for (int si = s0; si < s1; ++si) {
@@ -371,40 +373,43 @@ __device__ void kv4_mergers(const AttendParams& p, unsigned char* gen, Kv4Ctrl<K
         for (int n = 0; n * 8 < sg.nrow; ++n) {
             if (!wait_asleep(&c->ex_full, ph, &c->abort, 128u, p)) return;
             ph ^= 1u;
-            const int rows = min(8, sg.nrow - n * 8);
-#pragma unroll 1
-            for (int u = tid; u < rows * (D / 4); u += kKv4Mergers * 32) {
-                const int r = u / (D / 4), col = (u - r * (D / 4)) * 4, rr = n * 8 + r;
-                float2 ml[kCons];
-                float mm = -INFINITY, ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+            const int rl = sg.nrow - n * 8 <= 4 ? 2 : 3, r = lane & ((1 << rl) - 1), c0 = lane >> rl, rr = n * 8 + r;
+            const float* ex = reinterpret_cast<const float*>(gen + C::EXOFF) + r * C::EXROW + c0 * 4;
+            float f[kCons], mm = -INFINITY, ll = 0.f;
+#pragma unroll
+            for (int k = 0; k < kCons; ++k) mm = fmaxf(mm, c->ml[k][r].x);
+#pragma unroll
+            for (int k = 0; k < kCons; ++k) {
+                const float2 ml = c->ml[k][r];
+                f[k] = ml.y == 0.f ? 0.f : ex2(ml.x - mm);  // saw no key: its sums are zero
+                ll = fmaf(ml.y, f[k], ll);
+            }
+            const float inv = ll > 0.f ? 1.f / ll : ll;  // no key seen: 0; NaN stays
+            const bool mine = rr < sg.nrow, part = sg.prow >= 0;
+            float* to = part && mine ? part_at(p, sg, rr, c0 * 4) : nullptr;
+            const size_t row = mine && !part ? row_index(p, sg, rr) * D + c0 * 4 : 0;
+            if (mine && part && c0 == 0) p.part_ml[sg.prow + rr] = make_float2(mm, ll);
+#pragma unroll 2
+            for (int i = 0; i < D / 4; i += 32 >> rl) {  // four columns each
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k < kCons; ++k) {
-                    ml[k] = c->ml[k][r];
-                    mm = fmaxf(mm, ml[k].x);
+                    const float4 v = *reinterpret_cast<const float4*>(ex + k * 8 * C::EXROW + i * 4);
+                    acc[0] = fmaf(v.x, f[k], acc[0]);
+                    acc[1] = fmaf(v.y, f[k], acc[1]);
+                    acc[2] = fmaf(v.z, f[k], acc[2]);
+                    acc[3] = fmaf(v.w, f[k], acc[3]);
                 }
-#pragma unroll
-                for (int k = 0; k < kCons; ++k) {
-                    const float f = ml[k].y == 0.f ? 0.f : ex2(ml[k].x - mm);  // saw no key: its sums are zero
-                    const float4 v = *reinterpret_cast<const float4*>(ex + (k * 8 + r) * C::EXROW + col);
-                    ll = fmaf(ml[k].y, f, ll);
-                    acc[0] = fmaf(v.x, f, acc[0]);
-                    acc[1] = fmaf(v.y, f, acc[1]);
-                    acc[2] = fmaf(v.z, f, acc[2]);
-                    acc[3] = fmaf(v.w, f, acc[3]);
-                }
-                if (sg.prow >= 0) {
-                    *reinterpret_cast<float4*>(part_at(p, sg, rr, col)) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                    if (col == 0) p.part_ml[sg.prow + rr] = make_float2(mm, ll);
-                    continue;
-                }
-                const float inv = ll > 0.f ? 1.f / ll : ll;  // no key seen: 0; NaN stays
-                const size_t at = row_index(p, sg, rr) * D + col;
-                if constexpr (kBF16)
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+                if (!mine) continue;
+                if (part) {
+                    *reinterpret_cast<float4*>(to + (size_t)i * 4 * sg.nrow) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                } else if constexpr (kBF16) {
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row + i * 4) =
                         make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-                else
-                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
+                } else {
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row + i * 4) =
                         make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->ex_free);
@@ -844,7 +849,7 @@ struct Kv4Consumer {
 
 // kDecode: one token of each sequence, so no item has more than 8 rows.
 template <bool kBF16, int D, int NG, int kCons, int KM, bool kDecode>
-__global__ void __launch_bounds__((kCons + kKv4Mergers + kKv4Producers + 1) * 32, 1) art_attend_kv4_kernel(const __grid_constant__ AttendKv4Params pp) {
+__global__ void __launch_bounds__((kCons + 2 + kKv4Producers) * 32, 1) art_attend_kv4_kernel(const __grid_constant__ AttendKv4Params pp) {
     using C = Kv4Cfg<kBF16, D, NG, kCons>;
     extern __shared__ __align__(1024) unsigned char gen[];
     const AttendParams& p = pp.a;
@@ -860,7 +865,7 @@ __global__ void __launch_bounds__((kCons + kKv4Mergers + kKv4Producers + 1) * 32
             mbar_init(&c->q_free[i], kCons);
         }
         mbar_init(&c->ex_full, kCons);
-        mbar_init(&c->ex_free, kKv4Mergers);
+        mbar_init(&c->ex_free, 1);
         mbar_init(&c->stall, 1);
         c->abort = 0;
         fence_mbar_init();
@@ -884,12 +889,12 @@ __global__ void __launch_bounds__((kCons + kKv4Mergers + kKv4Producers + 1) * 32
         if (p.stall && !wait_tc(&c->stall, 0u, &c->abort, p)) return;
         Kv4Consumer<kBF16, D, NG, kCons> k{pp, p, c, smem_addr(gen), gen, w, lane, pp.f16_1024};
         k.template run<KM, kDecode>(s0, s1);
-    } else if (w < kCons + kKv4Mergers) {
-        kv4_mergers<kBF16, D, NG, kCons>(p, gen, c, s0, s1);
-    } else if (w == kCons + kKv4Mergers) {
+    } else if (w == kCons) {
+        kv4_merger<kBF16, D, NG, kCons>(p, gen, c, s0, s1);
+    } else if (w == kCons + 1) {
         kv4_queries<kBF16, D, NG, kCons>(p, gen, c, s0, s1);
     } else {
-        kv4_producer<kBF16, D, NG, kCons>(pp, gen, c, s0, s1, w - kCons - kKv4Mergers - 1);
+        kv4_producer<kBF16, D, NG, kCons>(pp, gen, c, s0, s1, w - kCons - 2);
     }
 }
 
