@@ -11,6 +11,11 @@ fp32; A, C, V, n as in oracle.kv4.extend's terms):
                                    below 2^-14 of fp16's range a weight is off by 2^-25 at most, the
                                    largest being at least 2^4: n 2^-29 15 step < n 2^-29 V
   fp32 queries in two parts        2^-22 A in the exponent, on both sides of the quotient: 2 2^-22 A V
+  bf16 products with keys' codes   a code is a denormal there, and a step of the product (16 columns and the sum so far)
+                                   is cut at 2^-24 of the largest query times 2^-14, 2^-14 of that query in units of a
+                                   code: 17 d / 16 such cuts, uniform, as random at 4 sigma (0.29 each), times the
+                                   keys' largest step, on both sides of the quotient; only where queries have columns
+                                   far larger than the others is this seen beside the terms above
   fp32 sums                        as for dense_extend: 2^-24 (8 sqrt(d) A + 8 sqrt(n) + 16) V
 """
 import math
@@ -56,6 +61,11 @@ class Pool4:
         return dict(dict(batch=len(self.seq_lens), num_q_heads=hq, num_kv_heads=self.hkv, head_dim=self.d,
                          page_size=self.page, block_size=64, max_pages_per_seq=self.table.shape[1], max_visit=1,
                          num_probe=1, num_pages_total=self.num_pages, dtype=0 if self.dtype == "bf16" else 1), **kw)
+
+
+def cuts(top, step, v, d):
+    """The tolerance's part for the cuts in the products with keys' codes (top: a query's largest column)."""
+    return 2 * 4 * 0.29 * math.sqrt(17 * d / 16) * 2.0 ** -14 * top * step / math.sqrt(d) * v
 
 
 def attend_tol(ref, terms, d, dtype):

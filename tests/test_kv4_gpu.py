@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from cache_ops_harness import E24, U, rounded
-from kv4_harness import Pool4, attend_tol
+from kv4_harness import Pool4, attend_tol, cuts
 from oracle import cache_ops as O
 from oracle import kv4 as Q
 
@@ -458,6 +458,29 @@ def test_sizes_of_queries_and_keys(dtype):
     check(got, ref, terms, 64, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_with_large_columns(dtype, d):
+    """Columns of a query 64 times larger than the others, whose keys are small there: scores stay ordinary."""
+    rng = np.random.default_rng(64)
+    hq, page, group = 4, 16, 32
+    pool = Pool4(rng, dtype, 1, d, page, group, [500, 77])
+    small = np.where(np.arange(d) % 32 == 5, 1 / 64, 1.0)
+    for b, n in enumerate(pool.seq_lens):
+        for t in range(int(n)):
+            pool.put(b, t, 0, 0, rounded(rng.standard_normal(d) * small, dtype))
+            pool.put(b, t, 0, 1, rounded(rng.standard_normal(d), dtype))
+    q = rounded(rng.standard_normal((2, hq, d)) / small, dtype)
+    got, status = run_extend(pool, q, None, True, hq, offsets=False)
+    assert status == 0
+    ref, terms = Q.extend(q, pool.bytes, pool.table, pool.seq_lens, [0, 1, 2], False, page, group)
+    steps = max(Q.held(pool.bytes, pool.table[b], int(n), 0, page, d, group, 0)[1].max() for b, n in enumerate(pool.seq_lens))
+    tol = attend_tol(ref, terms, d, dtype)
+    if dtype == "bf16":
+        tol = tol + cuts(np.abs(q).max(-1)[..., None], steps, terms[..., 2][..., None], d)
+    assert np.all(np.abs(got - ref) <= tol), np.max(np.abs(got - ref) / tol)
+
+
 def test_flat_groups():
     """Groups without a step: codes mean nothing there."""
     rng = np.random.default_rng(57)
@@ -710,6 +733,59 @@ def test_serving_run(dtype):
             near(o1, reference(q1, [1] * B))
     torch.cuda.synchronize()
     assert all(K.art_read_device_status(w) == 0 for w in ws + [ws_d, ws_e])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_short_sequences(dtype):
+    """More sequences than a block has threads, some empty: decode, and one to three new tokens of some."""
+    lens = [(b * 37) % 50 for b in range(600)]
+    decode_case(62, dtype, (2, 1, 64), 8, 32, lens)
+    new = [min(n, b % 4) for b, n in enumerate(lens)]
+    extend_case(63, dtype, (4, 1, 64), 8, 64, new, lens)
+
+
+def test_cache_beyond_32_bits():
+    """Pages that lie more than 4 GiB into the cache and into the plain pool: the same results as in the first pages."""
+    torch.manual_seed(1)
+    hq, hkv, d, page, group, B = 8, 8, 128, 64, 128, 2
+    pages = 64000
+    shape = K.make_shape(batch=B, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, page_size=page, block_size=64,
+                         max_pages_per_seq=4, max_visit=1, num_probe=1, num_pages_total=pages, dtype=0)
+    cache = torch.zeros(pages, hkv, K.art_kv4_page_bytes(shape, group), dtype=torch.uint8, device="cuda")
+    assert cache.numel() > 1 << 32
+    lens = torch.tensor([200, 130], dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 200, 330], dtype=torch.int32, device="cuda")
+    rows = torch.randn(330, hq + 2 * hkv, d, device="cuda").bfloat16()
+    inv = (10000.0 ** (-torch.arange(0, d, 2, device="cuda", dtype=torch.float64) / d)).float()
+    ws = workspace(max(K.dense_extend_kv4_workspace_bytes(shape, 330, group), 64))
+    small = K.make_shape(**{n: getattr(shape, n) for n, _ in K.ArtShape._fields_ if n != "num_pages_total"}, num_pages_total=8)
+    results = []
+    for first in (0, pages - 8):
+        table = (first + torch.arange(8, device="cuda")).int().reshape(B, 4)
+        q = torch.empty(330, hq, d, dtype=torch.bfloat16, device="cuda")
+        K.art_append_kv4(rows[:, :hq], rows[:, hq:hq + hkv], rows[:, hq + hkv:], table, lens, off, inv, q, cache, shape, ws,
+                         group=group, rot_dim=d)
+        out, one = torch.empty_like(q), torch.empty(B, hq, d, dtype=torch.bfloat16, device="cuda")
+        K.dense_extend_kv4(q, cache, table, lens, off, out, shape, ws, group=group)
+        K.dense_extend_kv4(q[:2], cache, table, lens, None, one, shape, ws, group=group)
+        k, v = (torch.empty(330, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        K.art_read_kv4(cache, table, lens, off, k, v, shape, ws, group=group)
+        assert K.art_read_device_status(ws) == 0
+        results.append((q, out, one, k, v, cache[first:first + 8].clone()))
+    assert all(torch.equal(a, b) for a, b in zip(*results)) and results[0][5].any()
+    n = (1 << 32) // (hkv * page * d * 2) + 16  # pages of a plain pool beyond 4 GiB
+    kc, vc = (torch.zeros(n, hkv, page, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    to = (n - 8 + torch.arange(8, device="cuda")).int().reshape(B, 4)
+    K.art_read_kv4(results[0][5], torch.arange(8, device="cuda").int().reshape(B, 4), lens, None, kc, vc, small, ws,
+                   group=group, out_table=to)
+    assert K.art_read_device_status(ws) == 0
+    for b in range(B):
+        for c in range(4):
+            m = max(0, min(64, int(lens[b]) - 64 * c))
+            for pool, x in ((kc, results[0][3]), (vc, results[0][4])):
+                lo = int(off[b]) + 64 * c
+                assert torch.equal(pool[int(to[b, c]), :, :m].transpose(0, 1), x[lo:lo + m])
+                assert not pool[int(to[b, c]), :, m:].any()
 
 
 def test_calls_repeat_and_overlap():

@@ -119,6 +119,9 @@ def test_append_refusals(lib, kw, expect):
     (dict(out_table=FAKE, out_pages=3, off=0), INV), (dict(out_table=FAKE, out_pages=0, off=0, T=0), INV),
     (dict(out_table=FAKE, out_pages=3, off=0, T=0, ws_bytes=0), WS), (dict(out_table=FAKE, out_pages=3, off=0, T=0, k=0), INV),
     (dict(T=-1), INV), (dict(shape=good_shape(page_size=4096, max_pages_per_seq=1 << 19)), UNS), (dict(ws=0), INV),
+    (dict(shape=good_shape(batch=33, page_size=4096, max_pages_per_seq=1 << 16), out_table=FAKE, out_pages=3, off=0, T=0), UNS),
+    (dict(shape=good_shape(batch=32, page_size=4096, max_pages_per_seq=1 << 16), out_table=FAKE, out_pages=3, off=0, T=0,
+          ws_bytes=0), WS),
 ])
 def test_read_refusals(lib, kw, expect):
     kw = dict(kw)
