@@ -32,7 +32,10 @@
 
 namespace art {
 
-// Up to these many tokens a CTA takes one token's keys and values, beyond it kKvTile's.
+// Up to these many tokens a CTA takes one token's keys and values, beyond it kKvTile's. One prompt, a token each against
+// tiles, us: 32/8 heads, d 128: 256 tokens 5.4 / 11.2, 608 9.6 / 11.2, 700 11.1 / 11.5, 1024 14.9 / 11.6; in fp32 608
+// 8.3 / 10.7, 1024 12.6 / 11.0; 16/16 heads 608 11.5 / 15.7, 1024 17.6 / 15.5; 8/2 heads, d 64: 256 4.8 / 6.4,
+// 608 8.2 / 6.3. Tiles take the same time up to all SMs' worth of them: four tokens an SM, between the crossings.
 constexpr int kFewTokensKv4 = 608;
 // Tokens of a tile, and blocks an SM. 36,864 tokens (32/8 heads, d 128, groups of 64): 8 tokens 178 us, 16 183; two
 // blocks 195 (of 16 tokens), four 210, whose 64 registers spill.
