@@ -148,6 +148,17 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     return y;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 constexpr float kMaxRange = 0x1.ep103f;   // 15 * 2^100: groups of such a range, and those with an infinity or NaN, become NaN
 constexpr float kMinStep = 0x1p-100f;     // smaller steps are zero
 
@@ -159,21 +170,34 @@ __device__ __forceinline__ float floor_bf16(float x) {
 }
 
 // The codes of the thread's 8 values, the first in the lowest bits, and (step, lowest) of its
-// group of `kLanes` threads (consecutive lanes from a multiple of kLanes).
-template <int kLanes>
+// group of `kLanes` threads (consecutive lanes from a multiple of kLanes). kBF16: the values are bf16 numbers, so their
+// least is `lowest`, and a lane sends it and the largest, negated, in one word.
+template <bool kBF16, int kLanes>
 __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& scales) {
-    float mn = x[0], mx = x[0];
+    float mn = min_nan(x[0], x[1]), mx = max_nan(x[0], x[1]);
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        mn = min_nan(mn, x[i]);
-        mx = max_nan(mx, x[i]);
+    for (int i = 2; i < 8; i += 2) {
+        mn = min_nan(mn, x[i], x[i + 1]);
+        mx = max_nan(mx, x[i], x[i + 1]);
     }
+    float low;
+    if constexpr (kBF16) {
+        uint32_t both = __byte_perm(__float_as_uint(mn), __float_as_uint(mx), 0x7632) ^ 0x80000000u;
 #pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) {
-        mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        for (int o = 1; o < kLanes; o <<= 1) {
+            const uint32_t z = __shfl_xor_sync(0xffffffffu, both, o);
+            asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(both) : "r"(z));
+        }
+        low = bf16_lo_f(both);
+        mx = bf16_hi_f(both ^ 0x80000000u);
+    } else {
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) {
+            mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        }
+        low = floor_bf16(mn);
     }
-    const float low = floor_bf16(mn);
     const float d = __fadd_rn(mx, -low);
     // (d + de) / 15 = q + rest / 15: the quotient by a rounded 1 / 15, corrected once
     const float b = __fadd_rn(d, -mx);
@@ -193,12 +217,12 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& scal
     float r[8], w[8], off = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float v = __fmul_rn(__fadd_rn(x[i], -low), inv);
-        r[i] = __fadd_rn(__fadd_rn(v, 12582912.f), -12582912.f);
-        w[i] = __fadd_rn(v, -r[i]);
+        const float t = __fadd_rn(x[i], -low);
+        r[i] = __fadd_rn(fmaf(t, inv, 12582912.f), -12582912.f);
+        w[i] = fmaf(t, inv, -r[i]);
         off = fmaxf(off, fabsf(w[i]));
     }
-    if (off > 0.49998f) {  // v is within 16 * 4 * 2^-24 of (x - lowest) / step: near a border, by exact terms
+    if (off > 0.49998f) {  // t inv is within 16 * 4 * 2^-24 of (x - lowest) / step: near a border, by exact terms
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (fabsf(w[i]) <= 0.49998f) continue;
@@ -466,7 +490,7 @@ __device__ __forceinline__ void append_kv4_tile(const AppendKv4Params& pp, int t
             for (int e = 0; e < 8; ++e) x[e] = o[e];
         }
         uint32_t scales;
-        const uint32_t codes = quantise<D / NG / 8>(x, scales);
+        const uint32_t codes = quantise<kBF16, D / NG / 8>(x, scales);
         if (!live) return;
         *reinterpret_cast<uint32_t*>(page + code_at + (key ? 0 : v_codes)) = codes;
         if (ch % (PER / NG) == 0) *reinterpret_cast<uint32_t*>(page + scale_at + (key ? 0 : v_scales)) = scales;
