@@ -22,8 +22,10 @@
 // walks the heads; the lanes of a group of columns find its least and largest value by shuffles; eight codes are one
 // 32-bit store, and neighbouring lanes store to neighbouring tokens, so that a tile fills whole 128-byte units.
 //
-// Bound by instructions: 36,864 tokens (32/8 heads, d 128, bf16) take 178 us where their bytes take 117. Eight values of a
-// row are about 150 instructions (without rotation and queries 80 us), the rotation as in exact arithmetic 43 us more; what
+// Bound by instructions: 36,864 tokens (32/8 heads, d 128, bf16) take 176 us where their bytes take 117. Eight values of a
+// row are 228 instructions, a tile's fixed part with them, two thirds of the issue slots busy (without rotation and queries
+// 82 us), the rotation as in exact arithmetic 42 us more. Not by the loads' latency: a ring of eight steps of a warp's rows
+// (177), rows sent for into L2 ahead (175 for the tile's own, 186 and more for later tiles') change nothing. What
 // brought it from 265: 32-bit arithmetic with a bound that decides nearly always, ties resolved where they occur
 // only, fixed columns a thread (the general tile of art_append.cuh spends most on addresses), places and angles of
 // 8 tokens at a time.
@@ -37,7 +39,7 @@ namespace art {
 // 8.3 / 10.7, 1024 12.6 / 11.0; 16/16 heads 608 11.5 / 15.7, 1024 17.6 / 15.5; 8/2 heads, d 64: 256 4.8 / 6.4,
 // 608 8.2 / 6.3. Tiles take the same time up to all SMs' worth of them: four tokens an SM, between the crossings.
 constexpr int kFewTokensKv4 = 608;
-// Tokens of a tile, and blocks an SM. 36,864 tokens (32/8 heads, d 128, groups of 64): 8 tokens 178 us, 16 183; two
+// Tokens of a tile, and blocks an SM. 36,864 tokens (32/8 heads, d 128, groups of 64): 4 tokens 197 us, 8 176, 16 183; two
 // blocks 195 (of 16 tokens), four 210, whose 64 registers spill.
 constexpr int kKvTile = 8, kKvBlocks = 3;
 
