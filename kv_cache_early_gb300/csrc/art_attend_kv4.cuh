@@ -21,9 +21,11 @@
 // take a second part for what is left, and split the queries too, so about 22 bits). Scores,
 // weights, their sums and what is multiplied by low are fp32.
 //
-// Range: a row's reference follows the maximum of score + log2(step), not of the score alone, so W
-// stays within fp16's range whatever the values' scales are, and the row's sum l is brought to
-// [1, 2) before parts meet. Queries are scaled by a power of two to fp16's range.
+// Range: a row has two references. The weights' own, R, follows the scores: weights stay below 2^-12, so that sums of
+// weights times lowest stay finite whatever is held. W's, a power of two F beside it (W = p F step), follows the maximum
+// of score + log2(step), so that W stays within fp16's range; values without a step need no W. The row's sum l is
+// brought to [2^-10, 2^-9) before parts meet, so that their sums are finite too. Queries are scaled by a power of two to
+// fp16's range.
 //
 // One CTA per SM, of 16 (decode) or 12 warps, which meet at barriers in shared memory only:
 //   2 producers: page ids 32 at a time, one bulk copy for each slab of a page (art_kv4.cuh), into a ring of
@@ -58,11 +60,14 @@ namespace art {
 
 constexpr int kRowsKv4 = 16;  // rows of an item's tile
 constexpr int kKv4Producers = 2;
-// A row's reference is set so that its largest weight times step is about 2^kKv4Lift, and moves when
-// one passes 2^kKv4Most: fp16 holds 11 bits of whatever is within 2^-19 of the largest.
-constexpr float kKv4Lift = 5.f, kKv4Most = 14.f;
-constexpr float kMostWeight = 0x1p14f;
-constexpr float kMostSum = 0x1p100f;           // of weights without steps, which may be as small as 2^-80
+// W's factor is set so that a row's largest W is 2^5 to 2^6, and moves when one reaches 2^14: fp16 holds 11 bits of
+// whatever is within 2^-19 of the largest.
+constexpr int kKv4Lift = 5;
+constexpr uint32_t kMostW = 0x7400u;  // 2^14 in fp16
+// A row's reference is set 20 to 21 above its largest score (in log2), and moves when one comes within 12.
+constexpr float kWeightLift = 20.f;
+constexpr float kMostWeight = 0x1p-12f;
+constexpr int kMostFactor = 126;        // F = 2^126 at most: its inverse is a normal number
 constexpr float kNoReference = -1e30f;  // of a row that has seen no key: any key's weight passes the limit
 
 struct AttendKv4Params {
@@ -131,6 +136,16 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t v) {
 __device__ __forceinline__ uint32_t add_f16(uint32_t a, uint32_t c) {  // two sums
     uint32_t r;
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_f16(uint32_t a, uint32_t b) {  // of two pairs; no numbers are left out
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_s16(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
@@ -434,6 +449,7 @@ template <bool kBF16, int D, int NG, int kCons>
 struct Kv4Consumer {
     using C = Kv4Cfg<kBF16, D, NG, kCons>;
     static constexpr int NC = C::NC, CPG = NC / NG, KP = C::KP;
+    static constexpr int NF = 1;  // factors of W of a row
     const AttendKv4Params& pp;
     const AttendParams& p;
     Kv4Ctrl<C::NS, NG, kCons>* c;
@@ -518,16 +534,19 @@ struct Kv4Consumer {
         khi = __reduce_max_sync(0xffffffffu, khi);
         klo = __reduce_min_sync(0xffffffffu, klo);
 
-        float R[NT][2], l[NT][2], L[NT][NG][2], o[NT][2 * NC][4];
+        float R[NT][2], l[NT][2], o[NT][2 * NC][4];
+        uint64_t L2[NT][NG], W2[NT][NF];  // of rows 2 tq, 2 tq + 1: sums of weights times lowest; F
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 R[n][i] = kNoReference;
                 l[n][i] = 0.f;
-#pragma unroll
-                for (int g = 0; g < NG; ++g) L[n][g][i] = 0.f;
             }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) L2[n][g] = 0;
+#pragma unroll
+            for (int g = 0; g < NF; ++g) W2[n][g] = pk2(pow2i(kMostFactor), pow2i(kMostFactor));
 #pragma unroll
             for (int k = 0; k < 2 * NC; ++k) o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
         }
@@ -630,26 +649,23 @@ struct Kv4Consumer {
                     }
                 }
             }
-            // Weights against the references as they are; where a weight times its step, or a row's sum, goes
-            // too far, the references move and they are formed once more.
-            float pr[KM][NT][4], ln[NT][2], most_step[KM][2];
-#pragma unroll
-            for (int m = 0; m < KM; ++m)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {  // the largest of the groups'
-                    uint32_t x = pv[m][i][0] << 16;
-#pragma unroll
-                    for (int g = 1; g < NG; ++g) x = max(x, pv[m][i][g] << 16);
-                    most_step[m][i] = __uint_as_float(x);
+            // Weights, and weights times steps, against the references as they are; where one goes too far, the
+            // references move and they are formed once more.
+            float pr[KM][NT][4];
+            auto weight = [&](int m, int n, int g, int i, float p0, float p1, float& w0, float& w1) {
+                const float step = bf16_lo_f(pv[m][i][g]);
+                up2(mul2(mul2(pk2(p0, p1), W2[n][NF == 1 ? 0 : g]), pk2(step, step)), w0, w1);
+                if constexpr (!whole) {  // scales that a row does not see may be no numbers
+                    if (!vis[m][n][2 * i]) w0 = 0.f;
+                    if (!vis[m][n][2 * i + 1]) w1 = 0.f;
                 }
+            };
 #pragma unroll 1
             for (bool again = false;; again = true) {
                 float most = 0.f;
-                bool far = false;
+                uint32_t most_w = 0;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    ln[n][0] = l[n][0];
-                    ln[n][1] = l[n][1];
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int m = 0; m < KM; ++m)
 #pragma unroll
@@ -657,53 +673,100 @@ struct Kv4Consumer {
                             const float p0 = ex2(s[m][n][2 * i] - R[n][0]), p1 = ex2(s[m][n][2 * i + 1] - R[n][1]);
                             pr[m][n][2 * i] = p0;
                             pr[m][n][2 * i + 1] = p1;
-                            ln[n][0] += p0;
-                            ln[n][1] += p1;
-                            most = max3(most, p0 * most_step[m][i], p1 * most_step[m][i]);  // no number: left out
+                            most = max3(most, p0, p1);  // no number: left out
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) {
+                                float w0, w1;
+                                weight(m, n, g, i, p0, p1, w0, w1);
+                                most_w = max_f16(most_w, pack_f16(w0, w1));
+                            }
                         }
-                    far |= fmaxf(ln[n][0], ln[n][1]) > kMostSum;
-                }
-                if (again || !__any_sync(0xffffffffu, far || most > kMostWeight)) break;
-                // up to the maximum of score + log2 of the values' step (the largest of the groups')
-                float ev[KM][2];
+                // a half of most_w that is kMostW or more comes to its sign
+                const bool far = most > kMostWeight || ((most_w + (0x80008000u - kMostW * 0x10001u)) & 0x80008000u);
+                if (again || !__any_sync(0xffffffffu, far)) break;
 #pragma unroll
-                for (int m = 0; m < KM; ++m)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t x = min(max(__float_as_uint(most_step[m][i]) >> 23 & 255u, 47u), 227u);  // 2^-80 .. 2^100
-                        ev[m][i] = __uint_as_float(0x4b000000u | x) - (8388608.f + 127.f);
-                    }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
+                    float up[2], a[2];  // R's move, 2 to the opposite of it
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float top = -INFINITY;
 #pragma unroll
-                        for (int m = 0; m < KM; ++m)
-                            top = fmaxf(top, fmaxf(s[m][n][e] + ev[m][0], s[m][n][2 + e] + ev[m][1]));
+                        for (int m = 0; m < KM; ++m) top = fmaxf(top, fmaxf(s[m][n][e], s[m][n][2 + e]));
 #pragma unroll
                         for (int k = 4; k <= 16; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-                        if (top > R[n][e] + (kKv4Most - 1.f)) {  // the same for all lanes of the row
-                            top = ceilf(top) - kKv4Lift;
-                            const float f = ex2(R[n][e] - top);
-                            R[n][e] = top;
-                            l[n][e] *= f;
+                        const float r = fmaxf(R[n][e], ceilf(top) + kWeightLift);  // the same for all lanes of the row
+                        up[e] = r - R[n][e];
+                        a[e] = ex2(-up[e]);
+                        R[n][e] = r;
+                        l[n][e] *= a[e];
+                    }
 #pragma unroll
-                            for (int g = 0; g < NG; ++g) L[n][g][e] *= f;
+                    for (int g = 0; g < NG; ++g) L2[n][g] = mul2(L2[n][g], pk2(a[0], a[1]));
+                    // F: up with R, which leaves W as it is, and down where the largest W would be too large
 #pragma unroll
-                            for (int k = 0; k < 2 * NC; ++k) {
-                                o[n][k][e] *= f;
-                                o[n][k][2 + e] *= f;
+                    for (int g = 0; g < NF; ++g) {
+                        float top[2] = {0.f, 0.f};  // weight times step
+#pragma unroll
+                        for (int m = 0; m < KM; ++m)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t x = pv[m][i][g] << 16;
+#pragma unroll
+                                for (int k = 1; k < (NF == 1 ? NG : 1); ++k) x = max(x, pv[m][i][k] << 16);
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (whole || vis[m][n][2 * i + e])
+                                        top[e] = fmaxf(top[e], ex2(s[m][n][2 * i + e] - R[n][e]) * __uint_as_float(x));
+                            }
+                        uint32_t both = pack_bf16(top[0], top[1]);
+#pragma unroll
+                        for (int k = 4; k <= 16; k <<= 1) both = max_s16(both, __shfl_xor_sync(0xffffffffu, both, k));
+                        float f[2], fix[2];
+                        up2(W2[n][g], f[0], f[1]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int x = e ? both >> 23 : both >> 7 & 255u;  // its exponent
+                            const float most = __uint_as_float((uint32_t)min(kKv4Lift + 254 - x, kMostFactor + 127) << 23);
+                            const float now = fminf(f[e] * ex2(up[e]), most);
+                            const int by = (int)(__float_as_uint(now) - __float_as_uint(f[e])) >> 23;
+                            fix[e] = ex2((float)by - up[e]);  // 1 where W stays
+                            f[e] = now;
+                        }
+                        W2[n][g] = pk2(f[0], f[1]);
+#pragma unroll
+                        for (int k = NF == 1 ? 0 : 2 * CPG * g; k < (NF == 1 ? 2 * NC : 2 * CPG * (g + 1)); ++k) {
+                            o[n][k][0] *= fix[0];
+                            o[n][k][1] *= fix[1];
+                            o[n][k][2] *= fix[0];
+                            o[n][k][3] *= fix[1];
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int m = 0; m < KM; ++m)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float p0 = pr[m][n][2 * i], p1 = pr[m][n][2 * i + 1];
+                        l[n][0] += p0;
+                        l[n][1] += p1;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            const float low = fmaf(8.f, bf16_lo_f(pv[m][i][g]), bf16_hi_f(pv[m][i][g]));
+                            if constexpr (whole) {
+                                L2[n][g] = fma2(pk2(p0, p1), pk2(low, low), L2[n][g]);
+                            } else {
+                                float x, y;
+                                up2(L2[n][g], x, y);
+                                if (vis[m][n][2 * i]) x = fmaf(p0, low, x);
+                                if (vis[m][n][2 * i + 1]) y = fmaf(p1, low, y);
+                                L2[n][g] = pk2(x, y);
                             }
                         }
                     }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                l[n][0] = ln[n][0];
-                l[n][1] = ln[n][1];
-            }
-            // what is multiplied by low, and the products with the values' codes
+            // the products with the values' codes
 #pragma unroll
             for (int m = 0; m < KM; ++m) {
                 uint32_t wa[NC], wb[NC];
@@ -712,16 +775,11 @@ struct Kv4Consumer {
                 for (int g = 0; g < NG; ++g) {
                     uint32_t wf[KP][NT][2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float step = bf16_lo_f(pv[m][i][g]), low = fmaf(8.f, step, bf16_hi_f(pv[m][i][g]));
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            float w0 = pr[m][n][2 * i] * step, w1 = pr[m][n][2 * i + 1] * step;
-                            // scales that a row does not see may be no numbers
-                            if (whole || vis[m][n][2 * i]) L[n][g][0] = fmaf(pr[m][n][2 * i], low, L[n][g][0]);
-                            else w0 = 0.f;
-                            if (whole || vis[m][n][2 * i + 1]) L[n][g][1] = fmaf(pr[m][n][2 * i + 1], low, L[n][g][1]);
-                            else w1 = 0.f;
+                            float w0, w1;
+                            weight(m, n, g, i, pr[m][n][2 * i], pr[m][n][2 * i + 1], w0, w1);
                             const uint32_t u = pack_f16(w0, w1);
                             wf[0][n][i] = movm_t(u);
                             if constexpr (KP == 2) {
@@ -729,7 +787,6 @@ struct Kv4Consumer {
                                 wf[KP - 1][n][i] = movm_t(pack_f16(w0 - hi.x, w1 - hi.y));
                             }
                         }
-                    }
 #pragma unroll
                     for (int ch = g * CPG; ch < (g + 1) * CPG; ++ch) {
                         uint32_t a0[4], a1[4];
@@ -797,25 +854,29 @@ struct Kv4Consumer {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if (n * 8 >= sg.nrow) break;
-            float fa[2], fb[2];
+            float fa[NF][2], L[NG][2];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) up2(L2[n][g], L[g][0], L[g][1]);
+#pragma unroll
+            for (int g = 0; g < NF; ++g) up2(W2[n][g], fa[g][0], fa[g][1]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float sum = l[n][e];
 #pragma unroll
                 for (int k = 4; k <= 16; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-                // sums of any size come to [1, 2)
-                const int k = min(max((int)((__float_as_uint(sum) >> 23) & 255u) - 127, -100), 120);
+                // sums of any size come to [2^-10, 2^-9)
+                const int k = min(max((int)((__float_as_uint(sum) >> 23) & 255u) - 127 + 10, -100), 120);
                 const float f = sum > 0.f ? pow2i(-k) : 1.f;
-                fa[e] = f;
-                fb[e] = f * 0.0625f;
+#pragma unroll
+                for (int g = 0; g < NF; ++g) fa[g][e] = f * __uint_as_float((254u << 23) - __float_as_uint(fa[g][e]));  // f / F
                 l[n][e] = sum * f;
                 R[n][e] += sum > 0.f ? (float)k : 0.f;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    float x = L[n][g][e];
+                    float x = L[g][e];
 #pragma unroll
                     for (int k2 = 4; k2 <= 16; k2 <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k2);
-                    L[n][g][e] = x * f;
+                    L[g][e] = x * f;
                 }
             }
             if (ex_used) {
@@ -829,10 +890,10 @@ struct Kv4Consumer {
                 float* row = reinterpret_cast<float*>(gen + C::EXOFF) + (w * 8 + 2 * tq + e) * C::EXROW + gq * 4;
 #pragma unroll
                 for (int ch = 0; ch < NC; ++ch) {
-                    const float lw = L[n][ch / CPG][e];
+                    const float lw = L[ch / CPG][e], f = fa[NF == 1 ? 0 : ch / CPG][e], f16 = f * 0.0625f;
                     *reinterpret_cast<float4*>(row + ch * 32) =
-                        make_float4(fmaf(o[n][2 * ch][e], fa[e], lw), fmaf(o[n][2 * ch][2 + e], fb[e], lw),
-                                    fmaf(o[n][2 * ch + 1][e], fa[e], lw), fmaf(o[n][2 * ch + 1][2 + e], fb[e], lw));
+                        make_float4(fmaf(o[n][2 * ch][e], f, lw), fmaf(o[n][2 * ch][2 + e], f16, lw),
+                                    fmaf(o[n][2 * ch + 1][e], f, lw), fmaf(o[n][2 * ch + 1][2 + e], f16, lw));
                 }
             }
             __syncwarp();

@@ -145,3 +145,33 @@ def extend(q, cache, table, seq_lens, offsets, causal, page, group, skip=()):
                         terms[t, h] = ((ks * kc + np.abs(kl))[:seen] @ np.abs(q[t, h])).max() / np.sqrt(d), \
                             (p @ (vs * vc)[:seen]).max(), (15 * vs + np.abs(vl))[:seen].max(), seen
     return out, terms
+
+
+def column_terms(q, cache, table, seq_lens, offsets, causal, page, group):
+    """(out, score, mean, most, n): out as extend; score [T, hq] the largest sum of |q| (step 15 + |lowest|) / sqrt(d) over
+    the keys; by column [T, hq, d], of the values seen: mean attention over their steps, largest 15 step + |lowest|; n [T]
+    keys seen."""
+    T, hq, d = q.shape
+    out, score = np.full(q.shape, np.nan), np.zeros((T, hq))
+    mean, most, n = np.zeros(q.shape), np.zeros(q.shape), np.zeros(T)
+    per = hq // cache.shape[1]
+    for b in range(len(seq_lens)):
+        lo, hi, size = int(offsets[b]), int(offsets[b + 1]), int(seq_lens[b])
+        for g in range(cache.shape[1] if hi > lo else 0):
+            (kc, ks, kl), (vc, vs, vl) = (held(cache, table[b], size, g, page, d, group, kv) for kv in (0, 1))
+            k, v = kl + ks * kc, vl + vs * vc
+            for t in range(lo, hi):
+                seen = max(0, size - (hi - lo) + (t - lo) + 1) if causal else size
+                n[t] = seen
+                for h in range(g * per, (g + 1) * per):
+                    if seen == 0:
+                        out[t, h] = 0.0
+                        continue
+                    s = k[:seen] @ q[t, h] / np.sqrt(d)
+                    p = np.exp(s - s.max())
+                    p /= p.sum()
+                    out[t, h] = p @ v[:seen]
+                    score[t, h] = ((15 * ks + np.abs(kl))[:seen] @ np.abs(q[t, h])).max() / np.sqrt(d)
+                    mean[t, h] = p @ vs[:seen]
+                    most[t, h] = (15 * vs + np.abs(vl))[:seen].max(0)
+    return out, score, mean, most, n

@@ -74,3 +74,21 @@ def attend_tol(ref, terms, d, dtype):
     if dtype == "f32":
         tol = tol + 2.0 ** -21 * a * v
     return tol + E24 * (8 * math.sqrt(d) * a + 8 * np.sqrt(np.maximum(n, 1)) + 16) * v
+
+
+def column_tol(terms, q, key_step, d, dtype):
+    """By column, so that a group of small values is held to its own size. S: attention over the column's steps, V: the
+    largest 15 step + |lowest| seen there, A: score's terms, n: keys (oracle.kv4.column_terms); key_step: the keys' largest.
+      the output's own rounding         u |ref|
+      weights times step, with codes less 8 (8 at most)
+                                        8 S 2^-11 (bf16: fp16's rounding, 2^-11) or 8 S 2^-22 (fp32: two parts), and below
+                                        2^-14 off by 2^-25 at most where the largest W is at least 2^4: 8 n 2^-29 S
+      fp32 queries in two parts         2^-22 A in the exponent, on both sides of the quotient: 2 2^-22 A V
+      bf16 products with keys' codes    `cuts`
+      fp32 sums                         2^-24 (8 sqrt(d) A + 8 sqrt(n) + 16) V
+    and 2^-120 where a step is so small that its weights reach beyond fp32's range."""
+    ref, score, mean, most, n = terms
+    a, n = score[..., None], n[:, None, None]
+    tol = U[dtype] * np.abs(ref) + 8 * mean * ((2.0 ** -11 if dtype == "bf16" else 2.0 ** -22) + n * 2.0 ** -29) + 2.0 ** -120
+    tol = tol + (cuts(np.abs(q).max(-1)[..., None], key_step, most, d) if dtype == "bf16" else 2.0 ** -21 * a * most)
+    return tol + E24 * (8 * math.sqrt(d) * a + 8 * np.sqrt(np.maximum(n, 1)) + 16) * most

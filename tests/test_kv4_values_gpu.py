@@ -1,0 +1,76 @@
+"""GPU tests of dense_extend_kv4 over values of unequal and extreme sizes, against the fp64 oracle column by column
+(kv4_harness.column_tol): flat groups, of step 0, of any size; groups of a head that differ."""
+import numpy as np
+import pytest
+
+from cache_ops_harness import rounded
+from kv4_harness import Pool4, column_tol
+from oracle import kv4 as Q
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import kv_cache_early_gb300 as K  # noqa: E402
+
+
+def run(pool, q, off, causal, hq):
+    shape = K.make_shape(**pool.shape(hq))
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    tq = dev(q).to(torch.bfloat16 if pool.dtype == "bf16" else torch.float32)
+    out = torch.full_like(tq, 7.75)
+    ws = torch.full((K.dense_extend_kv4_min_workspace_bytes(shape, len(q), pool.group),), 0xA5, dtype=torch.uint8, device="cuda")
+    K.dense_extend_kv4(tq, dev(pool.bytes), dev(pool.table), dev(pool.seq_lens), None if off is None else dev(off), out, shape,
+                       ws, group=pool.group, causal=causal)
+    torch.cuda.synchronize()
+    assert K.art_read_device_status(ws) == 0
+    return out.double().cpu().numpy()
+
+
+def case(seed, dtype, d, group, lens, value, new=None, key=None, hq=4, page=16):
+    """value, key: rows of (rng, sequence, token); new None: a decode step."""
+    rng = np.random.default_rng(seed)
+    pool = Pool4(rng, dtype, 1, d, page, group, lens)
+    for b, n in enumerate(lens):
+        for t in range(n):
+            pool.put(b, t, 0, 0, rounded(rng.standard_normal(d) if key is None else key(rng, b, t), dtype))
+            pool.put(b, t, 0, 1, rounded(np.broadcast_to(value(rng, b, t), d), dtype))
+    off = np.concatenate([[0], np.cumsum([1] * len(lens) if new is None else new)]).astype(np.int32)
+    q = rounded(rng.standard_normal((off[-1], hq, d)) if key is None else np.ones((off[-1], hq, d)), dtype)
+    got = run(pool, q, None if new is None else off, new is not None, hq)
+    terms = Q.column_terms(q, pool.bytes, pool.table, pool.seq_lens, off, new is not None, page, group)
+    step = max(Q.held(pool.bytes, pool.table[b], n, 0, page, d, group, 0)[1].max() for b, n in enumerate(lens) if n)
+    tol = column_tol(terms, q, step, d, dtype)
+    err = np.abs(got - terms[0])
+    assert np.all(err <= tol), (np.nanmax(err / tol), np.argwhere(~(err <= tol))[:4])
+
+
+BOTH = pytest.mark.parametrize("dtype", ["bf16", "f32"])
+
+
+def rising(by):
+    """Keys whose scores against a query of ones rise by `by` (in log2) from token to token; flat, so that they are held
+    exactly enough."""
+    def key(rng, b, t):
+        return np.full(64, by * t / 64 ** 0.5 / 1.4426950408889634)
+    return key
+
+
+@BOTH
+@pytest.mark.parametrize("size", [2.0 ** 26, 2.0 ** 44, -2.0 ** 44, 2.0 ** 100, -2.0 ** 126])
+def test_flat_rows_of_any_size(dtype, size):
+    """Values of one number: attention over them is that number, however large."""
+    case(1, dtype, 64, 32, [1, 40, 300], lambda rng, b, t: size)
+    case(2, dtype, 64, 64, [700], lambda rng, b, t: size * (0.5 + (t % 2) / 2))
+    case(3, dtype, 128, 32, [9, 150], lambda rng, b, t: size, new=[9, 5])
+    case(4, dtype, 64, 32, [600], lambda rng, b, t: size, key=rising(0.1))
+    case(5, dtype, 64, 32, [40], lambda rng, b, t: size, key=rising(14.0))
+
+
+@BOTH
+def test_flat_rows_beside_small_steps(dtype):
+    """A large group without steps, beside one whose steps are very small, and rows of both kinds in turn."""
+    half = np.arange(64) < 32
+    case(6, dtype, 64, 32, [1, 200], lambda rng, b, t: np.where(half, 2.0 ** 60, rng.standard_normal(64) * 2.0 ** -80))
+    case(7, dtype, 64, 32, [1, 200], lambda rng, b, t: np.where(half, 2.0 ** 100, rng.standard_normal(64) * 2.0 ** -92),
+         new=[1, 4])
+    case(8, dtype, 64, 32, [300], lambda rng, b, t: 2.0 ** 44 if t % 3 else rng.standard_normal(64))
