@@ -11,8 +11,9 @@
 namespace art {
 
 // Cost units of items and of their tiles of 128 keys, by rows (8, more). Five drafts of 16 sequences (20 rows of 4 heads,
-// 16 and 4): tiles of 16 rows at 5, 6, 8, 10, 14 units 71.2, 68.0, 65.4, 68.0, 71.7 us.
-constexpr CostRule kCostKv4 = {13, 5, 20, 8, 20, 8};
+// 16 and 4): tiles of 16 rows at 5, 6, 8, 10, 14 units 71.2, 68.0, 65.4, 68.0, 71.7 us (items at 20); at 8 and 10 units with
+// items at 32 65.8 and 67.7; items at 20 67.6, at 44 68.2. 64 decoding sequences: items at 13, 17, 21 units 66.0, 65.8, 66.4 us.
+constexpr CostRule kCostKv4 = {17, 5, 32, 8, 32, 8};
 
 static void kv4_shape(AttendParams& p, const art_shape& s) {
     attend_shape(p, s);

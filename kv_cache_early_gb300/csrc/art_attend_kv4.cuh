@@ -21,9 +21,10 @@
 // take a second part for what is left, and split the queries too, so about 22 bits). Scores,
 // weights, their sums and what is multiplied by low are fp32.
 //
-// Range: a row has two references. The weights' own, R, follows the scores: weights stay below 2^-12, so that sums of
-// weights times lowest stay finite whatever is held. W's, a power of two F beside it (W = p F step), follows the maximum
-// of score + log2(step), so that W stays within fp16's range; values without a step need no W. The row's sum l is
+// Range: a row has a reference for its weights and one for each group's W. The weights' own, R, follows the scores:
+// weights stay below 2^-12, so that sums of weights times lowest stay finite whatever is held. W's, a power of two F
+// beside it (W = p F step), follows the maximum of score + log2(the group's step), so that W stays within fp16's range and
+// keeps its bits in every group, however small beside the others; values without a step need no W. The row's sum l is
 // brought to [2^-10, 2^-9) before parts meet, so that their sums are finite too. Queries are scaled by a power of two to
 // fp16's range.
 //
@@ -40,9 +41,9 @@
 // Keys and values outside a segment's keys may be anything: codes are always finite numbers, and
 // scales of keys that a row does not see are not used for it.
 //
-// Measured on a GB300 (32/8 heads, d 128, pages of 16, groups of 64): 64 sequences of 1 to 8192 tokens 65 us a call, the
+// Measured on a GB300 (32/8 heads, d 128, pages of 16, groups of 64): 64 sequences of 1 to 8192 tokens 66 us a call, the
 // cache's bytes at 5.0 TB/s while the main kernel streams; 8 sequences of 30k to 131k (28/4 heads, pages of 64, groups of
-// 128) 79 us, 5.8 TB/s. 16 keys of 8 rows take about 230 instructions of a warp (70 to take codes apart, 32 to centre,
+// 128) 81 us, 5.7 TB/s. 16 keys of 8 rows take about 230 instructions of a warp (70 to take codes apart, 32 to centre,
 // 16 products), which 12 warps issue in 0.47 us a tile of 128 keys; its bytes take 0.42. What made it fast, in order:
 //   producer lanes side by side instead of a tile after the other      88 -> 80 us (64 sequences)
 //   helper warps that sleep, masks only in steps with an edge, 2^10 from a register  80 -> 74
@@ -103,6 +104,7 @@ struct alignas(16) Kv4Ctrl {
         int lim[kRowsKv4];
     } rows[2];
     float2 ml[kCons][8];
+    float f[NG < 4 || kCons > 8 ? 1 : kCons][2 * NG][8];  // F of a warp's rows, fp32 (Kv4Consumer::rows)
     int abort, seg0, seg1;
 };
 
@@ -152,6 +154,14 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t r;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a));
     return r;
+}
+__device__ __forceinline__ uint64_t lds64(uint32_t a) {
+    uint64_t r;
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint64_t v) {
+    asm volatile("st.shared.b64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 __device__ __forceinline__ void lds128(uint32_t a, uint32_t (&r)[4]) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
@@ -449,7 +459,6 @@ template <bool kBF16, int D, int NG, int kCons>
 struct Kv4Consumer {
     using C = Kv4Cfg<kBF16, D, NG, kCons>;
     static constexpr int NC = C::NC, CPG = NC / NG, KP = C::KP;
-    static constexpr int NF = 1;  // factors of W of a row
     const AttendKv4Params& pp;
     const AttendParams& p;
     Kv4Ctrl<C::NS, NG, kCons>* c;
@@ -514,14 +523,19 @@ struct Kv4Consumer {
             for (int k = 0; k < KP; ++k)
 #pragma unroll
                 for (int ch = 0; ch < NC; ++ch) lds128(qaddr + (k * NC + ch) * 512, qr[k][ch]);
-        uint64_t F2[NT], qs2[NT][NG];  // of rows 2 tq and 2 tq + 1
+        // Of several new tokens and four groups the queries' sums, and in fp32 the factors F, are read from shared memory.
+        // Five drafts of 16 sequences, a pass in a graph: bf16 75.2 us with the sums in registers, 65.9 so, 3 more with F read
+        // too; fp32 123 with F in registers, 101 so.
+        constexpr bool kSums = NG < 4 || kCons > 8, kFRegs = kSums || kBF16;
+        uint64_t F2[NT], qs2[kSums ? NT : 1][kSums ? NG : 1];  // of rows 2 tq and 2 tq + 1
+        const uint32_t sum_addr = smem_addr(&c->rows[buf].sum[0][2 * tq]);
         int lim[NT][2], khi = sg.k0, klo = sg.k1;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = n * 8 + 2 * tq;
             F2[n] = *reinterpret_cast<const uint64_t*>(&c->rows[buf].f[r]);
 #pragma unroll
-            for (int g = 0; g < NG; ++g) qs2[n][g] = *reinterpret_cast<const uint64_t*>(&c->rows[buf].sum[g][r]);
+            for (int g = 0; g < (kSums ? NG : 0); ++g) qs2[n][g] = *reinterpret_cast<const uint64_t*>(&c->rows[buf].sum[g][r]);
             lim[n][0] = c->rows[buf].lim[r];
             lim[n][1] = c->rows[buf].lim[r + 1];
             // keys from khi on nobody sees; those below klo everybody (of the rows that are there)
@@ -535,7 +549,8 @@ struct Kv4Consumer {
         klo = __reduce_min_sync(0xffffffffu, klo);
 
         float R[NT][2], l[NT][2], o[NT][2 * NC][4];
-        uint64_t L2[NT][NG], W2[NT][NF];  // of rows 2 tq, 2 tq + 1: sums of weights times lowest; F
+        const uint32_t f_addr = smem_addr(&c->f[kFRegs ? 0 : w][0][2 * tq]);
+        uint64_t L2[NT][NG], W2[kFRegs ? NT : 1][kFRegs ? NG : 1];  // of rows 2 tq, 2 tq + 1: sums of weights times lowest; F
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -546,10 +561,15 @@ struct Kv4Consumer {
 #pragma unroll
             for (int g = 0; g < NG; ++g) L2[n][g] = 0;
 #pragma unroll
-            for (int g = 0; g < NF; ++g) W2[n][g] = pk2(pow2i(kMostFactor), pow2i(kMostFactor));
+            for (int g = 0; g < NG; ++g) {
+                const uint64_t f = pk2(pow2i(kMostFactor), pow2i(kMostFactor));
+                if constexpr (kFRegs) W2[n][g] = f;
+                else if (gq == 0) sts64(f_addr + (n * NG + g) * 32, f);
+            }
 #pragma unroll
             for (int k = 0; k < 2 * NC; ++k) o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
         }
+        __syncwarp();
         // the octets of this warp's 32 keys in a tile, two to each 16 keys: its bytes of the keys' codes, and its
         // keys' scales; the second 16 keys lie dk, ds bytes on whatever the slab
         uint32_t kc[2], sc[2], dk, ds;
@@ -613,6 +633,10 @@ struct Kv4Consumer {
                                 mma_f16(acc[k][n], a1[0], a1[2], a1[1], a1[3], q4[2], q4[3]);
                             }
                     }
+                    uint64_t sum2[kSums ? 1 : NT];
+                    if constexpr (!kSums)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) sum2[n] = lds64(sum_addr + (g * kRowsKv4 + n * 8) * 4);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float step = bf16_lo_f(pk[i][g]);
@@ -625,9 +649,9 @@ struct Kv4Consumer {
                                 x += acc[1][n][2 * i];
                                 y += acc[1][n][2 * i + 1];
                             }
-                            const uint64_t a2 = pk2(x, y);
+                            const uint64_t a2 = pk2(x, y), qs = kSums ? qs2[kSums ? n : 0][kSums ? g : 0] : sum2[kSums ? 0 : n];
                             tot[n][i] = g == 0 ? mul2(a2, step2) : fma2(a2, step2, tot[n][i]);
-                            lo2[n][i] = g == 0 ? mul2(low2, qs2[n][g]) : fma2(low2, qs2[n][g], lo2[n][i]);
+                            lo2[n][i] = g == 0 ? mul2(low2, qs) : fma2(low2, qs, lo2[n][i]);
                         }
                     }
                 }
@@ -652,9 +676,13 @@ struct Kv4Consumer {
             // Weights, and weights times steps, against the references as they are; where one goes too far, the
             // references move and they are formed once more.
             float pr[KM][NT][4];
+            auto factor = [&](int n, int g) -> uint64_t {
+                if constexpr (kFRegs) return W2[n][g];
+                else return lds64(f_addr + (n * NG + g) * 32);
+            };
             auto weight = [&](int m, int n, int g, int i, float p0, float p1, float& w0, float& w1) {
                 const float step = bf16_lo_f(pv[m][i][g]);
-                up2(mul2(mul2(pk2(p0, p1), W2[n][NF == 1 ? 0 : g]), pk2(step, step)), w0, w1);
+                up2(mul2(mul2(pk2(p0, p1), factor(n, g)), pk2(step, step)), w0, w1);
                 if constexpr (!whole) {  // scales that a row does not see may be no numbers
                     if (!vis[m][n][2 * i]) w0 = 0.f;
                     if (!vis[m][n][2 * i + 1]) w1 = 0.f;
@@ -704,25 +732,21 @@ struct Kv4Consumer {
                     for (int g = 0; g < NG; ++g) L2[n][g] = mul2(L2[n][g], pk2(a[0], a[1]));
                     // F: up with R, which leaves W as it is, and down where the largest W would be too large
 #pragma unroll
-                    for (int g = 0; g < NF; ++g) {
+                    for (int g = 0; g < NG; ++g) {
                         float top[2] = {0.f, 0.f};  // weight times step
 #pragma unroll
                         for (int m = 0; m < KM; ++m)
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                uint32_t x = pv[m][i][g] << 16;
-#pragma unroll
-                                for (int k = 1; k < (NF == 1 ? NG : 1); ++k) x = max(x, pv[m][i][k] << 16);
+                            for (int i = 0; i < 2; ++i)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e)
                                     if (whole || vis[m][n][2 * i + e])
-                                        top[e] = fmaxf(top[e], ex2(s[m][n][2 * i + e] - R[n][e]) * __uint_as_float(x));
-                            }
+                                        top[e] = fmaxf(top[e], ex2(s[m][n][2 * i + e] - R[n][e]) * bf16_lo_f(pv[m][i][g]));
                         uint32_t both = pack_bf16(top[0], top[1]);
 #pragma unroll
                         for (int k = 4; k <= 16; k <<= 1) both = max_s16(both, __shfl_xor_sync(0xffffffffu, both, k));
                         float f[2], fix[2];
-                        up2(W2[n][g], f[0], f[1]);
+                        up2(factor(n, g), f[0], f[1]);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int x = e ? both >> 23 : both >> 7 & 255u;  // its exponent
@@ -732,9 +756,14 @@ struct Kv4Consumer {
                             fix[e] = ex2((float)by - up[e]);  // 1 where W stays
                             f[e] = now;
                         }
-                        W2[n][g] = pk2(f[0], f[1]);
+                        if constexpr (kFRegs) W2[n][g] = pk2(f[0], f[1]);
+                        else {
+                            __syncwarp();
+                            if (gq == 0) sts64(f_addr + (n * NG + g) * 32, pk2(f[0], f[1]));
+                            __syncwarp();
+                        }
 #pragma unroll
-                        for (int k = NF == 1 ? 0 : 2 * CPG * g; k < (NF == 1 ? 2 * NC : 2 * CPG * (g + 1)); ++k) {
+                        for (int k = 2 * CPG * g; k < 2 * CPG * (g + 1); ++k) {
                             o[n][k][0] *= fix[0];
                             o[n][k][1] *= fix[1];
                             o[n][k][2] *= fix[0];
@@ -854,11 +883,14 @@ struct Kv4Consumer {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if (n * 8 >= sg.nrow) break;
-            float fa[NF][2], L[NG][2];
+            float fa[NG][2], L[NG][2];
 #pragma unroll
             for (int g = 0; g < NG; ++g) up2(L2[n][g], L[g][0], L[g][1]);
 #pragma unroll
-            for (int g = 0; g < NF; ++g) up2(W2[n][g], fa[g][0], fa[g][1]);
+            for (int g = 0; g < NG; ++g) {
+                if constexpr (kFRegs) up2(W2[n][g], fa[g][0], fa[g][1]);
+                else up2(lds64(f_addr + (n * NG + g) * 32), fa[g][0], fa[g][1]);
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float sum = l[n][e];
@@ -868,7 +900,7 @@ struct Kv4Consumer {
                 const int k = min(max((int)((__float_as_uint(sum) >> 23) & 255u) - 127 + 10, -100), 120);
                 const float f = sum > 0.f ? pow2i(-k) : 1.f;
 #pragma unroll
-                for (int g = 0; g < NF; ++g) fa[g][e] = f * __uint_as_float((254u << 23) - __float_as_uint(fa[g][e]));  // f / F
+                for (int g = 0; g < NG; ++g) fa[g][e] = f * __uint_as_float((254u << 23) - __float_as_uint(fa[g][e]));  // f / F
                 l[n][e] = sum * f;
                 R[n][e] += sum > 0.f ? (float)k : 0.f;
 #pragma unroll
@@ -890,7 +922,7 @@ struct Kv4Consumer {
                 float* row = reinterpret_cast<float*>(gen + C::EXOFF) + (w * 8 + 2 * tq + e) * C::EXROW + gq * 4;
 #pragma unroll
                 for (int ch = 0; ch < NC; ++ch) {
-                    const float lw = L[ch / CPG][e], f = fa[NF == 1 ? 0 : ch / CPG][e], f16 = f * 0.0625f;
+                    const float lw = L[ch / CPG][e], f = fa[ch / CPG][e], f16 = f * 0.0625f;
                     *reinterpret_cast<float4*>(row + ch * 32) =
                         make_float4(fmaf(o[n][2 * ch][e], f, lw), fmaf(o[n][2 * ch][2 + e], f16, lw),
                                     fmaf(o[n][2 * ch + 1][e], f, lw), fmaf(o[n][2 * ch + 1][2 + e], f16, lw));

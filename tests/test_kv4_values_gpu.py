@@ -74,3 +74,46 @@ def test_flat_rows_beside_small_steps(dtype):
     case(7, dtype, 64, 32, [1, 200], lambda rng, b, t: np.where(half, 2.0 ** 100, rng.standard_normal(64) * 2.0 ** -92),
          new=[1, 4])
     case(8, dtype, 64, 32, [300], lambda rng, b, t: 2.0 ** 44 if t % 3 else rng.standard_normal(64))
+
+
+def sized(ratio, d, group):
+    """Sizes by column: groups 2^ratio apart around 1."""
+    n = d // group
+    return 2.0 ** (ratio * ((n - 1) / 2 - np.arange(d) // group))
+
+
+@BOTH
+@pytest.mark.parametrize("ratio", [8, 16, 24, 60])
+def test_groups_of_unequal_size(dtype, ratio):
+    """Every group of a head keeps its own bits."""
+    for d, group, seed in ((64, 32, 20), (128, 64, 21), (128, 32, 22)):
+        size = sized(ratio, d, group)
+        case(seed, dtype, d, group, [1, 77, 200], lambda rng, b, t: rng.standard_normal(d) * size)
+        case(seed + 10, dtype, d, group, [3, 150], lambda rng, b, t: rng.standard_normal(d) * size, new=[3, 5])
+
+
+@BOTH
+@pytest.mark.parametrize("ratio", [16, 40])
+def test_groups_whose_sizes_change_from_token_to_token(dtype, ratio):
+    """The large group is another one from token to token; and, once, far into the sequence."""
+    def turns(rng, b, t):
+        return rng.standard_normal(128) * np.where(np.arange(128) // 32 == t % 4, 2.0 ** ratio, 1.0)
+
+    def once(rng, b, t):
+        return rng.standard_normal(64) * np.where((np.arange(64) < 32) & (t == 130), 2.0 ** ratio, 1.0)
+    case(40, dtype, 128, 32, [150], turns)
+    case(41, dtype, 64, 32, [200, 131], once)
+    case(42, dtype, 64, 32, [140], once, new=[15])  # rows that see it and rows that do not, in one item
+
+
+@BOTH
+def test_large_group_of_little_weight(dtype):
+    """A token whose second group is large and whose weight is as much smaller: the others' bits stay in both groups."""
+    def key(rng, b, t):
+        return np.full(64, (-40.0 if t in (0, 70) else 0.02 * t) / 64 ** 0.5 / 1.4426950408889634)
+
+    def value(rng, b, t):
+        return rng.standard_normal(64) * np.where((np.arange(64) >= 32) & (t in (0, 70)), 2.0 ** 30, 1.0)
+    # seen by its tolerance only where V is small: the first group's columns
+    case(43, dtype, 64, 32, [100], value, key=key)
+    case(44, dtype, 64, 32, [90], value, new=[4], key=key)
