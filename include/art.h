@@ -461,7 +461,8 @@ int art_read_kv4(const void* cache, int32_t group, const int32_t* block_table, c
  * dense_extend over such a cache. q_offsets NULL: one new token for each sequence,
  * which sees all of its keys (a decode step), num_tokens = batch.
  *   workspace  dense_extend_kv4_workspace_bytes(shape, num_tokens, group) bytes
- *              (0: sizes beyond the supported range)
+ *              (0: sizes beyond the supported range); it serves calls of this shape with
+ *              fewer tokens too, decode steps among them
  * Paths (dense_extend_kv4_path): 0 attends over the codes; 1, for prompt chunks in
  * bf16 (with q_offsets, num_tokens * G of 96 * batch and num_tokens * num_q_heads of
  * 2048 or more), reads the cache of the sequences with new tokens back into the workspace, as art_read_kv4 does, and

@@ -84,9 +84,8 @@ static size_t kv4_bytes(const art_shape* shape, int32_t num_tokens, int32_t grou
     Kv4Workspace w = kv4_workspace(*shape, num_tokens, true);
     if (w.codes == 0) return 0;
     size_t need = !least && w.whole > w.codes ? w.whole : w.codes;
-    if (num_tokens == shape->batch) {  // a call without offsets
-        w = kv4_workspace(*shape, num_tokens, false);
-        if (w.codes == 0) return 0;
+    if (num_tokens >= shape->batch) {  // a call without offsets has no more tokens: room for it too, where it is supported
+        w = kv4_workspace(*shape, shape->batch, false);
         if (w.codes > need) need = w.codes;
     }
     return need;

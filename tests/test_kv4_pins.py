@@ -181,3 +181,14 @@ def test_binding_refuses_tensors_on_the_host():
         K.dense_extend_kv4(torch.zeros(2, 8, 128), cache, None, None, None, None, s, cache, group=64)
     with pytest.raises(K.ArtError, match="4 bits"):
         K.art_read_kv4(cache, None, None, None, None, None, s, cache, group=40)
+
+
+@pytest.mark.parametrize("size", [K.dense_extend_kv4_workspace_bytes, K.dense_extend_kv4_min_workspace_bytes])
+@pytest.mark.parametrize("batch", [1, 7, 128])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_a_workspace_serves_calls_with_fewer_tokens(lib, size, batch, dtype):
+    """Its bytes never fall as the tokens rise, the call without offsets (a decode step of the batch) among them."""
+    for heads in ((32, 8), (8, 1)):
+        s = good_shape(batch=batch, num_q_heads=heads[0], num_kv_heads=heads[1], dtype=dtype)
+        sizes = [size(s, t, 64) for t in [*range(2 * batch + 3), 5 * batch, 64 * batch, 96 * batch, 1000 * batch]]
+        assert sizes == sorted(sizes) and sizes[0] > 0
