@@ -204,6 +204,7 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& scal
     // (d + de) / 15 = q + rest / 15: the quotient by a rounded 1 / 15, corrected once
     const float b = __fadd_rn(d, -mx);
     const float de = __fadd_rn(__fadd_rn(mx, -__fadd_rn(d, -b)), -__fadd_rn(low, b));
+    const bool fine = d < kMaxRange || (d == kMaxRange && de < 0.f);  // the exact span is below it
     constexpr float kFifteenth = 0.0666666701f;
     const float q0 = __fmul_rn(d, kFifteenth), q = fmaf(fmaf(-15.f, q0, d), kFifteenth, q0);
     const float rest = fmaf(-15.f, q, d) + de;
@@ -238,7 +239,7 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& scal
     const float lo4 = fmaf(r[3], 4096.f, fmaf(r[2], 256.f, fmaf(r[1], 16.f, r[0])));
     const float hi4 = fmaf(r[7], 4096.f, fmaf(r[6], 256.f, fmaf(r[5], 16.f, r[4])));
     const uint32_t codes = (__float_as_uint(lo4 + 8388608.f) & 0xffffu) | (__float_as_uint(hi4 + 8388608.f) << 16);
-    if (!(d < kMaxRange)) {
+    if (!fine) {
         scales = 0x7fc00000u;
         return 0u;
     }
