@@ -449,7 +449,7 @@ int art_append_kv4(const void* q, const void* k, const void* v, int64_t q_stride
  *              Two sequences must not share a page of the output.
  *   workspace  art_read_kv4_workspace_bytes(shape) bytes: the status word
  * One kernel. Supported: a table row's tokens up to 2^30, with out_table those of all
- * rows up to 2^33.
+ * rows up to 2^33; these, or num_tokens, times num_kv_heads up to 2^40.
  */
 size_t art_read_kv4_workspace_bytes(const art_shape* shape);
 int art_read_kv4(const void* cache, int32_t group, const int32_t* block_table, const int32_t* seq_lens,

@@ -303,10 +303,10 @@ int art_read_kv4(const void* cache, int32_t group, const int32_t* block_table, c
     auto bad = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) != 0; };
     if (bad(cache) || bad(k_out) || bad(v_out) || bad(workspace)) return ART_ERR_INVALID_ARG;
     if (!kv4_group_ok(s.head_dim, group)) return ART_ERR_UNSUPPORTED;
-    // counts of 8-token units have 32 bits
-    if ((long long)s.max_pages_per_seq * s.page_size > (1LL << 30) ||
-        (out_table && (long long)s.batch * s.max_pages_per_seq * s.page_size > (1LL << 33)))
-        return ART_ERR_UNSUPPORTED;
+    // counts of 8-token units have 32 bits, and so do a CTA's units times heads
+    const long long row = (long long)s.max_pages_per_seq * s.page_size;
+    if (row > (1LL << 30) || (out_table && s.batch * row > (1LL << 33))) return ART_ERR_UNSUPPORTED;
+    if ((out_table ? s.batch * row : (long long)num_tokens) > (1LL << 40) / s.num_kv_heads) return ART_ERR_UNSUPPORTED;
     if (workspace_bytes < sizeof(WsHeader)) return ART_ERR_WORKSPACE;
     int dev = 0, sms = 0;
     cudaError_t e;

@@ -192,3 +192,13 @@ def test_a_workspace_serves_calls_with_fewer_tokens(lib, size, batch, dtype):
         s = good_shape(batch=batch, num_q_heads=heads[0], num_kv_heads=heads[1], dtype=dtype)
         sizes = [size(s, t, 64) for t in [*range(2 * batch + 3), 5 * batch, 64 * batch, 96 * batch, 1000 * batch]]
         assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+def test_read_refuses_tokens_times_heads_beyond_2_40(lib):
+    """2^33 tokens of a table's rows times 128 heads, at the limit and above it."""
+    def at(heads):
+        s = good_shape(batch=32, num_q_heads=heads, num_kv_heads=heads, page_size=4096, max_pages_per_seq=1 << 16)
+        return read(lib, s, out_table=FAKE, out_pages=3, off=0, T=0, ws_bytes=0)  # refused for its workspace at the latest
+    assert at(128) == WS and at(129) == UNS
+    s = good_shape(num_q_heads=1024, num_kv_heads=1024)
+    assert read(lib, s, T=1 << 30, ws_bytes=0) == WS and read(lib, s, T=(1 << 30) + 1, ws_bytes=0) == UNS
