@@ -8,10 +8,11 @@
 //     code   = the whole number nearest to (x - lowest) / step, 15 at most
 // with ties to even, all as in exact arithmetic. So the cache holds the same bits on any machine
 // and a test can ask for equality; a border between two codes moves by nothing. What that takes:
-//   - the angle's sine and cosine as sums of two fp32 numbers (turn_exact, within 1e-11), the
+//   - the angle's sine and cosine as sums of two fp32 numbers (turn_exact, within 1e-11 where
+//     position and angle are below 2^24; beyond, the angle is 64-bit arithmetic's, within 2e-16 of its size), the
 //     products x cos and y sin with their rounding errors (by the fused product) and the sum with
 //     its own (Knuth's two-sum): the turned key's rounding to fp32, and from there to bf16, is
-//     then the exact one's but for about one value in 10^8;
+//     then the exact one's but for about one value in 10^8 (below 2^24);
 //   - x - lowest with its rounding error, and where the quotient by the rounded 1 / step comes
 //     near a border, the sign of (x - lowest) - border * step, whose terms are exact (a border is
 //     a half-integer up to 15, step has 8 bits).
