@@ -24,9 +24,9 @@
 // Range: a row has a reference for its weights and one for each group's W. The weights' own, R, follows the scores:
 // weights stay below 2^-12, so that sums of weights times lowest stay finite whatever is held. W's, a power of two F
 // beside it (W = p F step), follows the maximum of score + log2(the group's step), so that W stays within fp16's range and
-// keeps its bits in every group, however small beside the others; values without a step need no W. The row's sum l is
-// brought to [2^-10, 2^-9) before parts meet, so that their sums are finite too. Queries are scaled by a power of two to
-// fp16's range.
+// keeps its bits in every group, however small beside the others; values without a step need no W. Parts meet with R
+// and the sums as they are: a sum's exponent added to R would be lost where scores are beyond 2^24. Queries are scaled by a
+// power of two to fp16's range.
 //
 // One CTA per SM, of 16 (decode) or 12 warps, which meet at barriers in shared memory only:
 //   2 producers: page ids 32 at a time, one bulk copy for each slab of a page (art_kv4.cuh), into a ring of
@@ -893,22 +893,13 @@ struct Kv4Consumer {
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float sum = l[n][e];
 #pragma unroll
-                for (int k = 4; k <= 16; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-                // sums of any size come to [2^-10, 2^-9)
-                const int k = min(max((int)((__float_as_uint(sum) >> 23) & 255u) - 127 + 10, -100), 120);
-                const float f = sum > 0.f ? pow2i(-k) : 1.f;
-#pragma unroll
-                for (int g = 0; g < NG; ++g) fa[g][e] = f * __uint_as_float((254u << 23) - __float_as_uint(fa[g][e]));  // f / F
-                l[n][e] = sum * f;
-                R[n][e] += sum > 0.f ? (float)k : 0.f;
+                for (int k = 4; k <= 16; k <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], k);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    float x = L[g][e];
+                    fa[g][e] = __uint_as_float((254u << 23) - __float_as_uint(fa[g][e]));  // 1 / F
 #pragma unroll
-                    for (int k2 = 4; k2 <= 16; k2 <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k2);
-                    L[g][e] = x * f;
+                    for (int k = 4; k <= 16; k <<= 1) L[g][e] += __shfl_xor_sync(0xffffffffu, L[g][e], k);
                 }
             }
             if (ex_used) {

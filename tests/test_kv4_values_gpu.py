@@ -117,3 +117,32 @@ def test_large_group_of_little_weight(dtype):
     # seen by its tolerance only where V is small: the first group's columns
     case(43, dtype, 64, 32, [100], value, key=key)
     case(44, dtype, 64, 32, [90], value, new=[4], key=key)
+
+
+@BOTH
+@pytest.mark.parametrize("size", [2.0 ** 24, 2.0 ** 40])
+@pytest.mark.parametrize("new", [None, 5])
+def test_scores_far_below_zero(dtype, size, new):
+    """Large queries against keys whose every score is large and negative: the nearest key, or the mean of equal ones."""
+    d, hq, page, group, n = 64, 4, 16, 32, 37
+    rng = np.random.default_rng(60)
+    pool = Pool4(rng, dtype, 1, d, page, group, [n, n])
+    for b in range(2):
+        for t in range(n):
+            # flat keys, held exactly: all alike in the first sequence; in the second one nearer than the others from token 3 on
+            pool.put(b, t, 0, 0, np.full(d, -4.0 if b == 0 else -2.0 if t == 3 else -4.0 - t))
+            pool.put(b, t, 0, 1, rounded(rng.standard_normal(d), dtype))
+    off = np.array([0, 1, 2] if new is None else [0, new, 2 * new], np.int32)
+    got = run(pool, np.full((off[-1], hq, d), size), None if new is None else off, new is not None, hq)
+    for b in range(2):
+        _, step, low = Q.held(pool.bytes, pool.table[b], n, 0, page, d, group, 1)
+        code = Q.held(pool.bytes, pool.table[b], n, 0, page, d, group, 1)[0]
+        v = low + step * code
+        for i in range(off[b + 1] - off[b]):
+            seen = n if new is None else n - new + i + 1
+            ref = v[:seen].mean(0) if b == 0 else v[3]
+            s = step[:seen].mean(0) if b == 0 else step[3]
+            # the output's rounding, weights' (equal: 2^-11 or 2^-22 of 8 steps) and fp32 sums of at most n values
+            u, w = (2.0 ** -8, 2.0 ** -11) if dtype == "bf16" else (2.0 ** -24, 2.0 ** -22)
+            tol = u * np.abs(ref) + 8 * w * s + (8 * n ** 0.5 + 16) * 2.0 ** -24 * (15 * step + np.abs(low))[:seen].max(0)
+            assert np.all(np.abs(got[off[b] + i] - ref) <= tol), (b, i, np.max(np.abs(got[off[b] + i] - ref) / tol))
