@@ -69,7 +69,7 @@ constexpr uint32_t kMostW = 0x7400u;  // 2^14 in fp16
 constexpr float kWeightLift = 20.f;
 constexpr float kMostWeight = 0x1p-12f;
 constexpr int kMostFactor = 126;        // F = 2^126 at most: its inverse is a normal number
-constexpr float kNoReference = -1e30f;  // of a row that has seen no key: any key's weight passes the limit
+constexpr float kNoReference = -3.40282347e38f;  // of a row that has seen no key, no score is lower: any key's weight passes the limit
 
 struct AttendKv4Params {
     AttendParams a;

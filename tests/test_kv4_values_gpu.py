@@ -120,10 +120,10 @@ def test_large_group_of_little_weight(dtype):
 
 
 @BOTH
-@pytest.mark.parametrize("size", [2.0 ** 24, 2.0 ** 40])
+@pytest.mark.parametrize("size", [2.0 ** 24, 2.0 ** 40, 2.0 ** 99])
 @pytest.mark.parametrize("new", [None, 5])
 def test_scores_far_below_zero(dtype, size, new):
-    """Large queries against keys whose every score is large and negative: the nearest key, or the mean of equal ones."""
+    """Queries of up to 2^99 against keys whose every score is large and negative: the nearest key, or the mean of equal ones."""
     d, hq, page, group, n = 64, 4, 16, 32, 37
     rng = np.random.default_rng(60)
     pool = Pool4(rng, dtype, 1, d, page, group, [n, n])
