@@ -8,7 +8,7 @@
 // eight codes of a 32-bit word become four operand registers by four masks and a shift: the keys'
 // of bf16 calls; 2^24 and the 16 of the odd ones go into queries and results. The products'
 // sums take a denormal's place for that of 2^-14 and cut off what lies 2^24 below, which leaves
-// about 17 bits. The values' codes, and fp32 calls' keys', are taken less 8 (and low more by 8 step)
+// about 17 bits beside the row's largest query column. The values' codes, and fp32 calls' keys', are taken less 8 (and low more by 8 step)
 // by one more fp16 sum: all of one sign, their sums over many tokens are far larger than what is
 // left of them (an fp32 decode of 100 to 4000 tokens was 3.9e-5 from the exact result without it,
 // 8e-6 with denormals less 8, 2.2e-7 so).
@@ -44,11 +44,14 @@
 // Measured on a GB300 (32/8 heads, d 128, pages of 16, groups of 64): 64 sequences of 1 to 8192 tokens 66 us a call, the
 // cache's bytes at 5.0 TB/s while the main kernel streams; 8 sequences of 30k to 131k (28/4 heads, pages of 64, groups of
 // 128) 81 us, 5.7 TB/s. 16 keys of 8 rows take about 230 instructions of a warp (70 to take codes apart, 32 to centre,
-// 16 products), which 12 warps issue in 0.47 us a tile of 128 keys; its bytes take 0.42. What made it fast, in order:
-//   producer lanes side by side instead of a tile after the other      88 -> 80 us (64 sequences)
+// 16 products), which 12 warps issue in 0.47 us a tile of 128 keys; its bytes take 0.42. What made it fast (64 sequences, in
+// the order of the steps; those between them are not listed):
+//   a ring of whole groups' stages, 12 consumers instead of 8          97 -> 88 us
+//   producer lanes side by side instead of a tile after the other      88 -> 80
 //   helper warps that sleep, masks only in steps with an edge, 2^10 from a register  80 -> 74
 //   two producer warps                                                76 -> 66
-//   a ring of whole groups' stages, 12 consumers instead of 8          97 -> 88
+// References of their own for the weights and for each group's W, without which large and small groups went wrong, cost
+// 65.2 -> 65.8 us (81 against 80 for the long ones, 65.8 against 62.8 for five drafts of 16 sequences with groups of 32).
 // Without effect: more consumers (16), 32 keys at a time with 12, products in two chains, a longer ring.
 #pragma once
 
