@@ -467,8 +467,9 @@ int art_read_kv4(const void* cache, int32_t group, const int32_t* block_table, c
  * bf16 (with q_offsets, num_tokens * G of 96 * batch and num_tokens * num_q_heads of
  * 2048 or more), reads the cache of the sequences with new tokens back into the workspace, as art_read_kv4 does, and
  * runs dense_extend's kernels on it. Path 1 is offered where batch * max_pages_per_seq
- * pages of keys and values take 4 GiB at most, and taken where the workspace holds
- * them; one of dense_extend_kv4_min_workspace_bytes keeps every call on path 0.
+ * pages of keys and values take 4 GiB at most, and taken where workspace_bytes holds
+ * them; dense_extend_kv4_min_workspace_bytes of the call's own num_tokens (the first
+ * bytes of a longer workspace may be passed) keep it on path 0.
  * Rounding. Path 0: codes enter the products as they are; queries exactly (bf16; columns
  * below 2^-26 of a row's largest lose bits) or to about 22 bits (fp32); weights times
  * step to 11 bits (bf16) or about 22 (fp32), or to 2^-30 of the row's largest in that

@@ -600,7 +600,7 @@ def dense_extend_kv4_workspace_bytes(shape: ArtShape, num_tokens: int, group: in
 
 
 def dense_extend_kv4_min_workspace_bytes(shape: ArtShape, num_tokens: int, group: int) -> int:
-    """The least that a call takes; with it every call attends over the codes (see include/art.h)."""
+    """The least that a call of so many tokens takes; with it the call attends over the codes (see include/art.h)."""
     return int(lib().dense_extend_kv4_min_workspace_bytes(ctypes.byref(shape), int(num_tokens), int(group)))
 
 

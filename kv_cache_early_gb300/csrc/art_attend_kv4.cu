@@ -46,6 +46,7 @@ constexpr size_t kReadBackMost = 4ull << 30;  // bytes of a pool at most
 // What a call needs of the workspace, by its path. Path 1: dense_extend's part, the pool's block table, the pool.
 struct Kv4Workspace {
     size_t codes;  // path 0; 0 where its sizes are not supported
+    size_t least;  // of a call with so many tokens or fewer, those without offsets (a token a sequence) among them
     size_t table, pool, whole;  // path 1: offsets of the last two and the bytes, whole 0 where it is not offered
 };
 static Kv4Workspace kv4_workspace(const art_shape& s, int num_tokens, bool offsets) {
@@ -54,7 +55,11 @@ static Kv4Workspace kv4_workspace(const art_shape& s, int num_tokens, bool offse
     kv4_shape(p, s);
     p.T = num_tokens;
     p.shared = !offsets;
-    w.codes = attend_layout(p, nullptr);
+    w.codes = w.least = attend_layout(p, nullptr);
+    if (offsets && w.codes != 0 && num_tokens >= s.batch) {
+        const size_t step = kv4_workspace(s, s.batch, false).codes;  // 0 where it is not supported
+        if (step > w.least) w.least = step;
+    }
     const int G = s.num_q_heads / s.num_kv_heads;
     if (!offsets || s.dtype != ART_DTYPE_BF16 || (long long)num_tokens * G < (long long)kReadBackRows * s.batch ||
         (long long)num_tokens * s.num_q_heads < kReadBackAll)
@@ -67,7 +72,7 @@ static Kv4Workspace kv4_workspace(const art_shape& s, int num_tokens, bool offse
     t.T = num_tokens;
     const size_t need = attend_layout(t, nullptr);
     if (need == 0) return w;
-    w.table = up256(need > w.codes ? need : w.codes);
+    w.table = up256(need > w.least ? need : w.least);  // so that the least workspace never holds path 1
     w.pool = up256(w.table + pages * sizeof(int32_t));
     w.whole = w.pool + 2 * pages * page;
     return w;
@@ -81,14 +86,8 @@ extern "C" {
 
 static size_t kv4_bytes(const art_shape* shape, int32_t num_tokens, int32_t group, bool least) {
     if (check_cache_shape(shape) != ART_OK || num_tokens < 0 || !kv4_group_ok(shape->head_dim, group)) return 0;
-    Kv4Workspace w = kv4_workspace(*shape, num_tokens, true);
-    if (w.codes == 0) return 0;
-    size_t need = !least && w.whole > w.codes ? w.whole : w.codes;
-    if (num_tokens >= shape->batch) {  // a call without offsets has no more tokens: room for it too, where it is supported
-        w = kv4_workspace(*shape, shape->batch, false);
-        if (w.codes > need) need = w.codes;
-    }
-    return need;
+    const Kv4Workspace w = kv4_workspace(*shape, num_tokens, true);
+    return !least && w.whole != 0 ? w.whole : w.least;
 }
 
 size_t dense_extend_kv4_workspace_bytes(const art_shape* shape, int32_t num_tokens, int32_t group) {

@@ -202,3 +202,14 @@ def test_read_refuses_tokens_times_heads_beyond_2_40(lib):
     assert at(128) == WS and at(129) == UNS
     s = good_shape(num_q_heads=1024, num_kv_heads=1024)
     assert read(lib, s, T=1 << 30, ws_bytes=0) == WS and read(lib, s, T=(1 << 30) + 1, ws_bytes=0) == UNS
+
+
+def test_the_least_workspace_keeps_path_0(lib):
+    """... where a decode step's part is larger than the pages of a small table, too (cross attention of many sequences)."""
+    for batch in (16, 4096):
+        for pages in (1, 2, 16):
+            s = good_shape(batch=batch, num_q_heads=64, num_kv_heads=8, page_size=8, max_pages_per_seq=pages)
+            for t in (12 * batch, 40 * batch):
+                least, full = (f(s, t, 64) for f in (K.dense_extend_kv4_min_workspace_bytes, K.dense_extend_kv4_workspace_bytes))
+                assert K.dense_extend_kv4_path(s, t, 64, least) == 0 and least < full
+                assert K.dense_extend_kv4_path(s, t, 64, full) == 1
