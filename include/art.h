@@ -414,6 +414,7 @@ int dense_decode_shared(const void* q, const void* k_cache, const void* v_cache,
  * whole number nearest to (x - lowest) / step, 15 at most, 0 where step is 0.
  * All as in exact arithmetic, with ties to even. A group that holds a NaN or an
  * infinity, or spans 15 * 2^100 or more, becomes NaN as a whole (step 0, lowest NaN).
+ * A lowest of zero may have either sign.
  */
 size_t art_kv4_page_bytes(const art_shape* shape, int32_t group); /* 0: unsupported */
 
