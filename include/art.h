@@ -474,7 +474,7 @@ int art_read_kv4(const void* cache, int32_t group, const int32_t* block_table, c
  * Rounding. Path 0: codes enter the products as they are; queries exactly (bf16; columns
  * below 2^-26 of a row's largest lose bits) or to about 22 bits (fp32); weights times
  * step to 11 bits (bf16) or about 22 (fp32), or to 2^-30 of the row's largest in that
- * group of columns, where that is more. In bf16 a step of the keys' product (16 columns and the
+ * group of columns (2^-23 where steps are below 2^-92), where that is more. In bf16 a step of the keys' product (16 columns and the
  * sum so far) is cut at 2^-14 of the row's largest query column times the key's step,
  * so that a score keeps about 17 bits beside that column; with fp32 queries at fp32's
  * own. Scores, the softmax's statistics and all sums are fp32. Path 1: keys and values are rounded
@@ -483,7 +483,8 @@ int art_read_kv4(const void* cache, int32_t group, const int32_t* block_table, c
  * sequence see must be finite for the others too. Which path a call takes goes by the batch and the
  * workspace, so a caller who wants the same bits whatever is in the batch keeps to path 0.
  * Steps must not be negative, queries be below 2^100 in magnitude, scores and the terms they
- * are summed from in fp32's range.
+ * are summed from in fp32's range. On path 0 values may have any size where a token sees up to 2^20 keys,
+ * and are below 2^117 in magnitude beyond.
  * A token that sees no key, and every token of a sequence with a bad length or
  * page, gets a zero output. With bad offsets no output is written. What lies
  * outside a row's keys may be anything, on path 0 a group of NaN that another row sees too.

@@ -22,7 +22,7 @@
 // weights, their sums and what is multiplied by low are fp32.
 //
 // Range: a row has a reference for its weights and one for each group's W. The weights' own, R, follows the scores:
-// weights stay below 2^-12, so that sums of weights times lowest stay finite whatever is held. W's, a power of two F
+// weights stay below 2^-20, so that sums of weights times lowest stay finite (kWeightLift). W's, a power of two F
 // beside it (W = p F step), follows the maximum of score + log2(the group's step), so that W stays within fp16's range and
 // keeps its bits in every group, however small beside the others; values without a step need no W. Parts meet with R
 // and the sums as they are: a sum's exponent added to R would be lost where scores are beyond 2^24. Queries are scaled by a
@@ -68,9 +68,10 @@ constexpr int kKv4Producers = 2;
 // whatever is within 2^-19 of the largest.
 constexpr int kKv4Lift = 5;
 constexpr uint32_t kMostW = 0x7400u;  // 2^14 in fp16
-// A row's reference is set 20 to 21 above its largest score (in log2), and moves when one comes within 12.
-constexpr float kWeightLift = 20.f;
-constexpr float kMostWeight = 0x1p-12f;
+// A row's reference is set 28 to 29 above its largest score (in log2), and moves when one comes within 20: sums of weights
+// times lowest are finite for 2^20 keys of whatever size, and for 2^30 of up to 2^117.
+constexpr float kWeightLift = 28.f;
+constexpr float kMostWeight = 0x1p-20f;
 constexpr int kMostFactor = 126;        // F = 2^126 at most: its inverse is a normal number
 constexpr float kNoReference = -3.40282347e38f;  // of a row that has seen no key, no score is lower: any key's weight passes the limit
 

@@ -146,3 +146,23 @@ def test_scores_far_below_zero(dtype, size, new):
             u, w = (2.0 ** -8, 2.0 ** -11) if dtype == "bf16" else (2.0 ** -24, 2.0 ** -22)
             tol = u * np.abs(ref) + 8 * w * s + (8 * n ** 0.5 + 16) * 2.0 ** -24 * (15 * step + np.abs(low))[:seen].max(0)
             assert np.all(np.abs(got[off[b] + i] - ref) <= tol), (b, i, np.max(np.abs(got[off[b] + i] - ref) / tol))
+
+
+@BOTH
+def test_many_keys_of_the_largest_values(dtype):
+    """160 sequences of 131,072 tokens whose values are one number near the type's largest; scores rise once, by 7.9 in log2,
+    after each warp's first keys. All tokens lie in two pages, which every table row names again and again."""
+    d, group, page, B, n = 64, 64, 64, 160, 1 << 17
+    value = -1.5 * 2.0 ** 127
+    pool = Pool4(np.random.default_rng(0), dtype, 1, d, page, group, [2 * page])
+    high = rounded(np.full(1, 7.9 * 8 / 1.4426950408889634 / d), "bf16").item()
+    for t in range(2 * page):
+        pool.put(0, t, 0, 0, np.full(d, 0.0 if t < page else high))
+        pool.put(0, t, 0, 1, np.full(d, value))
+    first, rest = (int(x) for x in pool.table[0, :2])
+    table = np.full((B, n // page), rest, np.int32)
+    table[:, :24] = first
+    pool.table, pool.seq_lens = table, np.full(B, n, np.int32)
+    got = run(pool, np.ones((B, 4, d)), None, False, 4)
+    # attention over one number: the output's rounding, and sums of n equal fp32 products as they grow
+    assert np.all(np.abs(got / value - 1) <= (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24 * 8 * n ** 0.5)), got.ravel()[:4]
